@@ -1,5 +1,6 @@
 /*
- * moe.h - C ABI of the GB300 (sm_103a) single-GPU Mixture-of-Experts layer forward.
+ * moe.h - C ABI of the GB300 (sm_103a) single-GPU Mixture-of-Experts layer forward, and of the
+ * operators that train one.
  *
  * The layer (page "DeepSeek V4 MegaMoE Kernel 深度解析", section 经典 MoE 的计算过程):
  *   gate GEMM -> score (softmax | sqrt(softplus)) -> top-K with e_score_correction_bias
@@ -472,6 +473,102 @@ moe_status moe_forward_batched_i8(const uint16_t* hidden, const float* w_gate, c
                                   int32_t* sorted_token_ids, int32_t* expert_ids, int32_t* inv_perm,
                                   int32_t* m_sum, int32_t* expert_num_tokens, void* ws, size_t ws_bytes,
                                   void* stream);
+
+/* --------------------------------------------------------------------------------------
+ * Training operators: the layer's row movement on 16- and 32-bit rows, the routing weights' gradient,
+ * and matrix products (dense or one weight per expert) with their gradients.  They have no counterpart
+ * in the method's description, which covers the forward; the layout is moe_permute's.
+ *
+ * Matrices are row-major with a pitch (moe_rows): row r starts at ptr + r * ld elements, ld >= columns.
+ * ptr NULL means "not given" where an argument is optional.  Rows are bf16, fp16 or fp32; every sum is
+ * taken in fp32 and rounded once, in a fixed order (equal inputs give equal bits).
+ * Sorted buffers have U rows (moe_msum_upper, or E * max_tokens for the BatchedExperts layout); padding
+ * rows are never read and never written.
+ * ws: a workspace whose first 256 bytes hold the device status word, zero-filled once before first use.
+ * ------------------------------------------------------------------------------------ */
+typedef enum { MOE_BF16 = 0, MOE_F16 = 1, MOE_F32 = 2 } moe_dtype;
+typedef struct {
+  void* ptr;
+  int64_t ld;             /* elements from one row to the next */
+} moe_rows;
+
+/* Workspace bytes of moe_dispatch, moe_combine, their backward calls and moe_route_backward. */
+moe_status moe_workspace_size_rows(int T, int K, int E, size_t* bytes);
+
+/* Token rows sorted by expert: the index outputs of moe_permute for (topk_ids, align) and
+ *   x_perm[inv_perm[t,k]] = x[t].
+ * x [T, H], x_perm [U, H] of type dt with U = moe_msum_upper(T, K, E, align); the index outputs as in
+ * moe_permute (expert_counts may be NULL).  H >= 1, 1 <= K <= 32.  An id outside [0, E) records
+ * MOE_ERR_DEVICE_INDEX and the outputs are unspecified. */
+moe_status moe_dispatch(moe_dtype dt, const int32_t* topk_ids, moe_rows x, int T, int H, int E, int K, int align,
+                        moe_rows x_perm, int32_t* sorted_token_ids, int32_t* expert_ids, int32_t* inv_perm,
+                        int32_t* m_sum, int32_t* expert_counts, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradient of moe_dispatch's rows: dx[t] = sum_k dx_perm[inv_perm[t,k]] + residual[t].
+ * dx_perm [U, H], residual [T, H] (optional; may be dx itself), dx [T, H].  inv_perm entries of -1 (pairs a
+ * full BatchedExperts slot dropped) add nothing; others outside [0, U) record MOE_ERR_DEVICE_INDEX and are
+ * skipped. */
+moe_status moe_dispatch_backward(moe_dtype dt, moe_rows dx_perm, const int32_t* inv_perm, moe_rows residual, int T, int H,
+                                 int K, int U, moe_rows dx, void* ws, size_t ws_bytes, void* stream);
+
+/* out[t] = sum_k topk_w[t,k] * y_perm[inv_perm[t,k]] + residual[t], summed in k order, the residual last.
+ * y_perm [U, H], topk_w [T, K] fp32 or NULL (plain sum), residual [T, H] (optional; may be out itself), out
+ * [T, H].  inv_perm entries as in moe_dispatch_backward. */
+moe_status moe_combine(moe_dtype dt, moe_rows y_perm, const int32_t* inv_perm, const float* topk_w, moe_rows residual,
+                       int T, int H, int K, int U, moe_rows out, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradients of moe_combine (the residual's is dout itself):
+ *   dy_perm[inv_perm[t,k]] = topk_w[t,k] * dout[t]
+ *   dtopk_w[t,k]           = sum_h dout[t,h] * y_perm[inv_perm[t,k], h]      (0 for a dropped pair)
+ * dtopk_w [T, K] fp32 and y_perm are both given or both left out (topk_w fixed, or NULL for a plain sum).
+ * dy_perm may be y_perm itself. */
+moe_status moe_combine_backward(moe_dtype dt, moe_rows dout, moe_rows y_perm, const int32_t* inv_perm,
+                                const float* topk_w, int T, int H, int K, int U, moe_rows dy_perm, float* dtopk_w,
+                                void* ws, size_t ws_bytes, void* stream);
+
+/* Gradient of moe_route's weights with respect to its logits: dlogits [T, E] of type dt from dtopk_w [T, K],
+ * with logits [T, E] (moe_route's logits_out), topk_ids and topk_w as moe_route wrote them for the same fn
+ * and renormalize.  The selection has no gradient.  E <= 1024, K <= 32; logits and dlogits 16-byte aligned. */
+moe_status moe_route_backward(const float* logits, const int32_t* topk_ids, const float* topk_w, const float* dtopk_w,
+                              int T, int E, int K, moe_score_fn fn, int renormalize, moe_dtype dt, void* dlogits, void* ws,
+                              size_t ws_bytes, void* stream);
+
+/* Activations of moe_linear.  GELU is z * Phi(z).  SWIGLU: z has N = 2I columns, y has I:
+ * y = silu(z[:, 0:I]) * z[:, I:2I] (W13's row order: gate first). */
+typedef enum {
+  MOE_ACT_NONE = 0,
+  MOE_ACT_RELU = 1,
+  MOE_ACT_SILU = 2,
+  MOE_ACT_GELU = 3,
+  MOE_ACT_SWIGLU = 4
+} moe_act;
+
+/* Workspace bytes of moe_linear (which needs its first 256 only) and moe_linear_backward. */
+moe_status moe_workspace_size_linear(int rows, int N, int K, int E, moe_act act, size_t* bytes);
+
+/* Matrix product with bias, activation and residual in its epilogue:
+ *   z = x @ w^T + bias;  y = act(z) + residual.
+ * Dense (E = 0, expert_counts NULL): x [rows, K], w [N, K], bias [N].
+ * Per expert (E >= 1): w [E, N, K], bias [E, N]; the rows of expert e are expert_counts[e] rows from row
+ * sum_{e' < e} round_up(expert_counts[e'], align) of buffers with `rows` rows (moe_dispatch's x_perm);
+ * a segment that would leave the buffers records MOE_ERR_DEVICE_INDEX and is cut.
+ * x, w, y, z, residual are bf16 or fp16 (fp32 returns MOE_ERR_UNSUPPORTED); bias fp32 or NULL.  residual and
+ * y have the columns of act(z); residual may be y itself.  z (optional) receives the products before the
+ * activation, for the backward call.  K and N are multiples of 8 (SWIGLU: N of 16), pitches multiples of
+ * 8, pointers 16-byte aligned; w is contiguous.  E <= 1024. */
+moe_status moe_linear(moe_dtype dt, moe_rows x, const void* w, const float* bias, moe_rows residual, moe_act act,
+                      const int32_t* expert_counts, int rows, int N, int K, int E, int align, moe_rows y, moe_rows z,
+                      void* ws, size_t ws_bytes, void* stream);
+
+/* Gradients of moe_linear: with dz = dy * act'(z), rounded to the rows' type,
+ *   dx = dz @ w + dx_residual;  dw[e] = dz_e^T @ x_e;  dbias[e] = sum over e's rows of dz before its rounding.
+ * dx, dw ([N, K] or [E, N, K], contiguous) and dbias ([N] or [E, N] fp32) are optional, one at least; w is
+ * read for dx, x for dw, z (as moe_linear wrote it) for act other than NONE.  dx_residual may be dx itself.
+ * An expert without rows gets zero dw and dbias.  ws: moe_workspace_size_linear bytes. */
+moe_status moe_linear_backward(moe_dtype dt, moe_rows dy, moe_rows x, const void* w, moe_rows z, moe_act act,
+                               const int32_t* expert_counts, int rows, int N, int K, int E, int align,
+                               moe_rows dx_residual, moe_rows dx, void* dw, float* dbias, void* ws, size_t ws_bytes,
+                               void* stream);
 
 /* Self-test of the device failure path (no counterpart in the method's description): launches one
  * bounded wait that nothing can satisfy, through the primitives the hot path uses.  mode 0: a

@@ -18,6 +18,8 @@ W_MXFP4, W_NVFP4, W_INT8, W_INT8_B256 = 0, 1, 2, 3
 SCORE_FNS = {"softmax": SCORE_SOFTMAX, "sqrt_softplus": SCORE_SQRT_SOFTPLUS}
 WFMTS = {"mxfp4": W_MXFP4, "nvfp4": W_NVFP4, "int8": W_INT8, "int8b": W_INT8_B256}
 I8_FMTS = (W_INT8, W_INT8_B256)
+DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "swiglu": 4}
 
 
 class MoeError(RuntimeError):
@@ -29,6 +31,10 @@ class MoeError(RuntimeError):
 class _Weight(ctypes.Structure):
     _fields_ = [("packed", ctypes.c_void_p), ("tscale", ctypes.c_void_p), ("fmt", ctypes.c_int),
                 ("E", ctypes.c_int), ("N", ctypes.c_int), ("Kd", ctypes.c_int), ("pair", ctypes.c_int)]
+
+
+class _Rows(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("ld", ctypes.c_int64)]
 
 
 _lib = None
@@ -114,6 +120,25 @@ def lib():
         L.moe_forward_batched_i8.argtypes = L.moe_forward_batched.argtypes
         L.moe_forward_batched_i8.restype = S
         L.moe_selftest_wait_timeout.argtypes = [P, Z, I, P]
+        R = _Rows
+        L.moe_workspace_size_rows.restype = S
+        L.moe_workspace_size_rows.argtypes = [I, I, I, ctypes.POINTER(Z)]
+        L.moe_dispatch.restype = S
+        L.moe_dispatch.argtypes = [I, P, R, I, I, I, I, I, R, P, P, P, P, P, P, Z, P]
+        L.moe_dispatch_backward.restype = S
+        L.moe_dispatch_backward.argtypes = [I, R, P, R, I, I, I, I, R, P, Z, P]
+        L.moe_combine.restype = S
+        L.moe_combine.argtypes = [I, R, P, P, R, I, I, I, I, R, P, Z, P]
+        L.moe_combine_backward.restype = S
+        L.moe_combine_backward.argtypes = [I, R, R, P, P, I, I, I, I, R, P, P, Z, P]
+        L.moe_route_backward.restype = S
+        L.moe_route_backward.argtypes = [P, P, P, P, I, I, I, I, I, I, P, P, Z, P]
+        L.moe_workspace_size_linear.restype = S
+        L.moe_workspace_size_linear.argtypes = [I, I, I, I, I, ctypes.POINTER(Z)]
+        L.moe_linear.restype = S
+        L.moe_linear.argtypes = [I, R, P, P, R, I, P, I, I, I, I, I, R, R, P, Z, P]
+        L.moe_linear_backward.restype = S
+        L.moe_linear_backward.argtypes = [I, R, R, P, R, I, P, I, I, I, I, I, R, R, P, P, P, Z, P]
         L.moe_get_error.restype = S
         L.moe_get_error.argtypes = [P, P, ctypes.POINTER(ctypes.c_int)]
         L.moe_status_str.restype = ctypes.c_char_p
@@ -539,6 +564,159 @@ def forward_batched_i8(hidden, w_gate, gate_bias, e_score_bias, I, K, max_tokens
         _ptr(inv_perm, torch.int32, "inv_perm"), _ptr(m_sum, torch.int32, "m_sum"),
         _ptr(expert_num_tokens, torch.int32, "expert_num_tokens"), _ptr(ws, torch.uint8, "ws"), ws.numel(),
         _stream()), "moe_forward_batched_i8")
+
+
+# ------------------------------------------------------------------ training operators
+
+def _rows(t, dtype, cols, name, rows=None):
+    """A row-major matrix argument: any row pitch, unit column stride.  None: not given."""
+    if t is None:
+        return _Rows(None, 0)
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must have dtype {dtype}, got {t.dtype}")
+    if t.dim() != 2 or t.shape[1] != cols or (rows is not None and t.shape[0] != rows):
+        raise ValueError(f"{name} must have shape [{'*' if rows is None else rows}, {cols}], got {list(t.shape)}")
+    if (cols > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < cols):
+        raise ValueError(f"{name} must be row-major with unit column stride and rows that do not overlap")
+    # one row: the pitch is never used, its width (in whole 16-byte units) stands in
+    return _Rows(t.data_ptr(), t.stride(0) if t.shape[0] > 1 else (cols + 7) // 8 * 8)
+
+
+def _full(t, dtype, shape, name):
+    """A contiguous argument of exactly this shape.  None: not given."""
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+    return _ptr(t, dtype, name)
+
+
+def _dtype(t, name):
+    if t.dtype not in DTYPES:
+        raise TypeError(f"{name} must be bfloat16, float16 or float32, got {t.dtype}")
+    return DTYPES[t.dtype]
+
+
+def workspace_size_rows(T, K, E):
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_workspace_size_rows(T, K, E, ctypes.byref(n)), "moe_workspace_size_rows")
+    return int(n.value)
+
+
+def new_workspace_rows(T, K, E, device="cuda"):
+    """A zero-filled workspace for dispatch, combine, their backward calls and route_backward."""
+    return torch.zeros(workspace_size_rows(T, K, E), dtype=torch.uint8, device=device)
+
+
+def dispatch(topk_ids, x, E, align, x_perm, sorted_token_ids, expert_ids, inv_perm, m_sum, ws, expert_counts=None):
+    """Token rows x [T, H] sorted by expert into x_perm [msum_upper(T, K, E, align), H], with permute's index outputs."""
+    T, K = topk_ids.shape
+    H = x.shape[1]
+    U = msum_upper(T, K, E, align)
+    dt = _dtype(x, "x")
+    _check(lib().moe_dispatch(dt, _ptr(topk_ids, torch.int32, "topk_ids"), _rows(x, x.dtype, H, "x", T), T, H, E, K, align,
+                              _rows(x_perm, x.dtype, H, "x_perm", U),
+                              _full(sorted_token_ids, torch.int32, (U,), "sorted_token_ids"),
+                              _full(expert_ids, torch.int32, (U,), "expert_ids"),
+                              _full(inv_perm, torch.int32, (T, K), "inv_perm"), _full(m_sum, torch.int32, (1,), "m_sum"),
+                              _full(expert_counts, torch.int32, (E,), "expert_counts"), _ptr(ws, torch.uint8, "ws"),
+                              ws.numel(), _stream()), "moe_dispatch")
+
+
+def dispatch_backward(dx_perm, inv_perm, dx, ws, residual=None):
+    """dx[t] = sum_k dx_perm[inv_perm[t, k]] (+ residual[t])."""
+    T, K = inv_perm.shape
+    H, U = dx_perm.shape[1], dx_perm.shape[0]
+    dt = _dtype(dx, "dx")
+    _check(lib().moe_dispatch_backward(dt, _rows(dx_perm, dx.dtype, H, "dx_perm"), _ptr(inv_perm, torch.int32, "inv_perm"),
+                                       _rows(residual, dx.dtype, H, "residual", T), T, H, K, U,
+                                       _rows(dx, dx.dtype, H, "dx", T), _ptr(ws, torch.uint8, "ws"), ws.numel(),
+                                       _stream()), "moe_dispatch_backward")
+
+
+def combine(y_perm, inv_perm, topk_w, out, ws, residual=None):
+    """out[t] = sum_k topk_w[t, k] * y_perm[inv_perm[t, k]] (+ residual[t]); topk_w None: plain sum."""
+    T, K = inv_perm.shape
+    H, U = y_perm.shape[1], y_perm.shape[0]
+    dt = _dtype(out, "out")
+    _check(lib().moe_combine(dt, _rows(y_perm, out.dtype, H, "y_perm"), _ptr(inv_perm, torch.int32, "inv_perm"),
+                             _full(topk_w, torch.float32, (T, K), "topk_w"), _rows(residual, out.dtype, H, "residual", T),
+                             T, H, K, U, _rows(out, out.dtype, H, "out", T), _ptr(ws, torch.uint8, "ws"), ws.numel(),
+                             _stream()), "moe_combine")
+
+
+def combine_backward(dout, y_perm, inv_perm, topk_w, dy_perm, dtopk_w, ws):
+    """dy_perm[inv_perm[t, k]] = topk_w[t, k] * dout[t] and dtopk_w[t, k] = <dout[t], y_perm[inv_perm[t, k]]>.
+    y_perm and dtopk_w None: the rows' gradient alone."""
+    T, K = inv_perm.shape
+    H, U = dout.shape[1], dy_perm.shape[0]
+    dt = _dtype(dout, "dout")
+    _check(lib().moe_combine_backward(dt, _rows(dout, dout.dtype, H, "dout", T), _rows(y_perm, dout.dtype, H, "y_perm", U),
+                                      _ptr(inv_perm, torch.int32, "inv_perm"),
+                                      _full(topk_w, torch.float32, (T, K), "topk_w"), T, H, K, U,
+                                      _rows(dy_perm, dout.dtype, H, "dy_perm", U),
+                                      _full(dtopk_w, torch.float32, (T, K), "dtopk_w"), _ptr(ws, torch.uint8, "ws"),
+                                      ws.numel(), _stream()), "moe_combine_backward")
+
+
+def route_backward(logits, topk_ids, topk_w, dtopk_w, score_fn, renormalize, dlogits, ws):
+    """dlogits [T, E] (bf16, fp16 or fp32) from dtopk_w, for route's logits_out, topk_ids and topk_w."""
+    T, K = topk_ids.shape
+    E = logits.shape[1]
+    dt = _dtype(dlogits, "dlogits")
+    _check(lib().moe_route_backward(_full(logits, torch.float32, (T, E), "logits"), _ptr(topk_ids, torch.int32, "topk_ids"),
+                                    _full(topk_w, torch.float32, (T, K), "topk_w"),
+                                    _full(dtopk_w, torch.float32, (T, K), "dtopk_w"), T, E, K,
+                                    SCORE_FNS.get(score_fn, score_fn), int(renormalize), dt,
+                                    _full(dlogits, dlogits.dtype, (T, E), "dlogits"), _ptr(ws, torch.uint8, "ws"),
+                                    ws.numel(), _stream()), "moe_route_backward")
+
+
+def workspace_size_linear(rows, N, K, E=0, act="none"):
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_workspace_size_linear(rows, N, K, E, ACTS.get(act, act), ctypes.byref(n)), "moe_workspace_size_linear")
+    return int(n.value)
+
+
+def new_workspace_linear(rows, N, K, E=0, act="none", device="cuda"):
+    """A zero-filled workspace for linear and linear_backward."""
+    return torch.zeros(workspace_size_linear(rows, N, K, E, act), dtype=torch.uint8, device=device)
+
+
+def _linear_dims(x, w, act, expert_counts):
+    E = w.shape[0] if expert_counts is not None else 0
+    if w.dim() != (3 if E else 2):
+        raise ValueError("w must have shape [N, K], or [E, N, K] with expert_counts")
+    N, K = w.shape[-2], w.shape[-1]
+    return x.shape[0], N, K, E, (N // 2 if ACTS.get(act, act) == ACTS["swiglu"] else N)
+
+
+def linear(x, w, y, ws, bias=None, act="none", residual=None, z=None, expert_counts=None, align=0):
+    """y = act(x @ w^T + bias) (+ residual); z (optional) receives the products before the activation.
+    w [N, K] dense, or [E, N, K] with expert_counts [E]: expert e's rows are its segment of the sorted rows."""
+    rows, N, K, E, cols = _linear_dims(x, w, act, expert_counts)
+    dt = _dtype(x, "x")
+    _check(lib().moe_linear(dt, _rows(x, x.dtype, K, "x"), _ptr(w, x.dtype, "w"),
+                            _full(bias, torch.float32, w.shape[:-1], "bias"), _rows(residual, x.dtype, cols, "residual", rows),
+                            ACTS.get(act, act), _full(expert_counts, torch.int32, (E,), "expert_counts"), rows, N, K, E,
+                            int(align), _rows(y, x.dtype, cols, "y", rows), _rows(z, x.dtype, N, "z", rows),
+                            _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream()), "moe_linear")
+
+
+def linear_backward(dy, x, w, ws, dx=None, dw=None, dbias=None, act="none", z=None, dx_residual=None,
+                    expert_counts=None, align=0):
+    """Gradients of linear: dx = dz @ w (+ dx_residual), dw = dz^T @ x, dbias = sum of dz, dz = dy * act'(z)."""
+    rows, N, K, E, cols = _linear_dims(dy, w, act, expert_counts)
+    dt = _dtype(dy, "dy")
+    _check(lib().moe_linear_backward(dt, _rows(dy, dy.dtype, cols, "dy"), _rows(x, dy.dtype, K, "x", rows),
+                                     _ptr(w, dy.dtype, "w"), _rows(z, dy.dtype, N, "z", rows), ACTS.get(act, act),
+                                     _full(expert_counts, torch.int32, (E,), "expert_counts"), rows, N, K, E, int(align),
+                                     _rows(dx_residual, dy.dtype, K, "dx_residual", rows),
+                                     _rows(dx, dy.dtype, K, "dx", rows), _full(dw, dy.dtype, w.shape, "dw"),
+                                     _full(dbias, torch.float32, w.shape[:-1], "dbias"), _ptr(ws, torch.uint8, "ws"),
+                                     ws.numel(), _stream()), "moe_linear_backward")
 
 
 def selftest_wait_timeout(ws, mode):

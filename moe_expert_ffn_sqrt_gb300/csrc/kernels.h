@@ -185,6 +185,52 @@ cudaError_t launch_wait_selftest(const uint32_t* never_set, uint32_t* status, in
 cudaError_t launch_unpermute_reduce(const uint16_t* y, const int32_t* inv_perm, const float* topk_w, int T, int K,
                                     int H, uint16_t* out, cudaStream_t stream);
 
+// ------------------------------------------------------------------------------------------
+// Training operators.
+
+// Element type codes (the values of moe_dtype) and activations (moe_act) of include/moe.h.
+constexpr int kBf16 = 0, kF16 = 1, kF32 = 2;
+constexpr int kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActSwiglu = 4;
+inline size_t dtype_bytes(int dt) { return dt == kF32 ? 4 : 2; }
+
+// A row-major matrix: row r starts at ptr + r * ld elements (ptr null: not given).
+struct RowsView {
+  void* ptr;
+  long long ld;
+};
+
+// train_rows.cu: rows of T tokens to and from U sorted rows through inv [T, K] (-1: dropped pair).
+cudaError_t launch_scatter_rows(int dt, RowsView x, const int32_t* inv, int T, int K, int H, int U, RowsView out,
+                                uint32_t* status, cudaStream_t stream);
+// out[t] = sum_k w[t,k] y[inv[t,k]] (+ res[t]); w null: plain sum.
+cudaError_t launch_sum_rows(int dt, RowsView y, const int32_t* inv, const float* w, RowsView res, int T, int K, int H,
+                            int U, RowsView out, uint32_t* status, cudaStream_t stream);
+// dy[inv[t,k]] = w[t,k] dout[t]; dw[t,k] = <dout[t], y[inv[t,k]]> (dw null: y is not read).
+cudaError_t launch_combine_grad(int dt, RowsView dout, RowsView y, const int32_t* inv, const float* w, int T, int K,
+                                int H, int U, RowsView dy, float* dw, uint32_t* status, cudaStream_t stream);
+
+// route_grad.cu (dt: type of out [T, E])
+cudaError_t launch_route_grad(int dt, const float* logits, const int32_t* ids, const float* w, const float* dw, int T,
+                              int E, int K, int softmax, int renorm, void* out, uint32_t* status, cudaStream_t stream);
+
+// linear.cu: products of `rows` rows with w [N, K] (counts null), or of E experts' row segments (counts
+// [E], segments padded to `align` rows inside buffers of `rows` rows) with w [E, N, K].
+constexpr int kLinearMaxExperts = 1024;
+struct LinearShape {
+  int rows, N, K, E, align, f16;
+  const int32_t* counts;
+};
+cudaError_t launch_linear(const LinearShape& p, RowsView x, const uint16_t* w, const float* bias, RowsView res, int act,
+                          RowsView y, RowsView z, uint32_t* status, cudaStream_t stream);
+cudaError_t launch_linear_dx(const LinearShape& p, RowsView dz, const uint16_t* w, RowsView res, RowsView dx,
+                             uint32_t* status, cudaStream_t stream);
+cudaError_t launch_linear_dw(const LinearShape& p, RowsView dz, RowsView x, uint16_t* dw, uint32_t* status,
+                             cudaStream_t stream);
+// dz = dy * act'(z) (act none: not written) and, with db, the bias gradient (part: E * linear_bias_slices * N floats).
+int linear_bias_slices(int N, int E, int act);
+cudaError_t launch_act_grad(const LinearShape& p, RowsView dy, RowsView z, int act, RowsView dz, float* part, float* db,
+                            uint32_t* status, cudaStream_t stream);
+
 // Launches `kernel` with programmatic stream serialization: it may begin (up to its
 // grid_dependency_wait) while the stream's previous kernel finishes.
 template <typename... KArgs, typename... Args>

@@ -1,0 +1,311 @@
+"""Dispatch, combine, their gradients and the router gradient against float64."""
+import numpy as np
+import pytest
+import torch
+
+import train_ref as R
+from gpu_util import ensure_lib
+from oracle import moe as O
+
+pytestmark = pytest.mark.gpu
+
+BF, HF, FP = torch.bfloat16, torch.float16, torch.float32
+SENTINEL = 7.25      # exact in every type; marks what a call must not write
+
+
+@pytest.fixture(scope="module")
+def M():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    return ensure_lib()
+
+
+def routing(T, E, K, seed, skew=0.0):
+    g = torch.Generator().manual_seed(seed)
+    keys = torch.rand(T, E, generator=g) + skew * torch.linspace(1, 0, E)
+    ids = keys.topk(K, 1).indices.to(torch.int32)
+    w = torch.rand(T, K, generator=g) + 0.05
+    return ids, w
+
+
+def rows(n, H, dt, seed, pitch=0):
+    """A [n, H] CPU matrix and its CUDA copy, the latter a slice of a wider buffer when pitch > H."""
+    v = torch.randn(n, H, generator=torch.Generator().manual_seed(seed)).to(dt)
+    if not pitch:
+        return v, v.cuda()
+    wide = torch.full((n, pitch), SENTINEL, dtype=dt, device="cuda")
+    wide[:, :H] = v.cuda()
+    return v, wide[:, :H]
+
+
+CASES = [  # T, H, E, K, align, dtype, extra pitch
+    (1, 7168, 256, 6, 16, BF, 0), (8, 7168, 256, 6, 16, BF, 8), (3, 1, 2, 1, 1, FP, 0), (5, 33, 4, 4, 1, HF, 0),
+    (37, 129, 7, 3, 64, BF, 3), (64, 1000, 16, 4, 128, HF, 0), (130, 24, 300, 8, 16, FP, 0), (257, 520, 16, 5, 256, FP, 4),
+    (1111, 136, 16, 4, 1, HF, 0), (700, 7168, 64, 2, 32, BF, 0), (5, 264, 40, 32, 16, BF, 0), (40, 8200, 8, 3, 16, FP, 0),
+]
+
+
+@pytest.mark.parametrize("T,H,E,K,align,dt,extra", CASES)
+def test_dispatch_and_its_gradient(M, T, H, E, K, align, dt, extra):
+    ids, _ = routing(T, E, K, T + H, skew=0.5)
+    U = M.msum_upper(T, K, E, align)
+    x, xd = rows(T, H, dt, 1, H + extra if extra else 0)
+    xp = torch.full((U, H + extra), SENTINEL, dtype=dt, device="cuda")[:, :H]
+    out = {n: torch.full((s,), -7, dtype=torch.int32, device="cuda")
+           for n, s in (("sorted", U), ("experts", U), ("m_sum", 1), ("counts", E))}
+    inv = torch.full((T, K), -7, dtype=torch.int32, device="cuda")
+    ws = M.new_workspace_rows(T, K, E)
+    M.dispatch(ids.cuda(), xd, E, align, xp, out["sorted"], out["experts"], inv, out["m_sum"], ws,
+               expert_counts=out["counts"])
+    assert M.get_error(ws) == M.OK
+    p = O.permute(ids.numpy(), E, align)
+    assert np.array_equal(inv.cpu().numpy(), p["inv_perm"])
+    assert np.array_equal(out["sorted"].cpu().numpy(), p["sorted_token_ids"])
+    assert np.array_equal(out["experts"].cpu().numpy(), p["expert_ids"])
+    assert int(out["m_sum"]) == p["m_sum"]
+    assert np.array_equal(out["counts"].cpu().numpy(), np.bincount(ids.numpy().reshape(-1), minlength=E))
+    ref = torch.full((U, H), SENTINEL, dtype=dt)
+    ref[inv.cpu().reshape(-1).long()] = x.repeat_interleave(K, 0)
+    assert torch.equal(xp.cpu(), ref), "rows moved exactly, padding rows untouched"
+    # gradient: padding rows hold NaN and must not be read; with and without a residual, and in place
+    g, gd = rows(U, H, dt, 2, H + extra if extra else 0)
+    pad = torch.ones(U, dtype=torch.bool)
+    pad[inv.cpu().reshape(-1).long()] = False
+    gd[pad.cuda()] = float("nan")
+    res, resd = rows(T, H, dt, 3)
+    for r in (None, res):
+        ref, mag = R.combine(g, inv.cpu(), None, r)
+        dx = torch.full((T, H + extra), SENTINEL, dtype=dt, device="cuda")
+        M.dispatch_backward(gd, inv, dx[:, :H], ws, residual=None if r is None else resd)
+        bound = R.half_step(dt) * ref.abs() * 1.01 + (K + 2) * R.U32 * mag + R.tiny(dt)
+        R.check(dx[:, :H], ref, bound, "dx")
+        assert (dx[:, H:] == SENTINEL).all()
+    first = dx[:, :H].clone()
+    M.dispatch_backward(gd, inv, resd, ws, residual=resd)
+    assert torch.equal(resd, first)
+    assert M.get_error(ws) == M.OK
+
+
+@pytest.mark.parametrize("T,H,E,K,align,dt,extra", CASES)
+def test_combine_and_its_gradients(M, T, H, E, K, align, dt, extra):
+    ids, w = routing(T, E, K, T * 3 + H)
+    inv, _ = R.positions(ids, E, align)
+    U = M.msum_upper(T, K, E, align)
+    if T > 4:
+        inv[1, 0] = -1                                   # dropped pairs, one token without any row
+        inv[T - 1] = -1
+    y, yd = rows(U, H, dt, 4, H + extra if extra else 0)
+    pad = torch.ones(U, dtype=torch.bool)
+    pad[inv[inv >= 0].long()] = False
+    yd[pad.cuda()] = float("nan")
+    res, resd = rows(T, H, dt, 5)
+    ws = M.new_workspace_rows(T, K, E)
+    for ww in (w, None):
+        for r in (None, res):
+            ref, mag = R.combine(y, inv, ww, r)
+            out = torch.full((T, H + extra), SENTINEL, dtype=dt, device="cuda")
+            M.combine(yd, inv.cuda(), None if ww is None else w.cuda(), out[:, :H], ws, residual=None if r is None else resd)
+            R.check(out[:, :H], ref, R.half_step(dt) * ref.abs() * 1.01 + (K + 2) * R.U32 * mag + R.tiny(dt), "out")
+            assert (out[:, H:] == SENTINEL).all()
+    d, dd = rows(T, H, dt, 6, H + extra if extra else 0)
+    ref, dwref, mag = R.combine_grad(d, y, inv, w, U)
+    dy = torch.full((U, H + extra), SENTINEL, dtype=dt, device="cuda")
+    dw = torch.full((T, K), float("nan"), device="cuda")
+    M.combine_backward(dd, yd, inv.cuda(), w.cuda(), dy[:, :H], dw, ws)
+    live = ~pad
+    R.check(dy[:, :H][live.cuda()], ref[live], (R.half_step(dt) * 1.01 + R.U32) * ref[live].abs() + R.tiny(dt), "dy")
+    assert (dy[:, :H][pad.cuda()] == SENTINEL).all() and (dy[:, H:] == SENTINEL).all()
+    R.check(dw, dwref, (H + 2) * R.U32 * mag + 1e-30, "dw")
+    assert (dw.cpu()[inv < 0] == 0).all()
+    # the rows' gradient alone gives the same rows; of the plain sum, dout's rows
+    dy2 = torch.full((U, H), SENTINEL, dtype=dt, device="cuda")
+    M.combine_backward(dd, None, inv.cuda(), w.cuda(), dy2, None, ws)
+    assert torch.equal(dy2, dy[:, :H])
+    M.combine_backward(dd, None, inv.cuda(), None, dy2, None, ws)
+    assert torch.equal(dy2[int(inv[0, 0])], dd[0])
+    assert M.get_error(ws) == M.OK
+
+
+def test_combine_gradient_against_differences(M):
+    # fp32 rows: the directional derivative of <c, combine(y, w)> by central differences of the kernel itself.
+    # The function is linear in y and in w, so the difference has no truncation error, only rounding.
+    T, H, E, K = 6, 96, 5, 3
+    ids, w = routing(T, E, K, 11)
+    inv, _ = R.positions(ids, E, 4)
+    U = M.msum_upper(T, K, E, 4)
+    y, c = torch.randn(U, H), torch.randn(T, H)
+    vy, vw = torch.randn(U, H), torch.randn(T, K)
+    ws = M.new_workspace_rows(T, K, E)
+    dy, dw = torch.zeros(U, H, device="cuda"), torch.zeros(T, K, device="cuda")
+    M.combine_backward(c.cuda(), y.cuda(), inv.cuda(), w.cuda(), dy, dw, ws)
+
+    def f(yy, ww):
+        out = torch.empty(T, H, device="cuda")
+        M.combine(yy.cuda(), inv.cuda(), ww.cuda(), out, ws)
+        return float((out.double().cpu() * c.double()).sum())
+
+    mag = float((c.abs().double()).sum() * K * 20)       # magnitudes in the sums below
+    tol = 64 * R.U32 * mag
+    assert abs((f(y + vy, w) - f(y - vy, w)) / 2 - float((dy.cpu().double() * vy.double()).sum())) <= tol
+    assert abs((f(y, w + vw) - f(y, w - vw)) / 2 - float((dw.cpu().double() * vw.double()).sum())) <= tol
+
+
+def test_bad_rows_are_reported_and_skipped(M):
+    T, H, E, K, U = 4, 64, 3, 2, 8
+    inv = torch.tensor([[0, 1], [2, 99], [-5, 3], [4, 5]], dtype=torch.int32)
+    y = torch.randn(U, H)
+    ws = M.new_workspace_rows(T, K, E)
+    out = torch.empty(T, H, device="cuda")
+    M.combine(y.cuda(), inv.cuda(), None, out, ws)
+    assert M.get_error(ws) == M.ERR_DEVICE_INDEX
+    good = torch.where((inv >= 0) & (inv < U), inv, torch.full_like(inv, -1))
+    ref, mag = R.combine(y, good, None)
+    R.check(out, ref, 8 * R.U32 * mag, "out")
+    dy, dw = torch.zeros(U, H, device="cuda"), torch.full((T, K), 5.0, device="cuda")
+    M.combine_backward(out, y.cuda(), inv.cuda(), torch.ones(T, K, device="cuda"), dy, dw, ws)
+    assert M.get_error(ws) == M.ERR_DEVICE_INDEX
+    assert (dw.cpu()[good < 0] == 0).all() and (dy[6:] == 0).all()
+    # an expert id out of range
+    ids = torch.tensor([[0, 1], [2, 3], [0, 2], [1, 0]], dtype=torch.int32)
+    n = M.msum_upper(T, K, E, 1)
+    i = [torch.empty(s, dtype=torch.int32, device="cuda") for s in (n, n, 1)]
+    M.dispatch(ids.cuda(), y[:T].cuda(), E, 1, torch.zeros(n, H, device="cuda"), i[0], i[1],
+               torch.zeros(T, K, dtype=torch.int32, device="cuda"), i[2], ws)
+    assert M.get_error(ws) == M.ERR_DEVICE_INDEX
+    assert M.get_error(ws) == M.OK
+
+
+def test_no_tokens(M):
+    ws = M.new_workspace_rows(0, 2, 4)
+    z = torch.zeros(0, 64, dtype=BF, device="cuda")
+    e = torch.zeros(0, 2, dtype=torch.int32, device="cuda")
+    U = M.msum_upper(0, 2, 4, 16)
+    s = [torch.full((n,), 3, dtype=torch.int32, device="cuda") for n in (U, U, 1, 4)]
+    M.dispatch(e, z, 4, 16, torch.zeros(U, 64, dtype=BF, device="cuda"), s[0], s[1], e, s[2], ws, expert_counts=s[3])
+    assert (s[0] == 0).all() and (s[1] == -1).all() and int(s[2]) == 0 and (s[3] == 0).all()
+    M.combine(torch.zeros(U, 64, dtype=BF, device="cuda"), e, None, z, ws)
+    M.combine_backward(z, None, e, None, torch.zeros(U, 64, dtype=BF, device="cuda"), None, ws)
+    f = torch.zeros(0, 2, device="cuda")
+    M.route_backward(torch.zeros(0, 4, device="cuda"), e, f, f, "softmax", True, torch.zeros(0, 4, device="cuda"), ws)
+    assert M.get_error(ws) == M.OK
+
+
+def test_rows_beyond_32_bit_offsets(M):
+    # row offsets past 2^31 elements: a sorted buffer of 2^31 + elements with the live rows at its end
+    H, U = 65536, 32800                                   # 2.15e9 elements, 4.3 GB
+    y = torch.empty(U, H, dtype=BF, device="cuda")
+    last = torch.randn(2, H, device="cuda").to(BF)
+    y[U - 2:] = last
+    inv = torch.tensor([[U - 1, U - 2]], dtype=torch.int32, device="cuda")
+    ws = M.new_workspace_rows(1, 2, 4)
+    out = torch.empty(1, H, dtype=BF, device="cuda")
+    w = torch.tensor([[0.5, 2.0]], device="cuda")
+    M.combine(y, inv, w, out, ws)
+    ref = 0.5 * last[1].double() + 2 * last[0].double()
+    R.check(out[0], ref.cpu(), (R.half_step(BF) * 1.01 * ref.abs() + 4 * R.U32 * (last.double().abs().sum(0) * 2)).cpu(), "out")
+    dw = torch.empty(1, 2, device="cuda")
+    M.combine_backward(out, y, inv, w, y, dw, ws)          # the gradient over the rows themselves
+    assert torch.equal(y[U - 2], (out[0].float() * 2).to(BF)) and torch.equal(y[U - 1], (out[0].float() * 0.5).to(BF))
+    assert M.get_error(ws) == M.OK
+
+
+# ------------------------------------------------------------------------------------- router gradient
+
+@pytest.mark.parametrize("fn", ["softmax", "sqrt_softplus"])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("T,E,K,dt", [(1, 256, 6, FP), (8, 256, 6, BF), (33, 4, 4, FP), (77, 1024, 8, FP), (500, 33, 1, FP),
+                                      (3, 1, 1, FP), (20, 70, 32, HF), (2049, 64, 6, FP)])
+def test_route_gradient(M, fn, renorm, T, E, K, dt):
+    g = torch.Generator().manual_seed(T + E + K)
+    logits = torch.randn(T, E, generator=g) * 3
+    ids = torch.rand(T, E, generator=g).topk(K, 1).indices.to(torch.int32)       # any selection, not only the best
+    w = R.route_weights(logits, ids, fn, renorm).float()
+    dw = torch.randn(T, K, generator=g)
+    ref = R.route_grad(logits, ids, dw, fn, renorm)
+    ws = M.new_workspace_rows(T, K, E)
+    out = torch.full((T, E), float("nan"), dtype=dt, device="cuda")
+    M.route_backward(logits.cuda(), ids.cuda(), w.cuda(), dw.cuda(), fn, renorm, out, ws)
+    assert M.get_error(ws) == M.OK
+    terms = (w.double() * dw.double()).abs()
+    scale = terms + w.double() * terms.sum(1, keepdim=True)          # what each w (dw - c) is made of
+    bound = torch.zeros(T, E, dtype=R.F64).scatter_(1, ids.long(), scale)
+    if fn == "softmax":
+        bound = bound + torch.softmax(logits.double(), 1) * terms.sum(1, keepdim=True)
+    # sums of up to E terms, an exponential whose argument is off by |l| half steps, about 64 roundings in all
+    bound = bound * (E + 64 + 2 * logits.abs().max()) * R.U32
+    R.check(out, ref, bound + R.half_step(dt) * ref.abs() * 1.01 + R.tiny(dt), "dlogits")
+
+
+def test_route_gradient_of_underflowing_scores(M):
+    # logits so low that every sqrt(softplus) score underflows in the formula s'(l) = sigmoid / (2 s): the
+    # gradient of the normalised weights is still w_k (dw_k - c) / 2; masked experts (-inf) get none
+    logits = torch.tensor([[-150.0, -150.0, -160.0, float("-inf")], [-30.0, 0.0, 60.0, float("-inf")]])
+    ids = torch.tensor([[0, 1], [2, 0]], dtype=torch.int32)
+    l = logits.double().gather(1, ids.long())
+    s = torch.where(l < -20, (l / 2).exp(), torch.nn.functional.softplus(l, threshold=1e9).sqrt())
+    w = (s / s.sum(1, keepdim=True)).float()
+    dw = torch.tensor([[1.0, -0.5], [0.25, 2.0]])
+    ws = M.new_workspace_rows(2, 2, 4)
+    out = torch.empty(2, 4, device="cuda")
+    M.route_backward(logits.cuda(), ids.cuda(), w.cuda(), dw.cuda(), "sqrt_softplus", True, out, ws)
+    c = (w.double() * dw.double()).sum(1, keepdim=True)
+    ratio = torch.where(l < -20, torch.ones_like(l), torch.sigmoid(l) / torch.nn.functional.softplus(l, threshold=1e9))
+    ref = torch.zeros(2, 4, dtype=R.F64).scatter_(1, ids.long(), w.double() * (dw.double() - c) * ratio / 2)
+    part = torch.zeros(2, 4, dtype=R.F64).scatter_(1, ids.long(), w.double() * (dw.double().abs() + c.abs()) * ratio / 2)
+    R.check(out, ref, 64 * R.U32 * part + 1e-30, "dlogits")
+    M.route_backward(logits.cuda(), ids.cuda(), w.cuda(), dw.cuda(), "softmax", False, out, ws)
+    assert torch.isfinite(out).all() and (out[:, 3] == 0).all()
+
+
+def test_route_gradient_reports_bad_ids_and_adds_repeated_ones(M):
+    logits = torch.randn(2, 8)
+    ids = torch.tensor([[3, 3], [1, 8]], dtype=torch.int32)
+    w, dw = torch.tensor([[0.5, 0.25], [0.5, 0.5]]), torch.tensor([[1.0, 2.0], [1.0, 1.0]])
+    ws = M.new_workspace_rows(2, 2, 8)
+    out = torch.empty(2, 8, device="cuda")
+    M.route_backward(logits.cuda(), ids.cuda(), w.cuda(), dw.cuda(), "sqrt_softplus", False, out, ws)
+    assert M.get_error(ws) == M.ERR_DEVICE_INDEX
+    l = logits.double()
+    r = torch.sigmoid(l) / torch.nn.functional.softplus(l) / 2
+    assert abs(float(out[0, 3]) - float(1.0 * r[0, 3])) < 1e-5 and int((out[0] != 0).sum()) == 1
+    assert abs(float(out[1, 1]) - float(0.5 * r[1, 1])) < 1e-5 and int((out[1] != 0).sum()) == 1
+
+
+def test_rows_on_another_stream_and_in_a_graph(M):
+    T, H, E, K, align = 50, 256, 8, 3, 16
+    ids, w = routing(T, E, K, 3)
+    inv, _ = R.positions(ids, E, align)
+    U = M.msum_upper(T, K, E, align)
+    y = torch.zeros(U, H, dtype=BF, device="cuda")
+    idd, wd, invd = ids.cuda(), w.cuda(), inv.cuda()
+    ws = M.new_workspace_rows(T, K, E)
+    x = torch.randn(T, H, device="cuda").to(BF)
+    out = torch.zeros(T, H, dtype=BF, device="cuda")
+    i = [torch.zeros(n, dtype=torch.int32, device="cuda") for n in (U, U, 1)]
+
+    def step():
+        M.dispatch(idd, x, E, align, y, i[0], i[1], invd, i[2], ws)
+        M.combine(y, invd, wd, out, ws, residual=x)
+
+    step()
+    torch.cuda.synchronize()
+    want = out.clone()
+    s = torch.cuda.Stream()
+    out.zero_()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    s.synchronize()
+    assert torch.equal(out, want)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for k in range(3):
+        x.copy_(torch.randn(T, H, device="cuda").to(BF))
+        step()
+        want = out.clone()
+        out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+    assert M.get_error(ws) == M.OK
