@@ -14,8 +14,9 @@
 // Rows of experts: expert e's rows start at seg_e = sum_{e' < e} round_up(counts[e'], align) (the layout
 // of moe_permute).  Padding rows are never read into a result nor written: in the forward and the input
 // gradient a padding row is a column of the product that is not stored; in the weight gradient, where
-// rows are summed over, the last partial slab of a segment is fetched row by row with the padding
-// rows replaced by out-of-range ones, which read as zeros.
+// rows are summed over, each expert has tensor maps of its own whose rows end with its segment
+// (expert_maps_kernel), so that what a copy takes past the end reads as zeros.  (Fetching the last partial
+// slab row by row instead cost the 32-expert gradient 87 of 470 us.)
 //
 // Two kernels:
 //  * linear_pair_kernel: a CTA pair per 256 x 256 tile (cta_group::2, each CTA 128 output columns i and
@@ -43,13 +44,13 @@ constexpr int kLinMaxE = kLinearMaxExperts;
 constexpr int kPairB = 128 * 128;
 constexpr int kPairStage = kLinABytes + kPairB;      // 32 KB
 constexpr int kPairStages = 6;
-constexpr int kPairSmem = 1024 + kPairStages * kPairStage + 256 + 2 * (kLinMaxE + 1) * 4;
+constexpr int kPairSmem = 1024 + kPairStages * kPairStage + 256 + 4 * 32 * 80 + 2 * (kLinMaxE + 1) * 4;
 // split kernel: stages of A and the tile's B rows, as many as fit
-constexpr int kSplitRing = 208 * 1024;
+constexpr int kSplitRing = 208 * 1024;          // also: the slice's sums, then a piece per epilogue warp
 constexpr int kSplitMaxStages = 12;
 constexpr int kSplitSmem = 1024 + kSplitRing + 512;
 static_assert(kPairSmem <= 227 * 1024 && kSplitSmem <= 227 * 1024, "shared memory budget");
-static_assert(kSplitRing >= kLinBI * kLinBJ * 4, "the slices' sums fit the ring");
+static_assert(kSplitRing >= kLinBI * kLinBJ * 4 + 4 * 32 * 80, "the slices' sums and the pieces fit the ring");
 
 enum LinMode { kLinFwd = 0, kLinFwdGated = 1, kLinDx = 2, kLinDw = 3 };
 
@@ -108,16 +109,6 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map
         "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(bar)
         : "memory");
 }
-// Four rows of a map with a one-row box; rows outside the matrix read as zeros.
-__device__ __forceinline__ void tma_rows4_pair(uint32_t dst, const CUtensorMap* map, int c0, int y0, int y1, int y2, int y3,
-                                               uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.cta_group::2"
-      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
-      "l"(map), "r"(c0), "r"(y0), "r"(y1), "r"(y2), "r"(y3), "r"(bar)
-      : "memory");
-}
-
 // Instruction descriptor of kind::f16 (bf16 or fp16 operands, fp32 accumulation); a_mn / b_mn: the
 // operand's tile is contiguous along M / N instead of along the sum.
 __device__ __forceinline__ uint32_t lin_idesc(int f16, int a_mn, int b_mn, uint32_t M, uint32_t N) {
@@ -195,30 +186,37 @@ __device__ __forceinline__ float lin_silu(float v) { return __fdividef(v, 1.f + 
 // v Phi(v); erfc keeps its relative accuracy in the negative tail, where 1 + erf would cancel
 __device__ __forceinline__ float lin_gelu(float v) { return 0.5f * v * erfcf(v * -0.70710678118654752f); }
 
-// v holds 32 accumulator columns (output rows) of this lane's output column; neighbouring lanes
-// exchange halves so that each holds two neighbouring columns of 16 output rows: pair p of an even
-// lane is row 2p, of an odd lane row 2p + 1.
-__device__ __forceinline__ void lin_pairs(const float (&v)[32], float (&lo)[16], float (&hi)[16]) {
-  const bool odd = threadIdx.x & 1;
-#pragma unroll
-  for (int p = 0; p < 16; ++p) {
-    const float got = __shfl_xor_sync(0xffffffffu, odd ? v[2 * p] : v[2 * p + 1], 1);
-    lo[p] = odd ? got : v[2 * p];
-    hi[p] = odd ? v[2 * p + 1] : got;
-  }
-}
+// The epilogue works on pieces of 32 accumulator lanes (output columns) x 32 columns (output rows) per
+// warp, held as four 8-column groups of 8x8 fragments: v[8n + 2h + k] of thread t is lane t/4 + 8h,
+// column 8n + 2(t%4) + k of the piece (h, n, k: 0..3, 0..3, 0..1).  That is how tensor memory is read
+// (16 lanes x 256 bits) and what stmatrix / ldmatrix move, transposed, to and from rows of the output
+// type in shared memory; from there each row's 32 columns leave (or the residual's arrive) 16 bytes per
+// thread.
+constexpr int kPiecePitch = 80;                      // bytes per row: 64 + 16, free of bank conflicts both ways
+constexpr int kPieceBytes = 32 * kPiecePitch;
 
-// Where the epilogue's sums come from: this CTA's tensor memory, or the slices in the shared memory of
-// the cluster's CTAs ([column][128 lanes] fp32), added in slice order.
+// Where the sums come from: this CTA's tensor memory, or the slices that the cluster's CTAs keep in
+// shared memory, added in slice order.
 struct TmemSums {
   uint32_t acc;               // this warp's lane quarter, accumulator column 0
   __device__ __forceinline__ void operator()(int c0, int, float (&v)[32]) const {
     uint32_t r[2][16];
-    tc_ld_x16(acc + c0, r[0]);
-    tc_ld_x16(acc + c0 + 16, r[1]);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      asm volatile(
+          "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+          : "=r"(r[h][0]), "=r"(r[h][1]), "=r"(r[h][2]), "=r"(r[h][3]), "=r"(r[h][4]), "=r"(r[h][5]), "=r"(r[h][6]),
+            "=r"(r[h][7]), "=r"(r[h][8]), "=r"(r[h][9]), "=r"(r[h][10]), "=r"(r[h][11]), "=r"(r[h][12]), "=r"(r[h][13]),
+            "=r"(r[h][14]), "=r"(r[h][15])
+          : "r"(acc + c0 + (static_cast<uint32_t>(16 * h) << 16)));
     tc_wait_ld();
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j >> 4][j & 15]);
+    for (int n = 0; n < 4; ++n)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        v[8 * n + k] = __uint_as_float(r[0][4 * n + k]);
+        v[8 * n + 4 + k] = __uint_as_float(r[1][4 * n + k]);
+      }
   }
 };
 struct ZeroSums {
@@ -228,123 +226,186 @@ struct ZeroSums {
   }
 };
 struct ClusterSums {
-  uint32_t base;              // this lane's column 0 in the CTA's own shared memory
-  int slices;
+  uint32_t base;              // this thread's first value in its own shared memory; value i of 8-column group g
+  int slices;                 // is (8g + i) * 128 values further
   __device__ __forceinline__ void operator()(int c0, int left, float (&v)[32]) const {
 #pragma unroll
     for (int j = 0; j < 32; ++j) v[j] = 0.f;
     for (int s = 0; s < slices; ++s) {
-      const uint32_t p = mapa_shared(base, static_cast<uint32_t>(s)) + static_cast<uint32_t>(c0) * (kLinBI * 4);
+      const uint32_t p = mapa_shared(base, static_cast<uint32_t>(s)) + static_cast<uint32_t>(c0) * (128 * 4);
 #pragma unroll
       for (int j = 0; j < 32; ++j)
-        if (j < left) {
+        if ((j & ~7) < left) {
           float x;
-          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(p + j * (kLinBI * 4)) : "memory");
+          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(p + j * (128 * 4)) : "memory");
           v[j] += x;
         }
     }
   }
 };
 
-// Turns the sums of output rows [j0 + cb, j0 + ce) of tile t into outputs; this warp has lanes 32q .. of
-// the CTA's output columns, which start at column i0 (gated forward: at column i0 of y).
+__device__ __forceinline__ void stmatrix_x4_t(uint32_t addr, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r0), "r"(r1),
+               "r"(r2), "r"(r3)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix_x4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts16(uint32_t addr, const uint4& v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// Rows of 8 * U columns (U 16-byte units) between shared memory and the thread's share of global rows:
+// unit lane % U of rows lane / U + (32 / U) s, s = 0 .. U-1.
+template <int U>
+struct PieceRows {
+  int row, unit;
+  __device__ __forceinline__ explicit PieceRows(int lane) : row(lane / U), unit(lane % U) {}
+  __device__ __forceinline__ uint32_t at(uint32_t stage, int s) const {
+    return stage + static_cast<uint32_t>((row + 32 / U * s) * kPiecePitch + unit * 16);
+  }
+  // p: this thread's unit of row 0 of the piece; live: its columns exist; left: rows of the piece
+  __device__ __forceinline__ void store(uint32_t stage, uint16_t* p, long long ld, bool live, int left) const {
+#pragma unroll
+    for (int s = 0; s < U; ++s) {
+      const int r = row + 32 / U * s;
+      if (live && r < left) *reinterpret_cast<uint4*>(p + r * ld) = lds16(at(stage, s));
+    }
+  }
+  __device__ __forceinline__ void fetch(uint4 (&v)[U], const uint16_t* p, long long ld, bool live, int left) const {
+#pragma unroll
+    for (int s = 0; s < U; ++s) {
+      const int r = row + 32 / U * s;
+      v[s] = live && r < left ? *reinterpret_cast<const uint4*>(p + r * ld) : make_uint4(0, 0, 0, 0);
+    }
+  }
+};
+
+// Turns the sums of output rows [j0 + cb, j0 + ce) of tile t into outputs (cb a multiple of 8); this
+// warp has lanes 32q .. of the CTA's output columns, which start at column i0 (gated forward: of y).
+// stage: the warp's piece in shared memory.
 template <int MODE, class Sums>
 __device__ __forceinline__ void lin_drain(const LinArgs& a, const LinTile& t, int i0, int cb, int ce, const Sums& sums, int q,
-                                          int lane) {
-  // output column of this lane.  Gated forward: lanes 0..7 are gate rows, 8..15 the up rows of the same
-  // eight columns, 16..31 the next eight columns' likewise.
-  const int up = MODE == kLinFwdGated ? (lane >> 3) & 1 : 0;
-  const int i = MODE == kLinFwdGated ? i0 + q * 16 + (lane >> 4) * 8 + (lane & 7) : i0 + q * 32 + lane;
-  const bool live = i < a.i_ext;           // i_ext is a multiple of 8
-  const int i2 = i & ~1, odd = lane & 1;
-  const int zcol = MODE == kLinFwdGated ? i + up * a.i_ext : i;
-  const int n_all = MODE == kLinFwdGated ? 2 * a.i_ext : a.i_ext;
-  float bias = 0.f;
-  if ((MODE == kLinFwd || MODE == kLinFwdGated) && a.bias && live)
-    bias = __ldg(a.bias + static_cast<size_t>(t.e) * n_all + zcol);
+                                          int lane, uint32_t stage) {
+  constexpr bool kGated = MODE == kLinFwdGated, kFwd = MODE == kLinFwd || kGated;
+  constexpr int kU = kGated ? 2 : 4;                  // 16-byte units per output row
+  // accumulator lane l of the warp is output column iw + l; gated: lanes 16m + 0..7 are the gate rows of
+  // columns iw + 8m .., lanes 16m + 8..15 their up rows
+  const int iw = kGated ? i0 + q * 16 : i0 + q * 32;
+  float bias[4] = {0.f, 0.f, 0.f, 0.f};
+  if (kFwd && a.bias) {
+    const float* b = a.bias + static_cast<size_t>(t.e) * (kGated ? 2 * a.i_ext : a.i_ext);
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      const int col = kGated ? iw + (h >> 1) * 8 + (lane >> 2) : iw + 8 * h + (lane >> 2);
+      if (col < a.i_ext) bias[h] = __ldg(b + col + (kGated && (h & 1) ? a.i_ext : 0));
+    }
+  }
   // output row of accumulator column 0
   const long long jr = MODE == kLinDw ? static_cast<long long>(t.e) * a.j_ext + t.j0 : static_cast<long long>(t.row0) + t.j0;
-  // the residual of the next 32 columns is on its way while these are worked on
-  constexpr int kWords = MODE == kLinFwdGated ? 8 : 16;
-  auto row_of = [&](int p) { return MODE == kLinFwdGated ? 2 * (2 * p + odd) + up : 2 * p + odd; };
-  uint32_t res[kWords];
-  auto fetch = [&](int c) {
-    const uint16_t* rp = a.res + (jr + c) * a.ldr + i2;
-#pragma unroll
-    for (int p = 0; p < kWords; ++p)
-      res[p] = live && c + row_of(p) < ce ? *reinterpret_cast<const uint32_t*>(rp + row_of(p) * a.ldr) : 0u;
-  };
+  const PieceRows<kU> rows(lane);
+  const int col = iw + rows.unit * 8;
+  const bool live = col < a.i_ext;                    // i_ext is a multiple of 8
+  // this thread's matrix row for stmatrix / ldmatrix: row lane % 8 of matrix lane / 8
+  const uint32_t mat = stage + static_cast<uint32_t>((lane & 7) * kPiecePitch + (lane >> 3) * 16);
+  // the residual of the next piece is on its way while this one is worked on
   const bool has_res = MODE != kLinDw && a.res != nullptr;
-  if (has_res) fetch(cb);
+  uint4 res[kU];
+  if (has_res) rows.fetch(res, a.res + (jr + cb) * a.ldr + col, a.ldr, live, ce - cb);
 #pragma unroll 1
   for (int c0 = cb; c0 < ce; c0 += 32) {
     const int left = ce - c0;
     float v[32];
     sums(c0, left, v);
-    if (MODE == kLinFwd || MODE == kLinFwdGated) {
+    if (kFwd) {
 #pragma unroll
-      for (int j = 0; j < 32; ++j) v[j] += bias;
+      for (int j = 0; j < 32; ++j) v[j] += bias[(j >> 1) & 3];
       if (a.z) {
-        float lo[16], hi[16];
-        lin_pairs(v, lo, hi);
-        uint16_t* zp = a.z + (jr + c0) * a.ldz + (zcol & ~1);
+        const PieceRows<4> zr(lane);
+        const int zc = kGated ? iw + (zr.unit >> 1) * 8 : iw + zr.unit * 8;
+        __syncwarp();
 #pragma unroll
-        for (int p = 0; p < 16; ++p) {
-          const int j = 2 * p + odd;
-          if (live && j < left) *reinterpret_cast<uint32_t*>(zp + j * a.ldz) = lin_pack(lo[p], hi[p], a.f16);
-        }
+        for (int n = 0; n < 4; ++n)
+          stmatrix_x4_t(mat + n * 8 * kPiecePitch, lin_pack(v[8 * n], v[8 * n + 1], a.f16),
+                        lin_pack(v[8 * n + 2], v[8 * n + 3], a.f16), lin_pack(v[8 * n + 4], v[8 * n + 5], a.f16),
+                        lin_pack(v[8 * n + 6], v[8 * n + 7], a.f16));
+        __syncwarp();
+        zr.store(stage, a.z + (jr + c0) * a.ldz + zc + (kGated && (zr.unit & 1) ? a.i_ext : 0), a.ldz, zc < a.i_ext, left);
       }
     }
-    float lo[kWords], hi[kWords];
-    if constexpr (MODE == kLinFwdGated) {
-      // gate and up meet: the gate lanes take column 2p, the up lanes column 2p + 1
-      float h[16];
+    constexpr int kV = kGated ? 16 : 32;              // gated: o[4n + 2m + k] is column iw + 8m + t/4
+    float o[kV];
+    if constexpr (kGated) {
 #pragma unroll
-      for (int p = 0; p < 16; ++p) {
-        const float got = __shfl_xor_sync(0xffffffffu, up ? v[2 * p] : v[2 * p + 1], 8);
-        h[p] = up ? lin_silu(got) * v[2 * p + 1] : lin_silu(v[2 * p]) * got;
-      }
+      for (int n = 0; n < 4; ++n)
 #pragma unroll
-      for (int p = 0; p < 8; ++p) {
-        const float got = __shfl_xor_sync(0xffffffffu, odd ? h[2 * p] : h[2 * p + 1], 1);
-        lo[p] = odd ? got : h[2 * p];
-        hi[p] = odd ? h[2 * p + 1] : got;
-      }
+        for (int k = 0; k < 2; ++k) {
+          o[4 * n + k] = lin_silu(v[8 * n + k]) * v[8 * n + 2 + k];
+          o[4 * n + 2 + k] = lin_silu(v[8 * n + 4 + k]) * v[8 * n + 6 + k];
+        }
     } else {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) o[j] = v[j];
       if (MODE == kLinFwd) {
         switch (a.act) {
           case kActRelu:
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = v[j] < 0.f ? 0.f : v[j];   // keeps NaN
+            for (int j = 0; j < 32; ++j) o[j] = v[j] < 0.f ? 0.f : v[j];   // keeps NaN
             break;
           case kActSilu:
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = lin_silu(v[j]);
+            for (int j = 0; j < 32; ++j) o[j] = lin_silu(v[j]);
             break;
           case kActGelu:
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = lin_gelu(v[j]);
+            for (int j = 0; j < 32; ++j) o[j] = lin_gelu(v[j]);
             break;
           default:
             break;
         }
       }
-      lin_pairs(v, lo, hi);
     }
+    // gated: two 8-column groups of rows make one x4 (matrix m: columns 8 (m & 1), rows 8 (m >> 1))
+    const uint32_t om = kGated ? stage + static_cast<uint32_t>(((lane >> 4) * 8 + (lane & 7)) * kPiecePitch + ((lane >> 3) & 1) * 16)
+                               : mat;
+    constexpr int kSteps = kGated ? 2 : 4, kStepRows = 32 / kSteps;
+    __syncwarp();
     if (has_res) {
 #pragma unroll
-      for (int p = 0; p < kWords; ++p) {
-        const float2 x = lin_unpack(res[p], a.f16);
-        lo[p] += x.x;
-        hi[p] += x.y;
-      }
-      if (c0 + 32 < ce) fetch(c0 + 32);
-    }
-    uint16_t* op = a.out + (jr + c0) * a.ldo + i2;
+      for (int s = 0; s < kU; ++s) sts16(rows.at(stage, s), res[s]);
+      __syncwarp();
 #pragma unroll
-    for (int p = 0; p < kWords; ++p)
-      if (live && row_of(p) < left) *reinterpret_cast<uint32_t*>(op + row_of(p) * a.ldo) = lin_pack(lo[p], hi[p], a.f16);
+      for (int n = 0; n < kSteps; ++n) {
+        uint32_t r[4];
+        ldmatrix_x4_t(om + n * kStepRows * kPiecePitch, r);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          const float2 x = lin_unpack(r[m], a.f16);
+          o[8 * n + 2 * m] += x.x;
+          o[8 * n + 2 * m + 1] += x.y;
+        }
+      }
+      if (c0 + 32 < ce) rows.fetch(res, a.res + (jr + c0 + 32) * a.ldr + col, a.ldr, live, left - 32);
+      __syncwarp();
+    }
+#pragma unroll
+    for (int n = 0; n < kSteps; ++n)
+      stmatrix_x4_t(om + n * kStepRows * kPiecePitch, lin_pack(o[8 * n], o[8 * n + 1], a.f16),
+                    lin_pack(o[8 * n + 2], o[8 * n + 3], a.f16), lin_pack(o[8 * n + 4], o[8 * n + 5], a.f16),
+                    lin_pack(o[8 * n + 6], o[8 * n + 7], a.f16));
+    __syncwarp();
+    rows.store(stage, a.out + (jr + c0) * a.ldo + col, a.ldo, live, left);
   }
+  __syncwarp();
 }
 
 // Loads A's 128 output columns (from column i0; gated: i0 of y) and q0 .. of the sum.
@@ -389,13 +450,48 @@ __device__ __forceinline__ uint32_t lin_b_bytes(const LinArgs& a, int n) {
 
 // ------------------------------------------------------------------------------------------
 
-// mapa / mapb: maps of the operands (see the launches); mapa4 / mapb4: one-row boxes of the same rows
-// for the weight gradient's partial slabs.
+__device__ __forceinline__ void tensormap_acquire(const CUtensorMap* m) {
+  asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(m) : "memory");
+}
+
+// Copies of the weight gradient's two maps for each expert, their rows (dimension 1) ending with the
+// expert's segment.  One CTA, thread = expert.
+__global__ void __launch_bounds__(kLinMaxE) expert_maps_kernel(const __grid_constant__ CUtensorMap mapa,
+                                                               const __grid_constant__ CUtensorMap mapb,
+                                                               const int32_t* __restrict__ counts, int E, int align, int rows,
+                                                               CUtensorMap* emaps) {
+  __shared__ int sums[kLinMaxE / 32];
+  const int e = threadIdx.x, warp = e / 32, lane = e % 32;
+  const int c = e < E ? min(max(__ldg(counts + e), 0), rows) : 0;
+  const int padded = (c + align - 1) / align * align;
+  int s = padded;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, s, d);
+    if (lane >= d) s = min(s + o, 0x3fffffff);
+  }
+  if (lane == 31) sums[warp] = s;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) s = min(s + sums[w], 0x3fffffff);
+  if (e >= E) return;
+  const int end = max(min(s - padded + c, rows), 1);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    CUtensorMap* m = emaps + 2 * e + k;
+    const uint4* src = reinterpret_cast<const uint4*>(k ? &mapb : &mapa);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) reinterpret_cast<uint4*>(m)[i] = src[i];
+    asm volatile("tensormap.replace.tile.global_dim.global.b1024.b32 [%0], 1, %1;" ::"l"(m), "r"(end) : "memory");
+  }
+  asm volatile("fence.proxy.tensormap::generic.release.gpu;" ::: "memory");
+}
+
+// mapa / mapb: maps of the operands (see the launches).  emaps: the weight gradient's maps of experts' rows,
+// A's and B's of expert e at 2e and 2e + 1.
 template <int MODE>
 __global__ void __launch_bounds__(kLinThreads, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap mapa, const __grid_constant__ CUtensorMap mapb,
-                       const __grid_constant__ CUtensorMap mapa4, const __grid_constant__ CUtensorMap mapb4,
-                       const LinArgs a) {
+                       const CUtensorMap* __restrict__ emaps, const LinArgs a) {
   constexpr bool kAMn = MODE == kLinDx || MODE == kLinDw, kBMn = MODE == kLinDw;
   constexpr int kCtaI = MODE == kLinFwdGated ? 64 : kLinBI;     // output columns per CTA
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -406,7 +502,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   uint64_t* acc_empty = acc_full + 2;          // [2] even CTA: drained by both CTAs
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int* seg = reinterpret_cast<int*>(smem + kPairStages * kPairStage + 256);   // [E + 1] first row of each expert
+  uint8_t* pieces = smem + kPairStages * kPairStage + 256;                    // one per epilogue warp
+  int* seg = reinterpret_cast<int*>(pieces + 4 * kPieceBytes);                // [E + 1] first row of each expert
   int* pfx = seg + kLinMaxE + 1;                                              // [E + 1] tiles before each expert
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -482,9 +579,20 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     const uint32_t full0 = mapa_shared(smem_u32(full), 0);
     int st = 0;
     uint32_t ph = 0;
+    int e_maps = -1;
     bool ok = true;
     for (int ti = pair; ok && ti < n_tiles; ti += pairs) {
       const LinTile t = lin_tile<MODE>(a, seg, pfx, ti);
+      const CUtensorMap *ma = &mapa, *mb = &mapb;
+      if (MODE == kLinDw && a.counts) {
+        ma = emaps + 2 * t.e;
+        mb = ma + 1;
+        if (e_maps != t.e && t.slabs) {      // written by the launch before this one
+          e_maps = t.e;
+          tensormap_acquire(ma);
+          tensormap_acquire(mb);
+        }
+      }
       const int half = ((t.ncols + kPairStep - 1) & ~(kPairStep - 1)) / 2;
       const int i0 = (t.it * 2 + rank) * kCtaI, j0 = t.j0 + rank * half;
       const uint32_t bytes = kLinABytes + lin_b_bytes<MODE>(a, half);
@@ -493,28 +601,11 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         if (!ok) break;
         const uint32_t sa = smem_u32(smem + st * kPairStage), sb = sa + kLinABytes, fb = full0 + st * 8;
         const int q0 = s * kLinSlab;
-        const bool partial = MODE == kLinDw && a.counts && t.cnt - q0 < kLinSlab;
-        if (rank == 0 && lane == 0)
-          mbar_arrive_expect_tx(smem_u32(full + st), 2 * (partial ? kPairStage : bytes));
+        if (rank == 0 && lane == 0) mbar_arrive_expect_tx(smem_u32(full + st), 2 * bytes);
         __syncwarp();
-        if (partial) {
-          // rows past the segment's end become row `rows`, which reads as zeros
-          for (int u = lane; u < 4 * 16; u += 32) {
-            const int b = u >> 4, r4 = (u & 15) * 4;
-            int y[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) y[k] = q0 + r4 + k < t.cnt ? t.row0 + q0 + r4 + k : a.rows;
-            const uint32_t dst = sa + b * 8192 + r4 * 128;
-            // a block of columns past the matrix: any columns do, it is never stored
-            const int col = b < 2 ? i0 + b * 64 : j0 + (b - 2) * 64;
-            if (b < 2)
-              tma_rows4_pair(dst, &mapa4, col < a.i_ext ? col : 0, y[0], y[1], y[2], y[3], fb);
-            else
-              tma_rows4_pair(dst, &mapb4, col < a.j_ext ? col : 0, y[0], y[1], y[2], y[3], fb);
-          }
-        } else if (lane == 0) {
-          lin_load_a<MODE, true>(a, &mapa, sa, t, i0, q0, fb);
-          lin_load_b<MODE, true>(a, &mapb, sb, t, j0, half, q0, fb);
+        if (lane == 0) {
+          lin_load_a<MODE, true>(a, ma, sa, t, i0, q0, fb);
+          lin_load_b<MODE, true>(a, mb, sb, t, j0, half, q0, fb);
         }
         __syncwarp();
         if (++st == kPairStages) {
@@ -581,7 +672,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   } else {
     // ---------------- epilogue: this CTA's 128 output columns ----------------
     const int q = warp & 3;      // the TMEM lane quarter this warp may read
-    const uint32_t acc_empty0 = mapa_shared(smem_u32(acc_empty), 0);
+    const uint32_t acc_empty0 = mapa_shared(smem_u32(acc_empty), 0), stage = smem_u32(pieces + q * kPieceBytes);
     int b = 0;
     uint32_t aph = 0;
     bool ok = true;
@@ -589,7 +680,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       const LinTile t = lin_tile<MODE>(a, seg, pfx, ti);
       const int i0 = (t.it * 2 + rank) * kCtaI;
       if (t.slabs == 0) {
-        lin_drain<MODE>(a, t, i0, 0, t.ncols, ZeroSums{}, q, lane);
+        lin_drain<MODE>(a, t, i0, 0, t.ncols, ZeroSums{}, q, lane, stage);
         continue;
       }
       ok = mbar_wait(smem_u32(acc_full + b), (aph >> b) & 1u, a.status) && *abort_flag == 0;
@@ -597,7 +688,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       if (!ok) break;
       tc_fence_after();
       lin_drain<MODE>(a, t, i0, 0, t.ncols,
-                      TmemSums{tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(b * kLinBJ)}, q, lane);
+                      TmemSums{tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(b * kLinBJ)}, q, lane,
+                      stage);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(acc_empty0 + b * 8);
@@ -666,6 +758,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   const int s1 = static_cast<int>(static_cast<long long>(t.slabs) * (slice + 1) / S);    // never empty (host)
   const uint32_t b_bytes = lin_b_bytes<MODE>(a, a.bj);
   const int stage = kLinABytes + static_cast<int>((b_bytes + 1023) & ~1023u);
+  const uint32_t piece = smem_u32(smem) + kLinBI * kLinBJ * 4 + static_cast<uint32_t>(warp & 3) * kPieceBytes;
 
   if (warp == 0) {
     int st = 0;
@@ -728,9 +821,9 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     } else {
       const TmemSums mine{tmem + (static_cast<uint32_t>(q * 32) << 16)};
       if (S == 1) {
-        lin_drain<MODE>(a, t, i0, 0, t.ncols, mine, q, lane);
+        lin_drain<MODE>(a, t, i0, 0, t.ncols, mine, q, lane, piece);
       } else {
-        // every MMA has read the ring: it takes this slice's sums, [column][128 lanes]
+        // every MMA has read the ring: it takes this slice's sums, as ClusterSums reads them
         float* part = reinterpret_cast<float*>(smem) + q * 32 + lane;
 #pragma unroll 1
         for (int c0 = 0; c0 < t.ncols; c0 += 32) {
@@ -738,7 +831,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           mine(c0, 32, v);
 #pragma unroll
           for (int j = 0; j < 32; ++j)
-            if (c0 + j < t.ncols) part[(c0 + j) * kLinBI] = v[j];
+            if (c0 + (j & ~7) < t.ncols) part[(c0 + j) * 128] = v[j];
         }
       }
     }
@@ -749,9 +842,9 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     cluster_sync();
     if (warp >= 2 && ok) {
       const int q = warp & 3;
-      const int w = (t.ncols + S - 1) / S, cb = min(slice * w, t.ncols), ce = min(cb + w, t.ncols);
-      lin_drain<MODE>(a, t, i0, cb, ce,
-                      ClusterSums{smem_u32(reinterpret_cast<float*>(smem) + q * 32 + lane), S}, q, lane);
+      const int w = ((t.ncols + S - 1) / S + 7) & ~7, cb = min(slice * w, t.ncols), ce = min(cb + w, t.ncols);
+      lin_drain<MODE>(a, t, i0, cb, ce, ClusterSums{smem_u32(reinterpret_cast<float*>(smem) + q * 32 + lane), S}, q, lane,
+                      piece);
     }
     cluster_sync();    // the slices stay until every CTA has read them
   }
@@ -821,20 +914,16 @@ bool map_mn_major(CUtensorMap* m, int f16, const void* p, long long cols, long l
   return lin_map(m, f16, p, 4, d, s, b);
 }
 
-bool map_one_row(CUtensorMap* m, int f16, const void* p, long long cols, long long rows, long long ld) {
-  const long long d[2] = {cols, rows}, s[2] = {0, ld};
-  const int b[2] = {64, 1};
-  return lin_map(m, f16, p, 2, d, s, b);
-}
-
 // How a problem runs.  j: rows of the output (dense) or of the row buffers (experts).
 struct LinPlan {
   bool pair;
   int split, bj, stages, grid, b_box;
 };
 
-LinPlan lin_plan(bool dense, int i_cols, int cta_i, long long j, long long q, bool b_mn) {
+// experts: 0 for a dense problem.
+LinPlan lin_plan(int experts, int i_cols, int cta_i, long long j, long long q, bool b_mn) {
   LinPlan p{};
+  const bool dense = experts == 0;
   const int sms = num_sms(), pairs = sms / 2;
   const long long slabs = (q + kLinSlab - 1) / kLinSlab;
   p.bj = lin_tile_rows(static_cast<int>(j), kPairStep);
@@ -844,7 +933,11 @@ LinPlan lin_plan(bool dense, int i_cols, int cta_i, long long j, long long q, bo
   if (p.pair) {
     p.grid = 2 * static_cast<int>(dense && tiles < pairs ? tiles : pairs);
     p.split = 1;
-    p.b_box = dense ? p.bj / 2 : 32;
+    // One copy per stage where that can be: the copies are issued one after another, and four of 32 rows in
+    // place of one of 128 cost an 8192^3 product 22% (741 against 606 us) and 12288 rows of 32 experts 20%.
+    // Rows past a tile's end are fetched for nothing then, so experts with few rows take smaller copies.
+    const long long each = dense ? 0 : j / experts;
+    p.b_box = dense ? p.bj / 2 : each >= 96 ? 128 : each >= 48 ? 64 : 32;
     return p;
   }
   p.bj = lin_tile_rows(static_cast<int>(j), kSplitStep);
@@ -860,7 +953,8 @@ LinPlan lin_plan(bool dense, int i_cols, int cta_i, long long j, long long q, bo
 }
 
 template <int MODE>
-cudaError_t lin_launch(const LinPlan& p, const CUtensorMap (&m)[4], LinArgs a, cudaStream_t stream) {
+cudaError_t lin_launch(const LinPlan& p, const CUtensorMap (&m)[2], const CUtensorMap* emaps, LinArgs a,
+                       cudaStream_t stream) {
   a.split = p.split;
   a.bj = p.bj;
   a.stages = p.stages;
@@ -881,7 +975,7 @@ cudaError_t lin_launch(const LinPlan& p, const CUtensorMap (&m)[4], LinArgs a, c
     const cudaError_t err =
         cudaFuncSetAttribute(linear_pair_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem);
     if (err != cudaSuccess) return err;
-    return cudaLaunchKernelEx(&cfg, linear_pair_kernel<MODE>, m[0], m[1], m[2], m[3], static_cast<const LinArgs>(a));
+    return cudaLaunchKernelEx(&cfg, linear_pair_kernel<MODE>, m[0], m[1], emaps, static_cast<const LinArgs>(a));
   }
   const cudaError_t err =
       cudaFuncSetAttribute(linear_split_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSplitSmem);
@@ -918,10 +1012,10 @@ cudaError_t launch_linear(const LinearShape& p, RowsView x, const uint16_t* w, c
   a.ldr = res.ld;
   a.bias = bias;
   const int cta_i = gated ? 64 : kLinBI;
-  const LinPlan pl = lin_plan(!p.counts, a.i_ext, cta_i, p.rows, p.K, false);
+  const LinPlan pl = lin_plan(p.counts ? p.E : 0, a.i_ext, cta_i, p.rows, p.K, false);
   const int tile_i = pl.pair ? 2 * cta_i : cta_i;
   a.n_it = (a.i_ext + tile_i - 1) / tile_i;
-  CUtensorMap m[4] = {};
+  CUtensorMap m[2] = {};
   bool ok;
   if (gated) {
     // [E][N/2 / 8][2][8][K]: a copy takes, eight columns at a time, their gate rows and then their up rows
@@ -933,7 +1027,7 @@ cudaError_t launch_linear(const LinearShape& p, RowsView x, const uint16_t* w, c
     ok = map_k_major(&m[0], p.f16, w, p.K, p.N, a.E, p.K, kLinBI);
   }
   if (!ok || !map_k_major(&m[1], p.f16, x.ptr, p.K, p.rows, 1, x.ld, pl.b_box)) return cudaErrorInvalidValue;
-  return gated ? lin_launch<kLinFwdGated>(pl, m, a, stream) : lin_launch<kLinFwd>(pl, m, a, stream);
+  return gated ? lin_launch<kLinFwdGated>(pl, m, nullptr, a, stream) : lin_launch<kLinFwd>(pl, m, nullptr, a, stream);
 }
 
 cudaError_t launch_linear_dx(const LinearShape& p, RowsView dz, const uint16_t* w, RowsView res, RowsView dx,
@@ -945,37 +1039,42 @@ cudaError_t launch_linear_dx(const LinearShape& p, RowsView dz, const uint16_t* 
   a.ldo = dx.ld;
   a.res = static_cast<const uint16_t*>(res.ptr);
   a.ldr = res.ld;
-  const LinPlan pl = lin_plan(!p.counts, p.K, kLinBI, p.rows, p.N, false);
+  const LinPlan pl = lin_plan(p.counts ? p.E : 0, p.K, kLinBI, p.rows, p.N, false);
   const int tile_i = pl.pair ? 2 * kLinBI : kLinBI;
   a.n_it = (p.K + tile_i - 1) / tile_i;
-  CUtensorMap m[4] = {};
+  CUtensorMap m[2] = {};
   a.a_blocks = 2;
   if (!map_mn_major(&m[0], p.f16, w, p.K, p.N, a.E, p.K, &a.a_blocks) ||
       !map_k_major(&m[1], p.f16, dz.ptr, p.N, p.rows, 1, dz.ld, pl.b_box))
     return cudaErrorInvalidValue;
-  return lin_launch<kLinDx>(pl, m, a, stream);
+  return lin_launch<kLinDx>(pl, m, nullptr, a, stream);
 }
 
-cudaError_t launch_linear_dw(const LinearShape& p, RowsView dz, RowsView x, uint16_t* dw, uint32_t* status,
+cudaError_t launch_linear_dw(const LinearShape& p, RowsView dz, RowsView x, uint16_t* dw, void* maps, uint32_t* status,
                              cudaStream_t stream) {
   LinArgs a = lin_args(p, status);
   a.i_ext = p.K;
   a.j_ext = p.N;
   a.out = dw;
   a.ldo = p.K;
-  const LinPlan pl = lin_plan(!p.counts, p.K, kLinBI, p.N, p.rows, true);
+  const LinPlan pl = lin_plan(p.counts ? p.E : 0, p.K, kLinBI, p.N, p.rows, true);
   const int tile_i = pl.pair ? 2 * kLinBI : kLinBI;
   a.n_it = (p.K + tile_i - 1) / tile_i;
-  CUtensorMap m[4] = {};
+  CUtensorMap m[2] = {};
   a.a_blocks = 2;
   // B in one copy where every tile (over a pair: every half) starts on a block
   const int cta_j = pl.pair ? pl.bj / 2 : pl.bj;
   a.b_blocks = cta_j % 64 == 0 && (!pl.pair || p.N % pl.bj == 0) ? cta_j / 64 : 0;
   if (!map_mn_major(&m[0], p.f16, x.ptr, p.K, p.rows, 1, x.ld, &a.a_blocks) ||
-      !map_mn_major(&m[1], p.f16, dz.ptr, p.N, p.rows, 1, dz.ld, &a.b_blocks) ||
-      !map_one_row(&m[2], p.f16, x.ptr, p.K, p.rows, x.ld) || !map_one_row(&m[3], p.f16, dz.ptr, p.N, p.rows, dz.ld))
+      !map_mn_major(&m[1], p.f16, dz.ptr, p.N, p.rows, 1, dz.ld, &a.b_blocks))
     return cudaErrorInvalidValue;
-  return lin_launch<kLinDw>(pl, m, a, stream);
+  CUtensorMap* emaps = static_cast<CUtensorMap*>(maps);
+  if (p.counts) {
+    expert_maps_kernel<<<1, kLinMaxE, 0, stream>>>(m[0], m[1], p.counts, p.E, p.align, p.rows, emaps);
+    const cudaError_t err = cudaGetLastError();
+    if (err != cudaSuccess) return err;
+  }
+  return lin_launch<kLinDw>(pl, m, emaps, a, stream);
 }
 
 // ------------------------------------------------------------------------------------------

@@ -35,7 +35,7 @@ bool sorted_dims_ok(int T, int K, int H, int U) {
 bool pow2_align(int a) { return a >= 1 && a <= 256 && (a & (a - 1)) == 0; }
 
 struct LinearWs {
-  size_t dz = 0, part = 0, total = 0;
+  size_t maps = 0, dz = 0, part = 0, total = 0;
 };
 
 bool linear_dims_ok(int rows, int N, int K, int E, int act) {
@@ -49,6 +49,8 @@ bool linear_dims_ok(int rows, int N, int K, int E, int act) {
 LinearWs linear_layout(int rows, int N, int E, int act) {
   LinearWs w;
   size_t off = kAlign;                         // [0, 256): status word
+  w.maps = off;
+  off = up(off + static_cast<size_t>(E) * kLinearMapBytes);
   w.dz = off;
   if (act != kActNone) off = up(off + static_cast<size_t>(rows) * N * 2);
   w.part = off;
@@ -63,7 +65,7 @@ moe_status linear_common(moe_dtype dt, const int32_t* counts, int rows, int N, i
   if (!dtype_ok(dt) || !linear_dims_ok(rows, N, K, E, act)) return MOE_ERR_INVALID_ARG;
   if (dt == MOE_F32) return MOE_ERR_UNSUPPORTED;
   if ((E > 0) != (counts != nullptr) || (E > 0 && !pow2_align(align))) return MOE_ERR_INVALID_ARG;
-  if (!ws) return MOE_ERR_WORKSPACE;
+  if (!ws || !aligned(ws, kAlign)) return MOE_ERR_WORKSPACE;
   return MOE_OK;
 }
 
@@ -205,7 +207,7 @@ moe_status moe_linear_backward(moe_dtype dt, moe_rows dy, moe_rows x, const void
   if (dx.ptr && launch_linear_dx(p, dz, static_cast<const uint16_t*>(w), view(dx_residual), view(dx), status_of(ws),
                                  S(stream)) != cudaSuccess)
     return MOE_ERR_CUDA;
-  if (dw && launch_linear_dw(p, dz, view(x), static_cast<uint16_t*>(dw), status_of(ws), S(stream)) != cudaSuccess)
+  if (dw && launch_linear_dw(p, dz, view(x), static_cast<uint16_t*>(dw), base + L.maps, status_of(ws), S(stream)) != cudaSuccess)
     return MOE_ERR_CUDA;
   return MOE_OK;
 }
