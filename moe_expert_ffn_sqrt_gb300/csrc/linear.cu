@@ -24,6 +24,7 @@
 //    epilogue runs under the next tile's MMAs.
 //  * linear_split_kernel: for dense problems with too few tiles to fill the GPU: a cluster of up to eight
 //    CTAs per 128-column tile, each with a slice of the sum; the slices meet in shared memory.
+#include <atomic>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -34,7 +35,8 @@ namespace moe {
 
 namespace {
 
-constexpr int kLinThreads = 192;            // warp 0 loads, 1 MMA, 2..5 epilogue
+constexpr int kLinEpiWarps = 8;             // two per TMEM lane quarter, on alternate pieces of 32 columns
+constexpr int kLinThreads = 64 + 32 * kLinEpiWarps;   // warp 0 loads, 1 MMA, the others drain
 constexpr int kLinBI = 128;                 // output columns i per CTA (accumulator lanes)
 constexpr int kLinBJ = 256;                 // output rows j per tile (MMA N), at most
 constexpr int kLinSlab = 64;                // terms of the sum per pipeline stage
@@ -44,15 +46,16 @@ constexpr int kLinMaxE = kLinearMaxExperts;
 constexpr int kPairB = 128 * 128;
 constexpr int kPairStage = kLinABytes + kPairB;      // 32 KB
 constexpr int kPairStages = 6;
-constexpr int kPairSmem = 1024 + kPairStages * kPairStage + 256 + 4 * 32 * 80 + 2 * (kLinMaxE + 1) * 4;
+constexpr int kPairSmem = 1024 + kPairStages * kPairStage + 256 + kLinEpiWarps * 32 * 80 + (3 * kLinMaxE + 1) * 4;
 // split kernel: stages of A and the tile's B rows, as many as fit
 constexpr int kSplitRing = 208 * 1024;          // also: the slice's sums, then a piece per epilogue warp
 constexpr int kSplitMaxStages = 12;
 constexpr int kSplitSmem = 1024 + kSplitRing + 512;
 static_assert(kPairSmem <= 227 * 1024 && kSplitSmem <= 227 * 1024, "shared memory budget");
-static_assert(kSplitRing >= kLinBI * kLinBJ * 4 + 4 * 32 * 80, "the slices' sums and the pieces fit the ring");
+static_assert(kSplitRing >= kLinBI * kLinBJ * 4 + kLinEpiWarps * 32 * 80, "the slices' sums and the pieces fit the ring");
 
-enum LinMode { kLinFwd = 0, kLinFwdGated = 1, kLinDx = 2, kLinDw = 3 };
+// The GELU forward is a mode of its own: erfc over a whole piece takes registers that the others need not pay.
+enum LinMode { kLinFwd = 0, kLinFwdGated = 1, kLinDx = 2, kLinDw = 3, kLinFwdGelu = 4 };
 
 struct LinArgs {
   const int32_t* counts;      // [E] rows per expert; nullptr: one dense segment of `rows` rows
@@ -63,7 +66,7 @@ struct LinArgs {
   int q_ext;                  // forward: K, input gradient: N
   int act, f16;
   int a_blocks, b_blocks;     // > 0: operand map with 64-column blocks as a dimension, blocks per copy
-  int b_box;                  // rows of B per copy (operands contiguous along the sum)
+  int b_box;                  // rows of B per copy (contiguous along the sum; 0: the tile's height picks its map)
   int split, bj, stages;      // split kernel: slices, rows j per tile, ring stages
   uint16_t* out;
   long long ldo;
@@ -140,34 +143,57 @@ struct LinTile {
   int e, it, row0, cnt, j0, ncols, slabs;
 };
 
-// Tiles in order of expert, then groups of 16 j tiles, then i tile, then j tile: the tiles that run at
-// one time share their operands in L2 along both sides.
+// What a pair keeps about the experts' segments in shared memory.
+struct LinSegs {
+  int* row0;                  // [E] first row
+  int* cnt;                   // [E] rows
+  int* pfx;                   // [E + 1] tiles before the expert
+};
+
+// A pair's tiles t = pair, pair + pairs, ...: in order of expert, then groups of 16 j tiles, then i tile,
+// then j tile, so that the tiles that run at one time share their operands in L2 along both sides.  Every
+// role walks them by itself; a step costs a division and, on a new expert, a few shared-memory reads
+// (a search per tile took up to half of a short tile's time).
 template <int MODE>
-__device__ __forceinline__ LinTile lin_tile(const LinArgs& a, const int* seg, const int* pfx, int t) {
+struct LinWalk {
+  const LinArgs& a;
+  const LinSegs& g;
+  int t, step, next, nj, bj;
   LinTile r;
-  int lo = 0, hi = a.E - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (pfx[mid] <= t)
-      lo = mid;
-    else
-      hi = mid - 1;
+  __device__ __forceinline__ LinWalk(const LinArgs& a_, const LinSegs& g_, int first, int step_)
+      : a(a_), g(g_), t(first - step_), step(step_), next(0), nj(1), bj(kPairStep) {
+    r.e = -1;
   }
-  r.e = lo;
-  r.row0 = seg[lo];
-  r.cnt = a.counts ? min(max(__ldg(a.counts + lo), 0), max(a.rows - r.row0, 0)) : a.rows;
-  int u = t - pfx[lo];
-  const int n = MODE == kLinDw ? a.j_ext : r.cnt;
-  const int bj = lin_tile_rows(n, kPairStep), nj = (n + bj - 1) / bj;
-  const int g = u / (16 * a.n_it);
-  u -= g * 16 * a.n_it;
-  const int gj = min(16, nj - g * 16);
-  r.it = u / gj;
-  r.j0 = (g * 16 + u - r.it * gj) * bj;
-  r.ncols = min(bj, n - r.j0);
-  r.slabs = ((MODE == kLinDw ? r.cnt : a.q_ext) + kLinSlab - 1) / kLinSlab;
-  return r;
-}
+  __device__ __forceinline__ bool advance() {
+    t += step;
+    if (t >= g.pfx[a.E]) return false;
+    if (t >= next) {
+      int e = r.e;
+      do {
+        ++e;
+        next = g.pfx[e + 1];
+      } while (t >= next);
+      r.e = e;
+      r.row0 = g.row0[e];
+      r.cnt = g.cnt[e];
+      const int n = MODE == kLinDw ? a.j_ext : r.cnt;
+      bj = lin_tile_rows(n, kPairStep);
+      nj = (n + bj - 1) / bj;
+      r.slabs = ((MODE == kLinDw ? r.cnt : a.q_ext) + kLinSlab - 1) / kLinSlab;
+    }
+    unsigned u = static_cast<unsigned>(t - g.pfx[r.e]);
+    int j16 = 0, gj = nj;
+    if (nj > 16) {
+      j16 = static_cast<int>(u / (16u * a.n_it)) * 16;
+      u -= static_cast<unsigned>(j16) * a.n_it;
+      gj = min(16, nj - j16);
+    }
+    r.it = static_cast<int>(u / static_cast<unsigned>(gj));
+    r.j0 = (j16 + static_cast<int>(u) - r.it * gj) * bj;
+    r.ncols = min(bj, (MODE == kLinDw ? a.j_ext : r.cnt) - r.j0);
+    return true;
+  }
+};
 
 __device__ __forceinline__ uint32_t lin_pack(float lo, float hi, int f16) {
   if (f16) {
@@ -291,12 +317,12 @@ struct PieceRows {
 };
 
 // Turns the sums of output rows [j0 + cb, j0 + ce) of tile t into outputs (cb a multiple of 8); this
-// warp has lanes 32q .. of the CTA's output columns, which start at column i0 (gated forward: of y).
-// stage: the warp's piece in shared memory.
+// warp has lanes 32q .. of the CTA's output columns, which start at column i0 (gated forward: of y), and
+// every second piece of rows from piece `par` on.  stage: the warp's piece in shared memory.
 template <int MODE, class Sums>
 __device__ __forceinline__ void lin_drain(const LinArgs& a, const LinTile& t, int i0, int cb, int ce, const Sums& sums, int q,
-                                          int lane, uint32_t stage) {
-  constexpr bool kGated = MODE == kLinFwdGated, kFwd = MODE == kLinFwd || kGated;
+                                          int par, int lane, uint32_t stage) {
+  constexpr bool kGated = MODE == kLinFwdGated, kFwd = MODE == kLinFwd || MODE == kLinFwdGelu || kGated;
   constexpr int kU = kGated ? 2 : 4;                  // 16-byte units per output row
   // accumulator lane l of the warp is output column iw + l; gated: lanes 16m + 0..7 are the gate rows of
   // columns iw + 8m .., lanes 16m + 8..15 their up rows
@@ -320,9 +346,10 @@ __device__ __forceinline__ void lin_drain(const LinArgs& a, const LinTile& t, in
   // the residual of the next piece is on its way while this one is worked on
   const bool has_res = MODE != kLinDw && a.res != nullptr;
   uint4 res[kU];
+  cb += 32 * par;
   if (has_res) rows.fetch(res, a.res + (jr + cb) * a.ldr + col, a.ldr, live, ce - cb);
 #pragma unroll 1
-  for (int c0 = cb; c0 < ce; c0 += 32) {
+  for (int c0 = cb; c0 < ce; c0 += 64) {
     const int left = ce - c0;
     float v[32];
     sums(c0, left, v);
@@ -354,7 +381,7 @@ __device__ __forceinline__ void lin_drain(const LinArgs& a, const LinTile& t, in
         }
     } else {
 #pragma unroll
-      for (int j = 0; j < 32; ++j) o[j] = v[j];
+      for (int j = 0; j < 32; ++j) o[j] = MODE == kLinFwdGelu ? lin_gelu(v[j]) : v[j];
       if (MODE == kLinFwd) {
         switch (a.act) {
           case kActRelu:
@@ -364,10 +391,6 @@ __device__ __forceinline__ void lin_drain(const LinArgs& a, const LinTile& t, in
           case kActSilu:
 #pragma unroll
             for (int j = 0; j < 32; ++j) o[j] = lin_silu(v[j]);
-            break;
-          case kActGelu:
-#pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = lin_gelu(v[j]);
             break;
           default:
             break;
@@ -394,7 +417,7 @@ __device__ __forceinline__ void lin_drain(const LinArgs& a, const LinTile& t, in
           o[8 * n + 2 * m + 1] += x.y;
         }
       }
-      if (c0 + 32 < ce) rows.fetch(res, a.res + (jr + c0 + 32) * a.ldr + col, a.ldr, live, left - 32);
+      if (c0 + 64 < ce) rows.fetch(res, a.res + (jr + c0 + 64) * a.ldr + col, a.ldr, live, left - 64);
       __syncwarp();
     }
 #pragma unroll
@@ -412,7 +435,7 @@ __device__ __forceinline__ void lin_drain(const LinArgs& a, const LinTile& t, in
 template <int MODE, bool PAIR>
 __device__ __forceinline__ void lin_load_a(const LinArgs& a, const CUtensorMap* map, uint32_t dst, const LinTile& t, int i0,
                                            int q0, uint32_t bar) {
-  if (MODE == kLinFwd) {
+  if (MODE == kLinFwd || MODE == kLinFwdGelu) {
     tma_load_4d<PAIR>(dst, map, q0, i0, t.e, 0, bar);
   } else if (MODE == kLinFwdGated) {
     tma_load_5d<PAIR>(dst, map, q0, 0, 0, i0 >> 3, t.e, bar);
@@ -429,6 +452,12 @@ __device__ __forceinline__ void lin_load_a(const LinArgs& a, const CUtensorMap* 
 }
 
 // Loads rows j .. j + n of B (n a multiple of 8), q0 .. of the sum: lin_b_bytes in all.
+// Maps of B.  Experts' tiles differ in height: [h] copies 16 (h + 1) rows at a time, so that a stage is one copy
+// and fetches only what it uses; where one height serves all, it is [0].
+struct LinMapsB {
+  CUtensorMap m[8];
+};
+
 template <int MODE, bool PAIR>
 __device__ __forceinline__ void lin_load_b(const LinArgs& a, const CUtensorMap* map, uint32_t dst, const LinTile& t, int j,
                                            int n, int q0, uint32_t bar) {
@@ -439,13 +468,13 @@ __device__ __forceinline__ void lin_load_b(const LinArgs& a, const CUtensorMap* 
       for (int b = 0; b * 64 < n; ++b) tma_load_4d<PAIR>(dst + b * 8192, map, j + b * 64, t.row0 + q0, 0, 0, bar);
     }
   } else {
-    for (int b = 0; b < n; b += a.b_box) tma_load_4d<PAIR>(dst + b * 128, map, q0, t.row0 + j + b, 0, 0, bar);
+    tma_load_4d<PAIR>(dst, map, q0, t.row0 + j, 0, 0, bar);
   }
 }
 template <int MODE>
 __device__ __forceinline__ uint32_t lin_b_bytes(const LinArgs& a, int n) {
   if (MODE == kLinDw) return static_cast<uint32_t>(a.b_blocks ? a.b_blocks : (n + 63) / 64) * 8192u;
-  return static_cast<uint32_t>((n + a.b_box - 1) / a.b_box * a.b_box) * 128u;
+  return static_cast<uint32_t>(a.b_box ? a.b_box : n) * 128u;
 }
 
 // ------------------------------------------------------------------------------------------
@@ -490,7 +519,7 @@ __global__ void __launch_bounds__(kLinMaxE) expert_maps_kernel(const __grid_cons
 // A's and B's of expert e at 2e and 2e + 1.
 template <int MODE>
 __global__ void __launch_bounds__(kLinThreads, 1)
-    linear_pair_kernel(const __grid_constant__ CUtensorMap mapa, const __grid_constant__ CUtensorMap mapb,
+    linear_pair_kernel(const __grid_constant__ CUtensorMap mapa, const __grid_constant__ LinMapsB mapsb,
                        const CUtensorMap* __restrict__ emaps, const LinArgs a) {
   constexpr bool kAMn = MODE == kLinDx || MODE == kLinDw, kBMn = MODE == kLinDw;
   constexpr int kCtaI = MODE == kLinFwdGated ? 64 : kLinBI;     // output columns per CTA
@@ -503,8 +532,10 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   uint8_t* pieces = smem + kPairStages * kPairStage + 256;                    // one per epilogue warp
-  int* seg = reinterpret_cast<int*>(pieces + 4 * kPieceBytes);                // [E + 1] first row of each expert
-  int* pfx = seg + kLinMaxE + 1;                                              // [E + 1] tiles before each expert
+  LinSegs segs;
+  segs.row0 = reinterpret_cast<int*>(pieces + kLinEpiWarps * kPieceBytes);
+  segs.cnt = segs.row0 + kLinMaxE;
+  segs.pfx = segs.cnt + kLinMaxE;
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int rank = static_cast<int>(cluster_ctarank());
@@ -516,12 +547,12 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(acc_full + b), 1);
-      mbar_init(smem_u32(acc_empty + b), 2 * 4);
+      mbar_init(smem_u32(acc_empty + b), 2 * kLinEpiWarps);
     }
     *abort_flag = 0;
     fence_barrier_init();
     prefetch_tmap(&mapa);
-    prefetch_tmap(&mapb);
+    prefetch_tmap(&mapsb.m[0]);
   }
   if (warp == 1) {
     tmem_alloc_pair(smem_u32(tmem_slot), 2 * kLinBJ);
@@ -560,19 +591,19 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         if (lane >= d) p += o;
       }
       if (e < a.E) {
-        seg[e] = start;
-        pfx[e] = prun + p - n;
+        segs.row0[e] = start;
+        segs.cnt[e] = c;
+        segs.pfx[e] = prun + p - n;
       }
       prun += __shfl_sync(0xffffffffu, p, 31);
     }
-    if (lane == 0) pfx[a.E] = prun;
+    if (lane == 0) segs.pfx[a.E] = prun;
   }
   tc_fence_before();
   __syncthreads();
   cluster_sync();      // both CTAs' barriers exist before any cross-CTA arrival
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int n_tiles = pfx[a.E];
 
   if (warp == 0) {
     // ---------------- loads: this CTA's 128 columns of A, its half of B's rows ----------------
@@ -581,9 +612,11 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     uint32_t ph = 0;
     int e_maps = -1;
     bool ok = true;
-    for (int ti = pair; ok && ti < n_tiles; ti += pairs) {
-      const LinTile t = lin_tile<MODE>(a, seg, pfx, ti);
-      const CUtensorMap *ma = &mapa, *mb = &mapb;
+    LinWalk<MODE> walk(a, segs, pair, pairs);
+    while (ok && walk.advance()) {
+      const LinTile& t = walk.r;
+      const int half = ((t.ncols + kPairStep - 1) & ~(kPairStep - 1)) / 2;
+      const CUtensorMap *ma = &mapa, *mb = &mapsb.m[a.b_box ? 0 : half / 16 - 1];
       if (MODE == kLinDw && a.counts) {
         ma = emaps + 2 * t.e;
         mb = ma + 1;
@@ -593,7 +626,6 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           tensormap_acquire(mb);
         }
       }
-      const int half = ((t.ncols + kPairStep - 1) & ~(kPairStep - 1)) / 2;
       const int i0 = (t.it * 2 + rank) * kCtaI, j0 = t.j0 + rank * half;
       const uint32_t bytes = kLinABytes + lin_b_bytes<MODE>(a, half);
       for (int s = 0; s < t.slabs; ++s) {
@@ -636,8 +668,9 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       uint32_t ph = 0, aph = 0;
       bool ok = true;
       const uint64_t da0 = lin_desc<kAMn>(smem_u32(smem)), db0 = lin_desc<kBMn>(smem_u32(smem) + kLinABytes);
-      for (int ti = pair; ok && ti < n_tiles; ti += pairs) {
-        const LinTile t = lin_tile<MODE>(a, seg, pfx, ti);
+      LinWalk<MODE> walk(a, segs, pair, pairs);
+      while (ok && walk.advance()) {
+        const LinTile& t = walk.r;
         if (t.slabs == 0) continue;
         const uint32_t id = lin_idesc(a.f16, kAMn, kBMn, 2 * kLinBI,
                                       static_cast<uint32_t>((t.ncols + kPairStep - 1) & ~(kPairStep - 1)));
@@ -671,25 +704,26 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     __syncwarp();
   } else {
     // ---------------- epilogue: this CTA's 128 output columns ----------------
-    const int q = warp & 3;      // the TMEM lane quarter this warp may read
-    const uint32_t acc_empty0 = mapa_shared(smem_u32(acc_empty), 0), stage = smem_u32(pieces + q * kPieceBytes);
+    const int q = warp & 3, par = (warp - 2) >> 2;   // the TMEM lane quarter this warp may read
+    const uint32_t acc_empty0 = mapa_shared(smem_u32(acc_empty), 0), stage = smem_u32(pieces + (warp - 2) * kPieceBytes);
     int b = 0;
     uint32_t aph = 0;
     bool ok = true;
-    for (int ti = pair; ok && ti < n_tiles; ti += pairs) {
-      const LinTile t = lin_tile<MODE>(a, seg, pfx, ti);
+    LinWalk<MODE> walk(a, segs, pair, pairs);
+    while (ok && walk.advance()) {
+      const LinTile& t = walk.r;
       const int i0 = (t.it * 2 + rank) * kCtaI;
       if (t.slabs == 0) {
-        lin_drain<MODE>(a, t, i0, 0, t.ncols, ZeroSums{}, q, lane, stage);
+        lin_drain<MODE>(a, t, i0, 0, t.ncols, ZeroSums{}, q, par, lane, stage);
         continue;
       }
       ok = mbar_wait(smem_u32(acc_full + b), (aph >> b) & 1u, a.status) && *abort_flag == 0;
-      ok = named_barrier_and(1, 128, ok);
+      ok = named_barrier_and(1, 32 * kLinEpiWarps, ok);
       if (!ok) break;
       tc_fence_after();
       lin_drain<MODE>(a, t, i0, 0, t.ncols,
-                      TmemSums{tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(b * kLinBJ)}, q, lane,
-                      stage);
+                      TmemSums{tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(b * kLinBJ)}, q, par,
+                      lane, stage);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(acc_empty0 + b * 8);
@@ -758,7 +792,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   const int s1 = static_cast<int>(static_cast<long long>(t.slabs) * (slice + 1) / S);    // never empty (host)
   const uint32_t b_bytes = lin_b_bytes<MODE>(a, a.bj);
   const int stage = kLinABytes + static_cast<int>((b_bytes + 1023) & ~1023u);
-  const uint32_t piece = smem_u32(smem) + kLinBI * kLinBJ * 4 + static_cast<uint32_t>(warp & 3) * kPieceBytes;
+  const uint32_t piece = smem_u32(smem) + kLinBI * kLinBJ * 4 + static_cast<uint32_t>(warp >= 2 ? warp - 2 : 0) * kPieceBytes;
 
   if (warp == 0) {
     int st = 0;
@@ -812,21 +846,21 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     }
     __syncwarp();
   } else {
-    const int q = warp & 3;
+    const int q = warp & 3, par = (warp - 2) >> 2;
     bool ok = mbar_wait(smem_u32(acc_full), 0, a.status) && *abort_flag == 0;
-    ok = named_barrier_and(1, 128, ok);
+    ok = named_barrier_and(1, 32 * kLinEpiWarps, ok);
     tc_fence_after();
     if (!ok) {
       *abort_flag = 1;
     } else {
       const TmemSums mine{tmem + (static_cast<uint32_t>(q * 32) << 16)};
       if (S == 1) {
-        lin_drain<MODE>(a, t, i0, 0, t.ncols, mine, q, lane, piece);
+        lin_drain<MODE>(a, t, i0, 0, t.ncols, mine, q, par, lane, piece);
       } else {
         // every MMA has read the ring: it takes this slice's sums, as ClusterSums reads them
         float* part = reinterpret_cast<float*>(smem) + q * 32 + lane;
 #pragma unroll 1
-        for (int c0 = 0; c0 < t.ncols; c0 += 32) {
+        for (int c0 = 32 * par; c0 < t.ncols; c0 += 64) {
           float v[32];
           mine(c0, 32, v);
 #pragma unroll
@@ -841,10 +875,10 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     const bool ok = *abort_flag == 0;
     cluster_sync();
     if (warp >= 2 && ok) {
-      const int q = warp & 3;
+      const int q = warp & 3, par = (warp - 2) >> 2;
       const int w = ((t.ncols + S - 1) / S + 7) & ~7, cb = min(slice * w, t.ncols), ce = min(cb + w, t.ncols);
-      lin_drain<MODE>(a, t, i0, cb, ce, ClusterSums{smem_u32(reinterpret_cast<float*>(smem) + q * 32 + lane), S}, q, lane,
-                      piece);
+      lin_drain<MODE>(a, t, i0, cb, ce, ClusterSums{smem_u32(reinterpret_cast<float*>(smem) + q * 32 + lane), S}, q,
+                      par, lane, piece);
     }
     cluster_sync();    // the slices stay until every CTA has read them
   }
@@ -933,11 +967,7 @@ LinPlan lin_plan(int experts, int i_cols, int cta_i, long long j, long long q, b
   if (p.pair) {
     p.grid = 2 * static_cast<int>(dense && tiles < pairs ? tiles : pairs);
     p.split = 1;
-    // One copy per stage where that can be: the copies are issued one after another, and four of 32 rows in
-    // place of one of 128 cost an 8192^3 product 22% (741 against 606 us) and 12288 rows of 32 experts 20%.
-    // Rows past a tile's end are fetched for nothing then, so experts with few rows take smaller copies.
-    const long long each = dense ? 0 : j / experts;
-    p.b_box = dense ? p.bj / 2 : each >= 96 ? 128 : each >= 48 ? 64 : 32;
+    p.b_box = dense ? p.bj / 2 : 0;
     return p;
   }
   p.bj = lin_tile_rows(static_cast<int>(j), kSplitStep);
@@ -952,9 +982,22 @@ LinPlan lin_plan(int experts, int i_cols, int cta_i, long long j, long long q, b
   return p;
 }
 
+// Lets a kernel use more than 48 KB of shared memory, once per device.
+cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<unsigned long long>& done) {
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (err == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
+  return err;
+}
+
 template <int MODE>
-cudaError_t lin_launch(const LinPlan& p, const CUtensorMap (&m)[2], const CUtensorMap* emaps, LinArgs a,
+cudaError_t lin_launch(const LinPlan& p, const CUtensorMap& ma, const LinMapsB& mb, const CUtensorMap* emaps, LinArgs a,
                        cudaStream_t stream) {
+  static std::atomic<unsigned long long> pair_done{0}, split_done{0};
   a.split = p.split;
   a.bj = p.bj;
   a.stages = p.stages;
@@ -972,15 +1015,21 @@ cudaError_t lin_launch(const LinPlan& p, const CUtensorMap (&m)[2], const CUtens
   cfg.attrs = at;
   cfg.numAttrs = 1;
   if (p.pair) {
-    const cudaError_t err =
-        cudaFuncSetAttribute(linear_pair_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem);
+    const cudaError_t err = allow_smem(reinterpret_cast<const void*>(&linear_pair_kernel<MODE>), kPairSmem, pair_done);
     if (err != cudaSuccess) return err;
-    return cudaLaunchKernelEx(&cfg, linear_pair_kernel<MODE>, m[0], m[1], emaps, static_cast<const LinArgs>(a));
+    return cudaLaunchKernelEx(&cfg, linear_pair_kernel<MODE>, ma, mb, emaps, static_cast<const LinArgs>(a));
   }
-  const cudaError_t err =
-      cudaFuncSetAttribute(linear_split_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSplitSmem);
+  const cudaError_t err = allow_smem(reinterpret_cast<const void*>(&linear_split_kernel<MODE>), kSplitSmem, split_done);
   if (err != cudaSuccess) return err;
-  return cudaLaunchKernelEx(&cfg, linear_split_kernel<MODE>, m[0], m[1], static_cast<const LinArgs>(a));
+  return cudaLaunchKernelEx(&cfg, linear_split_kernel<MODE>, ma, mb.m[0], static_cast<const LinArgs>(a));
+}
+
+// The rows operand of the forward and the input gradient.
+bool map_rows(LinMapsB& mb, const LinPlan& p, int f16, RowsView x, long long cols, long long rows) {
+  if (p.b_box) return map_k_major(&mb.m[0], f16, x.ptr, cols, rows, 1, x.ld, p.b_box);
+  for (int h = 0; h < 8; ++h)
+    if (!map_k_major(&mb.m[h], f16, x.ptr, cols, rows, 1, x.ld, 16 * (h + 1))) return false;
+  return true;
 }
 
 LinArgs lin_args(const LinearShape& p, uint32_t* status) {
@@ -1015,19 +1064,22 @@ cudaError_t launch_linear(const LinearShape& p, RowsView x, const uint16_t* w, c
   const LinPlan pl = lin_plan(p.counts ? p.E : 0, a.i_ext, cta_i, p.rows, p.K, false);
   const int tile_i = pl.pair ? 2 * cta_i : cta_i;
   a.n_it = (a.i_ext + tile_i - 1) / tile_i;
-  CUtensorMap m[2] = {};
+  CUtensorMap ma = {};
+  LinMapsB mb = {};
   bool ok;
   if (gated) {
     // [E][N/2 / 8][2][8][K]: a copy takes, eight columns at a time, their gate rows and then their up rows
     const long long I = p.N / 2, K = p.K;
     const long long d[5] = {K, 8, 2, I / 8, a.E}, s[5] = {0, K, I * K, 8 * K, 2 * I * K};
     const int b[5] = {kLinSlab, 8, 2, 8, 1};
-    ok = lin_map(&m[0], p.f16, w, 5, d, s, b);
+    ok = lin_map(&ma, p.f16, w, 5, d, s, b);
   } else {
-    ok = map_k_major(&m[0], p.f16, w, p.K, p.N, a.E, p.K, kLinBI);
+    ok = map_k_major(&ma, p.f16, w, p.K, p.N, a.E, p.K, kLinBI);
   }
-  if (!ok || !map_k_major(&m[1], p.f16, x.ptr, p.K, p.rows, 1, x.ld, pl.b_box)) return cudaErrorInvalidValue;
-  return gated ? lin_launch<kLinFwdGated>(pl, m, nullptr, a, stream) : lin_launch<kLinFwd>(pl, m, nullptr, a, stream);
+  if (!ok || !map_rows(mb, pl, p.f16, x, p.K, p.rows)) return cudaErrorInvalidValue;
+  if (gated) return lin_launch<kLinFwdGated>(pl, ma, mb, nullptr, a, stream);
+  if (act == kActGelu) return lin_launch<kLinFwdGelu>(pl, ma, mb, nullptr, a, stream);
+  return lin_launch<kLinFwd>(pl, ma, mb, nullptr, a, stream);
 }
 
 cudaError_t launch_linear_dx(const LinearShape& p, RowsView dz, const uint16_t* w, RowsView res, RowsView dx,
@@ -1042,12 +1094,13 @@ cudaError_t launch_linear_dx(const LinearShape& p, RowsView dz, const uint16_t* 
   const LinPlan pl = lin_plan(p.counts ? p.E : 0, p.K, kLinBI, p.rows, p.N, false);
   const int tile_i = pl.pair ? 2 * kLinBI : kLinBI;
   a.n_it = (p.K + tile_i - 1) / tile_i;
-  CUtensorMap m[2] = {};
+  CUtensorMap ma = {};
+  LinMapsB mb = {};
   a.a_blocks = 2;
-  if (!map_mn_major(&m[0], p.f16, w, p.K, p.N, a.E, p.K, &a.a_blocks) ||
-      !map_k_major(&m[1], p.f16, dz.ptr, p.N, p.rows, 1, dz.ld, pl.b_box))
+  if (!map_mn_major(&ma, p.f16, w, p.K, p.N, a.E, p.K, &a.a_blocks) ||
+      !map_rows(mb, pl, p.f16, dz, p.N, p.rows))
     return cudaErrorInvalidValue;
-  return lin_launch<kLinDx>(pl, m, nullptr, a, stream);
+  return lin_launch<kLinDx>(pl, ma, mb, nullptr, a, stream);
 }
 
 cudaError_t launch_linear_dw(const LinearShape& p, RowsView dz, RowsView x, uint16_t* dw, void* maps, uint32_t* status,
@@ -1060,21 +1113,22 @@ cudaError_t launch_linear_dw(const LinearShape& p, RowsView dz, RowsView x, uint
   const LinPlan pl = lin_plan(p.counts ? p.E : 0, p.K, kLinBI, p.N, p.rows, true);
   const int tile_i = pl.pair ? 2 * kLinBI : kLinBI;
   a.n_it = (p.K + tile_i - 1) / tile_i;
-  CUtensorMap m[2] = {};
+  CUtensorMap ma = {};
+  LinMapsB mb = {};
   a.a_blocks = 2;
   // B in one copy where every tile (over a pair: every half) starts on a block
   const int cta_j = pl.pair ? pl.bj / 2 : pl.bj;
   a.b_blocks = cta_j % 64 == 0 && (!pl.pair || p.N % pl.bj == 0) ? cta_j / 64 : 0;
-  if (!map_mn_major(&m[0], p.f16, x.ptr, p.K, p.rows, 1, x.ld, &a.a_blocks) ||
-      !map_mn_major(&m[1], p.f16, dz.ptr, p.N, p.rows, 1, dz.ld, &a.b_blocks))
+  if (!map_mn_major(&ma, p.f16, x.ptr, p.K, p.rows, 1, x.ld, &a.a_blocks) ||
+      !map_mn_major(&mb.m[0], p.f16, dz.ptr, p.N, p.rows, 1, dz.ld, &a.b_blocks))
     return cudaErrorInvalidValue;
   CUtensorMap* emaps = static_cast<CUtensorMap*>(maps);
   if (p.counts) {
-    expert_maps_kernel<<<1, kLinMaxE, 0, stream>>>(m[0], m[1], p.counts, p.E, p.align, p.rows, emaps);
+    expert_maps_kernel<<<1, kLinMaxE, 0, stream>>>(ma, mb.m[0], p.counts, p.E, p.align, p.rows, emaps);
     const cudaError_t err = cudaGetLastError();
     if (err != cudaSuccess) return err;
   }
-  return lin_launch<kLinDw>(pl, m, emaps, a, stream);
+  return lin_launch<kLinDw>(pl, ma, mb, emaps, a, stream);
 }
 
 // ------------------------------------------------------------------------------------------
@@ -1089,6 +1143,18 @@ __device__ __forceinline__ float silu_grad(float z, float& silu) {
   const float s = __fdividef(1.f, 1.f + __expf(-z));
   silu = z * s;
   return s * (1.f + z * (1.f - s));
+}
+
+// (v Phi(v))' = Phi(v) + v phi(v).  Phi by formula 7.1.26 of Abramowitz and Stegun's Handbook (Hastings):
+// erfc(x) = (a1 t + ... + a5 t^5) e^{-x^2}, t = 1 / (1 + p x), x >= 0, off by at most 1.5e-7; the exponential
+// is phi's own.  (With erfcf the pass is bound by its instructions: 25 us for 4096 x 2048 values.)
+__device__ __forceinline__ float gelu_grad(float v) {
+  const float x = fabsf(v) * 0.70710678118654752f;
+  const float t = __fdividef(1.f, fmaf(0.3275911f, x, 1.f));
+  const float e = __expf(-x * x);
+  const float p = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f), 0.254829592f);
+  const float tail = 0.5f * p * e;                   // Phi(-|v|)
+  return (v >= 0.f ? 1.f - tail : tail) + v * 0.39894228040143268f * e;
 }
 
 template <class T>
@@ -1154,7 +1220,7 @@ __global__ void __launch_bounds__(32 * kActRowLanes)
             float s;
             d = g.f(i) * silu_grad(v, s);
           } else {
-            d = g.f(i) * (0.5f * erfcf(v * -0.70710678118654752f) + v * 0.39894228040143268f * __expf(-0.5f * v * v));
+            d = g.f(i) * gelu_grad(v);
           }
           acc[0][i] += d;
           o.set(i, d);
