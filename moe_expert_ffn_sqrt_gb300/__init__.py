@@ -572,21 +572,15 @@ def forward_batched_i8(hidden, w_gate, gate_bias, e_score_bias, I, K, max_tokens
 
 # ------------------------------------------------------------------ training operators
 
-def _rows(t, dtype, cols, name, rows=None):
-    """A row-major matrix argument: any row pitch, unit column stride.  None: not given."""
+def _rows(t, dtype, shape, name):
+    """A row-major matrix argument of this shape: any row pitch, unit column stride.  None: not given."""
     if t is None:
         return _NO_ROWS
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must have dtype {dtype}, got {t.dtype}")
-    shape = t.shape
-    if len(shape) != 2 or shape[1] != cols or (rows is not None and shape[0] != rows):
-        raise ValueError(f"{name} must have shape [{'*' if rows is None else rows}, {cols}], got {list(shape)}")
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.shape == shape):
+        _wrong(t, dtype, shape, name)
+    n, cols = shape
     pitch, unit = t.stride()
-    if shape[0] <= 1:     # the pitch is never used: the width, in whole 16-byte units, stands in
+    if n <= 1:            # the pitch is never used: the width, in whole 16-byte units, stands in
         pitch = (cols + 7) // 8 * 8
     if (unit != 1 and cols > 1) or pitch < cols:
         raise ValueError(f"{name} must be row-major with unit column stride and rows that do not overlap")
@@ -595,9 +589,18 @@ def _rows(t, dtype, cols, name, rows=None):
 
 def _full(t, dtype, shape, name):
     """A contiguous argument of exactly this shape.  None: not given."""
-    if t is not None and t.shape != shape:
+    if t is None:
+        return None
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.shape == shape and t.is_contiguous()):
+        _wrong(t, dtype, shape, name)
+    return t.data_ptr()
+
+
+def _wrong(t, dtype, shape, name):
+    _ptr(t if not isinstance(t, torch.Tensor) else t.reshape(-1)[:0], dtype, name)     # type, device
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
-    return _ptr(t, dtype, name)
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _dtype(t, name):
@@ -620,11 +623,10 @@ def new_workspace_rows(T, K, E, device="cuda"):
 def dispatch(topk_ids, x, E, align, x_perm, sorted_token_ids, expert_ids, inv_perm, m_sum, ws, expert_counts=None):
     """Token rows x [T, H] sorted by expert into x_perm [msum_upper(T, K, E, align), H], with permute's index outputs."""
     T, K = topk_ids.shape
-    H = x.shape[1]
-    U = msum_upper(T, K, E, align)
-    dt = _dtype(x, "x")
-    _check(lib().moe_dispatch(dt, _ptr(topk_ids, torch.int32, "topk_ids"), _rows(x, x.dtype, H, "x", T), T, H, E, K, align,
-                              _rows(x_perm, x.dtype, H, "x_perm", U),
+    H, dt = x.shape[1], x.dtype
+    U = T * K + E * (align - 1)        # msum_upper
+    _check(lib().moe_dispatch(_dtype(x, "x"), _full(topk_ids, torch.int32, (T, K), "topk_ids"), _rows(x, dt, (T, H), "x"), T,
+                              H, E, K, align, _rows(x_perm, dt, (U, H), "x_perm"),
                               _full(sorted_token_ids, torch.int32, (U,), "sorted_token_ids"),
                               _full(expert_ids, torch.int32, (U,), "expert_ids"),
                               _full(inv_perm, torch.int32, (T, K), "inv_perm"), _full(m_sum, torch.int32, (1,), "m_sum"),
@@ -635,48 +637,43 @@ def dispatch(topk_ids, x, E, align, x_perm, sorted_token_ids, expert_ids, inv_pe
 def dispatch_backward(dx_perm, inv_perm, dx, ws, residual=None):
     """dx[t] = sum_k dx_perm[inv_perm[t, k]] (+ residual[t])."""
     T, K = inv_perm.shape
-    H, U = dx_perm.shape[1], dx_perm.shape[0]
-    dt = _dtype(dx, "dx")
-    _check(lib().moe_dispatch_backward(dt, _rows(dx_perm, dx.dtype, H, "dx_perm"), _ptr(inv_perm, torch.int32, "inv_perm"),
-                                       _rows(residual, dx.dtype, H, "residual", T), T, H, K, U,
-                                       _rows(dx, dx.dtype, H, "dx", T), _ptr(ws, torch.uint8, "ws"), ws.numel(),
-                                       _stream()), "moe_dispatch_backward")
+    (U, H), dt = dx_perm.shape, dx.dtype
+    _check(lib().moe_dispatch_backward(_dtype(dx, "dx"), _rows(dx_perm, dt, (U, H), "dx_perm"),
+                                       _full(inv_perm, torch.int32, (T, K), "inv_perm"),
+                                       _rows(residual, dt, (T, H), "residual"), T, H, K, U, _rows(dx, dt, (T, H), "dx"),
+                                       _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream()), "moe_dispatch_backward")
 
 
 def combine(y_perm, inv_perm, topk_w, out, ws, residual=None):
     """out[t] = sum_k topk_w[t, k] * y_perm[inv_perm[t, k]] (+ residual[t]); topk_w None: plain sum."""
     T, K = inv_perm.shape
-    H, U = y_perm.shape[1], y_perm.shape[0]
-    dt = _dtype(out, "out")
-    _check(lib().moe_combine(dt, _rows(y_perm, out.dtype, H, "y_perm"), _ptr(inv_perm, torch.int32, "inv_perm"),
-                             _full(topk_w, torch.float32, (T, K), "topk_w"), _rows(residual, out.dtype, H, "residual", T),
-                             T, H, K, U, _rows(out, out.dtype, H, "out", T), _ptr(ws, torch.uint8, "ws"), ws.numel(),
-                             _stream()), "moe_combine")
+    (U, H), dt = y_perm.shape, out.dtype
+    _check(lib().moe_combine(_dtype(out, "out"), _rows(y_perm, dt, (U, H), "y_perm"),
+                             _full(inv_perm, torch.int32, (T, K), "inv_perm"), _full(topk_w, torch.float32, (T, K), "topk_w"),
+                             _rows(residual, dt, (T, H), "residual"), T, H, K, U, _rows(out, dt, (T, H), "out"),
+                             _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream()), "moe_combine")
 
 
 def combine_backward(dout, y_perm, inv_perm, topk_w, dy_perm, dtopk_w, ws):
     """dy_perm[inv_perm[t, k]] = topk_w[t, k] * dout[t] and dtopk_w[t, k] = <dout[t], y_perm[inv_perm[t, k]]>.
     y_perm and dtopk_w None: the rows' gradient alone."""
     T, K = inv_perm.shape
-    H, U = dout.shape[1], dy_perm.shape[0]
-    dt = _dtype(dout, "dout")
-    _check(lib().moe_combine_backward(dt, _rows(dout, dout.dtype, H, "dout", T), _rows(y_perm, dout.dtype, H, "y_perm", U),
-                                      _ptr(inv_perm, torch.int32, "inv_perm"),
+    H, U, dt = dout.shape[1], dy_perm.shape[0], dout.dtype
+    _check(lib().moe_combine_backward(_dtype(dout, "dout"), _rows(dout, dt, (T, H), "dout"), _rows(y_perm, dt, (U, H), "y_perm"),
+                                      _full(inv_perm, torch.int32, (T, K), "inv_perm"),
                                       _full(topk_w, torch.float32, (T, K), "topk_w"), T, H, K, U,
-                                      _rows(dy_perm, dout.dtype, H, "dy_perm", U),
+                                      _rows(dy_perm, dt, (U, H), "dy_perm"),
                                       _full(dtopk_w, torch.float32, (T, K), "dtopk_w"), _ptr(ws, torch.uint8, "ws"),
                                       ws.numel(), _stream()), "moe_combine_backward")
 
 
 def route_backward(logits, topk_ids, topk_w, dtopk_w, score_fn, renormalize, dlogits, ws):
     """dlogits [T, E] (bf16, fp16 or fp32) from dtopk_w, for route's logits_out, topk_ids and topk_w."""
-    T, K = topk_ids.shape
+    TK = T, K = topk_ids.shape
     E = logits.shape[1]
-    dt = _dtype(dlogits, "dlogits")
-    _check(lib().moe_route_backward(_full(logits, torch.float32, (T, E), "logits"), _ptr(topk_ids, torch.int32, "topk_ids"),
-                                    _full(topk_w, torch.float32, (T, K), "topk_w"),
-                                    _full(dtopk_w, torch.float32, (T, K), "dtopk_w"), T, E, K,
-                                    SCORE_FNS.get(score_fn, score_fn), int(renormalize), dt,
+    _check(lib().moe_route_backward(_full(logits, torch.float32, (T, E), "logits"), _full(topk_ids, torch.int32, TK, "topk_ids"),
+                                    _full(topk_w, torch.float32, TK, "topk_w"), _full(dtopk_w, torch.float32, TK, "dtopk_w"),
+                                    T, E, K, SCORE_FNS.get(score_fn, score_fn), int(renormalize), _dtype(dlogits, "dlogits"),
                                     _full(dlogits, dlogits.dtype, (T, E), "dlogits"), _ptr(ws, torch.uint8, "ws"),
                                     ws.numel(), _stream()), "moe_route_backward")
 
@@ -693,37 +690,38 @@ def new_workspace_linear(rows, N, K, E=0, act="none", device="cuda"):
 
 
 def _linear_dims(x, w, act, expert_counts):
-    E = w.shape[0] if expert_counts is not None else 0
-    if w.dim() != (3 if E else 2):
+    """(rows, N, K, E, activation code, columns of its output)"""
+    shape = w.shape
+    if len(shape) != (2 if expert_counts is None else 3):
         raise ValueError("w must have shape [N, K], or [E, N, K] with expert_counts")
-    N, K = w.shape[-2], w.shape[-1]
-    return x.shape[0], N, K, E, (N // 2 if ACTS.get(act, act) == ACTS["swiglu"] else N)
+    act = ACTS.get(act, act)
+    N = shape[-2]
+    return x.shape[0], N, shape[-1], 0 if expert_counts is None else shape[0], act, N // 2 if act == 4 else N
 
 
 def linear(x, w, y, ws, bias=None, act="none", residual=None, z=None, expert_counts=None, align=0):
     """y = act(x @ w^T + bias) (+ residual); z (optional) receives the products before the activation.
     w [N, K] dense, or [E, N, K] with expert_counts [E]: expert e's rows are its segment of the sorted rows."""
-    rows, N, K, E, cols = _linear_dims(x, w, act, expert_counts)
-    dt = _dtype(x, "x")
-    _check(lib().moe_linear(dt, _rows(x, x.dtype, K, "x"), _ptr(w, x.dtype, "w"),
-                            _full(bias, torch.float32, w.shape[:-1], "bias"), _rows(residual, x.dtype, cols, "residual", rows),
-                            ACTS.get(act, act), _full(expert_counts, torch.int32, (E,), "expert_counts"), rows, N, K, E,
-                            int(align), _rows(y, x.dtype, cols, "y", rows), _rows(z, x.dtype, N, "z", rows),
-                            _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream()), "moe_linear")
+    rows, N, K, E, act, cols = _linear_dims(x, w, act, expert_counts)
+    dt = x.dtype
+    _check(lib().moe_linear(_dtype(x, "x"), _rows(x, dt, (rows, K), "x"), _ptr(w, dt, "w"),
+                            _full(bias, torch.float32, w.shape[:-1], "bias"), _rows(residual, dt, (rows, cols), "residual"),
+                            act, _full(expert_counts, torch.int32, (E,), "expert_counts"), rows, N, K, E, align,
+                            _rows(y, dt, (rows, cols), "y"), _rows(z, dt, (rows, N), "z"), _ptr(ws, torch.uint8, "ws"),
+                            ws.numel(), _stream()), "moe_linear")
 
 
 def linear_backward(dy, x, w, ws, dx=None, dw=None, dbias=None, act="none", z=None, dx_residual=None,
                     expert_counts=None, align=0):
     """Gradients of linear: dx = dz @ w (+ dx_residual), dw = dz^T @ x, dbias = sum of dz, dz = dy * act'(z)."""
-    rows, N, K, E, cols = _linear_dims(dy, w, act, expert_counts)
-    dt = _dtype(dy, "dy")
-    _check(lib().moe_linear_backward(dt, _rows(dy, dy.dtype, cols, "dy"), _rows(x, dy.dtype, K, "x", rows),
-                                     _ptr(w, dy.dtype, "w"), _rows(z, dy.dtype, N, "z", rows), ACTS.get(act, act),
-                                     _full(expert_counts, torch.int32, (E,), "expert_counts"), rows, N, K, E, int(align),
-                                     _rows(dx_residual, dy.dtype, K, "dx_residual", rows),
-                                     _rows(dx, dy.dtype, K, "dx", rows), _full(dw, dy.dtype, w.shape, "dw"),
-                                     _full(dbias, torch.float32, w.shape[:-1], "dbias"), _ptr(ws, torch.uint8, "ws"),
-                                     ws.numel(), _stream()), "moe_linear_backward")
+    rows, N, K, E, act, cols = _linear_dims(dy, w, act, expert_counts)
+    dt = dy.dtype
+    _check(lib().moe_linear_backward(_dtype(dy, "dy"), _rows(dy, dt, (rows, cols), "dy"), _rows(x, dt, (rows, K), "x"),
+                                     _ptr(w, dt, "w"), _rows(z, dt, (rows, N), "z"), act,
+                                     _full(expert_counts, torch.int32, (E,), "expert_counts"), rows, N, K, E, align,
+                                     _rows(dx_residual, dt, (rows, K), "dx_residual"), _rows(dx, dt, (rows, K), "dx"),
+                                     _full(dw, dt, w.shape, "dw"), _full(dbias, torch.float32, w.shape[:-1], "dbias"),
+                                     _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream()), "moe_linear_backward")
 
 
 def selftest_wait_timeout(ws, mode):

@@ -27,7 +27,9 @@ __device__ __forceinline__ float sigmoid_over_softplus(float l) {
   return sig / (fmaxf(l, 0.f) + log1pf(e));
 }
 
-template <class T>
+// Value i of a lane is expert V * lane + 32 * V * (i / V) + i % V: V = 4 where rows are whole groups of four
+// (16-byte accesses), else 1.  PER: values per lane.
+template <class T, int PER, int V>
 __global__ void __launch_bounds__(kGradWarps * 32) route_grad_kernel(const float* __restrict__ logits,
                                                                      const int32_t* __restrict__ ids,
                                                                      const float* __restrict__ w,
@@ -40,8 +42,24 @@ __global__ void __launch_bounds__(kGradWarps * 32) route_grad_kernel(const float
   if (t >= T_) return;
   const float* lrow = logits + static_cast<size_t>(t) * E;
   typename T::raw* orow = out + static_cast<size_t>(t) * E;
+  const bool dense = softmax && !renorm;
+  float p[PER];
+#pragma unroll
+  for (int i = 0; i < PER; i += V) {
+    const int e = V * lane + 32 * i;
+    if constexpr (V == 4) {
+      float4 q = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      if (dense && e < E) q = __ldg(reinterpret_cast<const float4*>(lrow + e));
+      p[i] = q.x;
+      p[i + 1] = q.y;
+      p[i + 2] = q.z;
+      p[i + 3] = q.w;
+    } else {
+      p[i] = dense && e < E ? __ldg(lrow + e) : -INFINITY;
+    }
+  }
   int id = -1;
-  float wk = 0.f, dk = 0.f;
+  float wk = 0.f, dk = 0.f, lk = 0.f;
   if (lane < K) {
     id = __ldg(ids + static_cast<size_t>(t) * K + lane);
     wk = __ldg(w + static_cast<size_t>(t) * K + lane);
@@ -50,6 +68,8 @@ __global__ void __launch_bounds__(kGradWarps * 32) route_grad_kernel(const float
       record_error(status, kDevErrIndex);
       id = -1;
       wk = dk = 0.f;
+    } else if (dense || !softmax) {
+      lk = __ldg(lrow + id);
     }
   }
   float g = wk * dk;
@@ -59,21 +79,48 @@ __global__ void __launch_bounds__(kGradWarps * 32) route_grad_kernel(const float
     for (int off = 16; off > 0; off >>= 1) c += __shfl_xor_sync(0xffffffffu, c, off);
     g = id >= 0 ? wk * (dk - c) : 0.f;
   }
+  // p becomes the row's -p_e sum_j g_j (dense) or zeros
   float total = 0.f, lmax = -INFINITY, sum = 0.f;
-  const bool dense = softmax && !renorm;
   if (dense) {
     total = g;
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
-    for (int e = lane; e < E; e += 32) lmax = fmaxf(lmax, __ldg(lrow + e));
+    for (int i = 0; i < PER; ++i) lmax = fmaxf(lmax, p[i]);
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) lmax = fmaxf(lmax, __shfl_xor_sync(0xffffffffu, lmax, off));
-    for (int e = lane; e < E; e += 32) sum += expf(__ldg(lrow + e) - lmax);
+    for (int off = 16; off > 0; off >>= 1) {
+      total += __shfl_xor_sync(0xffffffffu, total, off);
+      lmax = fmaxf(lmax, __shfl_xor_sync(0xffffffffu, lmax, off));
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      p[i] = expf(p[i] - lmax);
+      sum += V * lane + 32 * (i / V * V) + i % V < E ? p[i] : 0.f;
+    }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
   }
-  for (int e = lane; e < E; e += 32)
-    orow[e] = T::from_f(dense ? -(expf(__ldg(lrow + e) - lmax) / sum) * total : 0.f);
+#pragma unroll
+  for (int i = 0; i < PER; i += V) {
+    const int e = V * lane + 32 * i;
+    if (e >= E) continue;
+#pragma unroll
+    for (int j = 0; j < V; ++j) p[i + j] = dense ? -(p[i + j] / sum) * total : 0.f;
+    if constexpr (V == 4) {
+      typename T::raw o[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[j] = T::from_f(p[i + j]);
+      if constexpr (sizeof(o) == 16) {
+        uint4 u;
+        memcpy(&u, o, 16);
+        *reinterpret_cast<uint4*>(orow + e) = u;
+      } else {
+        uint2 u;
+        memcpy(&u, o, 8);
+        *reinterpret_cast<uint2*>(orow + e) = u;
+      }
+    } else {
+      orow[e] = T::from_f(p[i]);
+    }
+  }
   // an expert named twice gets both terms, from its first slot
   float mine = 0.f;
   bool first = id >= 0;
@@ -85,16 +132,38 @@ __global__ void __launch_bounds__(kGradWarps * 32) route_grad_kernel(const float
       if (k < lane) first = false;
     }
   }
-  __syncwarp();
+  __syncwarp();                                     // the row is written before its selected entries
   if (first) {
-    const float l = __ldg(lrow + id);
     float v = mine;
     if (!softmax)
-      v = 0.5f * mine * sigmoid_over_softplus(l);
+      v = 0.5f * mine * sigmoid_over_softplus(lk);
     else if (dense)
-      v = mine - (expf(l - lmax) / sum) * total;
+      v = mine - (expf(lk - lmax) / sum) * total;
     orow[id] = T::from_f(v);
   }
+}
+
+template <class T, int PER, int V>
+cudaError_t route_grad_launch(const float* logits, const int32_t* ids, const float* w, const float* dw, int T_, int E, int K,
+                              int softmax, int renorm, void* out, uint32_t* status, cudaStream_t stream) {
+  route_grad_kernel<T, PER, V><<<(T_ + kGradWarps - 1) / kGradWarps, kGradWarps * 32, 0, stream>>>(
+      logits, ids, w, dw, T_, E, K, softmax, renorm, static_cast<typename T::raw*>(out), status);
+  return cudaGetLastError();
+}
+
+template <class T>
+cudaError_t route_grad_by_size(const float* l, const int32_t* i, const float* w, const float* d, int T_, int E, int K, int s,
+                               int r, void* o, uint32_t* st, cudaStream_t q) {
+  const int per = (E + 31) / 32;
+  if (E % 4 == 0) {
+    if (per <= 4) return route_grad_launch<T, 4, 4>(l, i, w, d, T_, E, K, s, r, o, st, q);
+    if (per <= 8) return route_grad_launch<T, 8, 4>(l, i, w, d, T_, E, K, s, r, o, st, q);
+    if (per <= 16) return route_grad_launch<T, 16, 4>(l, i, w, d, T_, E, K, s, r, o, st, q);
+    return route_grad_launch<T, 32, 4>(l, i, w, d, T_, E, K, s, r, o, st, q);
+  }
+  if (per <= 4) return route_grad_launch<T, 4, 1>(l, i, w, d, T_, E, K, s, r, o, st, q);
+  if (per <= 16) return route_grad_launch<T, 16, 1>(l, i, w, d, T_, E, K, s, r, o, st, q);
+  return route_grad_launch<T, 32, 1>(l, i, w, d, T_, E, K, s, r, o, st, q);
 }
 
 }  // namespace
@@ -102,17 +171,9 @@ __global__ void __launch_bounds__(kGradWarps * 32) route_grad_kernel(const float
 cudaError_t launch_route_grad(int dt, const float* logits, const int32_t* ids, const float* w, const float* dw, int T,
                               int E, int K, int softmax, int renorm, void* out, uint32_t* status, cudaStream_t stream) {
   if (T == 0) return cudaSuccess;
-  const int grid = (T + kGradWarps - 1) / kGradWarps;
-  if (dt == kBf16)
-    route_grad_kernel<Bf16Elem><<<grid, kGradWarps * 32, 0, stream>>>(logits, ids, w, dw, T, E, K, softmax, renorm,
-                                                                      static_cast<uint16_t*>(out), status);
-  else if (dt == kF16)
-    route_grad_kernel<F16Elem><<<grid, kGradWarps * 32, 0, stream>>>(logits, ids, w, dw, T, E, K, softmax, renorm,
-                                                                     static_cast<uint16_t*>(out), status);
-  else
-    route_grad_kernel<F32Elem><<<grid, kGradWarps * 32, 0, stream>>>(logits, ids, w, dw, T, E, K, softmax, renorm,
-                                                                     static_cast<float*>(out), status);
-  return cudaGetLastError();
+  if (dt == kBf16) return route_grad_by_size<Bf16Elem>(logits, ids, w, dw, T, E, K, softmax, renorm, out, status, stream);
+  if (dt == kF16) return route_grad_by_size<F16Elem>(logits, ids, w, dw, T, E, K, softmax, renorm, out, status, stream);
+  return route_grad_by_size<F32Elem>(logits, ids, w, dw, T, E, K, softmax, renorm, out, status, stream);
 }
 
 }  // namespace moe

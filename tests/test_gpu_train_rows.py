@@ -309,3 +309,26 @@ def test_rows_on_another_stream_and_in_a_graph(M):
         torch.cuda.synchronize()
         assert torch.equal(out, want)
     assert M.get_error(ws) == M.OK
+
+
+def test_the_binding_refuses_wrong_tensors(M):
+    T, H, E, K = 4, 64, 3, 2
+    inv = torch.zeros(T, K, dtype=torch.int32, device="cuda")
+    y, out = torch.zeros(8, H, device="cuda"), torch.zeros(T, H, device="cuda")
+    ws = M.new_workspace_rows(T, K, E)
+    with pytest.raises(TypeError, match="y_perm must have dtype"):
+        M.combine(y.half(), inv, None, out, ws)
+    with pytest.raises(ValueError, match="residual must have shape"):
+        M.combine(y, inv, None, out, ws, residual=out[:2])
+    with pytest.raises(ValueError, match="unit column stride"):
+        M.combine(torch.zeros(H, 8, device="cuda").t(), inv, None, out, ws)
+    with pytest.raises(ValueError, match="do not overlap"):
+        M.combine(y[0].expand(8, H), inv, None, out, ws)
+    with pytest.raises(ValueError, match="inv_perm must be contiguous"):
+        M.combine(y, torch.zeros(K, T, dtype=torch.int32, device="cuda").t(), None, out, ws)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        M.combine(y, inv, torch.zeros(T, K), out, ws)
+    with pytest.raises(TypeError, match="torch.Tensor"):
+        M.combine(y, inv, [1.0], out, ws)
+    with pytest.raises(M.MoeError):
+        M.linear(y, torch.zeros(H, H, device="cuda"), torch.zeros(8, H, device="cuda"), M.new_workspace_linear(8, H, H))

@@ -129,13 +129,13 @@ def test_linear_refusals(M):
 def test_the_binding_checks_its_arguments(M):
     x = torch.zeros(4, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="CUDA tensor"):
-        M._rows(x, torch.bfloat16, 64, "x")
-    assert M._rows(None, torch.bfloat16, 64, "x").ptr is None
+        M._rows(x, torch.bfloat16, (4, 64), "x")
+    assert M._rows(None, torch.bfloat16, (4, 64), "x").ptr is None
     with pytest.raises(TypeError, match="torch.Tensor"):
-        M._rows([1], torch.bfloat16, 64, "x")
+        M._rows([1], torch.bfloat16, (4, 64), "x")
     with pytest.raises(TypeError, match="bfloat16, float16 or float32"):
         M._dtype(torch.zeros(1, dtype=torch.int32), "x")
-    with pytest.raises(ValueError, match="shape"):
+    with pytest.raises(ValueError, match="CUDA tensor"):
         M._full(torch.zeros(3), torch.float32, (4,), "bias")
     with pytest.raises(ValueError, match="w must have shape"):
         M._linear_dims(x, torch.zeros(2, 8, 64), "none", None)
