@@ -234,7 +234,7 @@ constexpr size_t kLinearMapBytes = 2 * 128;
 cudaError_t launch_linear_dw(const LinearShape& p, RowsView dz, RowsView x, uint16_t* dw, void* maps, uint32_t* status,
                              cudaStream_t stream);
 // dz = dy * act'(z) (act none: not written) and, with db, the bias gradient (part: E * linear_bias_slices * N floats).
-int linear_bias_slices(int N, int E, int act);
+int linear_bias_slices(int rows, int N, int E, int act);
 cudaError_t launch_act_grad(const LinearShape& p, RowsView dy, RowsView z, int act, RowsView dz, float* part, float* db,
                             uint32_t* status, cudaStream_t stream);
 

@@ -251,21 +251,37 @@ struct ZeroSums {
     for (int j = 0; j < 32; ++j) v[j] = 0.f;
   }
 };
+// A slice's sums in shared memory: value i of 8-column group g of epilogue thread t (of 128 of its parity) is
+// float 4 * ((2g + i / 4) * 128 + t) + i % 4.
 struct ClusterSums {
-  uint32_t base;              // this thread's first value in its own shared memory; value i of 8-column group g
-  int slices;                 // is (8g + i) * 128 values further
+  uint32_t base;              // this thread's first value in its own shared memory
+  int slices;
   __device__ __forceinline__ void operator()(int c0, int left, float (&v)[32]) const {
 #pragma unroll
     for (int j = 0; j < 32; ++j) v[j] = 0.f;
-    for (int s = 0; s < slices; ++s) {
-      const uint32_t p = mapa_shared(base, static_cast<uint32_t>(s)) + static_cast<uint32_t>(c0) * (128 * 4);
+    // the loads of four slices are under way before the first is added
+    for (int s0 = 0; s0 < slices; s0 += 4) {
 #pragma unroll
-      for (int j = 0; j < 32; ++j)
-        if ((j & ~7) < left) {
-          float x;
-          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(p + j * (128 * 4)) : "memory");
-          v[j] += x;
+      for (int n = 0; n < 4; ++n) {
+        if (8 * n >= left) continue;
+        float x[4][8];
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          const uint32_t p = mapa_shared(base, static_cast<uint32_t>(min(s0 + s, slices - 1))) +
+                             static_cast<uint32_t>(c0 / 8 + n) * (2 * 128 * 16);
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(x[s][4 * k]), "=f"(x[s][4 * k + 1]), "=f"(x[s][4 * k + 2]), "=f"(x[s][4 * k + 3])
+                         : "r"(p + k * (128 * 16))
+                         : "memory");
         }
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+          if (s0 + s < slices)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[8 * n + j] += x[s][j];
+      }
     }
   }
 };
@@ -490,6 +506,8 @@ __global__ void __launch_bounds__(kLinMaxE) expert_maps_kernel(const __grid_cons
                                                                const int32_t* __restrict__ counts, int E, int align, int rows,
                                                                CUtensorMap* emaps) {
   __shared__ int sums[kLinMaxE / 32];
+  grid_dependency_wait();
+  grid_launch_dependents();
   const int e = threadIdx.x, warp = e / 32, lane = e % 32;
   const int c = e < E ? min(max(__ldg(counts + e), 0), rows) : 0;
   const int padded = (c + align - 1) / align * align;
@@ -558,6 +576,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     tmem_alloc_pair(smem_u32(tmem_slot), 2 * kLinBJ);
     tmem_relinquish_pair();
   }
+  grid_dependency_wait();        // everything below reads what the stream's previous kernels wrote
+  grid_launch_dependents();
   if (warp == 2) {
     // segment starts and tile counts; a segment that would leave the buffers is an error and is cut
     int srun = 0, prun = 0;
@@ -777,6 +797,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  grid_dependency_wait();
+  grid_launch_dependents();
   const uint32_t tmem = *tmem_slot;
 
   LinTile t;
@@ -858,14 +880,14 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         lin_drain<MODE>(a, t, i0, 0, t.ncols, mine, q, par, lane, piece);
       } else {
         // every MMA has read the ring: it takes this slice's sums, as ClusterSums reads them
-        float* part = reinterpret_cast<float*>(smem) + q * 32 + lane;
+        float4* part = reinterpret_cast<float4*>(smem) + q * 32 + lane;
 #pragma unroll 1
         for (int c0 = 32 * par; c0 < t.ncols; c0 += 64) {
           float v[32];
           mine(c0, 32, v);
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (c0 + (j & ~7) < t.ncols) part[(c0 + j) * 128] = v[j];
+          for (int j = 0; j < 32; j += 4)
+            if (c0 + (j & ~7) < t.ncols) part[(c0 + j) / 4 * 128] = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
         }
       }
     }
@@ -877,7 +899,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     if (warp >= 2 && ok) {
       const int q = warp & 3, par = (warp - 2) >> 2;
       const int w = ((t.ncols + S - 1) / S + 7) & ~7, cb = min(slice * w, t.ncols), ce = min(cb + w, t.ncols);
-      lin_drain<MODE>(a, t, i0, cb, ce, ClusterSums{smem_u32(reinterpret_cast<float*>(smem) + q * 32 + lane), S}, q,
+      lin_drain<MODE>(a, t, i0, cb, ce, ClusterSums{smem_u32(reinterpret_cast<float4*>(smem) + q * 32 + lane), S}, q,
                       par, lane, piece);
     }
     cluster_sync();    // the slices stay until every CTA has read them
@@ -1003,17 +1025,19 @@ cudaError_t lin_launch(const LinPlan& p, const CUtensorMap& ma, const LinMapsB& 
   a.stages = p.stages;
   a.b_box = p.b_box;
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = static_cast<unsigned>(p.pair ? 2 : p.split);
   at[0].val.clusterDim.y = 1;
   at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3(p.grid);
   cfg.blockDim = dim3(kLinThreads);
   cfg.dynamicSmemBytes = p.pair ? kPairSmem : kSplitSmem;
   cfg.stream = stream;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   if (p.pair) {
     const cudaError_t err = allow_smem(reinterpret_cast<const void*>(&linear_pair_kernel<MODE>), kPairSmem, pair_done);
     if (err != cudaSuccess) return err;
@@ -1124,8 +1148,8 @@ cudaError_t launch_linear_dw(const LinearShape& p, RowsView dz, RowsView x, uint
     return cudaErrorInvalidValue;
   CUtensorMap* emaps = static_cast<CUtensorMap*>(maps);
   if (p.counts) {
-    expert_maps_kernel<<<1, kLinMaxE, 0, stream>>>(ma, mb.m[0], p.counts, p.E, p.align, p.rows, emaps);
-    const cudaError_t err = cudaGetLastError();
+    const cudaError_t err = launch_pdl(expert_maps_kernel, dim3(1), dim3(kLinMaxE), 0, stream, ma, mb.m[0], p.counts, p.E,
+                                       p.align, p.rows, emaps);
     if (err != cudaSuccess) return err;
   }
   return lin_launch<kLinDw>(pl, ma, mb, emaps, a, stream);
@@ -1166,6 +1190,8 @@ __global__ void __launch_bounds__(32 * kActRowLanes)
   __shared__ float red[kActRowLanes][2][32 * 8 + 8];
   const int lane = threadIdx.x & 31, rl = threadIdx.x >> 5;
   const int e = blockIdx.y;
+  grid_dependency_wait();
+  grid_launch_dependents();
   int cnt = rows, seg = 0;
   if (counts) {
     if (threadIdx.x == 0) s_seg = 0;
@@ -1250,6 +1276,8 @@ __global__ void __launch_bounds__(32 * kActRowLanes)
 __global__ void __launch_bounds__(256) bias_sum_kernel(const float* __restrict__ part, int S, int N, long long total,
                                                        float* __restrict__ db) {
   const long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+  grid_dependency_wait();
+  grid_launch_dependents();
   if (i >= total) return;
   const long long e = i / N, c = i - e * N;
   float s = 0.f;
@@ -1259,33 +1287,32 @@ __global__ void __launch_bounds__(256) bias_sum_kernel(const float* __restrict__
 
 }  // namespace
 
-// Row slices per expert: about eight CTAs per SM in all, at most 64.
-int linear_bias_slices(int N, int E, int act) {
-  const int cols = act == kActSwiglu ? N / 2 : N;
-  const long long cta = static_cast<long long>((cols + 255) / 256) * (E > 0 ? E : 1);
-  const long long s = (8LL * 152 + cta - 1) / cta;
+// Row slices per expert: about eight CTAs per SM in all, at most 64, none with less than 32 rows on average
+// (with one slice the bias gradient is the slice's sum and needs no second launch).
+int linear_bias_slices(int rows, int N, int E, int act) {
+  const int cols = act == kActSwiglu ? N / 2 : N, n = E > 0 ? E : 1;
+  const long long cta = static_cast<long long>((cols + 255) / 256) * n;
+  long long s = (8LL * 152 + cta - 1) / cta;
+  const long long most = static_cast<long long>(rows) / n / 32;
+  if (s > most) s = most;
   return static_cast<int>(s < 1 ? 1 : (s > 64 ? 64 : s));
 }
 
 cudaError_t launch_act_grad(const LinearShape& p, RowsView dy, RowsView z, int act, RowsView dz, float* part, float* db,
                             uint32_t* status, cudaStream_t stream) {
-  const int E = p.counts ? p.E : 1, S = linear_bias_slices(p.N, E, act);
+  const int E = p.counts ? p.E : 1, S = linear_bias_slices(p.rows, p.N, E, act);
   const int cols = act == kActSwiglu ? p.N / 2 : p.N;
   const dim3 grid((cols + 255) / 256, E, S);
-  float* pp = db ? part : nullptr;
-  if (p.f16)
-    act_grad_kernel<F16Elem><<<grid, 256, 0, stream>>>(static_cast<const uint16_t*>(dy.ptr), dy.ld,
-                                                       static_cast<const uint16_t*>(z.ptr), z.ld, act, p.counts, E, p.align,
-                                                       p.rows, p.N, static_cast<uint16_t*>(dz.ptr), dz.ld, pp, S, status);
-  else
-    act_grad_kernel<Bf16Elem><<<grid, 256, 0, stream>>>(static_cast<const uint16_t*>(dy.ptr), dy.ld,
-                                                        static_cast<const uint16_t*>(z.ptr), z.ld, act, p.counts, E, p.align,
-                                                        p.rows, p.N, static_cast<uint16_t*>(dz.ptr), dz.ld, pp, S, status);
-  cudaError_t err = cudaGetLastError();
-  if (err != cudaSuccess || !db) return err;
+  float* pp = !db ? nullptr : S == 1 ? db : part;
+  const auto kernel = p.f16 ? act_grad_kernel<F16Elem> : act_grad_kernel<Bf16Elem>;
+  const cudaError_t err =
+      launch_pdl(kernel, grid, dim3(32 * kActRowLanes), 0, stream, static_cast<const uint16_t*>(dy.ptr), dy.ld,
+                 static_cast<const uint16_t*>(z.ptr), z.ld, act, p.counts, E, p.align, p.rows, p.N,
+                 static_cast<uint16_t*>(dz.ptr), dz.ld, pp, S, status);
+  if (err != cudaSuccess || !db || S == 1) return err;
   const long long total = static_cast<long long>(E) * p.N;
-  bias_sum_kernel<<<static_cast<int>((total + 255) / 256), 256, 0, stream>>>(part, S, p.N, total, db);
-  return cudaGetLastError();
+  return launch_pdl(bias_sum_kernel, dim3(static_cast<int>((total + 255) / 256)), dim3(256), 0, stream,
+                    static_cast<const float*>(part), S, p.N, total, db);
 }
 
 }  // namespace moe

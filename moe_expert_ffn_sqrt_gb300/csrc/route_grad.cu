@@ -39,6 +39,8 @@ __global__ void __launch_bounds__(kGradWarps * 32) route_grad_kernel(const float
                                                                      uint32_t* status) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int t = blockIdx.x * kGradWarps + warp;
+  grid_dependency_wait();
+  grid_launch_dependents();
   if (t >= T_) return;
   const float* lrow = logits + static_cast<size_t>(t) * E;
   typename T::raw* orow = out + static_cast<size_t>(t) * E;
@@ -146,9 +148,8 @@ __global__ void __launch_bounds__(kGradWarps * 32) route_grad_kernel(const float
 template <class T, int PER, int V>
 cudaError_t route_grad_launch(const float* logits, const int32_t* ids, const float* w, const float* dw, int T_, int E, int K,
                               int softmax, int renorm, void* out, uint32_t* status, cudaStream_t stream) {
-  route_grad_kernel<T, PER, V><<<(T_ + kGradWarps - 1) / kGradWarps, kGradWarps * 32, 0, stream>>>(
-      logits, ids, w, dw, T_, E, K, softmax, renorm, static_cast<typename T::raw*>(out), status);
-  return cudaGetLastError();
+  return launch_pdl(route_grad_kernel<T, PER, V>, dim3((T_ + kGradWarps - 1) / kGradWarps), dim3(kGradWarps * 32), 0, stream,
+                    logits, ids, w, dw, T_, E, K, softmax, renorm, static_cast<typename T::raw*>(out), status);
 }
 
 template <class T>

@@ -54,7 +54,7 @@ LinearWs linear_layout(int rows, int N, int E, int act) {
   w.dz = off;
   if (act != kActNone) off = up(off + static_cast<size_t>(rows) * N * 2);
   w.part = off;
-  off = up(off + static_cast<size_t>(E > 0 ? E : 1) * linear_bias_slices(N, E, act) * N * 4);
+  off = up(off + static_cast<size_t>(E > 0 ? E : 1) * linear_bias_slices(rows, N, E, act) * N * 4);
   w.total = off;
   return w;
 }

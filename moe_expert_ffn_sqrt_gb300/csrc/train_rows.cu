@@ -16,6 +16,9 @@
 // has fewer packs than that (64-column rows one token per CTA leave 248 threads idle), and a call with
 // few tokens cuts their rows (or their slots) over more CTAs.
 //
+// Every launch may begin while the stream's previous kernel ends (programmatic dependent launch): the
+// kernels wait for it before they touch memory.
+//
 // inv_perm entries of -1 are pairs that a full BatchedExperts slot dropped: they add nothing and get a
 // zero weight gradient.  Any other entry outside [0, U) records MOE_ERR_DEVICE_INDEX and is skipped.
 #include <initializer_list>
@@ -69,6 +72,8 @@ __global__ void __launch_bounds__(kRowThreads) scatter_rows_kernel(const V* __re
   __shared__ SlotTable slots;
   const int tokens = kRowThreads / lanes, slot = threadIdx.x / lanes;
   const int t0 = blockIdx.x * tokens, t = t0 + slot;
+  grid_dependency_wait();
+  grid_launch_dependents();
   load_slots(slots, inv, nullptr, t0, tokens, T, K, U, status);
   if (t >= T) return;
   const int* rows = slots.row + slot * K;
@@ -98,6 +103,8 @@ __global__ void __launch_bounds__(kRowThreads) sum_rows_kernel(const typename T:
   __shared__ SlotTable slots;
   const int tokens = kRowThreads / lanes, slot = threadIdx.x / lanes;
   const int t0 = blockIdx.x * tokens, t = t0 + slot;
+  grid_dependency_wait();
+  grid_launch_dependents();
   load_slots(slots, inv, w, t0, tokens, T_, K, U, status);
   if (t >= T_) return;
   const int* rows = slots.row + slot * K;
@@ -142,6 +149,8 @@ __global__ void __launch_bounds__(kRowThreads) combine_grad_kernel(const typenam
   __shared__ float part[kMaxSlots][kRowThreads / 32];
   const int tokens = kRowThreads / lanes, slot = threadIdx.x / lanes, lane = threadIdx.x % lanes;
   const int t0 = blockIdx.x * tokens, t = t0 + slot;
+  grid_dependency_wait();
+  grid_launch_dependents();
   load_slots(slots, inv, w, t0, tokens, T_, K, U, status);
   const int k_end = min(K, static_cast<int>(blockIdx.y + 1) * per);
   for (int k = blockIdx.y * per; k < k_end; ++k) {
@@ -206,6 +215,9 @@ __global__ void __launch_bounds__(kFewThreads) dispatch_few_kernel(const Permute
   const int pieces = (n + 32 * kFewUnits - 1) / (32 * kFewUnits);
   const long long units = static_cast<long long>(N) * pieces;
   const long long u0 = static_cast<long long>(blockIdx.x) * (kFewThreads / 32) + warp;
+  for (int i = tid; i < a.E; i += kFewThreads) cnt[i] = 0;
+  grid_dependency_wait();
+  grid_launch_dependents();
   // the first piece, and the ids
   V v[kFewUnits];
   if (u0 < units) {
@@ -223,7 +235,6 @@ __global__ void __launch_bounds__(kFewThreads) dispatch_few_kernel(const Permute
     }
   }
   s_ids[tid] = e;
-  for (int i = tid; i < a.E; i += kFewThreads) cnt[i] = 0;
   __syncthreads();
   int rank = 0;
   if (e >= 0) {
@@ -345,9 +356,8 @@ cudaError_t launch_scatter_rows(int dt, RowsView x, const int32_t* inv, int T, i
     const int es = static_cast<int>(dtype_bytes(dt)), n = static_cast<int>(static_cast<long long>(H) * es / bytes);
     const int lanes = row_lanes(n), tokens = kRowThreads / lanes;
     const dim3 grid((T + tokens - 1) / tokens, row_cuts(T, lanes, n));
-    scatter_rows_kernel<V><<<grid, kRowThreads, 0, stream>>>(static_cast<const V*>(x.ptr), x.ld * es / bytes, inv, T, K, n, U,
-                                                             static_cast<V*>(out.ptr), out.ld * es / bytes, lanes, status);
-    return cudaGetLastError();
+    return launch_pdl(scatter_rows_kernel<V>, grid, dim3(kRowThreads), 0, stream, static_cast<const V*>(x.ptr),
+                      x.ld * es / bytes, inv, T, K, n, U, static_cast<V*>(out.ptr), out.ld * es / bytes, lanes, status);
   });
 }
 
@@ -363,9 +373,8 @@ cudaError_t launch_dispatch_few(int dt, const int32_t* topk_ids, RowsView x, int
     const long long units = static_cast<long long>(T) * K * ((n + 32 * kFewUnits - 1) / (32 * kFewUnits));
     const long long want = (units + kFewThreads / 32 - 1) / (kFewThreads / 32);
     const int grid = static_cast<int>(want < 1 ? 1 : want > 4 * num_sms() ? 4 * num_sms() : want);
-    dispatch_few_kernel<V><<<grid, kFewThreads, 2 * E * sizeof(int32_t), stream>>>(
-        a, static_cast<const V*>(x.ptr), x.ld * es / bytes, n, static_cast<V*>(out.ptr), out.ld * es / bytes);
-    return cudaGetLastError();
+    return launch_pdl(dispatch_few_kernel<V>, dim3(grid), dim3(kFewThreads), 2 * E * sizeof(int32_t), stream, a,
+                      static_cast<const V*>(x.ptr), x.ld * es / bytes, n, static_cast<V*>(out.ptr), out.ld * es / bytes);
   });
 }
 
@@ -377,10 +386,9 @@ cudaError_t launch_sum_rows(int dt, RowsView y, const int32_t* inv, const float*
     constexpr int N = decltype(width)::value;
     const int n = (H + N - 1) / N, lanes = row_lanes(n), tokens = kRowThreads / lanes;
     const dim3 grid((T + tokens - 1) / tokens, row_cuts(T, lanes, n));
-    sum_rows_kernel<E, N><<<grid, kRowThreads, 0, stream>>>(
-        static_cast<const typename E::raw*>(y.ptr), y.ld, inv, w, static_cast<const typename E::raw*>(res.ptr), res.ld, T, K,
-        H, U, static_cast<typename E::raw*>(out.ptr), out.ld, lanes, status);
-    return cudaGetLastError();
+    return launch_pdl(sum_rows_kernel<E, N>, grid, dim3(kRowThreads), 0, stream, static_cast<const typename E::raw*>(y.ptr),
+                      y.ld, inv, w, static_cast<const typename E::raw*>(res.ptr), res.ld, T, K, H, U,
+                      static_cast<typename E::raw*>(out.ptr), out.ld, lanes, status);
   });
 }
 
@@ -392,10 +400,9 @@ cudaError_t launch_combine_grad(int dt, RowsView dout, RowsView y, const int32_t
     constexpr int N = decltype(width)::value;
     const int lanes = row_lanes((H + N - 1) / N), tokens = kRowThreads / lanes, ctas = (T + tokens - 1) / tokens;
     const int per = ctas >= 4 * num_sms() ? K : 1;   // few tokens: a CTA per slot
-    combine_grad_kernel<E, N><<<dim3(ctas, (K + per - 1) / per), kRowThreads, 0, stream>>>(
-        static_cast<const typename E::raw*>(dout.ptr), dout.ld, static_cast<const typename E::raw*>(y.ptr), y.ld, inv, w, T,
-        K, H, U, static_cast<typename E::raw*>(dy.ptr), dy.ld, dw, lanes, per, status);
-    return cudaGetLastError();
+    return launch_pdl(combine_grad_kernel<E, N>, dim3(ctas, (K + per - 1) / per), dim3(kRowThreads), 0, stream,
+                      static_cast<const typename E::raw*>(dout.ptr), dout.ld, static_cast<const typename E::raw*>(y.ptr), y.ld,
+                      inv, w, T, K, H, U, static_cast<typename E::raw*>(dy.ptr), dy.ld, dw, lanes, per, status);
   });
 }
 

@@ -46,7 +46,9 @@ def poison(t, live):
 DENSE = [(1, 64, 64), (1, 2048, 1000), (8, 4096, 520), (7, 8, 8), (16, 200, 72), (31, 136, 264), (128, 1024, 512),
          (129, 264, 1032), (255, 128, 64), (256, 256, 192), (300, 520, 328), (1000, 776, 200), (2500, 640, 448)]
 EXPERTS = [([3, 0, 130, 1], 16, 144, 200), ([0, 0, 5], 1, 64, 64), ([300, 17, 256, 0, 64], 128, 272, 136),
-           ([1], 256, 2048, 72), ([0, 0], 64, 80, 80), ([700, 3, 90], 1, 528, 264), ([1] * 40, 16, 96, 128)]
+           ([1], 256, 2048, 72), ([0, 0], 64, 80, 80), ([700, 3, 90], 1, 528, 264), ([1] * 40, 16, 96, 128),
+           # some hundred rows each (pairs of 256-row tiles): sums of 2, 5 and 13 slabs in the forward
+           ([513, 0, 512, 31, 256, 257, 1000], 16, 272, 128), ([300, 290, 1], 1, 336, 264), ([1100, 600], 256, 784, 800)]
 ACTS = ["none", "relu", "silu", "gelu", "swiglu"]
 
 
