@@ -67,7 +67,8 @@ struct LinArgs {
   int act, f16;
   int a_blocks, b_blocks;     // > 0: operand map with 64-column blocks as a dimension, blocks per copy
   int b_box;                  // rows of B per copy (contiguous along the sum; 0: the tile's height picks its map)
-  int split, bj, stages;      // split kernel: slices, rows j per tile, ring stages
+  int bj, stages;             // split kernel: rows j per tile, ring stages,
+  int lanes;                  // rows of A per tile (the accumulator lanes in use): 128 or 64
   uint16_t* out;
   long long ldo;
   uint16_t* z;
@@ -252,36 +253,44 @@ struct ZeroSums {
   }
 };
 // A slice's sums in shared memory: value i of 8-column group g of epilogue thread t (of 128 of its parity) is
-// float 4 * ((2g + i / 4) * 128 + t) + i % 4.
+// float 4 * ((2g + i / 4) * 128 + t) + i % 4.  S slices, read from the CTA's own on round the cluster (so that
+// they do not all read one CTA at a time) and added in that order, which is fixed by the column.
+template <int S>
 struct ClusterSums {
   uint32_t base;              // this thread's first value in its own shared memory
-  int slices;
+  int slice;
   __device__ __forceinline__ void operator()(int c0, int left, float (&v)[32]) const {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = 0.f;
-    // the loads of four slices are under way before the first is added
-    for (int s0 = 0; s0 < slices; s0 += 4) {
+    for (int n = 0; n < 4; ++n) {
+      if (8 * n >= left) {
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        if (8 * n >= left) continue;
-        float x[4][8];
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          const uint32_t p = mapa_shared(base, static_cast<uint32_t>(min(s0 + s, slices - 1))) +
-                             static_cast<uint32_t>(c0 / 8 + n) * (2 * 128 * 16);
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-            asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                         : "=f"(x[s][4 * k]), "=f"(x[s][4 * k + 1]), "=f"(x[s][4 * k + 2]), "=f"(x[s][4 * k + 3])
-                         : "r"(p + k * (128 * 16))
-                         : "memory");
-        }
-#pragma unroll
-        for (int s = 0; s < 4; ++s)
-          if (s0 + s < slices)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[8 * n + j] += x[s][j];
+        for (int j = 0; j < 8; ++j) v[8 * n + j] = 0.f;
+        continue;
       }
+      const uint32_t off = base + static_cast<uint32_t>(c0 / 8 + n) * (2 * 128 * 16);
+      float x[S][8];
+#pragma unroll
+      for (int s = 1; s < S; ++s) {
+        const uint32_t p = mapa_shared(off, static_cast<uint32_t>((slice + s) & (S - 1)));
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                       : "=f"(x[s][4 * k]), "=f"(x[s][4 * k + 1]), "=f"(x[s][4 * k + 2]), "=f"(x[s][4 * k + 3])
+                       : "r"(p + k * (128 * 16))
+                       : "memory");
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(x[0][4 * k]), "=f"(x[0][4 * k + 1]), "=f"(x[0][4 * k + 2]), "=f"(x[0][4 * k + 3])
+                     : "r"(off + k * (128 * 16))
+                     : "memory");
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[8 * n + j] = x[0][j];
+#pragma unroll
+      for (int s = 1; s < S; ++s)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[8 * n + j] += x[s][j];
     }
   }
 };
@@ -447,7 +456,7 @@ __device__ __forceinline__ void lin_drain(const LinArgs& a, const LinTile& t, in
   __syncwarp();
 }
 
-// Loads A's 128 output columns (from column i0; gated: i0 of y) and q0 .. of the sum.
+// Loads A's output columns (128, or the tile's; from column i0; gated: i0 of y) and q0 .. of the sum.
 template <int MODE, bool PAIR>
 __device__ __forceinline__ void lin_load_a(const LinArgs& a, const CUtensorMap* map, uint32_t dst, const LinTile& t, int i0,
                                            int q0, uint32_t bar) {
@@ -462,7 +471,7 @@ __device__ __forceinline__ void lin_load_a(const LinArgs& a, const CUtensorMap* 
       tma_load_4d<PAIR>(dst, map, 0, row, i0 >> 6, plane, bar);
     } else {
       tma_load_4d<PAIR>(dst, map, i0, row, 0, plane, bar);
-      tma_load_4d<PAIR>(dst + 8192, map, i0 + 64, row, 0, plane, bar);
+      if (PAIR || a.lanes > 64) tma_load_4d<PAIR>(dst + 8192, map, i0 + 64, row, 0, plane, bar);
     }
   }
 }
@@ -763,12 +772,12 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 
 // ------------------------------------------------------------------------------------------
 
-// Dense problems with few tiles: cluster c computes tile c, its CTA r the r-th slice of the sum.
-template <int MODE>
+// Dense problems with few tiles: cluster c computes tile c, its CTA r the r-th of S slices of the sum.  A tile
+// may use 64 of the MMA's 128 lanes: the others multiply what the ring happens to hold and are not read.
+template <int MODE, int S>
 __global__ void __launch_bounds__(kLinThreads, 1)
     linear_split_kernel(const __grid_constant__ CUtensorMap mapa, const __grid_constant__ CUtensorMap mapb, const LinArgs a) {
   constexpr bool kAMn = MODE == kLinDx || MODE == kLinDw, kBMn = MODE == kLinDw;
-  constexpr int kCtaI = MODE == kLinFwdGated ? 64 : kLinBI;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + kSplitRing);
@@ -778,7 +787,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int S = a.split, slice = static_cast<int>(blockIdx.x) % S, tile = static_cast<int>(blockIdx.x) / S;
+  const int slice = static_cast<int>(blockIdx.x) % S, tile = static_cast<int>(blockIdx.x) / S;
   if (threadIdx.x == 0) {
     for (int s = 0; s < a.stages; ++s) {
       mbar_init(smem_u32(full + s), 1);
@@ -809,11 +818,12 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   t.j0 = tile / a.n_it * a.bj;
   t.ncols = min(a.bj, (MODE == kLinDw ? a.j_ext : a.rows) - t.j0);
   t.slabs = ((MODE == kLinDw ? a.rows : a.q_ext) + kLinSlab - 1) / kLinSlab;
-  const int i0 = t.it * kCtaI;
+  const int i0 = t.it * (MODE == kLinFwdGated ? a.lanes / 2 : a.lanes);
   const int s0 = static_cast<int>(static_cast<long long>(t.slabs) * slice / S);          // this CTA's slabs [s0, s1),
   const int s1 = static_cast<int>(static_cast<long long>(t.slabs) * (slice + 1) / S);    // never empty (host)
   const uint32_t b_bytes = lin_b_bytes<MODE>(a, a.bj);
-  const int stage = kLinABytes + static_cast<int>((b_bytes + 1023) & ~1023u);
+  const uint32_t a_bytes = static_cast<uint32_t>(a.lanes) * 128;
+  const int stage = static_cast<int>(a_bytes + ((b_bytes + 1023) & ~1023u));
   const uint32_t piece = smem_u32(smem) + kLinBI * kLinBJ * 4 + static_cast<uint32_t>(warp >= 2 ? warp - 2 : 0) * kPieceBytes;
 
   if (warp == 0) {
@@ -825,9 +835,9 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       if (!ok) break;
       if (lane == 0) {
         const uint32_t sa = smem_u32(smem + st * stage), fb = smem_u32(full + st);
-        mbar_arrive_expect_tx(fb, kLinABytes + b_bytes);
+        mbar_arrive_expect_tx(fb, a_bytes + b_bytes);
         lin_load_a<MODE, false>(a, &mapa, sa, t, i0, s * kLinSlab, fb);
-        lin_load_b<MODE, false>(a, &mapb, sa + kLinABytes, t, t.j0, a.bj, s * kLinSlab, fb);
+        lin_load_b<MODE, false>(a, &mapb, sa + a_bytes, t, t.j0, a.bj, s * kLinSlab, fb);
       }
       __syncwarp();
       if (++st == a.stages) {
@@ -850,7 +860,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         ok = mbar_wait(smem_u32(full + st), ph, a.status);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t sa = smem_u32(smem + st * stage), sb = sa + kLinABytes;
+        const uint32_t sa = smem_u32(smem + st * stage), sb = sa + a_bytes;
 #pragma unroll
         for (int k = 0; k < kLinSlab / 16; ++k)
           mma_bf16(tmem, lin_desc<kAMn>(sa + k * kLinStep<kAMn>), lin_desc<kBMn>(sb + k * kLinStep<kBMn>), id,
@@ -875,14 +885,15 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     if (!ok) {
       *abort_flag = 1;
     } else {
+      const bool used = q * 32 < a.lanes;
       const TmemSums mine{tmem + (static_cast<uint32_t>(q * 32) << 16)};
       if (S == 1) {
-        lin_drain<MODE>(a, t, i0, 0, t.ncols, mine, q, par, lane, piece);
+        if (used) lin_drain<MODE>(a, t, i0, 0, t.ncols, mine, q, par, lane, piece);
       } else {
         // every MMA has read the ring: it takes this slice's sums, as ClusterSums reads them
         float4* part = reinterpret_cast<float4*>(smem) + q * 32 + lane;
 #pragma unroll 1
-        for (int c0 = 32 * par; c0 < t.ncols; c0 += 64) {
+        for (int c0 = 32 * par; used && c0 < t.ncols; c0 += 64) {
           float v[32];
           mine(c0, 32, v);
 #pragma unroll
@@ -896,11 +907,11 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   if (S > 1) {
     const bool ok = *abort_flag == 0;
     cluster_sync();
-    if (warp >= 2 && ok) {
+    if (warp >= 2 && ok && (warp & 3) * 32 < a.lanes) {
       const int q = warp & 3, par = (warp - 2) >> 2;
       const int w = ((t.ncols + S - 1) / S + 7) & ~7, cb = min(slice * w, t.ncols), ce = min(cb + w, t.ncols);
-      lin_drain<MODE>(a, t, i0, cb, ce, ClusterSums{smem_u32(reinterpret_cast<float4*>(smem) + q * 32 + lane), S}, q,
-                      par, lane, piece);
+      lin_drain<MODE>(a, t, i0, cb, ce, ClusterSums<S>{smem_u32(reinterpret_cast<float4*>(smem) + q * 32 + lane), slice},
+                      q, par, lane, piece);
     }
     cluster_sync();    // the slices stay until every CTA has read them
   }
@@ -973,36 +984,65 @@ bool map_mn_major(CUtensorMap* m, int f16, const void* p, long long cols, long l
 // How a problem runs.  j: rows of the output (dense) or of the row buffers (experts).
 struct LinPlan {
   bool pair;
+  int lanes;
   int split, bj, stages, grid, b_box;
 };
 
-// experts: 0 for a dense problem.
-LinPlan lin_plan(int experts, int i_cols, int cta_i, long long j, long long q, bool b_mn) {
+// Dense problems take the cheaper of the two kernels by their cycles, from what was measured for each:
+//  * a pair's slab takes 560 cycles, 76 tiles at a time, and a tile's epilogue about 3000 at the end;
+//  * a split CTA's slab takes 4 MMAs of max(64, n / 2) cycles or its bytes at 56 a cycle; slices add a meeting of
+//    2500 cycles and their partial sums over the cluster at 24 bytes a cycle.
+// (Clusters of eight do not fill the GPU: 16 of them took two rounds.)  i_cols: output columns, gated: of y.
+LinPlan lin_plan(int experts, int i_cols, bool gated, long long j, long long q, bool b_mn) {
   LinPlan p{};
-  const bool dense = experts == 0;
   const int sms = num_sms(), pairs = sms / 2;
   const long long slabs = (q + kLinSlab - 1) / kLinSlab;
+  p.lanes = kLinBI;
+  p.split = 1;
   p.bj = lin_tile_rows(static_cast<int>(j), kPairStep);
-  const long long nj = (j + p.bj - 1) / p.bj;
-  const long long tiles = (i_cols + 2 * cta_i - 1) / (2 * cta_i) * nj;
-  p.pair = !dense || tiles * 2 > pairs;
-  if (p.pair) {
-    p.grid = 2 * static_cast<int>(dense && tiles < pairs ? tiles : pairs);
-    p.split = 1;
-    p.b_box = dense ? p.bj / 2 : 0;
+  const int pair_i = gated ? kLinBI : 2 * kLinBI;
+  const long long tiles = (i_cols + pair_i - 1) / pair_i * ((j + p.bj - 1) / p.bj);
+  p.pair = true;
+  if (experts) {
+    p.grid = 2 * pairs;
+    p.b_box = 0;
     return p;
   }
-  p.bj = lin_tile_rows(static_cast<int>(j), kSplitStep);
-  const long long t1 = (i_cols + cta_i - 1) / cta_i * ((j + p.bj - 1) / p.bj);
-  p.split = 1;
-  while (p.split < 8 && t1 * p.split * 2 <= sms && slabs >= 4 * p.split) p.split *= 2;
-  p.grid = static_cast<int>(t1) * p.split;
-  p.b_box = p.bj;
-  const int b_bytes = b_mn ? (p.bj + 63) / 64 * 8192 : p.bj * 128;
-  const int stage = kLinABytes + (b_bytes + 1023) / 1024 * 1024;
-  p.stages = kSplitRing / stage < kSplitMaxStages ? kSplitRing / stage : kSplitMaxStages;
+  long long best = (tiles + pairs - 1) / pairs * slabs * 560 + 3000;
+  const int bj = lin_tile_rows(static_cast<int>(j), kSplitStep);
+  const long long nj = (j + bj - 1) / bj;
+  for (int lanes = 128; lanes >= 64; lanes /= 2) {
+    const int tile_i = gated ? lanes / 2 : lanes;
+    const long long t1 = (i_cols + tile_i - 1) / tile_i * nj;
+    for (int S = 1; S <= 4 && slabs >= 2 * S; S *= 2) {
+      if (t1 * S > 4LL * sms) continue;
+      const long long mma = 4 * (bj / 2 > 64 ? bj / 2 : 64), bytes = (lanes + bj) * 128LL / 56;
+      const long long cost = (t1 * S + sms - 1) / sms * ((slabs + S - 1) / S * (mma > bytes ? mma : bytes) + bj * 12LL / S) +
+                             (S > 1 ? 2500 + (S - 1) * (bj / S) * lanes * 4LL / 24 : 0);
+      if (cost >= best) continue;
+      best = cost;
+      p.pair = false;
+      p.lanes = lanes;
+      p.split = S;
+      p.grid = static_cast<int>(t1) * S;
+    }
+  }
+  if (p.pair) {
+    p.grid = 2 * static_cast<int>(tiles < pairs ? tiles : pairs);
+    p.b_box = p.bj / 2;
+    return p;
+  }
+  p.bj = bj;
+  p.b_box = bj;
+  const int b_bytes = b_mn ? (bj + 63) / 64 * 8192 : bj * 128;
+  const int stage = p.lanes * 128 + (b_bytes + 1023) / 1024 * 1024;
+  // (64 lanes: the MMA reads 8 KB past a stage's A, which stays inside the ring)
+  p.stages = (kSplitRing - 8192) / stage < kSplitMaxStages ? (kSplitRing - 8192) / stage : kSplitMaxStages;
   return p;
 }
+
+// Output columns per tile (of a pair: both CTAs').
+int lin_tile_i(const LinPlan& p, bool gated) { return (p.pair ? 2 * p.lanes : p.lanes) / (gated ? 2 : 1); }
 
 // Lets a kernel use more than 48 KB of shared memory, once per device.
 cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<unsigned long long>& done) {
@@ -1019,10 +1059,10 @@ cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<unsigned long 
 template <int MODE>
 cudaError_t lin_launch(const LinPlan& p, const CUtensorMap& ma, const LinMapsB& mb, const CUtensorMap* emaps, LinArgs a,
                        cudaStream_t stream) {
-  static std::atomic<unsigned long long> pair_done{0}, split_done{0};
-  a.split = p.split;
+  static std::atomic<unsigned long long> pair_done{0}, split_done[3] = {};
   a.bj = p.bj;
   a.stages = p.stages;
+  a.lanes = p.lanes;
   a.b_box = p.b_box;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute at[2];
@@ -1043,9 +1083,12 @@ cudaError_t lin_launch(const LinPlan& p, const CUtensorMap& ma, const LinMapsB& 
     if (err != cudaSuccess) return err;
     return cudaLaunchKernelEx(&cfg, linear_pair_kernel<MODE>, ma, mb, emaps, static_cast<const LinArgs>(a));
   }
-  const cudaError_t err = allow_smem(reinterpret_cast<const void*>(&linear_split_kernel<MODE>), kSplitSmem, split_done);
+  const auto kernel = p.split == 1   ? linear_split_kernel<MODE, 1>
+                      : p.split == 2 ? linear_split_kernel<MODE, 2>
+                                     : linear_split_kernel<MODE, 4>;
+  const cudaError_t err = allow_smem(reinterpret_cast<const void*>(kernel), kSplitSmem, split_done[p.split / 2]);
   if (err != cudaSuccess) return err;
-  return cudaLaunchKernelEx(&cfg, linear_split_kernel<MODE>, ma, mb.m[0], static_cast<const LinArgs>(a));
+  return cudaLaunchKernelEx(&cfg, kernel, ma, mb.m[0], static_cast<const LinArgs>(a));
 }
 
 // The rows operand of the forward and the input gradient.
@@ -1084,9 +1127,8 @@ cudaError_t launch_linear(const LinearShape& p, RowsView x, const uint16_t* w, c
   a.res = static_cast<const uint16_t*>(res.ptr);
   a.ldr = res.ld;
   a.bias = bias;
-  const int cta_i = gated ? 64 : kLinBI;
-  const LinPlan pl = lin_plan(p.counts ? p.E : 0, a.i_ext, cta_i, p.rows, p.K, false);
-  const int tile_i = pl.pair ? 2 * cta_i : cta_i;
+  const LinPlan pl = lin_plan(p.counts ? p.E : 0, a.i_ext, gated, p.rows, p.K, false);
+  const int tile_i = lin_tile_i(pl, gated);
   a.n_it = (a.i_ext + tile_i - 1) / tile_i;
   CUtensorMap ma = {};
   LinMapsB mb = {};
@@ -1095,10 +1137,10 @@ cudaError_t launch_linear(const LinearShape& p, RowsView x, const uint16_t* w, c
     // [E][N/2 / 8][2][8][K]: a copy takes, eight columns at a time, their gate rows and then their up rows
     const long long I = p.N / 2, K = p.K;
     const long long d[5] = {K, 8, 2, I / 8, a.E}, s[5] = {0, K, I * K, 8 * K, 2 * I * K};
-    const int b[5] = {kLinSlab, 8, 2, 8, 1};
+    const int b[5] = {kLinSlab, 8, 2, pl.lanes / 16, 1};
     ok = lin_map(&ma, p.f16, w, 5, d, s, b);
   } else {
-    ok = map_k_major(&ma, p.f16, w, p.K, p.N, a.E, p.K, kLinBI);
+    ok = map_k_major(&ma, p.f16, w, p.K, p.N, a.E, p.K, pl.lanes);
   }
   if (!ok || !map_rows(mb, pl, p.f16, x, p.K, p.rows)) return cudaErrorInvalidValue;
   if (gated) return lin_launch<kLinFwdGated>(pl, ma, mb, nullptr, a, stream);
@@ -1115,12 +1157,12 @@ cudaError_t launch_linear_dx(const LinearShape& p, RowsView dz, const uint16_t* 
   a.ldo = dx.ld;
   a.res = static_cast<const uint16_t*>(res.ptr);
   a.ldr = res.ld;
-  const LinPlan pl = lin_plan(p.counts ? p.E : 0, p.K, kLinBI, p.rows, p.N, false);
-  const int tile_i = pl.pair ? 2 * kLinBI : kLinBI;
+  const LinPlan pl = lin_plan(p.counts ? p.E : 0, p.K, false, p.rows, p.N, false);
+  const int tile_i = lin_tile_i(pl, false);
   a.n_it = (p.K + tile_i - 1) / tile_i;
   CUtensorMap ma = {};
   LinMapsB mb = {};
-  a.a_blocks = 2;
+  a.a_blocks = pl.lanes / 64;
   if (!map_mn_major(&ma, p.f16, w, p.K, p.N, a.E, p.K, &a.a_blocks) ||
       !map_rows(mb, pl, p.f16, dz, p.N, p.rows))
     return cudaErrorInvalidValue;
@@ -1134,12 +1176,12 @@ cudaError_t launch_linear_dw(const LinearShape& p, RowsView dz, RowsView x, uint
   a.j_ext = p.N;
   a.out = dw;
   a.ldo = p.K;
-  const LinPlan pl = lin_plan(p.counts ? p.E : 0, p.K, kLinBI, p.N, p.rows, true);
-  const int tile_i = pl.pair ? 2 * kLinBI : kLinBI;
+  const LinPlan pl = lin_plan(p.counts ? p.E : 0, p.K, false, p.N, p.rows, true);
+  const int tile_i = lin_tile_i(pl, false);
   a.n_it = (p.K + tile_i - 1) / tile_i;
   CUtensorMap ma = {};
   LinMapsB mb = {};
-  a.a_blocks = 2;
+  a.a_blocks = pl.lanes / 64;
   // B in one copy where every tile (over a pair: every half) starts on a block
   const int cta_j = pl.pair ? pl.bj / 2 : pl.bj;
   a.b_blocks = cta_j % 64 == 0 && (!pl.pair || p.N % pl.bj == 0) ? cta_j / 64 : 0;
