@@ -988,11 +988,15 @@ struct LinPlan {
   int split, bj, stages, grid, b_box;
 };
 
-// Dense problems take the cheaper of the two kernels by their cycles, from what was measured for each:
-//  * a pair's slab takes 560 cycles, 76 tiles at a time, and a tile's epilogue about 3000 at the end;
-//  * a split CTA's slab takes 4 MMAs of max(64, n / 2) cycles or its bytes at 56 a cycle; slices add a meeting of
-//    2500 cycles and their partial sums over the cluster at 24 bytes a cycle.
-// (Clusters of eight do not fill the GPU: 16 of them took two rounds.)  i_cols: output columns, gated: of y.
+// Dense problems take the cheapest way to run them by a count of cycles that was fitted to measurements of every
+// way (pair; split with 128 or 64 lanes and 1, 2 or 4 slices) over 126 shapes of 1 to 4096 rows, 256 to 7168
+// columns and terms: the way it picks is on average 0.1% off the fastest one, 3% at most.
+//  * pair: 76 tiles at a time, 470 a slab, 26 per row j of the epilogue at the end;
+//  * split: 590 a slab (the MMA feeds its 128 rows of A at one a cycle, so short tiles are no cheaper), 5200 for each
+//    further round of CTAs; slices halve or quarter that for a meeting of 1900 + 250 S and 27 per row j and 128
+//    lanes for the partial sums over the cluster.
+// (Clusters of eight do not fill the GPU: 16 of them took two rounds.)  i_cols: output columns, gated: of y;
+// experts: 0 for a dense problem.
 LinPlan lin_plan(int experts, int i_cols, bool gated, long long j, long long q, bool b_mn) {
   LinPlan p{};
   const int sms = num_sms(), pairs = sms / 2;
@@ -1008,17 +1012,16 @@ LinPlan lin_plan(int experts, int i_cols, bool gated, long long j, long long q, 
     p.b_box = 0;
     return p;
   }
-  long long best = (tiles + pairs - 1) / pairs * slabs * 560 + 3000;
+  long long best = (tiles + pairs - 1) / pairs * slabs * 470 + 220 + 26 * p.bj;
   const int bj = lin_tile_rows(static_cast<int>(j), kSplitStep);
   const long long nj = (j + bj - 1) / bj;
   for (int lanes = 128; lanes >= 64; lanes /= 2) {
     const int tile_i = gated ? lanes / 2 : lanes;
     const long long t1 = (i_cols + tile_i - 1) / tile_i * nj;
     for (int S = 1; S <= 4 && slabs >= 2 * S; S *= 2) {
-      if (t1 * S > 4LL * sms) continue;
-      const long long mma = 4 * (bj / 2 > 64 ? bj / 2 : 64), bytes = (lanes + bj) * 128LL / 56;
-      const long long cost = (t1 * S + sms - 1) / sms * ((slabs + S - 1) / S * (mma > bytes ? mma : bytes) + bj * 12LL / S) +
-                             (S > 1 ? 2500 + (S - 1) * (bj / S) * lanes * 4LL / 24 : 0);
+      const long long rounds = (t1 * S + sms - 1) / sms;
+      long long cost = rounds * ((slabs + S - 1) / S * 590 + 2 * bj / S) + 5200 * (rounds - 1);
+      if (S > 1) cost += rounds * (1900 + 250 * S + 27LL * bj * lanes / 128 * (S - 1) / S);
       if (cost >= best) continue;
       best = cost;
       p.pair = false;
