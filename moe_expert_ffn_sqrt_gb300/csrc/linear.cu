@@ -5,11 +5,15 @@
 //   input     dx[r, k] = sum_n dz[r, n] w[e, n, k] (+ residual[r, k])
 //   weight    dw[e, n, k] = sum_r dz[r, n] x[r, k]        over expert e's rows
 //
-// All three are out[j, i] = sum_q A[i, q] B[j, q] with i the contiguous column of the output: i runs
-// over the MMA's M rows (accumulator lanes) and j over its N columns.  So the tokens are on N, where the
-// MMA takes any multiple of 16: a ragged or short expert segment costs what it holds.  What changes is
-// which operand is contiguous along the sum: w is (forward), w and x are not (gradients); the
-// shared-memory descriptors take either order, so no operand is ever transposed in memory.
+// What changes between the three is which operand is contiguous along the sum: x, dz and (forward) w are, w
+// and x in the gradients are not; the shared-memory descriptors take either order, so no operand is ever
+// transposed in memory.
+//
+// The tensor core feeds its M side one row a cycle: an MMA of 128 rows of A per CTA takes 128 cycles however
+// few columns N it has (measured; 256 columns fill them), one of 64 rows takes 64.  So what is ragged goes on M
+// and N is 256: in the pair kernel's forward and input gradient the rows of x or dz are on M, 256 or 128 of
+// them per tile, and a segment's rest of up to 128 rows costs half a tile.  (With the weights on M and the rows
+// on N, every started 256 rows cost a whole one: 12288 rows of 32 uneven experts took 494 us.)
 //
 // Rows of experts: expert e's rows start at seg_e = sum_{e' < e} round_up(counts[e'], align) (the layout
 // of moe_permute).  Padding rows are never read into a result nor written: in the forward and the input
@@ -19,11 +23,11 @@
 // slab row by row instead cost the 32-expert gradient 87 of 470 us.)
 //
 // Two kernels:
-//  * linear_pair_kernel: a CTA pair per 256 x 256 tile (cta_group::2, each CTA 128 output columns i and
-//    half of the tile's rows j in shared memory), persistent, two accumulators so that one tile's
-//    epilogue runs under the next tile's MMAs.
-//  * linear_split_kernel: for dense problems with too few tiles to fill the GPU: a cluster of up to eight
-//    CTAs per 128-column tile, each with a slice of the sum; the slices meet in shared memory.
+//  * linear_pair_kernel: a CTA pair per 256 x 256 tile (cta_group::2, each CTA half of either operand's rows in
+//    shared memory), persistent, two accumulators so that one tile's epilogue runs under the next tile's MMAs.
+//  * linear_split_kernel: for dense problems with too few tiles to fill the GPU: a cluster of up to four
+//    CTAs per tile of 128 or 64 columns, each with a slice of the sum; the slices meet in shared memory.  Few
+//    rows are the rule there, so the weights (or, for dw, x's columns) are on M and the rows on N.
 #include <atomic>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -46,7 +50,7 @@ constexpr int kLinMaxE = kLinearMaxExperts;
 constexpr int kPairB = 128 * 128;
 constexpr int kPairStage = kLinABytes + kPairB;      // 32 KB
 constexpr int kPairStages = 6;
-constexpr int kPairSmem = 1024 + kPairStages * kPairStage + 256 + kLinEpiWarps * 32 * 80 + (3 * kLinMaxE + 1) * 4;
+constexpr int kPairSmem = 1024 + kPairStages * kPairStage + 256 + kLinEpiWarps * 32 * 80 + 2 * kLinMaxE * 4;
 // split kernel: stages of A and the tile's B rows, as many as fit
 constexpr int kSplitRing = 208 * 1024;          // also: the slice's sums, then a piece per epilogue warp
 constexpr int kSplitMaxStages = 12;
@@ -60,13 +64,13 @@ enum LinMode { kLinFwd = 0, kLinFwdGated = 1, kLinDx = 2, kLinDw = 3, kLinFwdGel
 struct LinArgs {
   const int32_t* counts;      // [E] rows per expert; nullptr: one dense segment of `rows` rows
   int E, align, rows;         // rows: rows of the row buffers
-  int n_it;                   // i tiles
+  int n_it;                   // i tiles (i: output columns, j: output rows)
   int i_ext;                  // output columns (gated forward: of y; z has twice as many)
   int j_ext;                  // weight gradient: N
   int q_ext;                  // forward: K, input gradient: N
   int act, f16;
   int a_blocks, b_blocks;     // > 0: operand map with 64-column blocks as a dimension, blocks per copy
-  int b_box;                  // rows of B per copy (contiguous along the sum; 0: the tile's height picks its map)
+  int b_box;                  // split kernel: rows of B per copy (operands contiguous along the sum)
   int bj, stages;             // split kernel: rows j per tile, ring stages,
   int lanes;                  // rows of A per tile (the accumulator lanes in use): 128 or 64
   uint16_t* out;
@@ -132,8 +136,8 @@ __device__ __forceinline__ uint64_t lin_desc(uint32_t addr) {
 template <bool MN>
 constexpr int kLinStep = MN ? 2048 : 32;
 
-// Rows j per tile when n rows are cut into ceil(n / 256) tiles of equal height, a multiple of the MMA's
-// step in N (16, over a pair 32): equal tiles keep the CTAs' work even where 256 + a rest would not.
+// Rows j per tile where they are on N (split kernel, weight gradient) and n rows are cut into ceil(n / 256) tiles
+// of equal height, a multiple of the MMA's step in N (16, over a pair 32).
 constexpr int kPairStep = 32, kSplitStep = 16;
 __host__ __device__ __forceinline__ int lin_tile_rows(int n, int step) {
   const int nj = (n + kLinBJ - 1) / kLinBJ;
@@ -148,41 +152,45 @@ struct LinTile {
 struct LinSegs {
   int* row0;                  // [E] first row
   int* cnt;                   // [E] rows
-  int* pfx;                   // [E + 1] tiles before the expert
 };
 
-// A pair's tiles t = pair, pair + pairs, ...: in order of expert, then groups of 16 j tiles, then i tile,
-// then j tile, so that the tiles that run at one time share their operands in L2 along both sides.  Every
-// role walks them by itself; a step costs a division and, on a new expert, a few shared-memory reads
+// A pair's tiles: one of each round of `pairs` tiles, in order of expert, groups of 16 j tiles, i tile, j tile, so
+// that the tiles that run at one time share their operands in L2 along both sides (all tall tiles before all short
+// ones read every expert's weights from HBM twice: 371 against 282 us for 19 experts of 384 rows).  The pair's
+// place in the round moves on by three each time: with a fixed place and experts of a tall and a short tile, an
+// even number of pairs gives half of them nothing but tall ones.
+// Every role walks the tiles by itself; a step costs a division and, on a new expert, a few shared-memory reads
 // (a search per tile took up to half of a short tile's time).
 template <int MODE>
 struct LinWalk {
   const LinArgs& a;
   const LinSegs& g;
-  int t, step, next, nj, bj;
+  int first, place, pairs, base, next, nj, bj;
   LinTile r;
-  __device__ __forceinline__ LinWalk(const LinArgs& a_, const LinSegs& g_, int first, int step_)
-      : a(a_), g(g_), t(first - step_), step(step_), next(0), nj(1), bj(kPairStep) {
+  __device__ __forceinline__ LinWalk(const LinArgs& a_, const LinSegs& g_, int pair, int pairs_)
+      : a(a_), g(g_), first(0), place(pair), pairs(pairs_), base(0), next(0), nj(1),
+        bj(MODE == kLinDw ? lin_tile_rows(a_.j_ext, kPairStep) : kLinBJ) {
     r.e = -1;
   }
   __device__ __forceinline__ bool advance() {
-    t += step;
-    if (t >= g.pfx[a.E]) return false;
+    const int t = first + place;
+    first += pairs;
+    place += 3;
+    if (place >= pairs) place -= pairs;
     if (t >= next) {
-      int e = r.e;
+      int n;
       do {
-        ++e;
-        next = g.pfx[e + 1];
+        if (++r.e >= a.E) return false;
+        n = MODE == kLinDw ? a.j_ext : g.cnt[r.e];
+        nj = (n + bj - 1) / bj;
+        base = next;
+        next += a.n_it * nj;
       } while (t >= next);
-      r.e = e;
-      r.row0 = g.row0[e];
-      r.cnt = g.cnt[e];
-      const int n = MODE == kLinDw ? a.j_ext : r.cnt;
-      bj = lin_tile_rows(n, kPairStep);
-      nj = (n + bj - 1) / bj;
+      r.row0 = g.row0[r.e];
+      r.cnt = g.cnt[r.e];
       r.slabs = ((MODE == kLinDw ? r.cnt : a.q_ext) + kLinSlab - 1) / kLinSlab;
     }
-    unsigned u = static_cast<unsigned>(t - g.pfx[r.e]);
+    unsigned u = static_cast<unsigned>(t - base);
     int j16 = 0, gj = nj;
     if (nj > 16) {
       j16 = static_cast<int>(u / (16u * a.n_it)) * 16;
@@ -213,11 +221,11 @@ __device__ __forceinline__ float lin_silu(float v) { return __fdividef(v, 1.f + 
 // v Phi(v); erfc keeps its relative accuracy in the negative tail, where 1 + erf would cancel
 __device__ __forceinline__ float lin_gelu(float v) { return 0.5f * v * erfcf(v * -0.70710678118654752f); }
 
-// The epilogue works on pieces of 32 accumulator lanes (output columns) x 32 columns (output rows) per
+// The epilogue works on pieces of 32 accumulator lanes x 32 columns per
 // warp, held as four 8-column groups of 8x8 fragments: v[8n + 2h + k] of thread t is lane t/4 + 8h,
 // column 8n + 2(t%4) + k of the piece (h, n, k: 0..3, 0..3, 0..1).  That is how tensor memory is read
-// (16 lanes x 256 bits) and what stmatrix / ldmatrix move, transposed, to and from rows of the output
-// type in shared memory; from there each row's 32 columns leave (or the residual's arrive) 16 bytes per
+// (16 lanes x 256 bits) and what stmatrix / ldmatrix move (transposed where the rows are on N) to and from rows
+// of the output type in shared memory; from there each row's 32 columns leave (or the residual's arrive) 16 bytes per
 // thread.
 constexpr int kPiecePitch = 80;                      // bytes per row: 64 + 16, free of bank conflicts both ways
 constexpr int kPieceBytes = 32 * kPiecePitch;
@@ -306,6 +314,17 @@ __device__ __forceinline__ void ldmatrix_x4_t(uint32_t addr, uint32_t (&r)[4]) {
                : "r"(addr)
                : "memory");
 }
+__device__ __forceinline__ void stmatrix_x4(uint32_t addr, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r0), "r"(r1), "r"(r2),
+               "r"(r3)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix_x4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
 __device__ __forceinline__ uint4 lds16(uint32_t addr) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
@@ -341,7 +360,120 @@ struct PieceRows {
   }
 };
 
-// Turns the sums of output rows [j0 + cb, j0 + ce) of tile t into outputs (cb a multiple of 8); this
+// The forward's activation of a piece, but for the gated one.
+template <int MODE>
+__device__ __forceinline__ void lin_act(const LinArgs& a, const float (&v)[32], float (&o)[32]) {
+#pragma unroll
+  for (int j = 0; j < 32; ++j) o[j] = MODE == kLinFwdGelu ? lin_gelu(v[j]) : v[j];
+  if (MODE == kLinFwd) {
+    if (a.act == kActRelu) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) o[j] = v[j] < 0.f ? 0.f : v[j];   // keeps NaN
+    } else if (a.act == kActSilu) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) o[j] = lin_silu(v[j]);
+    }
+  }
+}
+
+// Rows on M: the warp's 32 lanes are output rows [jw, jw + 32) of tile t, and accumulator columns [cb, ce)
+// output columns from i0 + cb on (gated forward: columns 16m + 0..7 are the gate columns of y's columns
+// i0 + 8m .., columns 16m + 8..15 their up columns).  Every second piece of columns from piece `par` on.
+template <int MODE>
+__device__ __forceinline__ void lin_drain_rows(const LinArgs& a, const LinTile& t, int i0, int jw, int cb, int ce,
+                                               uint32_t acc, int par, int lane, uint32_t stage) {
+  constexpr bool kGated = MODE == kLinFwdGated, kFwd = MODE == kLinFwd || MODE == kLinFwdGelu || kGated;
+  constexpr int kU = kGated ? 2 : 4;                  // 16-byte units per output row
+  const int left = t.ncols - jw;
+  if (left <= 0) return;
+  const long long jr = static_cast<long long>(t.row0) + t.j0 + jw;
+  const PieceRows<kU> rows(lane);
+  const TmemSums sums{acc};
+  // this thread's matrix row for stmatrix / ldmatrix: row lane of the piece, 16-byte unit n with + 16 n
+  const uint32_t mat = stage + static_cast<uint32_t>(lane * kPiecePitch);
+  auto col_of = [&](int c) { return i0 + (kGated ? c / 2 : c); };
+  // the residual of the next piece is on its way while this one is worked on
+  const bool has_res = a.res != nullptr;
+  uint4 res[kU];
+  auto fetch = [&](int c) {
+    const int col = col_of(c) + rows.unit * 8;
+    rows.fetch(res, a.res + jr * a.ldr + col, a.ldr, col < a.i_ext, left);
+  };
+  cb += 32 * par;
+  if (has_res && cb < ce) fetch(cb);
+#pragma unroll 1
+  for (int c0 = cb; c0 < ce; c0 += 64) {
+    const int col0 = col_of(c0);
+    if (col0 >= a.i_ext) break;
+    float v[32];
+    sums(c0 - (cb & ~63), 32, v);
+    if (kFwd) {
+      if (a.bias) {
+        const float* b = a.bias + static_cast<size_t>(t.e) * (kGated ? 2 * a.i_ext : a.i_ext);
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const int col = col0 + (kGated ? (n >> 1) * 8 : n * 8) + 2 * (lane & 3);
+          if (col >= a.i_ext) continue;               // i_ext is a multiple of 8
+          const float2 x = __ldg(reinterpret_cast<const float2*>(b + col + (kGated && (n & 1) ? a.i_ext : 0)));
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            v[8 * n + 2 * h] += x.x;
+            v[8 * n + 2 * h + 1] += x.y;
+          }
+        }
+      }
+      if (a.z) {
+        const PieceRows<4> zr(lane);
+        const int zc = kGated ? col0 + (zr.unit >> 1) * 8 : col0 + zr.unit * 8;
+        __syncwarp();
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+          stmatrix_x4(mat + n * 16, lin_pack(v[8 * n], v[8 * n + 1], a.f16), lin_pack(v[8 * n + 2], v[8 * n + 3], a.f16),
+                      lin_pack(v[8 * n + 4], v[8 * n + 5], a.f16), lin_pack(v[8 * n + 6], v[8 * n + 7], a.f16));
+        __syncwarp();
+        zr.store(stage, a.z + jr * a.ldz + zc + (kGated && (zr.unit & 1) ? a.i_ext : 0), a.ldz, zc < a.i_ext, left);
+      }
+    }
+    float o[kGated ? 16 : 32];                        // o[8m + 2h + k]: column 8m + 2(t%4) + k, row t/4 + 8h
+    if constexpr (kGated) {
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[8 * m + i] = lin_silu(v[16 * m + i]) * v[16 * m + 8 + i];
+    } else {
+      lin_act<MODE>(a, v, o);
+    }
+    __syncwarp();
+    if (has_res) {
+#pragma unroll
+      for (int s = 0; s < kU; ++s) sts16(rows.at(stage, s), res[s]);
+      __syncwarp();
+#pragma unroll
+      for (int m = 0; m < kU; ++m) {
+        uint32_t r[4];
+        ldmatrix_x4(mat + m * 16, r);
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          const float2 x = lin_unpack(r[h], a.f16);
+          o[8 * m + 2 * h] += x.x;
+          o[8 * m + 2 * h + 1] += x.y;
+        }
+      }
+      if (c0 + 64 < ce) fetch(c0 + 64);
+      __syncwarp();
+    }
+#pragma unroll
+    for (int m = 0; m < kU; ++m)
+      stmatrix_x4(mat + m * 16, lin_pack(o[8 * m], o[8 * m + 1], a.f16), lin_pack(o[8 * m + 2], o[8 * m + 3], a.f16),
+                  lin_pack(o[8 * m + 4], o[8 * m + 5], a.f16), lin_pack(o[8 * m + 6], o[8 * m + 7], a.f16));
+    __syncwarp();
+    const int col = col0 + rows.unit * 8;
+    rows.store(stage, a.out + jr * a.ldo + col, a.ldo, col < a.i_ext, left);
+  }
+  __syncwarp();
+}
+
+// Rows on N: turns the sums of output rows [j0 + cb, j0 + ce) of tile t into outputs (cb a multiple of 8); this
 // warp has lanes 32q .. of the CTA's output columns, which start at column i0 (gated forward: of y), and
 // every second piece of rows from piece `par` on.  stage: the warp's piece in shared memory.
 template <int MODE, class Sums>
@@ -405,22 +537,7 @@ __device__ __forceinline__ void lin_drain(const LinArgs& a, const LinTile& t, in
           o[4 * n + 2 + k] = lin_silu(v[8 * n + 4 + k]) * v[8 * n + 6 + k];
         }
     } else {
-#pragma unroll
-      for (int j = 0; j < 32; ++j) o[j] = MODE == kLinFwdGelu ? lin_gelu(v[j]) : v[j];
-      if (MODE == kLinFwd) {
-        switch (a.act) {
-          case kActRelu:
-#pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = v[j] < 0.f ? 0.f : v[j];   // keeps NaN
-            break;
-          case kActSilu:
-#pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = lin_silu(v[j]);
-            break;
-          default:
-            break;
-        }
-      }
+      lin_act<MODE>(a, v, o);
     }
     // gated: two 8-column groups of rows make one x4 (matrix m: columns 8 (m & 1), rows 8 (m >> 1))
     const uint32_t om = kGated ? stage + static_cast<uint32_t>(((lane >> 4) * 8 + (lane & 7)) * kPiecePitch + ((lane >> 3) & 1) * 16)
@@ -477,10 +594,10 @@ __device__ __forceinline__ void lin_load_a(const LinArgs& a, const CUtensorMap* 
 }
 
 // Loads rows j .. j + n of B (n a multiple of 8), q0 .. of the sum: lin_b_bytes in all.
-// Maps of B.  Experts' tiles differ in height: [h] copies 16 (h + 1) rows at a time, so that a stage is one copy
-// and fetches only what it uses; where one height serves all, it is [0].
+// Maps of the rows operand (x or dz).  Pair kernel: [0] copies 128 rows at a time, [1] 64; split kernel and weight
+// gradient: [0].
 struct LinMapsB {
-  CUtensorMap m[8];
+  CUtensorMap m[2];
 };
 
 template <int MODE, bool PAIR>
@@ -499,7 +616,7 @@ __device__ __forceinline__ void lin_load_b(const LinArgs& a, const CUtensorMap* 
 template <int MODE>
 __device__ __forceinline__ uint32_t lin_b_bytes(const LinArgs& a, int n) {
   if (MODE == kLinDw) return static_cast<uint32_t>(a.b_blocks ? a.b_blocks : (n + 63) / 64) * 8192u;
-  return static_cast<uint32_t>(a.b_box ? a.b_box : n) * 128u;
+  return static_cast<uint32_t>(a.b_box) * 128u;
 }
 
 // ------------------------------------------------------------------------------------------
@@ -548,7 +665,8 @@ template <int MODE>
 __global__ void __launch_bounds__(kLinThreads, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap mapa, const __grid_constant__ LinMapsB mapsb,
                        const CUtensorMap* __restrict__ emaps, const LinArgs a) {
-  constexpr bool kAMn = MODE == kLinDx || MODE == kLinDw, kBMn = MODE == kLinDw;
+  constexpr bool kRowsM = MODE != kLinDw;                       // A: rows of x or dz, B: weights; else A: x, B: dz
+  constexpr bool kAMn = MODE == kLinDw, kBMn = MODE == kLinDx || MODE == kLinDw;
   constexpr int kCtaI = MODE == kLinFwdGated ? 64 : kLinBI;     // output columns per CTA
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -562,7 +680,6 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   LinSegs segs;
   segs.row0 = reinterpret_cast<int*>(pieces + kLinEpiWarps * kPieceBytes);
   segs.cnt = segs.row0 + kLinMaxE;
-  segs.pfx = segs.cnt + kLinMaxE;
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int rank = static_cast<int>(cluster_ctarank());
@@ -588,8 +705,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   grid_dependency_wait();        // everything below reads what the stream's previous kernels wrote
   grid_launch_dependents();
   if (warp == 2) {
-    // segment starts and tile counts; a segment that would leave the buffers is an error and is cut
-    int srun = 0, prun = 0;
+    // segment starts; a segment that would leave the buffers is an error and is cut
+    int srun = 0;
     for (int e0 = 0; e0 < a.E; e0 += 32) {
       const int e = e0 + lane;
       int c = 0;
@@ -611,22 +728,11 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         record_error(a.status, kDevErrIndex);
         c = max(a.rows - start, 0);
       }
-      const int nj = MODE == kLinDw ? a.j_ext : c, bj = lin_tile_rows(nj, kPairStep);
-      const int n = e < a.E ? a.n_it * ((nj + bj - 1) / bj) : 0;
-      int p = n;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int o = __shfl_up_sync(0xffffffffu, p, d);
-        if (lane >= d) p += o;
-      }
       if (e < a.E) {
         segs.row0[e] = start;
         segs.cnt[e] = c;
-        segs.pfx[e] = prun + p - n;
       }
-      prun += __shfl_sync(0xffffffffu, p, 31);
     }
-    if (lane == 0) segs.pfx[a.E] = prun;
   }
   tc_fence_before();
   __syncthreads();
@@ -645,7 +751,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     while (ok && walk.advance()) {
       const LinTile& t = walk.r;
       const int half = ((t.ncols + kPairStep - 1) & ~(kPairStep - 1)) / 2;
-      const CUtensorMap *ma = &mapa, *mb = &mapsb.m[a.b_box ? 0 : half / 16 - 1];
+      const int mrows = t.ncols <= 128 ? 64 : 128;
+      const CUtensorMap *ma = &mapa, *mb = &mapsb.m[0];
       if (MODE == kLinDw && a.counts) {
         ma = emaps + 2 * t.e;
         mb = ma + 1;
@@ -656,7 +763,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         }
       }
       const int i0 = (t.it * 2 + rank) * kCtaI, j0 = t.j0 + rank * half;
-      const uint32_t bytes = kLinABytes + lin_b_bytes<MODE>(a, half);
+      const uint32_t bytes = kPairB + (kRowsM ? static_cast<uint32_t>(mrows) * 128u : lin_b_bytes<MODE>(a, half));
       for (int s = 0; s < t.slabs; ++s) {
         ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(empty + st), ph ^ 1, a.status) && *abort_flag == 0);
         if (!ok) break;
@@ -665,8 +772,13 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         if (rank == 0 && lane == 0) mbar_arrive_expect_tx(smem_u32(full + st), 2 * bytes);
         __syncwarp();
         if (lane == 0) {
-          lin_load_a<MODE, true>(a, ma, sa, t, i0, q0, fb);
-          lin_load_b<MODE, true>(a, mb, sb, t, j0, half, q0, fb);
+          if (kRowsM) {
+            tma_load_4d<true>(sa, &mapsb.m[mrows == 64], q0, t.row0 + t.j0 + rank * mrows, 0, 0, fb);
+            lin_load_a<MODE, true>(a, ma, sb, t, i0, q0, fb);
+          } else {
+            lin_load_a<MODE, true>(a, ma, sa, t, i0, q0, fb);
+            lin_load_b<MODE, true>(a, mb, sb, t, j0, half, q0, fb);
+          }
         }
         __syncwarp();
         if (++st == kPairStages) {
@@ -701,8 +813,9 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       while (ok && walk.advance()) {
         const LinTile& t = walk.r;
         if (t.slabs == 0) continue;
-        const uint32_t id = lin_idesc(a.f16, kAMn, kBMn, 2 * kLinBI,
-                                      static_cast<uint32_t>((t.ncols + kPairStep - 1) & ~(kPairStep - 1)));
+        const uint32_t id =
+            kRowsM ? lin_idesc(a.f16, kAMn, kBMn, t.ncols <= 128 ? kLinBI : 2 * kLinBI, kLinBJ)
+                   : lin_idesc(a.f16, kAMn, kBMn, 2 * kLinBI, static_cast<uint32_t>((t.ncols + kPairStep - 1) & ~(kPairStep - 1)));
         ok = mbar_wait(smem_u32(acc_empty + b), ((aph >> b) & 1u) ^ 1u, a.status) && *abort_flag == 0;
         if (!ok) break;
         tc_fence_after();
@@ -742,7 +855,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     while (ok && walk.advance()) {
       const LinTile& t = walk.r;
       const int i0 = (t.it * 2 + rank) * kCtaI;
-      if (t.slabs == 0) {
+      if (MODE == kLinDw && t.slabs == 0) {
         lin_drain<MODE>(a, t, i0, 0, t.ncols, ZeroSums{}, q, par, lane, stage);
         continue;
       }
@@ -750,9 +863,17 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       ok = named_barrier_and(1, 32 * kLinEpiWarps, ok);
       if (!ok) break;
       tc_fence_after();
-      lin_drain<MODE>(a, t, i0, 0, t.ncols,
-                      TmemSums{tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(b * kLinBJ)}, q, par,
-                      lane, stage);
+      const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(b * kLinBJ);
+      if constexpr (!kRowsM) {
+        lin_drain<MODE>(a, t, i0, 0, t.ncols, TmemSums{acc}, q, par, lane, stage);
+      } else if (t.ncols > 128) {
+        // M = 256: this CTA's 128 rows, all 256 columns
+        lin_drain_rows<MODE>(a, t, t.it * 2 * kCtaI, rank * 128 + q * 32, 0, kLinBJ, acc, par, lane, stage);
+      } else {
+        // M = 128: this CTA's 64 rows twice, columns 0..127 in lanes 0..63 and 128..255 in lanes 64..127
+        lin_drain_rows<MODE>(a, t, t.it * 2 * kCtaI, rank * 64 + (q & 1) * 32, (q >> 1) * 128, (q >> 1) * 128 + 128, acc, par,
+                             lane, stage);
+      }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(acc_empty0 + b * 8);
@@ -1009,7 +1130,6 @@ LinPlan lin_plan(int experts, int i_cols, bool gated, long long j, long long q, 
   p.pair = true;
   if (experts) {
     p.grid = 2 * pairs;
-    p.b_box = 0;
     return p;
   }
   long long best = (tiles + pairs - 1) / pairs * slabs * 470 + 220 + 26 * p.bj;
@@ -1032,7 +1152,6 @@ LinPlan lin_plan(int experts, int i_cols, bool gated, long long j, long long q, 
   }
   if (p.pair) {
     p.grid = 2 * static_cast<int>(tiles < pairs ? tiles : pairs);
-    p.b_box = p.bj / 2;
     return p;
   }
   p.bj = bj;
@@ -1096,10 +1215,8 @@ cudaError_t lin_launch(const LinPlan& p, const CUtensorMap& ma, const LinMapsB& 
 
 // The rows operand of the forward and the input gradient.
 bool map_rows(LinMapsB& mb, const LinPlan& p, int f16, RowsView x, long long cols, long long rows) {
-  if (p.b_box) return map_k_major(&mb.m[0], f16, x.ptr, cols, rows, 1, x.ld, p.b_box);
-  for (int h = 0; h < 8; ++h)
-    if (!map_k_major(&mb.m[h], f16, x.ptr, cols, rows, 1, x.ld, 16 * (h + 1))) return false;
-  return true;
+  if (!p.pair) return map_k_major(&mb.m[0], f16, x.ptr, cols, rows, 1, x.ld, p.b_box);
+  return map_k_major(&mb.m[0], f16, x.ptr, cols, rows, 1, x.ld, 128) && map_k_major(&mb.m[1], f16, x.ptr, cols, rows, 1, x.ld, 64);
 }
 
 LinArgs lin_args(const LinearShape& p, uint32_t* status) {
