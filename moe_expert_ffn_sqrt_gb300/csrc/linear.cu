@@ -50,13 +50,13 @@ constexpr int kLinMaxE = kLinearMaxExperts;
 constexpr int kPairB = 128 * 128;
 constexpr int kPairStage = kLinABytes + kPairB;      // 32 KB
 constexpr int kPairStages = 6;
-constexpr int kPairSmem = 1024 + kPairStages * kPairStage + 256 + kLinEpiWarps * 32 * 80 + 2 * kLinMaxE * 4;
+constexpr int kPairSmem = 1024 + kPairStages * kPairStage + 512 + kLinEpiWarps * 2048 + 2 * kLinMaxE * 4;
 // split kernel: stages of A and the tile's B rows, as many as fit
 constexpr int kSplitRing = 208 * 1024;          // also: the slice's sums, then a piece per epilogue warp
 constexpr int kSplitMaxStages = 12;
 constexpr int kSplitSmem = 1024 + kSplitRing + 512;
 static_assert(kPairSmem <= 227 * 1024 && kSplitSmem <= 227 * 1024, "shared memory budget");
-static_assert(kSplitRing >= kLinBI * kLinBJ * 4 + kLinEpiWarps * 32 * 80, "the slices' sums and the pieces fit the ring");
+static_assert(kSplitRing >= kLinBI * kLinBJ * 4 + kLinEpiWarps * 2048, "the slices' sums and the pieces fit the ring");
 
 // The GELU forward is a mode of its own: erfc over a whole piece takes registers that the others need not pay.
 enum LinMode { kLinFwd = 0, kLinFwdGated = 1, kLinDx = 2, kLinDw = 3, kLinFwdGelu = 4 };
@@ -227,8 +227,13 @@ __device__ __forceinline__ float lin_gelu(float v) { return 0.5f * v * erfcf(v *
 // (16 lanes x 256 bits) and what stmatrix / ldmatrix move (transposed where the rows are on N) to and from rows
 // of the output type in shared memory; from there each row's 32 columns leave (or the residual's arrive) 16 bytes per
 // thread.
-constexpr int kPiecePitch = 80;                      // bytes per row: 64 + 16, free of bank conflicts both ways
+constexpr int kPiecePitch = 64;
 constexpr int kPieceBytes = 32 * kPiecePitch;
+// 16-byte unit u of row r: two neighbouring rows fill the banks, and four such pairs are turned against each other,
+// so that neither eight rows' units (stmatrix) nor two rows' (the stores) share a bank.
+__device__ __forceinline__ uint32_t piece_at(uint32_t stage, int r, int u) {
+  return stage + static_cast<uint32_t>(r * kPiecePitch + ((u ^ ((r >> 1) & 3)) << 4));
+}
 
 // Where the sums come from: this CTA's tensor memory, or the slices that the cluster's CTAs keep in
 // shared memory, added in slice order.
@@ -334,6 +339,24 @@ __device__ __forceinline__ void sts16(uint32_t addr, const uint4& v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
+// A whole piece (32 rows of 32 columns) to an output matrix by one tensor copy, whose 64-byte swizzle is
+// piece_at's; rows and columns past the matrix are left out.  Called by the whole warp after its shared-memory
+// writes; piece_free before the next ones.
+__device__ __forceinline__ void piece_send(uint32_t stage, const CUtensorMap* map, int c0, int c1, int c2, int lane) {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncwarp();
+  if (lane == 0)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];\n\t"
+        "cp.async.bulk.commit_group;" ::"l"(map),
+        "r"(c0), "r"(c1), "r"(c2), "r"(stage)
+        : "memory");
+}
+__device__ __forceinline__ void piece_free(int lane) {
+  if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+  __syncwarp();
+}
+
 // Rows of 8 * U columns (U 16-byte units) between shared memory and the thread's share of global rows:
 // unit lane % U of rows lane / U + (32 / U) s, s = 0 .. U-1.
 template <int U>
@@ -341,7 +364,7 @@ struct PieceRows {
   int row, unit;
   __device__ __forceinline__ explicit PieceRows(int lane) : row(lane / U), unit(lane % U) {}
   __device__ __forceinline__ uint32_t at(uint32_t stage, int s) const {
-    return stage + static_cast<uint32_t>((row + 32 / U * s) * kPiecePitch + unit * 16);
+    return piece_at(stage, row, unit) + static_cast<uint32_t>(32 / U * s * kPiecePitch);   // (whole turns further)
   }
   // p: this thread's unit of row 0 of the piece; live: its columns exist; left: rows of the piece
   __device__ __forceinline__ void store(uint32_t stage, uint16_t* p, long long ld, bool live, int left) const {
@@ -381,7 +404,7 @@ __device__ __forceinline__ void lin_act(const LinArgs& a, const float (&v)[32], 
 // i0 + 8m .., columns 16m + 8..15 their up columns).  Every second piece of columns from piece `par` on.
 template <int MODE>
 __device__ __forceinline__ void lin_drain_rows(const LinArgs& a, const LinTile& t, int i0, int jw, int cb, int ce,
-                                               uint32_t acc, int par, int lane, uint32_t stage) {
+                                               uint32_t acc, int par, int lane, uint32_t stage, const CUtensorMap* mapo) {
   constexpr bool kGated = MODE == kLinFwdGated, kFwd = MODE == kLinFwd || MODE == kLinFwdGelu || kGated;
   constexpr int kU = kGated ? 2 : 4;                  // 16-byte units per output row
   const int left = t.ncols - jw;
@@ -389,8 +412,8 @@ __device__ __forceinline__ void lin_drain_rows(const LinArgs& a, const LinTile& 
   const long long jr = static_cast<long long>(t.row0) + t.j0 + jw;
   const PieceRows<kU> rows(lane);
   const TmemSums sums{acc};
-  // this thread's matrix row for stmatrix / ldmatrix: row lane of the piece, 16-byte unit n with + 16 n
-  const uint32_t mat = stage + static_cast<uint32_t>(lane * kPiecePitch);
+  // this thread's matrix row for stmatrix / ldmatrix: row `lane` of the piece, 16-byte unit n
+  auto mat = [&](int n) { return piece_at(stage, lane, n); };
   auto col_of = [&](int c) { return i0 + (kGated ? c / 2 : c); };
   // the residual of the next piece is on its way while this one is worked on
   const bool has_res = a.res != nullptr;
@@ -407,6 +430,7 @@ __device__ __forceinline__ void lin_drain_rows(const LinArgs& a, const LinTile& 
     if (col0 >= a.i_ext) break;
     float v[32];
     sums(c0 - (cb & ~63), 32, v);
+    piece_free(lane);
     if (kFwd) {
       if (a.bias) {
         const float* b = a.bias + static_cast<size_t>(t.e) * (kGated ? 2 * a.i_ext : a.i_ext);
@@ -428,7 +452,7 @@ __device__ __forceinline__ void lin_drain_rows(const LinArgs& a, const LinTile& 
         __syncwarp();
 #pragma unroll
         for (int n = 0; n < 4; ++n)
-          stmatrix_x4(mat + n * 16, lin_pack(v[8 * n], v[8 * n + 1], a.f16), lin_pack(v[8 * n + 2], v[8 * n + 3], a.f16),
+          stmatrix_x4(mat(n), lin_pack(v[8 * n], v[8 * n + 1], a.f16), lin_pack(v[8 * n + 2], v[8 * n + 3], a.f16),
                       lin_pack(v[8 * n + 4], v[8 * n + 5], a.f16), lin_pack(v[8 * n + 6], v[8 * n + 7], a.f16));
         __syncwarp();
         zr.store(stage, a.z + jr * a.ldz + zc + (kGated && (zr.unit & 1) ? a.i_ext : 0), a.ldz, zc < a.i_ext, left);
@@ -451,7 +475,7 @@ __device__ __forceinline__ void lin_drain_rows(const LinArgs& a, const LinTile& 
 #pragma unroll
       for (int m = 0; m < kU; ++m) {
         uint32_t r[4];
-        ldmatrix_x4(mat + m * 16, r);
+        ldmatrix_x4(mat(m), r);
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
           const float2 x = lin_unpack(r[h], a.f16);
@@ -464,11 +488,15 @@ __device__ __forceinline__ void lin_drain_rows(const LinArgs& a, const LinTile& 
     }
 #pragma unroll
     for (int m = 0; m < kU; ++m)
-      stmatrix_x4(mat + m * 16, lin_pack(o[8 * m], o[8 * m + 1], a.f16), lin_pack(o[8 * m + 2], o[8 * m + 3], a.f16),
+      stmatrix_x4(mat(m), lin_pack(o[8 * m], o[8 * m + 1], a.f16), lin_pack(o[8 * m + 2], o[8 * m + 3], a.f16),
                   lin_pack(o[8 * m + 4], o[8 * m + 5], a.f16), lin_pack(o[8 * m + 6], o[8 * m + 7], a.f16));
     __syncwarp();
-    const int col = col0 + rows.unit * 8;
-    rows.store(stage, a.out + jr * a.ldo + col, a.ldo, col < a.i_ext, left);
+    if (!kGated && (left >= 32 || !a.counts)) {       // (an expert's rows end before the matrix does)
+      piece_send(stage, mapo, col0, static_cast<int>(jr), 0, lane);
+    } else {
+      const int col = col0 + rows.unit * 8;
+      rows.store(stage, a.out + jr * a.ldo + col, a.ldo, col < a.i_ext, left);
+    }
   }
   __syncwarp();
 }
@@ -478,7 +506,7 @@ __device__ __forceinline__ void lin_drain_rows(const LinArgs& a, const LinTile& 
 // every second piece of rows from piece `par` on.  stage: the warp's piece in shared memory.
 template <int MODE, class Sums>
 __device__ __forceinline__ void lin_drain(const LinArgs& a, const LinTile& t, int i0, int cb, int ce, const Sums& sums, int q,
-                                          int par, int lane, uint32_t stage) {
+                                          int par, int lane, uint32_t stage, const CUtensorMap* mapo = nullptr) {
   constexpr bool kGated = MODE == kLinFwdGated, kFwd = MODE == kLinFwd || MODE == kLinFwdGelu || kGated;
   constexpr int kU = kGated ? 2 : 4;                  // 16-byte units per output row
   // accumulator lane l of the warp is output column iw + l; gated: lanes 16m + 0..7 are the gate rows of
@@ -499,7 +527,7 @@ __device__ __forceinline__ void lin_drain(const LinArgs& a, const LinTile& t, in
   const int col = iw + rows.unit * 8;
   const bool live = col < a.i_ext;                    // i_ext is a multiple of 8
   // this thread's matrix row for stmatrix / ldmatrix: row lane % 8 of matrix lane / 8
-  const uint32_t mat = stage + static_cast<uint32_t>((lane & 7) * kPiecePitch + (lane >> 3) * 16);
+  const uint32_t mat = piece_at(stage, lane & 7, lane >> 3);
   // the residual of the next piece is on its way while this one is worked on
   const bool has_res = MODE != kLinDw && a.res != nullptr;
   uint4 res[kU];
@@ -510,6 +538,7 @@ __device__ __forceinline__ void lin_drain(const LinArgs& a, const LinTile& t, in
     const int left = ce - c0;
     float v[32];
     sums(c0, left, v);
+    if (mapo) piece_free(lane);
     if (kFwd) {
 #pragma unroll
       for (int j = 0; j < 32; ++j) v[j] += bias[(j >> 1) & 3];
@@ -540,8 +569,7 @@ __device__ __forceinline__ void lin_drain(const LinArgs& a, const LinTile& t, in
       lin_act<MODE>(a, v, o);
     }
     // gated: two 8-column groups of rows make one x4 (matrix m: columns 8 (m & 1), rows 8 (m >> 1))
-    const uint32_t om = kGated ? stage + static_cast<uint32_t>(((lane >> 4) * 8 + (lane & 7)) * kPiecePitch + ((lane >> 3) & 1) * 16)
-                               : mat;
+    const uint32_t om = kGated ? piece_at(stage, (lane >> 4) * 8 + (lane & 7), (lane >> 3) & 1) : mat;
     constexpr int kSteps = kGated ? 2 : 4, kStepRows = 32 / kSteps;
     __syncwarp();
     if (has_res) {
@@ -568,7 +596,10 @@ __device__ __forceinline__ void lin_drain(const LinArgs& a, const LinTile& t, in
                     lin_pack(o[8 * n + 2], o[8 * n + 3], a.f16), lin_pack(o[8 * n + 4], o[8 * n + 5], a.f16),
                     lin_pack(o[8 * n + 6], o[8 * n + 7], a.f16));
     __syncwarp();
-    rows.store(stage, a.out + (jr + c0) * a.ldo + col, a.ldo, live, left);
+    if (mapo)       // weight gradient of the pair kernel
+      piece_send(stage, mapo, iw, t.j0 + c0, t.e, lane);
+    else
+      rows.store(stage, a.out + (jr + c0) * a.ldo + col, a.ldo, live, left);
   }
   __syncwarp();
 }
@@ -659,12 +690,12 @@ __global__ void __launch_bounds__(kLinMaxE) expert_maps_kernel(const __grid_cons
   asm volatile("fence.proxy.tensormap::generic.release.gpu;" ::: "memory");
 }
 
-// mapa / mapb: maps of the operands (see the launches).  emaps: the weight gradient's maps of experts' rows,
+// mapa / mapsb: maps of the operands (see the launches); mapo: of the output, 32 x 32 pieces.  emaps: the weight gradient's maps of experts' rows,
 // A's and B's of expert e at 2e and 2e + 1.
 template <int MODE>
 __global__ void __launch_bounds__(kLinThreads, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap mapa, const __grid_constant__ LinMapsB mapsb,
-                       const CUtensorMap* __restrict__ emaps, const LinArgs a) {
+                       const __grid_constant__ CUtensorMap mapo, const CUtensorMap* __restrict__ emaps, const LinArgs a) {
   constexpr bool kRowsM = MODE != kLinDw;                       // A: rows of x or dz, B: weights; else A: x, B: dz
   constexpr bool kAMn = MODE == kLinDw, kBMn = MODE == kLinDx || MODE == kLinDw;
   constexpr int kCtaI = MODE == kLinFwdGated ? 64 : kLinBI;     // output columns per CTA
@@ -676,7 +707,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   uint64_t* acc_empty = acc_full + 2;          // [2] even CTA: drained by both CTAs
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  uint8_t* pieces = smem + kPairStages * kPairStage + 256;                    // one per epilogue warp
+  uint8_t* pieces = smem + kPairStages * kPairStage + 512;                    // one per epilogue warp
   LinSegs segs;
   segs.row0 = reinterpret_cast<int*>(pieces + kLinEpiWarps * kPieceBytes);
   segs.cnt = segs.row0 + kLinMaxE;
@@ -856,7 +887,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       const LinTile& t = walk.r;
       const int i0 = (t.it * 2 + rank) * kCtaI;
       if (MODE == kLinDw && t.slabs == 0) {
-        lin_drain<MODE>(a, t, i0, 0, t.ncols, ZeroSums{}, q, par, lane, stage);
+        lin_drain<MODE>(a, t, i0, 0, t.ncols, ZeroSums{}, q, par, lane, stage, &mapo);
         continue;
       }
       ok = mbar_wait(smem_u32(acc_full + b), (aph >> b) & 1u, a.status) && *abort_flag == 0;
@@ -865,14 +896,14 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       tc_fence_after();
       const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(b * kLinBJ);
       if constexpr (!kRowsM) {
-        lin_drain<MODE>(a, t, i0, 0, t.ncols, TmemSums{acc}, q, par, lane, stage);
+        lin_drain<MODE>(a, t, i0, 0, t.ncols, TmemSums{acc}, q, par, lane, stage, &mapo);
       } else if (t.ncols > 128) {
         // M = 256: this CTA's 128 rows, all 256 columns
-        lin_drain_rows<MODE>(a, t, t.it * 2 * kCtaI, rank * 128 + q * 32, 0, kLinBJ, acc, par, lane, stage);
+        lin_drain_rows<MODE>(a, t, t.it * 2 * kCtaI, rank * 128 + q * 32, 0, kLinBJ, acc, par, lane, stage, &mapo);
       } else {
         // M = 128: this CTA's 64 rows twice, columns 0..127 in lanes 0..63 and 128..255 in lanes 64..127
         lin_drain_rows<MODE>(a, t, t.it * 2 * kCtaI, rank * 64 + (q & 1) * 32, (q >> 1) * 128, (q >> 1) * 128 + 128, acc, par,
-                             lane, stage);
+                             lane, stage, &mapo);
       }
       tc_fence_before();
       __syncwarp();
@@ -880,6 +911,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       aph ^= 1u << b;
       b ^= 1;
     }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     if (!ok) *abort_flag = 1;
   }
   tc_fence_before();
@@ -1063,7 +1095,8 @@ EncodeTiledFnLin get_encode_lin() {
 }
 
 // A map of 16-bit elements: extents d[0..n), strides (elements) s[1..n) of dimensions 1 .., box b[0..n).
-bool lin_map(CUtensorMap* m, int f16, const void* p, int n, const long long* d, const long long* s, const int* b) {
+bool lin_map(CUtensorMap* m, int f16, const void* p, int n, const long long* d, const long long* s, const int* b,
+             CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   EncodeTiledFnLin enc = get_encode_lin();
   if (!enc) return false;
   cuuint64_t dims[5], strides[4];
@@ -1075,7 +1108,7 @@ bool lin_map(CUtensorMap* m, int f16, const void* p, int n, const long long* d, 
     if (i) strides[i - 1] = static_cast<cuuint64_t>(s[i]) * 2;
   }
   return enc(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(n),
-             const_cast<void*>(p), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             const_cast<void*>(p), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1181,6 +1214,14 @@ cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<unsigned long 
 template <int MODE>
 cudaError_t lin_launch(const LinPlan& p, const CUtensorMap& ma, const LinMapsB& mb, const CUtensorMap* emaps, LinArgs a,
                        cudaStream_t stream) {
+  CUtensorMap mo = {};
+  if (p.pair) {
+    // the output (weight gradient: [E][N][K]) in pieces of 32 rows of 32 columns
+    const long long rows = MODE == kLinDw ? a.j_ext : a.rows;
+    const long long d[3] = {a.i_ext, rows, MODE == kLinDw ? a.E : 1}, st[3] = {0, a.ldo, a.ldo * rows};
+    const int b[3] = {32, 32, 1};
+    if (!lin_map(&mo, a.f16, a.out, 3, d, st, b, CU_TENSOR_MAP_SWIZZLE_64B)) return cudaErrorInvalidValue;
+  }
   static std::atomic<unsigned long long> pair_done{0}, split_done[3] = {};
   a.bj = p.bj;
   a.stages = p.stages;
@@ -1203,7 +1244,7 @@ cudaError_t lin_launch(const LinPlan& p, const CUtensorMap& ma, const LinMapsB& 
   if (p.pair) {
     const cudaError_t err = allow_smem(reinterpret_cast<const void*>(&linear_pair_kernel<MODE>), kPairSmem, pair_done);
     if (err != cudaSuccess) return err;
-    return cudaLaunchKernelEx(&cfg, linear_pair_kernel<MODE>, ma, mb, emaps, static_cast<const LinArgs>(a));
+    return cudaLaunchKernelEx(&cfg, linear_pair_kernel<MODE>, ma, mb, mo, emaps, static_cast<const LinArgs>(a));
   }
   const auto kernel = p.split == 1   ? linear_split_kernel<MODE, 1>
                       : p.split == 2 ? linear_split_kernel<MODE, 2>
