@@ -3,7 +3,9 @@
 //
 // With s = softmax(l) or sqrt(softplus(l)), w_k = s_k of the K selected experts (divided by their sum
 // when renormalised) and dw = dL/dw:
-//   g_k = s_k dL/ds_k = w_k (dw_k - sum_j w_j dw_j)   renormalised,   w_k dw_k   otherwise
+//   g_k = s_k dL/ds_k = w_k sum_j w_j (dw_k - dw_j)   renormalised,   w_k dw_k   otherwise
+// (the same as w_k (dw_k - sum_j w_j dw_j), since the weights add up to 1, but without its cancellation where one
+// weight is nearly 1)
 //   softmax:         dl_i = [i selected] g_i - p_i sum_j g_j     (renormalised: sum_j g_j = 0)
 //   sqrt(softplus):  dl_k = g_k sigmoid(l_k) / (2 softplus(l_k)), zero elsewhere
 // so only the unnormalised softmax needs the whole row of logits.  The forward's own weights stand in
@@ -76,10 +78,9 @@ __global__ void __launch_bounds__(kGradWarps * 32) route_grad_kernel(const float
   }
   float g = wk * dk;
   if (renorm) {
-    float c = g;
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) c += __shfl_xor_sync(0xffffffffu, c, off);
-    g = id >= 0 ? wk * (dk - c) : 0.f;
+    float c = 0.f;
+    for (int j = 0; j < K; ++j) c = fmaf(__shfl_sync(0xffffffffu, wk, j), dk - __shfl_sync(0xffffffffu, dk, j), c);
+    g = id >= 0 ? wk * c : 0.f;
   }
   // p becomes the row's -p_e sum_j g_j (dense) or zeros
   float total = 0.f, lmax = -INFINITY, sum = 0.f;

@@ -69,6 +69,13 @@ def route_weights(logits, ids, fn, renorm):
     return w / w.sum(1, keepdim=True) if renorm else w
 
 
+def route_weights_autograd(logits, ids, fn):
+    """Normalised weights of the selected experts, differentiable in the logits."""
+    s = torch.softmax(logits, 1) if fn == "softmax" else torch.nn.functional.softplus(logits, threshold=1e9).sqrt()
+    w = s.gather(1, ids)
+    return w / w.sum(1, keepdim=True)
+
+
 def route_grad(logits, ids, dw, fn, renorm):
     """dL/dlogits by the chain rule over the whole row."""
     l = logits.to(F64)
