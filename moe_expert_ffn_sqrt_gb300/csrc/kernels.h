@@ -202,11 +202,11 @@ struct RowsView {
 // train_rows.cu: rows of T tokens to and from U sorted rows through inv [T, K] (-1: dropped pair).
 cudaError_t launch_scatter_rows(int dt, RowsView x, const int32_t* inv, int T, int K, int H, int U, RowsView out,
                                 uint32_t* status, cudaStream_t stream);
-// Index arrays (as launch_permute's) and rows in one launch, for few (token, slot) pairs.
-bool dispatch_few_supported(int T, int K, int E);
-cudaError_t launch_dispatch_few(int dt, const int32_t* topk_ids, RowsView x, int T, int H, int E, int K, int align, int U,
-                                RowsView out, int32_t* sorted_ids, int32_t* expert_ids, int32_t* inv_perm, int32_t* m_sum,
-                                int32_t* counts, uint32_t* status, cudaStream_t stream);
+// Index arrays (as launch_permute's) and rows for up to some thousand (token, slot) pairs.
+bool dispatch_layout_supported(int T, int K, int E);
+cudaError_t launch_dispatch_layout(int dt, const int32_t* topk_ids, RowsView x, int T, int H, int E, int K, int align, int U,
+                                   RowsView out, int32_t* sorted_ids, int32_t* expert_ids, int32_t* inv_perm, int32_t* m_sum,
+                                   int32_t* counts, uint32_t* status, cudaStream_t stream);
 // out[t] = sum_k w[t,k] y[inv[t,k]] (+ res[t]); w null: plain sum.
 cudaError_t launch_sum_rows(int dt, RowsView y, const int32_t* inv, const float* w, RowsView res, int T, int K, int H,
                             int U, RowsView out, uint32_t* status, cudaStream_t stream);

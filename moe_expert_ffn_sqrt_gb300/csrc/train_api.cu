@@ -101,10 +101,10 @@ moe_status moe_dispatch(moe_dtype dt, const int32_t* topk_ids, moe_rows x, int T
   if (!m_sum || (U > 0 && (!sorted_token_ids || !expert_ids))) return MOE_ERR_INVALID_ARG;
   if (T > 0 && (!topk_ids || !inv_perm || !rows_ok(x, H, dt) || !rows_ok(x_perm, H, dt))) return MOE_ERR_INVALID_ARG;
   if (!ws || ws_bytes < kAlign + permute_scratch_bytes(T, K, E)) return MOE_ERR_WORKSPACE;
-  if (dispatch_few_supported(T, K, E))
-    return cuda_status(launch_dispatch_few(dt, topk_ids, view(x), T, H, E, K, align, static_cast<int>(U), view(x_perm),
-                                           sorted_token_ids, expert_ids, inv_perm, m_sum, expert_counts, status_of(ws),
-                                           S(stream)));
+  if (dispatch_layout_supported(T, K, E))
+    return cuda_status(launch_dispatch_layout(dt, topk_ids, view(x), T, H, E, K, align, static_cast<int>(U), view(x_perm),
+                                              sorted_token_ids, expert_ids, inv_perm, m_sum, expert_counts,
+                                              status_of(ws), S(stream)));
   int32_t* scratch = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + kAlign);
   const cudaError_t err =
       launch_permute(topk_ids, T, K, E, align, static_cast<int>(U), sorted_token_ids, expert_ids, inv_perm, m_sum,
