@@ -543,7 +543,8 @@ typedef enum {
   MOE_ACT_SWIGLU = 4
 } moe_act;
 
-/* Workspace bytes of moe_linear (which needs its first 256 only) and moe_linear_backward. */
+/* Workspace bytes of moe_linear (which needs the first 256 * (E + 1) only) and moe_linear_backward.  The
+ * workspace of these two calls starts on a 256-byte boundary. */
 moe_status moe_workspace_size_linear(int rows, int N, int K, int E, moe_act act, size_t* bytes);
 
 /* Matrix product with bias, activation and residual in its epilogue:

@@ -225,12 +225,12 @@ struct LinearShape {
   int rows, N, K, E, align, f16;
   const int32_t* counts;
 };
-cudaError_t launch_linear(const LinearShape& p, RowsView x, const uint16_t* w, const float* bias, RowsView res, int act,
-                          RowsView y, RowsView z, uint32_t* status, cudaStream_t stream);
-cudaError_t launch_linear_dx(const LinearShape& p, RowsView dz, const uint16_t* w, RowsView res, RowsView dx,
-                             uint32_t* status, cudaStream_t stream);
 // maps: kLinearMapBytes per expert of scratch, 128-byte aligned (counts null: not used).
 constexpr size_t kLinearMapBytes = 2 * 128;
+cudaError_t launch_linear(const LinearShape& p, RowsView x, const uint16_t* w, const float* bias, RowsView res, int act,
+                          RowsView y, RowsView z, void* maps, uint32_t* status, cudaStream_t stream);
+cudaError_t launch_linear_dx(const LinearShape& p, RowsView dz, const uint16_t* w, RowsView res, RowsView dx, void* maps,
+                             uint32_t* status, cudaStream_t stream);
 cudaError_t launch_linear_dw(const LinearShape& p, RowsView dz, RowsView x, uint16_t* dw, void* maps, uint32_t* status,
                              cudaStream_t stream);
 // dz = dy * act'(z) (act none: not written) and, with db, the bias gradient (part: E * linear_bias_slices * N floats).

@@ -10,14 +10,18 @@
 // transposed in memory.
 //
 // The tensor core feeds its M side one row a cycle: an MMA of 128 rows of A per CTA takes 128 cycles however
-// few columns N it has (measured; 256 columns fill them), one of 64 rows takes 64.  So what is ragged goes on M
-// and N is 256: in the pair kernel's forward and input gradient the rows of x or dz are on M, 256 or 128 of
-// them per tile, and a segment's rest of up to 128 rows costs half a tile.  (With the weights on M and the rows
-// on N, every started 256 rows cost a whole one: 12288 rows of 32 uneven experts took 494 us.)
+// few columns N it has (measured; 256 columns fill them).  In the pair kernel's forward and input gradient the
+// rows of x or dz are on M, 256 or 128 of them per tile, and 256 output columns on N: 8192^3 runs at 1.80 to
+// 1.92 PFLOP/s, near what the copy of both operands into shared memory allows.  A segment's rest of up to 128
+// rows takes a half tile, which its weights' way to shared memory keeps from half the time (19 experts of 384
+// rows: 275 us, with whole tiles 303).  Both parts of a segment in one tile on both accumulators were slower (32
+// experts of about 400 rows: 490 -> 568 us).  Weights on M and the rows on a trimmed N: the same 32 experts'
+// forward, back to back, 545 us against 563, but their gradients 595 against 581 and a dense 4096 x 8192 x 2048
+// product 84 against 81.
 //
 // Rows of experts: expert e's rows start at seg_e = sum_{e' < e} round_up(counts[e'], align) (the layout
 // of moe_permute).  Padding rows are never read into a result nor written: in the forward and the input
-// gradient a padding row is a column of the product that is not stored; in the weight gradient, where
+// gradient a padding row is a row of the product that is not stored; in the weight gradient, where
 // rows are summed over, each expert has tensor maps of its own whose rows end with its segment
 // (expert_maps_kernel), so that what a copy takes past the end reads as zeros.  (Fetching the last partial
 // slab row by row instead cost the 32-expert gradient 87 of 470 us.)
@@ -41,8 +45,8 @@ namespace {
 
 constexpr int kLinEpiWarps = 8;             // two per TMEM lane quarter, on alternate pieces of 32 columns
 constexpr int kLinThreads = 64 + 32 * kLinEpiWarps;   // warp 0 loads, 1 MMA, the others drain
-constexpr int kLinBI = 128;                 // output columns i per CTA (accumulator lanes)
-constexpr int kLinBJ = 256;                 // output rows j per tile (MMA N), at most
+constexpr int kLinBI = 128;                 // rows of A per CTA (accumulator lanes)
+constexpr int kLinBJ = 256;                 // rows of B per tile (MMA N, accumulator columns), at most
 constexpr int kLinSlab = 64;                // terms of the sum per pipeline stage
 constexpr int kLinABytes = kLinBI * 128;
 constexpr int kLinMaxE = kLinearMaxExperts;
@@ -604,7 +608,8 @@ __device__ __forceinline__ void lin_drain(const LinArgs& a, const LinTile& t, in
   __syncwarp();
 }
 
-// Loads A's output columns (128, or the tile's; from column i0; gated: i0 of y) and q0 .. of the sum.
+// Loads the operand of the output's columns, from column i0 on (gated: i0 of y), and q0 .. of the sum: w, in the
+// weight gradient x.
 template <int MODE, bool PAIR>
 __device__ __forceinline__ void lin_load_a(const LinArgs& a, const CUtensorMap* map, uint32_t dst, const LinTile& t, int i0,
                                            int q0, uint32_t bar) {
@@ -624,13 +629,13 @@ __device__ __forceinline__ void lin_load_a(const LinArgs& a, const CUtensorMap* 
   }
 }
 
-// Loads rows j .. j + n of B (n a multiple of 8), q0 .. of the sum: lin_b_bytes in all.
-// Maps of the rows operand (x or dz).  Pair kernel: [0] copies 128 rows at a time, [1] 64; split kernel and weight
-// gradient: [0].
+// Maps of the operand of the output's rows (x or dz).  Pair kernel: [0] copies 128 rows at a time, [1] 64; split
+// kernel and weight gradient: [0].
 struct LinMapsB {
   CUtensorMap m[2];
 };
 
+// Loads that operand's rows j .. j + n (n a multiple of 8), q0 .. of the sum: lin_b_bytes in all.
 template <int MODE, bool PAIR>
 __device__ __forceinline__ void lin_load_b(const LinArgs& a, const CUtensorMap* map, uint32_t dst, const LinTile& t, int j,
                                            int n, int q0, uint32_t bar) {
@@ -656,8 +661,8 @@ __device__ __forceinline__ void tensormap_acquire(const CUtensorMap* m) {
   asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(m) : "memory");
 }
 
-// Copies of the weight gradient's two maps for each expert, their rows (dimension 1) ending with the
-// expert's segment.  One CTA, thread = expert.
+// Copies of two maps (the weight gradient's of x and dz, else the rows operand's for 128 and 64 rows) for each
+// expert, their rows (dimension 1) ending with the expert's segment.  One CTA, thread = expert.
 __global__ void __launch_bounds__(kLinMaxE) expert_maps_kernel(const __grid_constant__ CUtensorMap mapa,
                                                                const __grid_constant__ CUtensorMap mapb,
                                                                const int32_t* __restrict__ counts, int E, int align, int rows,
@@ -690,8 +695,8 @@ __global__ void __launch_bounds__(kLinMaxE) expert_maps_kernel(const __grid_cons
   asm volatile("fence.proxy.tensormap::generic.release.gpu;" ::: "memory");
 }
 
-// mapa / mapsb: maps of the operands (see the launches); mapo: of the output, 32 x 32 pieces.  emaps: the weight gradient's maps of experts' rows,
-// A's and B's of expert e at 2e and 2e + 1.
+// mapa: map of the operand of the output's columns (w, in the weight gradient x), mapsb: of its rows, mapo: of the
+// output, 32 x 32 pieces.  emaps: expert e's maps at 2e and 2e + 1 (see expert_maps_kernel), or null.
 template <int MODE>
 __global__ void __launch_bounds__(kLinThreads, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap mapa, const __grid_constant__ LinMapsB mapsb,
@@ -772,7 +777,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   const uint32_t tmem = *tmem_slot;
 
   if (warp == 0) {
-    // ---------------- loads: this CTA's 128 columns of A, its half of B's rows ----------------
+    // ---------------- loads: this CTA's half of A and of B ----------------
     const uint32_t full0 = mapa_shared(smem_u32(full), 0);
     int st = 0;
     uint32_t ph = 0;
@@ -783,14 +788,19 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       const LinTile& t = walk.r;
       const int half = ((t.ncols + kPairStep - 1) & ~(kPairStep - 1)) / 2;
       const int mrows = t.ncols <= 128 ? 64 : 128;
-      const CUtensorMap *ma = &mapa, *mb = &mapsb.m[0];
-      if (MODE == kLinDw && a.counts) {
-        ma = emaps + 2 * t.e;
-        mb = ma + 1;
+      const CUtensorMap *ma = &mapa, *mb = &mapsb.m[0], *mr = &mapsb.m[mrows == 64];
+      if (emaps != nullptr) {
+        const CUtensorMap* em = emaps + 2 * t.e;
         if (e_maps != t.e && t.slabs) {      // written by the launch before this one
           e_maps = t.e;
-          tensormap_acquire(ma);
-          tensormap_acquire(mb);
+          tensormap_acquire(em);
+          tensormap_acquire(em + 1);
+        }
+        if (kRowsM) {
+          mr = em + (mrows == 64);
+        } else {
+          ma = em;
+          mb = em + 1;
         }
       }
       const int i0 = (t.it * 2 + rank) * kCtaI, j0 = t.j0 + rank * half;
@@ -804,7 +814,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         __syncwarp();
         if (lane == 0) {
           if (kRowsM) {
-            tma_load_4d<true>(sa, &mapsb.m[mrows == 64], q0, t.row0 + t.j0 + rank * mrows, 0, 0, fb);
+            tma_load_4d<true>(sa, mr, q0, t.row0 + t.j0 + rank * mrows, 0, 0, fb);
             lin_load_a<MODE, true>(a, ma, sb, t, i0, q0, fb);
           } else {
             lin_load_a<MODE, true>(a, ma, sa, t, i0, q0, fb);
@@ -876,7 +886,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     }
     __syncwarp();
   } else {
-    // ---------------- epilogue: this CTA's 128 output columns ----------------
+    // ---------------- epilogue: this CTA's accumulator lanes ----------------
     const int q = warp & 3, par = (warp - 2) >> 2;   // the TMEM lane quarter this warp may read
     const uint32_t acc_empty0 = mapa_shared(smem_u32(acc_empty), 0), stage = smem_u32(pieces + (warp - 2) * kPieceBytes);
     int b = 0;
@@ -1143,9 +1153,9 @@ struct LinPlan {
 };
 
 // Dense problems take the cheapest way to run them by a count of cycles that was fitted to measurements of every
-// way (pair; split with 128 or 64 lanes and 1, 2 or 4 slices) over 126 shapes of 1 to 4096 rows, 256 to 7168
-// columns and terms: the way it picks is on average 0.1% off the fastest one, 3% at most.
-//  * pair: 76 tiles at a time, 470 a slab, 26 per row j of the epilogue at the end;
+// way (pair; split with 128 or 64 lanes and 1, 2 or 4 slices) over 132 shapes of 1 to 4096 rows, 256 to 7168
+// columns and terms: the way it picks is on average 0.2% off the fastest one, 4% at most.
+//  * pair: 76 tiles at a time, 420 a slab, 1000 and 16 per row j of the epilogue at the end;
 //  * split: 590 a slab (the MMA feeds its 128 rows of A at one a cycle, so short tiles are no cheaper), 5200 for each
 //    further round of CTAs; slices halve or quarter that for a meeting of 1900 + 250 S and 27 per row j and 128
 //    lanes for the partial sums over the cluster.
@@ -1165,7 +1175,7 @@ LinPlan lin_plan(int experts, int i_cols, bool gated, long long j, long long q, 
     p.grid = 2 * pairs;
     return p;
   }
-  long long best = (tiles + pairs - 1) / pairs * slabs * 470 + 220 + 26 * p.bj;
+  long long best = (tiles + pairs - 1) / pairs * slabs * 420 + 1000 + 16 * p.bj;
   const int bj = lin_tile_rows(static_cast<int>(j), kSplitStep);
   const long long nj = (j + bj - 1) / bj;
   for (int lanes = 128; lanes >= 64; lanes /= 2) {
@@ -1274,8 +1284,27 @@ LinArgs lin_args(const LinearShape& p, uint32_t* status) {
 
 }  // namespace
 
+namespace {
+
+// Experts' maps (see expert_maps_kernel) into `emaps`, *out = emaps.
+cudaError_t expert_maps(const LinearShape& p, const CUtensorMap& m0, const CUtensorMap& m1, void* maps, const CUtensorMap** out,
+                        cudaStream_t stream) {
+  CUtensorMap* emaps = static_cast<CUtensorMap*>(maps);
+  *out = emaps;
+  return launch_pdl(expert_maps_kernel, dim3(1), dim3(kLinMaxE), 0, stream, m0, m1, p.counts, p.E, p.align, p.rows, emaps);
+}
+
+// Forward and input gradient: whether a tile's rows past its expert's end are to read as zeros instead of the next
+// expert's rows.  The result is the same; zeros are not fetched and cost the tensor core less power, which a
+// long run is bound by (32 experts of about 400 rows, back to back: forward 571 -> 563 us, both gradients
+// 597 -> 581); with few rows the weights' way from HBM is all there is, and the maps' launch would only add its
+// 2 us.
+bool expert_rows_apart(const LinearShape& p) { return p.counts && p.rows >= 64LL * p.E; }
+
+}  // namespace
+
 cudaError_t launch_linear(const LinearShape& p, RowsView x, const uint16_t* w, const float* bias, RowsView res, int act,
-                          RowsView y, RowsView z, uint32_t* status, cudaStream_t stream) {
+                          RowsView y, RowsView z, void* maps, uint32_t* status, cudaStream_t stream) {
   LinArgs a = lin_args(p, status);
   const bool gated = act == kActSwiglu;
   a.act = act;
@@ -1304,12 +1333,17 @@ cudaError_t launch_linear(const LinearShape& p, RowsView x, const uint16_t* w, c
     ok = map_k_major(&ma, p.f16, w, p.K, p.N, a.E, p.K, pl.lanes);
   }
   if (!ok || !map_rows(mb, pl, p.f16, x, p.K, p.rows)) return cudaErrorInvalidValue;
-  if (gated) return lin_launch<kLinFwdGated>(pl, ma, mb, nullptr, a, stream);
-  if (act == kActGelu) return lin_launch<kLinFwdGelu>(pl, ma, mb, nullptr, a, stream);
-  return lin_launch<kLinFwd>(pl, ma, mb, nullptr, a, stream);
+  const CUtensorMap* emaps = nullptr;
+  if (expert_rows_apart(p)) {
+    const cudaError_t err = expert_maps(p, mb.m[0], mb.m[1], maps, &emaps, stream);
+    if (err != cudaSuccess) return err;
+  }
+  if (gated) return lin_launch<kLinFwdGated>(pl, ma, mb, emaps, a, stream);
+  if (act == kActGelu) return lin_launch<kLinFwdGelu>(pl, ma, mb, emaps, a, stream);
+  return lin_launch<kLinFwd>(pl, ma, mb, emaps, a, stream);
 }
 
-cudaError_t launch_linear_dx(const LinearShape& p, RowsView dz, const uint16_t* w, RowsView res, RowsView dx,
+cudaError_t launch_linear_dx(const LinearShape& p, RowsView dz, const uint16_t* w, RowsView res, RowsView dx, void* maps,
                              uint32_t* status, cudaStream_t stream) {
   LinArgs a = lin_args(p, status);
   a.i_ext = p.K;
@@ -1327,7 +1361,12 @@ cudaError_t launch_linear_dx(const LinearShape& p, RowsView dz, const uint16_t* 
   if (!map_mn_major(&ma, p.f16, w, p.K, p.N, a.E, p.K, &a.a_blocks) ||
       !map_rows(mb, pl, p.f16, dz, p.N, p.rows))
     return cudaErrorInvalidValue;
-  return lin_launch<kLinDx>(pl, ma, mb, nullptr, a, stream);
+  const CUtensorMap* emaps = nullptr;
+  if (expert_rows_apart(p)) {
+    const cudaError_t err = expert_maps(p, mb.m[0], mb.m[1], maps, &emaps, stream);
+    if (err != cudaSuccess) return err;
+  }
+  return lin_launch<kLinDx>(pl, ma, mb, emaps, a, stream);
 }
 
 cudaError_t launch_linear_dw(const LinearShape& p, RowsView dz, RowsView x, uint16_t* dw, void* maps, uint32_t* status,
@@ -1349,10 +1388,9 @@ cudaError_t launch_linear_dw(const LinearShape& p, RowsView dz, RowsView x, uint
   if (!map_mn_major(&ma, p.f16, x.ptr, p.K, p.rows, 1, x.ld, &a.a_blocks) ||
       !map_mn_major(&mb.m[0], p.f16, dz.ptr, p.N, p.rows, 1, dz.ld, &a.b_blocks))
     return cudaErrorInvalidValue;
-  CUtensorMap* emaps = static_cast<CUtensorMap*>(maps);
+  const CUtensorMap* emaps = nullptr;
   if (p.counts) {
-    const cudaError_t err = launch_pdl(expert_maps_kernel, dim3(1), dim3(kLinMaxE), 0, stream, ma, mb.m[0], p.counts, p.E,
-                                       p.align, p.rows, emaps);
+    const cudaError_t err = expert_maps(p, ma, mb.m[0], maps, &emaps, stream);
     if (err != cudaSuccess) return err;
   }
   return lin_launch<kLinDw>(pl, ma, mb, emaps, a, stream);

@@ -172,10 +172,10 @@ moe_status moe_linear(moe_dtype dt, moe_rows x, const void* w, const float* bias
   if (!rows16_ok(x, K) || !w || !aligned(w, 16) || !rows16_ok(y, cols)) return MOE_ERR_INVALID_ARG;
   if (!opt_rows16_ok(residual, cols) || !opt_rows16_ok(z, N)) return MOE_ERR_INVALID_ARG;
   if (bias && !aligned(bias, 16)) return MOE_ERR_INVALID_ARG;
-  if (ws_bytes < kAlign) return MOE_ERR_WORKSPACE;
+  if (ws_bytes < kAlign + E * kLinearMapBytes) return MOE_ERR_WORKSPACE;
   return cuda_status(launch_linear(linear_shape(dt, expert_counts, rows, N, K, E, align), view(x),
                                    static_cast<const uint16_t*>(w), bias, view(residual), act, view(y), view(z),
-                                   status_of(ws), S(stream)));
+                                   static_cast<char*>(ws) + kAlign, status_of(ws), S(stream)));
 }
 
 moe_status moe_linear_backward(moe_dtype dt, moe_rows dy, moe_rows x, const void* w, moe_rows z, moe_act act,
@@ -208,7 +208,8 @@ moe_status moe_linear_backward(moe_dtype dt, moe_rows dy, moe_rows x, const void
                         S(stream)) != cudaSuccess)
       return MOE_ERR_CUDA;
   }
-  if (dx.ptr && launch_linear_dx(p, dz, static_cast<const uint16_t*>(w), view(dx_residual), view(dx), status_of(ws),
+  if (dx.ptr && launch_linear_dx(p, dz, static_cast<const uint16_t*>(w), view(dx_residual), view(dx),
+                                 base + L.maps, status_of(ws),
                                  S(stream)) != cudaSuccess)
     return MOE_ERR_CUDA;
   if (dw && launch_linear_dw(p, dz, view(x), static_cast<uint16_t*>(dw), base + L.maps, status_of(ws), S(stream)) != cudaSuccess)
