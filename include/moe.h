@@ -481,9 +481,10 @@ moe_status moe_forward_batched_i8(const uint16_t* hidden, const float* w_gate, c
  *
  * Matrices are row-major with a pitch (moe_rows): row r starts at ptr + r * ld elements, ld >= columns.
  * ptr NULL means "not given" where an argument is optional.  Rows are bf16, fp16 or fp32; every sum is
- * taken in fp32 and rounded once, in a fixed order (equal inputs give equal bits).
+ * taken in fp32 and rounded once, in a fixed order: equal inputs give equal bits (the order in a weight
+ * gradient of moe_combine_backward goes by the rows' 16-byte alignment).
  * Sorted buffers have U rows (moe_msum_upper, or E * max_tokens for the BatchedExperts layout); padding
- * rows are never read and never written.
+ * rows never count and are never written.
  * ws: a workspace whose first 256 bytes hold the device status word, zero-filled once before first use.
  * ------------------------------------------------------------------------------------ */
 typedef enum { MOE_BF16 = 0, MOE_F16 = 1, MOE_F32 = 2 } moe_dtype;

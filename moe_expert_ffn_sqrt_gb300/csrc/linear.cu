@@ -1456,10 +1456,10 @@ __global__ void __launch_bounds__(32 * kActRowLanes)
   if (c < cols) {
     for (int r = blockIdx.z * kActRowLanes + rl; r < cnt; r += S * kActRowLanes) {
       const long long row = seg + r;
-      const Pack<T, 8> g = load_pack<T, 8>(dy + row * lddy + c);
-      Pack<T, 8> o, o2;
+      const Pack<T> g = load_pack<T>(dy + row * lddy + c);
+      Pack<T> o, o2;
       if (gated) {
-        const Pack<T, 8> a = load_pack<T, 8>(z + row * ldz + c), b = load_pack<T, 8>(z + row * ldz + cols + c);
+        const Pack<T> a = load_pack<T>(z + row * ldz + c), b = load_pack<T>(z + row * ldz + cols + c);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           float s;
@@ -1470,13 +1470,13 @@ __global__ void __launch_bounds__(32 * kActRowLanes)
           o.set(i, dg);
           o2.set(i, du);
         }
-        store_pack<T, 8>(dz + row * lddz + c, o);
-        store_pack<T, 8>(dz + row * lddz + cols + c, o2);
+        store_pack<T>(dz + row * lddz + c, o);
+        store_pack<T>(dz + row * lddz + cols + c, o2);
       } else if (act == kActNone) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) acc[0][i] += g.f(i);
       } else {
-        const Pack<T, 8> a = load_pack<T, 8>(z + row * ldz + c);
+        const Pack<T> a = load_pack<T>(z + row * ldz + c);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const float v = a.f(i);
@@ -1492,7 +1492,7 @@ __global__ void __launch_bounds__(32 * kActRowLanes)
           acc[0][i] += d;
           o.set(i, d);
         }
-        store_pack<T, 8>(dz + row * lddz + c, o);
+        store_pack<T>(dz + row * lddz + c, o);
       }
     }
   }

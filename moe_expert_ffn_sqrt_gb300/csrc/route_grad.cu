@@ -11,7 +11,9 @@
 // so only the unnormalised softmax needs the whole row of logits.  The forward's own weights stand in
 // for the scores, so nothing divides by a sum that may underflow.  The selection itself (and with it
 // e_score_correction_bias) has no gradient.
-// One warp per token; the [T, E] write (and the logits' read, where needed) bounds it.
+// One warp per token, 16-byte accesses where E is a multiple of four; the [T, E] write (and the logits' read, where
+// needed) bounds it.  16384 tokens, 256 experts, K = 6, fp32: 8.6 us (34.7 MB, 4.0 TB/s), renormalised 4.5 us
+// (18.4 MB, 4.1 TB/s); a few tokens 1.5 us, the launch.
 #include "kernels.h"
 #include "rows.cuh"
 
