@@ -129,6 +129,62 @@ def test_combine_and_its_gradients(M, T, H, E, K, align, dt, extra):
     assert M.get_error(ws) == M.OK
 
 
+def at(v, off, pitch):
+    """v's CUDA copy with rows `pitch` apart and row 0 `off` elements into its buffer, which ends with the last row;
+    all the rest is NaN."""
+    n, H = v.shape
+    flat = torch.full((off + (n - 1) * pitch + H,), float("nan"), dtype=v.dtype, device="cuda")
+    m = flat.as_strided((n, H), (pitch, 1), off)
+    m.copy_(v)
+    return flat, m
+
+
+@pytest.mark.parametrize("dt", [BF, HF, FP])
+@pytest.mark.parametrize("T,H,off,gap", [(70, 1, 1, 0), (70, 7, 3, 1), (70, 8, 1, 8), (70, 9, 0, 0), (70, 16, 5, 0), (70, 19, 2, 6),
+                                         (70, 64, 0, 1), (70, 261, 7, 2), (3, 23, 1, 1), (700, 1027, 1, 0)])
+def test_rows_at_any_alignment(M, dt, T, H, off, gap):
+    # every matrix starts off its 16-byte boundary by another number of elements, has its own pitch, and NaN around it
+    E, K, align = 6, 4, 8
+    ids, w = routing(T, E, K, H)
+    inv, _ = R.positions(ids, E, align)
+    U = M.msum_upper(T, K, E, align)
+    g = torch.Generator().manual_seed(H + off)
+    v = {n: torch.randn(r, H, generator=g).to(dt) for n, r in (("x", T), ("d", T), ("res", T), ("y", U))}
+    pad = torch.ones(U, dtype=torch.bool)
+    pad[inv.reshape(-1).long()] = False
+    v["y"][pad] = float("nan")
+    m = {n: at(a, off + i, H + gap + i)[1] for i, (n, a) in enumerate(v.items())}
+    new = lambda i, rows: at(torch.full((rows, H), SENTINEL, dtype=dt), off + i, H + gap + i)
+    ws = M.new_workspace_rows(T, K, E)
+    idx = [torch.empty(s, dtype=torch.int32, device="cuda") for s in (U, U, 1)]
+    invd, wd = inv.cuda(), w.cuda()
+    flat, xp = new(2, U)
+    M.dispatch(ids.cuda(), m["x"], E, align, xp, idx[0], idx[1], torch.empty_like(invd), idx[2], ws)
+    ref = torch.full((U, H), SENTINEL, dtype=dt)
+    ref[inv.reshape(-1).long()] = v["x"].repeat_interleave(K, 0)
+    assert torch.equal(xp.cpu(), ref)
+    assert int(flat.isnan().sum()) == flat.numel() - U * H
+    y = torch.where(pad[:, None], torch.zeros((), dtype=dt), v["y"])
+    for ww, fn in ((w, M.combine), (None, M.dispatch_backward)):
+        ref, mag = R.combine(y, inv, ww, v["res"])
+        bound = R.half_step(dt) * ref.abs() * 1.01 + (K + 2) * R.U32 * mag + R.tiny(dt)
+        flat, out = new(1, T)
+        if ww is None:
+            fn(m["y"], invd, out, ws, residual=m["res"])
+        else:
+            fn(m["y"], invd, wd, out, ws, residual=m["res"])
+        R.check(out, ref, bound, "sum")
+        assert int(flat.isnan().sum()) == flat.numel() - T * H
+    ref, dwref, mag = R.combine_grad(v["d"], y, inv, w, U)
+    flat, dy = new(5, U)
+    dw = torch.empty(T, K, device="cuda")
+    M.combine_backward(m["d"], m["y"], invd, wd, dy, dw, ws)
+    R.check(dy[~pad.cuda()], ref[~pad], (R.half_step(dt) * 1.01 + R.U32) * ref[~pad].abs() + R.tiny(dt), "dy")
+    R.check(dw, dwref, (H + 2) * R.U32 * mag + 1e-30, "dw")
+    assert (dy[pad.cuda()] == SENTINEL).all() and int(flat.isnan().sum()) == flat.numel() - U * H
+    assert M.get_error(ws) == M.OK
+
+
 def test_combine_gradient_against_differences(M):
     # fp32 rows: the directional derivative of <c, combine(y, w)> by central differences of the kernel itself.
     # The function is linear in y and in w, so the difference has no truncation error, only rounding.
