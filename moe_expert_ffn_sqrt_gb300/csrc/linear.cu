@@ -29,7 +29,7 @@
 // Two kernels:
 //  * linear_pair_kernel: a CTA pair per 256 x 256 tile (cta_group::2, each CTA half of either operand's rows in
 //    shared memory), persistent, two accumulators so that one tile's epilogue runs under the next tile's MMAs.
-//  * linear_split_kernel: for dense problems with too few tiles to fill the GPU: a cluster of up to four
+//  * linear_split_kernel: for problems with too few tiles to fill the GPU: a cluster of up to four
 //    CTAs per tile of 128 or 64 columns, each with a slice of the sum; the slices meet in shared memory.  Few
 //    rows are the rule there, so the weights (or, for dw, x's columns) are on M and the rows on N.
 #include <atomic>
@@ -62,7 +62,7 @@ constexpr int kSplitSmem = 1024 + kSplitRing + 512;
 static_assert(kPairSmem <= 227 * 1024 && kSplitSmem <= 227 * 1024, "shared memory budget");
 static_assert(kSplitRing >= kLinBI * kLinBJ * 4 + kLinEpiWarps * 2048, "the slices' sums and the pieces fit the ring");
 
-// The GELU forward is a mode of its own: erfc over a whole piece takes registers that the others need not pay.
+// The GELU forward is a mode of its own: its polynomial's registers cost the others 5% where the epilogue counts.
 enum LinMode { kLinFwd = 0, kLinFwdGated = 1, kLinDx = 2, kLinDw = 3, kLinFwdGelu = 4 };
 
 struct LinArgs {
@@ -222,8 +222,27 @@ __device__ __forceinline__ float2 lin_unpack(uint32_t w, int f16) {
 }
 
 __device__ __forceinline__ float lin_silu(float v) { return __fdividef(v, 1.f + __expf(-v)); }
-// v Phi(v); erfc keeps its relative accuracy in the negative tail, where 1 + erf would cancel
-__device__ __forceinline__ float lin_gelu(float v) { return 0.5f * v * erfcf(v * -0.70710678118654752f); }
+// Phi(-a), the normal distribution's tail, for 0 <= a <= 30, and e^(-a^2 / 2): Phi(-a) e^(a^2 / 2) is smooth in
+// t = 1 / (1 + 0.36 a) and vanishes with it, so t times a polynomial of degree 6 in t, fitted for the least relative
+// error (9e-7, for a up to 14; beyond it the exponential underflows).  (erfcf, which has more digits than a 16-bit
+// result: 155 us for 16384 x 4096 outputs of a product over 64, so 86.)
+__device__ __forceinline__ float normal_tail(float a, float& e) {
+  const float t = __fdividef(1.f, fmaf(0.36f, a, 1.f));
+  e = __expf(-0.5f * a * a);
+  float q = fmaf(t, 0.047056060f, -0.179763914f);
+  q = fmaf(t, q, 0.180952996f);
+  q = fmaf(t, q, 0.026549993f);
+  q = fmaf(t, q, 0.139719039f);
+  q = fmaf(t, q, 0.141772494f);
+  q = fmaf(t, q, 0.143713042f);
+  return t * q * e;
+}
+// v Phi(v) = max(v, 0) - |v| Phi(-|v|), which cancels nowhere
+__device__ __forceinline__ float lin_gelu(float v) {
+  float e;
+  const float a = fabsf(v) > 30.f ? 30.f : fabsf(v);   // (infinity times the tail's 0; keeps NaN)
+  return (v < 0.f ? 0.f : v) - a * normal_tail(a, e);
+}
 
 // The epilogue works on pieces of 32 accumulator lanes x 32 columns per
 // warp, held as four 8-column groups of 8x8 fragments: v[8n + 2h + k] of thread t is lane t/4 + 8h,
@@ -935,8 +954,51 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 
 // ------------------------------------------------------------------------------------------
 
-// Dense problems with few tiles: cluster c computes tile c, its CTA r the r-th of S slices of the sum.  A tile
-// may use 64 of the MMA's 128 lanes: the others multiply what the ring happens to hold and are not read.
+// The expert, its segment and the first row of tile tj of all experts' tiles of a.bj rows.  One warp; false: there are
+// not that many.  A segment that would leave the buffers is an error and is cut.
+__device__ __forceinline__ bool lin_find_tile(const LinArgs& a, int tj, int lane, LinTile& t) {
+  int row = 0, tiles = 0;
+  for (int e0 = 0; e0 < a.E; e0 += 32) {
+    const int e = e0 + lane;
+    int c = e < a.E ? __ldg(a.counts + e) : 0;
+    if (c < 0 || c > a.rows) {
+      record_error(a.status, kDevErrIndex);
+      c = c < 0 ? 0 : a.rows;
+    }
+    const int padded = (c + a.align - 1) / a.align * a.align, nt = (c + a.bj - 1) / a.bj;
+    int s = padded, n = nt;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int os = __shfl_up_sync(0xffffffffu, s, d), on = __shfl_up_sync(0xffffffffu, n, d);
+      if (lane >= d) {
+        s = min(s + os, 0x3fffffff);
+        n = min(n + on, 0x3fffffff);
+      }
+    }
+    const int start = min(row + s - padded, 0x3fffffff), first = min(tiles + n - nt, 0x3fffffff);
+    if (c > 0 && start + c > a.rows) {
+      record_error(a.status, kDevErrIndex);
+      c = max(a.rows - start, 0);
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, tj >= first && tj - first < nt);
+    if (hit) {
+      const int src = __ffs(static_cast<int>(hit)) - 1;
+      t.e = e0 + src;
+      t.row0 = __shfl_sync(0xffffffffu, start, src);
+      t.cnt = __shfl_sync(0xffffffffu, c, src);
+      t.j0 = (tj - __shfl_sync(0xffffffffu, first, src)) * a.bj;
+      return t.j0 < t.cnt;
+    }
+    row = min(row + __shfl_sync(0xffffffffu, s, 31), 0x3fffffff);
+    tiles = min(tiles + __shfl_sync(0xffffffffu, n, 31), 0x3fffffff);
+  }
+  return false;
+}
+
+// Few tiles: cluster c computes tile c, its CTA r the r-th of S slices of the sum.  A tile may use 64 of the MMA's
+// 128 lanes: the others multiply what the ring happens to hold and are not read.  Experts (forward and input
+// gradient): tiles of a.bj rows, as many clusters as there can be tiles; rows past an expert's end are other
+// columns of the product, which are not stored.
 template <int MODE, int S>
 __global__ void __launch_bounds__(kLinThreads, 1)
     linear_split_kernel(const __grid_constant__ CUtensorMap mapa, const __grid_constant__ CUtensorMap mapb, const LinArgs a) {
@@ -976,10 +1038,22 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   LinTile t;
   t.e = 0;
   t.row0 = 0;
-  t.cnt = a.rows;
+  t.cnt = MODE == kLinDw ? a.j_ext : a.rows;
   t.it = tile % a.n_it;
   t.j0 = tile / a.n_it * a.bj;
-  t.ncols = min(a.bj, (MODE == kLinDw ? a.j_ext : a.rows) - t.j0);
+  if (MODE != kLinDw && a.counts != nullptr) {
+    __shared__ LinTile found;
+    if (warp == 2) {
+      if (!lin_find_tile(a, tile / a.n_it, lane, t)) t.cnt = t.j0 = 0;
+      if (lane == 0) found = t;
+    }
+    __syncthreads();
+    t.e = found.e;
+    t.row0 = found.row0;
+    t.cnt = found.cnt;
+    t.j0 = found.j0;
+  }
+  t.ncols = min(a.bj, t.cnt - t.j0);          // 0 (experts): no tile for this cluster
   t.slabs = ((MODE == kLinDw ? a.rows : a.q_ext) + kLinSlab - 1) / kLinSlab;
   const int i0 = t.it * (MODE == kLinFwdGated ? a.lanes / 2 : a.lanes);
   const int s0 = static_cast<int>(static_cast<long long>(t.slabs) * slice / S);          // this CTA's slabs [s0, s1),
@@ -989,7 +1063,9 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   const int stage = static_cast<int>(a_bytes + ((b_bytes + 1023) & ~1023u));
   const uint32_t piece = smem_u32(smem) + kLinBI * kLinBJ * 4 + static_cast<uint32_t>(warp >= 2 ? warp - 2 : 0) * kPieceBytes;
 
-  if (warp == 0) {
+  if (t.ncols <= 0) {
+    // nothing to do but meet the cluster below
+  } else if (warp == 0) {
     int st = 0;
     uint32_t ph = 0;
     bool ok = true;
@@ -1070,7 +1146,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   if (S > 1) {
     const bool ok = *abort_flag == 0;
     cluster_sync();
-    if (warp >= 2 && ok && (warp & 3) * 32 < a.lanes) {
+    if (t.ncols > 0 && warp >= 2 && ok && (warp & 3) * 32 < a.lanes) {
       const int q = warp & 3, par = (warp - 2) >> 2;
       const int w = ((t.ncols + S - 1) / S + 7) & ~7, cb = min(slice * w, t.ncols), ce = min(cb + w, t.ncols);
       lin_drain<MODE>(a, t, i0, cb, ce, ClusterSums<S>{smem_u32(reinterpret_cast<float4*>(smem) + q * 32 + lane), slice},
@@ -1145,58 +1221,79 @@ bool map_mn_major(CUtensorMap* m, int f16, const void* p, long long cols, long l
   return lin_map(m, f16, p, 4, d, s, b);
 }
 
-// How a problem runs.  j: rows of the output (dense) or of the row buffers (experts).
+// How a problem runs.
 struct LinPlan {
   bool pair;
   int lanes;
   int split, bj, stages, grid, b_box;
 };
 
-// Dense problems take the cheapest way to run them by a count of cycles that was fitted to measurements of every
-// way (pair; split with 128 or 64 lanes and 1, 2 or 4 slices) over 132 shapes of 1 to 4096 rows, 256 to 7168
+// The cheapest way to run a problem by a count of cycles that was fitted to measurements of every
+// way (pair; split with 128 or 64 lanes and 1, 2 or 4 slices) over 132 dense shapes of 1 to 4096 rows, 256 to 7168
 // columns and terms: the way it picks is on average 0.2% off the fastest one, 4% at most.
 //  * pair: 76 tiles at a time, 420 a slab, 1000 and 16 per row j of the epilogue at the end;
 //  * split: 590 a slab (the MMA feeds its 128 rows of A at one a cycle, so short tiles are no cheaper), 5200 for each
 //    further round of CTAs; slices halve or quarter that for a meeting of 1900 + 250 S and 27 per row j and 128
 //    lanes for the partial sums over the cluster.
-// (Clusters of eight do not fill the GPU: 16 of them took two rounds.)  i_cols: output columns, gated: of y;
-// experts: 0 for a dense problem.
-LinPlan lin_plan(int experts, int i_cols, bool gated, long long j, long long q, bool b_mn) {
+// (Clusters of eight do not fill the GPU: 16 of them took two rounds.)
+// Experts' rows are not known here: taken are those of buffers that the experts' padding fills up, about evenly
+// spread, in split tiles of twice an expert's share.  Fitted to 89 shapes of 2 to 64 experts and 1 to 7000 rows (1.8%
+// from the fastest way on average, 24% faster than the pair kernel alone): pair 590 a slab, 6000 at the start and 300
+// an expert, whose segments every CTA lays out; split 10000 for a further round and 3000 for each round of clusters that
+// there might be tiles for.
+// i_cols: output columns, gated: of y; j: rows of the output (dense) or of the row buffers; whole: the pair kernel in
+// any case (experts' weight gradient).
+LinPlan lin_plan(const LinearShape& s, int i_cols, bool gated, long long j, long long q, bool b_mn, bool whole) {
   LinPlan p{};
-  const int sms = num_sms(), pairs = sms / 2;
+  const int sms = num_sms(), pairs = sms / 2, E = s.counts ? s.E : 0;
   const long long slabs = (q + kLinSlab - 1) / kLinSlab;
   p.lanes = kLinBI;
   p.split = 1;
-  p.bj = lin_tile_rows(static_cast<int>(j), kPairStep);
-  const int pair_i = gated ? kLinBI : 2 * kLinBI;
-  const long long tiles = (i_cols + pair_i - 1) / pair_i * ((j + p.bj - 1) / p.bj);
   p.pair = true;
-  if (experts) {
+  const int pair_i = gated ? kLinBI : 2 * kLinBI;
+  const long long n_it = (i_cols + pair_i - 1) / pair_i;
+  long long rows = j, live = 1, tiles, most = 0;       // live experts, tiles of rows of all of them, at most
+  int bj = lin_tile_rows(static_cast<int>(j), kSplitStep);
+  if (E) {
+    p.bj = kLinBJ;                                     // (the weight gradient's goes by N, as for a dense problem)
+    if (whole) p.bj = lin_tile_rows(static_cast<int>(j), kPairStep);
     p.grid = 2 * pairs;
-    return p;
+    if (whole) return p;
+    rows = j - static_cast<long long>(E) * (s.align - 1);
+    if (rows < 1) rows = 1;
+    live = rows < E ? rows : E;
+    const long long twice = (2 * rows + live - 1) / live;
+    bj = twice >= kLinBJ ? kLinBJ : static_cast<int>((twice + kSplitStep - 1) / kSplitStep * kSplitStep);
+    if (bj < 2 * kSplitStep) bj = 2 * kSplitStep;
+    const long long mean = (rows + kLinBJ / 2 * live) / kLinBJ;   // of sum_e ceil(rows_e / 256)
+    tiles = n_it * (mean > live ? mean : live);
+    most = j / bj + (j < E ? j : E);
+  } else {
+    p.bj = lin_tile_rows(static_cast<int>(j), kPairStep);
+    tiles = n_it * ((j + p.bj - 1) / p.bj);
+    p.grid = 2 * static_cast<int>(tiles < pairs ? tiles : pairs);
   }
-  long long best = (tiles + pairs - 1) / pairs * slabs * 420 + 1000 + 16 * p.bj;
-  const int bj = lin_tile_rows(static_cast<int>(j), kSplitStep);
-  const long long nj = (j + bj - 1) / bj;
+  const long long slab = E ? 590 : 420, more = E ? 10000 : 5200;
+  long long best = (tiles + pairs - 1) / pairs * slabs * slab + (E ? 6000 + 300 * E : 1000 + 16 * p.bj);
+  long long nj = E ? (2 * rows + live * bj) / (2 * bj) : (j + bj - 1) / bj;
+  if (nj < live) nj = live;
   for (int lanes = 128; lanes >= 64; lanes /= 2) {
     const int tile_i = gated ? lanes / 2 : lanes;
-    const long long t1 = (i_cols + tile_i - 1) / tile_i * nj;
+    const long long it = (i_cols + tile_i - 1) / tile_i, t1 = it * nj, all = E ? it * most : t1;
     for (int S = 1; S <= 4 && slabs >= 2 * S; S *= 2) {
-      const long long rounds = (t1 * S + sms - 1) / sms;
-      long long cost = rounds * ((slabs + S - 1) / S * 590 + 2 * bj / S) + 5200 * (rounds - 1);
+      if (all * S > 0x3fffffff) continue;
+      const long long rounds = (t1 * S + sms - 1) / sms, spare = ((all - t1) * S + sms - 1) / sms;
+      long long cost = rounds * ((slabs + S - 1) / S * 590 + 2 * bj / S) + more * (rounds - 1) + (spare > 0 ? 3000 * spare : 0);
       if (S > 1) cost += rounds * (1900 + 250 * S + 27LL * bj * lanes / 128 * (S - 1) / S);
       if (cost >= best) continue;
       best = cost;
       p.pair = false;
       p.lanes = lanes;
       p.split = S;
-      p.grid = static_cast<int>(t1) * S;
+      p.grid = static_cast<int>(all) * S;
     }
   }
-  if (p.pair) {
-    p.grid = 2 * static_cast<int>(tiles < pairs ? tiles : pairs);
-    return p;
-  }
+  if (p.pair) return p;
   p.bj = bj;
   p.b_box = bj;
   const int b_bytes = b_mn ? (bj + 63) / 64 * 8192 : bj * 128;
@@ -1294,12 +1391,14 @@ cudaError_t expert_maps(const LinearShape& p, const CUtensorMap& m0, const CUten
   return launch_pdl(expert_maps_kernel, dim3(1), dim3(kLinMaxE), 0, stream, m0, m1, p.counts, p.E, p.align, p.rows, emaps);
 }
 
-// Forward and input gradient: whether a tile's rows past its expert's end are to read as zeros instead of the next
-// expert's rows.  The result is the same; zeros are not fetched and cost the tensor core less power, which a
-// long run is bound by (32 experts of about 400 rows, back to back: forward 571 -> 563 us, both gradients
-// 597 -> 581); with few rows the weights' way from HBM is all there is, and the maps' launch would only add its
-// 2 us.
-bool expert_rows_apart(const LinearShape& p) { return p.counts && p.rows >= 64LL * p.E; }
+// Forward and input gradient in the pair kernel: whether a tile's rows past its expert's end are to read as zeros
+// instead of the next expert's rows.  The result is the same; zeros are not fetched and cost the tensor core less
+// power, which a long run is bound by (32 experts of about 400 rows, back to back: forward 571 -> 563 us, both
+// gradients 597 -> 581).  The maps' launch adds 2 us (and 3 on the host), so only where the product takes about 100 us
+// at least and it is not the weights' way from HBM that does.
+bool expert_rows_apart(const LinearShape& p, const LinPlan& pl) {
+  return p.counts && pl.pair && p.rows >= 64LL * p.E && static_cast<double>(p.rows) * p.N * p.K >= 1e11;
+}
 
 }  // namespace
 
@@ -1317,7 +1416,7 @@ cudaError_t launch_linear(const LinearShape& p, RowsView x, const uint16_t* w, c
   a.res = static_cast<const uint16_t*>(res.ptr);
   a.ldr = res.ld;
   a.bias = bias;
-  const LinPlan pl = lin_plan(p.counts ? p.E : 0, a.i_ext, gated, p.rows, p.K, false);
+  const LinPlan pl = lin_plan(p, a.i_ext, gated, p.rows, p.K, false, false);
   const int tile_i = lin_tile_i(pl, gated);
   a.n_it = (a.i_ext + tile_i - 1) / tile_i;
   CUtensorMap ma = {};
@@ -1334,7 +1433,7 @@ cudaError_t launch_linear(const LinearShape& p, RowsView x, const uint16_t* w, c
   }
   if (!ok || !map_rows(mb, pl, p.f16, x, p.K, p.rows)) return cudaErrorInvalidValue;
   const CUtensorMap* emaps = nullptr;
-  if (expert_rows_apart(p)) {
+  if (expert_rows_apart(p, pl)) {
     const cudaError_t err = expert_maps(p, mb.m[0], mb.m[1], maps, &emaps, stream);
     if (err != cudaSuccess) return err;
   }
@@ -1352,7 +1451,7 @@ cudaError_t launch_linear_dx(const LinearShape& p, RowsView dz, const uint16_t* 
   a.ldo = dx.ld;
   a.res = static_cast<const uint16_t*>(res.ptr);
   a.ldr = res.ld;
-  const LinPlan pl = lin_plan(p.counts ? p.E : 0, p.K, false, p.rows, p.N, false);
+  const LinPlan pl = lin_plan(p, p.K, false, p.rows, p.N, false, false);
   const int tile_i = lin_tile_i(pl, false);
   a.n_it = (p.K + tile_i - 1) / tile_i;
   CUtensorMap ma = {};
@@ -1362,7 +1461,7 @@ cudaError_t launch_linear_dx(const LinearShape& p, RowsView dz, const uint16_t* 
       !map_rows(mb, pl, p.f16, dz, p.N, p.rows))
     return cudaErrorInvalidValue;
   const CUtensorMap* emaps = nullptr;
-  if (expert_rows_apart(p)) {
+  if (expert_rows_apart(p, pl)) {
     const cudaError_t err = expert_maps(p, mb.m[0], mb.m[1], maps, &emaps, stream);
     if (err != cudaSuccess) return err;
   }
@@ -1376,7 +1475,7 @@ cudaError_t launch_linear_dw(const LinearShape& p, RowsView dz, RowsView x, uint
   a.j_ext = p.N;
   a.out = dw;
   a.ldo = p.K;
-  const LinPlan pl = lin_plan(p.counts ? p.E : 0, p.K, false, p.N, p.rows, true);
+  const LinPlan pl = lin_plan(p, p.K, false, p.N, p.rows, true, p.counts != nullptr);
   const int tile_i = lin_tile_i(pl, false);
   a.n_it = (p.K + tile_i - 1) / tile_i;
   CUtensorMap ma = {};
@@ -1410,16 +1509,11 @@ __device__ __forceinline__ float silu_grad(float z, float& silu) {
   return s * (1.f + z * (1.f - s));
 }
 
-// (v Phi(v))' = Phi(v) + v phi(v).  Phi by formula 7.1.26 of Abramowitz and Stegun's Handbook (Hastings):
-// erfc(x) = (a1 t + ... + a5 t^5) e^{-x^2}, t = 1 / (1 + p x), x >= 0, off by at most 1.5e-7; the exponential
-// is phi's own.  (With erfcf the pass is bound by its instructions: 25 us for 4096 x 2048 values.)
+// (v Phi(v))' = Phi(v) + v phi(v).  (With erfcf the pass is bound by its instructions: 25 us for 4096 x 2048 values.)
 __device__ __forceinline__ float gelu_grad(float v) {
-  const float x = fabsf(v) * 0.70710678118654752f;
-  const float t = __fdividef(1.f, fmaf(0.3275911f, x, 1.f));
-  const float e = __expf(-x * x);
-  const float p = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f), 0.254829592f);
-  const float tail = 0.5f * p * e;                   // Phi(-|v|)
-  return (v >= 0.f ? 1.f - tail : tail) + v * 0.39894228040143268f * e;
+  float e;
+  const float a = fabsf(v) > 30.f ? 30.f : fabsf(v), tail = normal_tail(a, e), vphi = a * 0.39894228040143268f * e;
+  return v < 0.f ? tail - vphi : 1.f - tail + vphi;
 }
 
 template <class T>
