@@ -154,6 +154,47 @@ def test_linear_large(M, rows, N, K, act):
     assert M.get_error(ws) == M.OK
 
 
+UNEVEN = [0 if e % 5 == 3 else 1 + (e * 37) % 90 for e in range(70)]
+
+
+@pytest.mark.parametrize("counts,align,N,K,act", [
+    ([20, 0, 9], 16, 64, 4096, "silu"), ([20, 0, 9], 64, 4096, 72, "none"),            # long sums, few tiles
+    ([33, 1, 0, 64, 500, 7, 0, 2], 8, 320, 1400, "swiglu"), (UNEVEN, 4, 96, 328, "gelu"), (UNEVEN, 64, 208, 200, "swiglu"),
+    ([1500, 0, 2, 1], 1, 176, 1032, "relu"), ([0] * 40 + [5] + [0] * 23, 256, 96, 264, "none"),   # one expert has them
+    ([500, 610, 0, 433, 256, 512, 1, 300, 470, 555, 128, 390], 32, 1536, 648, "swiglu"),
+    ([310, 200, 0, 513, 256, 333, 640, 301], 16, 4096, 9640, "swiglu")])               # long enough for maps of its own
+def test_experts_every_way(M, counts, align, N, K, act):
+    # the reference in float64 on the GPU; padding rows are NaN
+    E, dt = len(counts), BF
+    rows = sum(-(-c // align) * align for c in counts)
+    g = torch.Generator(device="cuda").manual_seed(rows + N)
+    rand = lambda *s: torch.randn(*s, generator=g, device="cuda")
+    cols = N // 2 if act == "swiglu" else N
+    x, w, bias, res = rand(rows, K).to(dt), (rand(E, N, K) * K ** -0.5).to(dt), rand(E, N), rand(rows, cols).to(dt)
+    live = torch.zeros(rows, dtype=torch.bool, device="cuda")
+    for _, r, c in R.segments(counts, align, rows):
+        live[r:r + c] = True
+    dy, dres = rand(rows, cols).to(dt), rand(rows, K).to(dt)
+    for t in (x, res, dy, dres):
+        t[~live] = float("nan")
+    kw = dict(act=act, expert_counts=torch.tensor(counts, dtype=torch.int32, device="cuda"), align=align)
+    ws = M.new_workspace_linear(rows, N, K, E, act)
+    y = torch.full((rows, cols), SENTINEL, dtype=dt, device="cuda")
+    z = torch.full((rows, N), SENTINEL, dtype=dt, device="cuda")
+    M.linear(x, w, y, ws, bias=bias, residual=res, z=z, **kw)
+    dx = torch.full((rows, K), SENTINEL, dtype=dt, device="cuda")
+    M.linear_backward(dy, x, w, ws, dx=dx, z=None if act == "none" else z, dx_residual=dres, **kw)
+    assert M.get_error(ws) == M.OK
+    for e, r, c in R.segments(counts, align, rows):
+        s = slice(r, r + c)
+        yr, ey, zr, ez = R.linear(x[s], w[e], bias[e], act, res[s], dt)
+        R.check(y[s], yr.cpu(), ey.cpu(), f"y of expert {e}")
+        R.check(z[s], zr.cpu(), ez.cpu(), f"z of expert {e}")
+        (a, ea), _, _ = R.linear_grad(dy[s], x[s], w[e], z[s], act, dres[s], dt)
+        R.check(dx[s], a.cpu(), ea.cpu(), f"dx of expert {e}")
+    assert (y[~live] == SENTINEL).all() and (z[~live] == SENTINEL).all() and (dx[~live] == SENTINEL).all()
+
+
 def test_special_values(M):
     # relu keeps NaN, large negative arguments vanish, infinities stay where they are
     x = torch.eye(8, dtype=BF)
