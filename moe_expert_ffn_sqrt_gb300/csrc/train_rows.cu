@@ -302,7 +302,8 @@ __global__ void __launch_bounds__(kRowThreads, ALIGNED && sizeof(typename T::raw
 // piece of a row is on its way: each 32 pairs' experts are counted by a warp's matches (hist[chunk][expert], 16
 // bits), then summed over the chunks before, so that a pair's rank is its chunk's sum and its place among the
 // chunk's matches.  The index arrays are written by the first CTA, padding entries by all.  One warp per (pair,
-// 1 KB of its row).  (Index arrays by launches of their own: 10 us for 384 pairs, 20 for 1020.)
+// 1 KB of its row).  8 tokens of 7168 bf16 columns, 256 experts, K = 6: 3.0 us, 42 tokens 4.1.  (Index arrays by
+// launches of their own: 10 us for 384 pairs, 20 for 1020.)
 // From 257 to 1024 pairs the same kernel, with more threads and no rows to move, only writes the index arrays
 // (every CTA of a copy that fills the GPU working them out would take longer than a launch).
 constexpr int kFewPairs = 256, kLayoutPairs = 1024;
