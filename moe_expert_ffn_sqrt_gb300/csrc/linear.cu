@@ -43,7 +43,8 @@ namespace moe {
 
 namespace {
 
-constexpr int kLinEpiWarps = 8;             // two per TMEM lane quarter, on alternate pieces of 32 columns
+constexpr int kLinEpiWarps = 12;            // three per TMEM lane quarter, each on every third piece of 32 columns
+constexpr int kLinHop = 32 * kLinEpiWarps / 4;      // from one of a warp's pieces to its next
 constexpr int kLinThreads = 64 + 32 * kLinEpiWarps;   // warp 0 loads, 1 MMA, the others drain
 constexpr int kLinBI = 128;                 // rows of A per CTA (accumulator lanes)
 constexpr int kLinBJ = 256;                 // rows of B per tile (MMA N, accumulator columns), at most
@@ -225,7 +226,7 @@ __device__ __forceinline__ float lin_silu(float v) { return __fdividef(v, 1.f + 
 // Phi(-a), the normal distribution's tail, for 0 <= a <= 30, and e^(-a^2 / 2): Phi(-a) e^(a^2 / 2) is smooth in
 // t = 1 / (1 + 0.36 a) and vanishes with it, so t times a polynomial of degree 6 in t, fitted for the least relative
 // error (9e-7, for a up to 14; beyond it the exponential underflows).  (erfcf, which has more digits than a 16-bit
-// result: 155 us for 16384 x 4096 outputs of a product over 64, so 86.)
+// result: 155 us for 16384 x 4096 outputs of a product over 64, so 82.)
 __device__ __forceinline__ float normal_tail(float a, float& e) {
   const float t = __fdividef(1.f, fmaf(0.36f, a, 1.f));
   e = __expf(-0.5f * a * a);
@@ -288,7 +289,7 @@ struct ZeroSums {
     for (int j = 0; j < 32; ++j) v[j] = 0.f;
   }
 };
-// A slice's sums in shared memory: value i of 8-column group g of epilogue thread t (of 128 of its parity) is
+// A slice's sums in shared memory: value i of 8-column group g of epilogue thread t (of 128, one per lane) is
 // float 4 * ((2g + i / 4) * 128 + t) + i % 4.  S slices, read from the CTA's own on round the cluster (so that
 // they do not all read one CTA at a time) and added in that order, which is fixed by the column.
 template <int S>
@@ -424,7 +425,7 @@ __device__ __forceinline__ void lin_act(const LinArgs& a, const float (&v)[32], 
 
 // Rows on M: the warp's 32 lanes are output rows [jw, jw + 32) of tile t, and accumulator columns [cb, ce)
 // output columns from i0 + cb on (gated forward: columns 16m + 0..7 are the gate columns of y's columns
-// i0 + 8m .., columns 16m + 8..15 their up columns).  Every second piece of columns from piece `par` on.
+// i0 + 8m .., columns 16m + 8..15 their up columns).  Every third piece of columns from piece `par` on.
 template <int MODE>
 __device__ __forceinline__ void lin_drain_rows(const LinArgs& a, const LinTile& t, int i0, int jw, int cb, int ce,
                                                uint32_t acc, int par, int lane, uint32_t stage, const CUtensorMap* mapo) {
@@ -445,14 +446,15 @@ __device__ __forceinline__ void lin_drain_rows(const LinArgs& a, const LinTile& 
     const int col = col_of(c) + rows.unit * 8;
     rows.fetch(res, a.res + jr * a.ldr + col, a.ldr, col < a.i_ext, left);
   };
+  const int c_acc = cb;       // accumulator column 0
   cb += 32 * par;
   if (has_res && cb < ce) fetch(cb);
 #pragma unroll 1
-  for (int c0 = cb; c0 < ce; c0 += 64) {
+  for (int c0 = cb; c0 < ce; c0 += kLinHop) {
     const int col0 = col_of(c0);
     if (col0 >= a.i_ext) break;
     float v[32];
-    sums(c0 - (cb & ~63), 32, v);
+    sums(c0 - c_acc, 32, v);
     piece_free(lane);
     if (kFwd) {
       if (a.bias) {
@@ -506,7 +508,7 @@ __device__ __forceinline__ void lin_drain_rows(const LinArgs& a, const LinTile& 
           o[8 * m + 2 * h + 1] += x.y;
         }
       }
-      if (c0 + 64 < ce) fetch(c0 + 64);
+      if (c0 + kLinHop < ce) fetch(c0 + kLinHop);
       __syncwarp();
     }
 #pragma unroll
@@ -526,7 +528,7 @@ __device__ __forceinline__ void lin_drain_rows(const LinArgs& a, const LinTile& 
 
 // Rows on N: turns the sums of output rows [j0 + cb, j0 + ce) of tile t into outputs (cb a multiple of 8); this
 // warp has lanes 32q .. of the CTA's output columns, which start at column i0 (gated forward: of y), and
-// every second piece of rows from piece `par` on.  stage: the warp's piece in shared memory.
+// every third piece of rows from piece `par` on.  stage: the warp's piece in shared memory.
 template <int MODE, class Sums>
 __device__ __forceinline__ void lin_drain(const LinArgs& a, const LinTile& t, int i0, int cb, int ce, const Sums& sums, int q,
                                           int par, int lane, uint32_t stage, const CUtensorMap* mapo = nullptr) {
@@ -557,7 +559,7 @@ __device__ __forceinline__ void lin_drain(const LinArgs& a, const LinTile& t, in
   cb += 32 * par;
   if (has_res) rows.fetch(res, a.res + (jr + cb) * a.ldr + col, a.ldr, live, ce - cb);
 #pragma unroll 1
-  for (int c0 = cb; c0 < ce; c0 += 64) {
+  for (int c0 = cb; c0 < ce; c0 += kLinHop) {
     const int left = ce - c0;
     float v[32];
     sums(c0, left, v);
@@ -610,7 +612,7 @@ __device__ __forceinline__ void lin_drain(const LinArgs& a, const LinTile& t, in
           o[8 * n + 2 * m + 1] += x.y;
         }
       }
-      if (c0 + 64 < ce) rows.fetch(res, a.res + (jr + c0 + 64) * a.ldr + col, a.ldr, live, left - 64);
+      if (c0 + kLinHop < ce) rows.fetch(res, a.res + (jr + c0 + kLinHop) * a.ldr + col, a.ldr, live, left - kLinHop);
       __syncwarp();
     }
 #pragma unroll
@@ -714,15 +716,19 @@ __global__ void __launch_bounds__(kLinMaxE) expert_maps_kernel(const __grid_cons
   asm volatile("fence.proxy.tensormap::generic.release.gpu;" ::: "memory");
 }
 
-// Bound by the tensor core and the operands' way into shared memory alike: a slab of 64 terms takes 512 cycles of
-// MMAs, and either CTA's 32 KB of it at the 60 bytes a cycle that an SM takes in 546.  8192^3 bf16 597 us (1.84
+// Bound by the tensor core and shared memory alike: a slab of 64 terms takes 512 cycles of MMAs, in which either CTA's
+// 32 KB of it are copied in and read by the MMAs, 128 bytes a cycle, all that an SM's shared memory moves (measured:
+// 546 to 590 cycles a slab).  An epilogue's pieces go through it too, 128 KB a tile: with six slabs to a tile (experts'
+// weight gradients) a slab takes 750.  8192^3 bf16 597 us (1.84
 // PFLOP/s, 97% of the measured rate of library products); 4096^3 82 us (1.68; 256 tiles on 76 pairs leave 16% of the
 // last round empty, and the tensor core is busy for 86% of the SMs' active cycles); 4096 x 7168 over 2048 with bias and
 // residual 79 us; 12288 rows of 32 experts, 4096 x 7168, SwiGLU 490 to 590 us by the box's power limit, 16% of it for
 // the rows that fill their tiles up.
 // Tried and not kept: tiles claimed from a counter instead of dealt out (both gradients of the 32 experts 585 -> 607 us);
-// two pieces per epilogue warp and five stages (16384 x 4096 over 64 36 -> 32 us, but both gradients of the 32
-// experts 562 -> 586); the last round's dense tiles in halves (1 to 4%, lost in the noise).
+// two pieces per epilogue warp in turn (within 2% either way); pieces of two warps as one copy of 128-byte rows
+// (16384 x 4096 over 64 36 -> 41 us); the last round's dense tiles in halves (1 to 4%, lost in the noise).
+// With sums below about 512 terms the epilogue is the longest way, 500 cycles a piece: 16384 x 4096 outputs over 64
+// 34.6 us, with a residual 74, SiLU 54, GELU 82 (with two warps per quarter 36, 84, 60 and 86).
 // mapa: map of the operand of the output's columns (w, in the weight gradient x), mapsb: of its rows, mapo: of the
 // output, 32 x 32 pieces.  emaps: expert e's maps at 2e and 2e + 1 (see expert_maps_kernel), or null.
 template <int MODE>
@@ -1143,7 +1149,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         // every MMA has read the ring: it takes this slice's sums, as ClusterSums reads them
         float4* part = reinterpret_cast<float4*>(smem) + q * 32 + lane;
 #pragma unroll 1
-        for (int c0 = 32 * par; used && c0 < t.ncols; c0 += 64) {
+        for (int c0 = 32 * par; used && c0 < t.ncols; c0 += kLinHop) {
           float v[32];
           mine(c0, 32, v);
 #pragma unroll
