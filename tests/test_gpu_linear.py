@@ -237,6 +237,25 @@ def test_segments_past_the_buffers_are_reported(M):
         assert M.get_error(ws) == M.ERR_DEVICE_INDEX
 
 
+def test_segments_past_large_buffers_are_reported(M):
+    # the same where the tiles are many, and the rows that do exist are still right
+    rows, N, K = 2000, 4096, 512
+    x = torch.randn(rows, K, device="cuda").to(BF)
+    w = (torch.randn(4, N, K, device="cuda") * K ** -0.5).to(BF)
+    ws = M.new_workspace_linear(rows, N, K, 4)
+    for counts in ([500, 1000, 480, 700], [300, -7, 4000, 5], [2 ** 31 - 1, 2 ** 31 - 1, 7, 0]):
+        buf = torch.full((rows + 300, N), SENTINEL, dtype=BF, device="cuda")
+        c = torch.tensor(counts, dtype=torch.int32, device="cuda")
+        M.linear(x, w, buf[:rows], ws, expert_counts=c, align=16)
+        assert M.get_error(ws) == M.ERR_DEVICE_INDEX
+        assert (buf[rows:] == SENTINEL).all()
+        n = min(counts[0], rows)
+        yr, ey, _, _ = R.linear(x[:n], w[0], None, "none", None, BF)
+        R.check(buf[:n], yr.cpu(), ey.cpu(), "y of expert 0")
+        M.linear_backward(buf[:rows], x, w, ws, dx=torch.empty_like(x), dw=torch.empty_like(w), expert_counts=c, align=16)
+        assert M.get_error(ws) == M.ERR_DEVICE_INDEX
+
+
 def test_linear_on_another_stream_and_in_a_graph(M):
     rows, N, K = 96, 256, 320
     x = torch.randn(rows, K, device="cuda").to(BF)
