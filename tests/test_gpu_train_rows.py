@@ -44,6 +44,7 @@ CASES = [  # T, H, E, K, align, dtype, extra pitch
     (1111, 136, 16, 4, 1, HF, 0), (700, 7168, 64, 2, 32, BF, 0), (5, 264, 40, 32, 16, BF, 0), (40, 8200, 8, 3, 16, FP, 0),
     # around the borders between the ways to work the layout out (pairs and experts), wide odd rows
     (64, 72, 4, 4, 16, BF, 0), (65, 72, 256, 4, 16, BF, 0), (682, 40, 256, 6, 1, BF, 0), (683, 40, 256, 6, 64, HF, 0),
+    (341, 40, 64, 6, 16, BF, 0), (342, 40, 64, 6, 16, BF, 0), (256, 24, 512, 8, 64, FP, 0), (256, 24, 513, 8, 64, FP, 0),
     (128, 24, 1024, 8, 16, FP, 0), (129, 24, 1024, 8, 16, FP, 0), (300, 3001, 16, 2, 32, HF, 0), (90, 4099, 5, 5, 8, FP, 1),
 ]
 
