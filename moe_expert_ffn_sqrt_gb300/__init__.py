@@ -173,9 +173,13 @@ def _ptr(t, dtype=None, name="tensor"):
     return t.data_ptr()
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)      # (a torch without CUDA has neither)
+_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _stream():
     # the current stream's handle without building a Stream object (about 3 us less per call)
-    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return _raw_stream(_device())
 
 
 # ---------------------------------------------------------------------------------- sizes
@@ -572,35 +576,53 @@ def forward_batched_i8(hidden, w_gate, gate_bias, e_score_bias, I, K, max_tokens
 
 # ------------------------------------------------------------------ training operators
 
+# A call's checks and its launch take about as long on the host as its smallest kernels' whole latency chain, so the
+# checks below ask each tensor for what they need once, and look for the reason only when they fail.
+
 def _rows(t, dtype, shape, name):
     """A row-major matrix argument of this shape: any row pitch, unit column stride.  None: not given."""
     if t is None:
         return _NO_ROWS
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.shape == shape):
-        _wrong(t, dtype, shape, name)
-    n, cols = shape
-    pitch, unit = t.stride()
-    if n <= 1:            # the pitch is never used: the width, in whole 16-byte units, stands in
-        pitch = (cols + 7) // 8 * 8
-    if (unit != 1 and cols > 1) or pitch < cols:
-        raise ValueError(f"{name} must be row-major with unit column stride and rows that do not overlap")
-    return _Rows(t.data_ptr(), pitch)
+    try:
+        if t.dtype is dtype and t.shape == shape and t.is_cuda:
+            n, cols = shape
+            pitch, unit = t.stride()
+            if n <= 1:        # the pitch is never used: the width, in whole 16-byte units, stands in
+                pitch = (cols + 7) // 8 * 8
+            if (unit == 1 or cols <= 1) and pitch >= cols:
+                return _Rows(t.data_ptr(), pitch)
+    except AttributeError:    # not a tensor
+        pass
+    _wrong(t, dtype, shape, name, "row-major with unit column stride and rows that do not overlap")
 
 
 def _full(t, dtype, shape, name):
     """A contiguous argument of exactly this shape.  None: not given."""
     if t is None:
         return None
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.shape == shape and t.is_contiguous()):
-        _wrong(t, dtype, shape, name)
-    return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _wrong(t, dtype, shape, name, "contiguous")
 
 
-def _wrong(t, dtype, shape, name):
+def _wrong(t, dtype, shape, name, layout):
     _ptr(t if not isinstance(t, torch.Tensor) else t.reshape(-1)[:0], dtype, name)     # type, device
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
-    raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be {layout}")
+
+
+def _space(ws):
+    """A workspace argument."""
+    try:
+        if ws.dtype is torch.uint8 and ws.is_cuda and ws.is_contiguous():
+            return ws.data_ptr()
+    except AttributeError:
+        pass
+    return _ptr(ws, torch.uint8, "ws")
 
 
 def _dtype(t, name):
@@ -630,7 +652,7 @@ def dispatch(topk_ids, x, E, align, x_perm, sorted_token_ids, expert_ids, inv_pe
                               _full(sorted_token_ids, torch.int32, (U,), "sorted_token_ids"),
                               _full(expert_ids, torch.int32, (U,), "expert_ids"),
                               _full(inv_perm, torch.int32, (T, K), "inv_perm"), _full(m_sum, torch.int32, (1,), "m_sum"),
-                              _full(expert_counts, torch.int32, (E,), "expert_counts"), _ptr(ws, torch.uint8, "ws"),
+                              _full(expert_counts, torch.int32, (E,), "expert_counts"), _space(ws),
                               ws.numel(), _stream()), "moe_dispatch")
 
 
@@ -641,7 +663,7 @@ def dispatch_backward(dx_perm, inv_perm, dx, ws, residual=None):
     _check(lib().moe_dispatch_backward(_dtype(dx, "dx"), _rows(dx_perm, dt, (U, H), "dx_perm"),
                                        _full(inv_perm, torch.int32, (T, K), "inv_perm"),
                                        _rows(residual, dt, (T, H), "residual"), T, H, K, U, _rows(dx, dt, (T, H), "dx"),
-                                       _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream()), "moe_dispatch_backward")
+                                       _space(ws), ws.numel(), _stream()), "moe_dispatch_backward")
 
 
 def combine(y_perm, inv_perm, topk_w, out, ws, residual=None):
@@ -651,7 +673,7 @@ def combine(y_perm, inv_perm, topk_w, out, ws, residual=None):
     _check(lib().moe_combine(_dtype(out, "out"), _rows(y_perm, dt, (U, H), "y_perm"),
                              _full(inv_perm, torch.int32, (T, K), "inv_perm"), _full(topk_w, torch.float32, (T, K), "topk_w"),
                              _rows(residual, dt, (T, H), "residual"), T, H, K, U, _rows(out, dt, (T, H), "out"),
-                             _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream()), "moe_combine")
+                             _space(ws), ws.numel(), _stream()), "moe_combine")
 
 
 def combine_backward(dout, y_perm, inv_perm, topk_w, dy_perm, dtopk_w, ws):
@@ -663,7 +685,7 @@ def combine_backward(dout, y_perm, inv_perm, topk_w, dy_perm, dtopk_w, ws):
                                       _full(inv_perm, torch.int32, (T, K), "inv_perm"),
                                       _full(topk_w, torch.float32, (T, K), "topk_w"), T, H, K, U,
                                       _rows(dy_perm, dt, (U, H), "dy_perm"),
-                                      _full(dtopk_w, torch.float32, (T, K), "dtopk_w"), _ptr(ws, torch.uint8, "ws"),
+                                      _full(dtopk_w, torch.float32, (T, K), "dtopk_w"), _space(ws),
                                       ws.numel(), _stream()), "moe_combine_backward")
 
 
@@ -674,7 +696,7 @@ def route_backward(logits, topk_ids, topk_w, dtopk_w, score_fn, renormalize, dlo
     _check(lib().moe_route_backward(_full(logits, torch.float32, (T, E), "logits"), _full(topk_ids, torch.int32, TK, "topk_ids"),
                                     _full(topk_w, torch.float32, TK, "topk_w"), _full(dtopk_w, torch.float32, TK, "dtopk_w"),
                                     T, E, K, SCORE_FNS.get(score_fn, score_fn), int(renormalize), _dtype(dlogits, "dlogits"),
-                                    _full(dlogits, dlogits.dtype, (T, E), "dlogits"), _ptr(ws, torch.uint8, "ws"),
+                                    _full(dlogits, dlogits.dtype, (T, E), "dlogits"), _space(ws),
                                     ws.numel(), _stream()), "moe_route_backward")
 
 
@@ -707,7 +729,7 @@ def linear(x, w, y, ws, bias=None, act="none", residual=None, z=None, expert_cou
     _check(lib().moe_linear(_dtype(x, "x"), _rows(x, dt, (rows, K), "x"), _ptr(w, dt, "w"),
                             _full(bias, torch.float32, w.shape[:-1], "bias"), _rows(residual, dt, (rows, cols), "residual"),
                             act, _full(expert_counts, torch.int32, (E,), "expert_counts"), rows, N, K, E, align,
-                            _rows(y, dt, (rows, cols), "y"), _rows(z, dt, (rows, N), "z"), _ptr(ws, torch.uint8, "ws"),
+                            _rows(y, dt, (rows, cols), "y"), _rows(z, dt, (rows, N), "z"), _space(ws),
                             ws.numel(), _stream()), "moe_linear")
 
 
@@ -721,7 +743,7 @@ def linear_backward(dy, x, w, ws, dx=None, dw=None, dbias=None, act="none", z=No
                                      _full(expert_counts, torch.int32, (E,), "expert_counts"), rows, N, K, E, align,
                                      _rows(dx_residual, dt, (rows, K), "dx_residual"), _rows(dx, dt, (rows, K), "dx"),
                                      _full(dw, dt, w.shape, "dw"), _full(dbias, torch.float32, w.shape[:-1], "dbias"),
-                                     _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream()), "moe_linear_backward")
+                                     _space(ws), ws.numel(), _stream()), "moe_linear_backward")
 
 
 def selftest_wait_timeout(ws, mode):
