@@ -140,13 +140,15 @@ __global__ void __launch_bounds__(kRowThreads) scatter_any_rows_kernel(const typ
 
 // (Four CTAs per SM: with the registers for six the loads no longer go out together, 301 -> 452 us for 16384 x 7168,
 // K = 6; unaligned without a limit 144 us instead of 109 for 16384 x 2049, K = 4, and element by element 133.)
-template <class T, bool ALIGNED>
+// G packs of a token's row per thread and pass, 8 / G of its sorted rows at a time: with few rows per token more packs
+// keep as many loads on their way.  (Four packs do not fit the registers: K = 1, 63 us with two, 73 with four.)
+template <class T, bool ALIGNED, int G>
 __global__ void __launch_bounds__(kRowThreads, 4)
     sum_rows_kernel(const typename T::raw* __restrict__ y, long long ldy, const int32_t* __restrict__ inv,
                     const float* __restrict__ w, const typename T::raw* res, long long ldr, int T_, int K, int H, int U,
                     typename T::raw* out, long long ldo, int lanes, uint32_t* status) {
   constexpr int N = Pack<T>::N;
-  constexpr int kBatch = ALIGNED ? 8 : 2;            // rows on their way at a time
+  constexpr int kBatch = ALIGNED ? 8 / G : 2;        // rows on their way at a time
   __shared__ SlotTable slots;
   const int tokens = kRowThreads / lanes, slot = threadIdx.x / lanes;
   const int t0 = blockIdx.x * tokens, t = t0 + slot;
@@ -158,30 +160,44 @@ __global__ void __launch_bounds__(kRowThreads, 4)
   const float* ws = slots.w + slot * K;
   typename T::raw* o_row = out + t * ldo;
   if constexpr (ALIGNED) {
-    for (int c = (blockIdx.y * lanes + threadIdx.x % lanes) * N; c < H; c += gridDim.y * lanes * N) {
-      float acc[N];
+    const int step = gridDim.y * lanes * N;
+    for (int c = (blockIdx.y * lanes + threadIdx.x % lanes) * N; c < H; c += G * step) {
+      float acc[G][N];
+      Pack<T> rv[G];
 #pragma unroll
-      for (int i = 0; i < N; ++i) acc[i] = 0.f;
-      Pack<T> rv;
-      if (res) rv = load_pack<T>(res + t * ldr + c);
+      for (int g = 0; g < G; ++g) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) acc[g][i] = 0.f;
+        if (res && c + g * step < H) rv[g] = load_pack<T>(res + t * ldr + c + g * step);
+      }
       for (int k0 = 0; k0 < K; k0 += kBatch) {
-        Pack<T> v[kBatch];
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k)
-          if (k0 + k < K && rows[k0 + k] >= 0) v[k] = load_pack<T>(y + rows[k0 + k] * ldy + c);
+        Pack<T> v[kBatch][G];
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
-          if (k0 + k < K && rows[k0 + k] >= 0) {
-            const float wk = ws[k0 + k];
+          if (k0 + k >= K || rows[k0 + k] < 0) continue;
+          const typename T::raw* p = y + rows[k0 + k] * ldy + c;
 #pragma unroll
-            for (int i = 0; i < N; ++i) acc[i] = fmaf(wk, v[k].f(i), acc[i]);
-          }
+          for (int g = 0; g < G; ++g)
+            if (c + g * step < H) v[k][g] = load_pack<T>(p + g * step);
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          if (k0 + k >= K || rows[k0 + k] < 0) continue;
+          const float wk = ws[k0 + k];
+#pragma unroll
+          for (int g = 0; g < G; ++g)
+#pragma unroll
+            for (int i = 0; i < N; ++i) acc[g][i] = fmaf(wk, v[k][g].f(i), acc[g][i]);
         }
       }
-      Pack<T> o;
 #pragma unroll
-      for (int i = 0; i < N; ++i) o.set(i, res ? acc[i] + rv.f(i) : acc[i]);
-      store_pack<T>(o_row + c, o);
+      for (int g = 0; g < G; ++g) {
+        if (c + g * step >= H) continue;
+        Pack<T> o;
+#pragma unroll
+        for (int i = 0; i < N; ++i) o.set(i, res ? acc[g][i] + rv[g].f(i) : acc[g][i]);
+        store_pack<T>(o_row + c + g * step, o);
+      }
     }
   } else {
     const typename T::raw* y_end = y + static_cast<long long>(U - 1) * ldy + H;
@@ -474,7 +490,7 @@ int row_packs(int dt, int H, bool vec) {
 }
 // Threads per token for rows of n packs: the largest power of two that leaves each `packs` of them, as far as that
 // goes.  Several passes per thread hide what a CTA needs before its first one: sums of 4 rows of 2048 16-bit columns
-// for 16384 tokens, 4 passes 73 us, one 87; rows just past a power of two (2064 columns) 79 instead of 105.
+// for 16384 tokens, a pack at a time: 4 passes 73 us, one 87; rows just past a power of two (2064 columns) 79 instead of 105.
 int row_lanes(int n, int packs) {
   int l = kMinLanes;
   while (2 * l <= kRowThreads && 2 * l * packs <= n) l *= 2;
@@ -552,7 +568,11 @@ cudaError_t launch_sum_rows(int dt, RowsView y, const int32_t* inv, const float*
   const dim3 grid((T + tokens - 1) / tokens, row_cuts(T, lanes, n));
   return by_type(dt, vec, [&](auto e, auto aligned) {
     using E = decltype(e);
-    return launch_pdl(sum_rows_kernel<E, decltype(aligned)::value>, grid, dim3(kRowThreads), 0, stream, static_cast<const typename E::raw*>(y.ptr),
+    constexpr bool kVec = decltype(aligned)::value;
+    // two packs at a time for up to four rows (16384 x 4096 bf16 with a residual, K = 1: 103 -> 84 us,
+    // K = 4: 141 -> 128; K = 6 has rows enough), where a thread has two (72 columns, K = 4: 4.3 us, with two 5.3)
+    const auto kernel = kVec && K <= 4 && n >= 2 * lanes ? sum_rows_kernel<E, kVec, kVec ? 2 : 1> : sum_rows_kernel<E, kVec, 1>;
+    return launch_pdl(kernel, grid, dim3(kRowThreads), 0, stream, static_cast<const typename E::raw*>(y.ptr),
                       y.ld, inv, w, static_cast<const typename E::raw*>(res.ptr), res.ld, T, K, H, U,
                       static_cast<typename E::raw*>(out.ptr), out.ld, lanes, status);
   });
