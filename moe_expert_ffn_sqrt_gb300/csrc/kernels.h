@@ -1,5 +1,6 @@
 // Internal launchers shared between the kernel files and the C ABI layer.
 #pragma once
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -237,6 +238,20 @@ cudaError_t launch_linear_dw(const LinearShape& p, RowsView dz, RowsView x, uint
 int linear_bias_slices(int rows, int N, int E, int act);
 cudaError_t launch_act_grad(const LinearShape& p, RowsView dy, RowsView z, int act, RowsView dz, float* part, float* db,
                             uint32_t* status, cudaStream_t stream);
+
+// Lets a kernel use up to `bytes` of dynamic shared memory, once per device (`done`: a bit per device).  The limit is
+// the function's, not the launch's, so it is the most that any call needs: one that went by the call's own size could be
+// lowered by another host thread between this thread's setting it and its launch, which is then refused.
+inline cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<unsigned long long>& done) {
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (err == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
+  return err;
+}
 
 // Launches `kernel` with programmatic stream serialization: it may begin (up to its
 // grid_dependency_wait) while the stream's previous kernel finishes.

@@ -32,7 +32,6 @@
 //  * linear_split_kernel: for problems with too few tiles to fill the GPU: a cluster of up to four
 //    CTAs per tile of 128 or 64 columns, each with a slice of the sum; the slices meet in shared memory.  Few
 //    rows are the rule there, so the weights (or, for dw, x's columns) are on M and the rows on N.
-#include <atomic>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -1322,18 +1321,6 @@ LinPlan lin_plan(const LinearShape& s, int i_cols, bool gated, long long j, long
 
 // Output columns per tile (of a pair: both CTAs').
 int lin_tile_i(const LinPlan& p, bool gated) { return (p.pair ? 2 * p.lanes : p.lanes) / (gated ? 2 : 1); }
-
-// Lets a kernel use more than 48 KB of shared memory, once per device.
-cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<unsigned long long>& done) {
-  int dev = 0;
-  cudaError_t err = cudaGetDevice(&dev);
-  if (err != cudaSuccess) return err;
-  const unsigned long long bit = 1ull << (dev & 63);
-  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
-  err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (err == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
-  return err;
-}
 
 template <int MODE>
 cudaError_t lin_launch(const LinPlan& p, const CUtensorMap& ma, const LinMapsB& mb, const CUtensorMap* emaps, LinArgs a,

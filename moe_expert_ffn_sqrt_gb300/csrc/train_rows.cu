@@ -332,6 +332,8 @@ inline int few_chunks(int pairs) { return (pairs + 31) / 32; }
 inline size_t few_smem(int pairs, int E) {
   return (static_cast<size_t>(few_chunks(pairs)) * E * 2 + 15) / 16 * 16 + (2 * static_cast<size_t>(E) + pairs) * 4;
 }
+constexpr int kFewExperts = 1024;
+constexpr int kLayoutSmem = kFewHist * 2 + (2 * kFewExperts + kLayoutPairs) * 4;    // few_smem at most (80 KB)
 
 template <class V, int kFewThreads>
 __global__ void __launch_bounds__(kFewThreads) dispatch_few_kernel(const PermuteArgs a, const V* __restrict__ x, long long ldx,
@@ -527,7 +529,7 @@ cudaError_t launch_scatter_rows(int dt, RowsView x, const int32_t* inv, int T, i
 
 bool dispatch_layout_supported(int T, int K, int E) {
   const long long pairs = static_cast<long long>(T) * K;
-  return pairs <= kLayoutPairs && E <= 1024 && static_cast<long long>(few_chunks(static_cast<int>(pairs))) * E <= kFewHist;
+  return pairs <= kLayoutPairs && E <= kFewExperts && static_cast<long long>(few_chunks(static_cast<int>(pairs))) * E <= kFewHist;
 }
 
 cudaError_t launch_dispatch_layout(int dt, const int32_t* topk_ids, RowsView x, int T, int H, int E, int K, int align, int U,
@@ -547,7 +549,8 @@ cudaError_t launch_dispatch_layout(int dt, const int32_t* topk_ids, RowsView x, 
     });
   }
   const auto kernel = dispatch_few_kernel<uint4, 1024>;
-  const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  static std::atomic<unsigned long long> done{0};
+  const cudaError_t err = allow_smem(reinterpret_cast<const void*>(kernel), kLayoutSmem, done);
   if (err != cudaSuccess) return err;
   const int grid = U > 4096 ? 16 : 4;                // shares of the padding entries
   const cudaError_t err2 = launch_pdl(kernel, dim3(grid), dim3(1024), smem, stream, a, static_cast<const uint4*>(nullptr), 0, 0,
