@@ -333,6 +333,7 @@ __global__ void __launch_bounds__(256) permute_rows_kernel(const int32_t* __rest
   for (int s = lane; s < slabs; s += 32) x_perm_sf[act_sf_offset(bt, nb, dst, s)] = x_sf[static_cast<size_t>(t) * slabs + s];
 }
 
+constexpr int kPermExperts = 1024;                 // E at most (the callers' check)
 size_t permute_smem_bytes(int E) { return static_cast<size_t>(kPermWarps + 2) * E * sizeof(int32_t); }
 
 
@@ -370,9 +371,7 @@ cudaError_t launch_permute(const int32_t* topk_ids, int T, int K, int E, int ali
   const long long npairs = static_cast<long long>(T) * K;
   cudaError_t err;
   if (npairs <= kSmallPairs) {
-    const size_t smem = 2 * static_cast<size_t>(E) * sizeof(int32_t);
-    err = cudaFuncSetAttribute(permute_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (err != cudaSuccess) return err;
+    const size_t smem = 2 * static_cast<size_t>(E) * sizeof(int32_t);     // 8 KB at most
     const bool any = x_perm != nullptr || x_perm_sf != nullptr;     // rows and scales, or scales alone
     const bool copy = any && npairs <= kSmallCopyPairs;
     const long long units = npairs * (x_perm != nullptr ? (H / 16 + kCopyPiece - 1) / kCopyPiece : 1);
@@ -383,13 +382,11 @@ cudaError_t launch_permute(const int32_t* topk_ids, int T, int K, int E, int ali
   } else {
     if (scratch == nullptr) return cudaErrorInvalidValue;
     const int G = permute_ctas(npairs), W = permute_warp_chunk(npairs, G);
-    err = cudaFuncSetAttribute(permute_count_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               static_cast<int>(E * sizeof(int32_t)));
-    if (err != cudaSuccess) return err;
     err = launch_pdl(permute_count_kernel, dim3(G), dim3(kPermThreads), E * sizeof(int32_t), stream, a, W, scratch);
     if (err != cudaSuccess) return err;
     const size_t smem = permute_smem_bytes(E);
-    err = cudaFuncSetAttribute(permute_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    static std::atomic<unsigned long long> done{0};
+    err = allow_smem(reinterpret_cast<const void*>(permute_place_kernel), static_cast<int>(permute_smem_bytes(kPermExperts)), done);
     if (err != cudaSuccess) return err;
     permute_place_kernel<<<G, kPermThreads, smem, stream>>>(a, W, scratch);
     err = cudaGetLastError();

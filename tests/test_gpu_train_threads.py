@@ -77,3 +77,27 @@ def check_together(M, jobs, calls):
 def test_dispatch_of_some_hundred_pairs(M):
     # index arrays in one launch, whose shared memory goes by pairs and experts: 78 KB and 2 KB
     check_together(M, [Dispatch(M, 340, 512, 6), Dispatch(M, 150, 8, 2)], 40000)
+
+
+class Permute(Dispatch):
+    """The layer's permute of as many pairs, without rows."""
+
+    def __init__(self, M, T, E, K, align=4):
+        super().__init__(M, T, E, K, align)
+        self.ws = M.new_workspace(T, 128, 128, E, K, align)
+
+    def call(self):
+        self.M.permute(self.ids, self.E, self.align, self.sorted, self.experts, self.inv, self.m_sum, self.ws)
+
+    def outputs(self):
+        return self.sorted, self.experts, self.inv, self.m_sum
+
+
+def test_dispatch_of_some_thousand_pairs(M):
+    # index arrays by the layer's permute: 136 KB and 1 KB of shared memory
+    check_together(M, [Dispatch(M, 2048, 1024, 2), Dispatch(M, 2048, 8, 2)], 40000)
+
+
+def test_permute_of_some_hundred_pairs(M):
+    # 8 KB and 64 bytes
+    check_together(M, [Permute(M, 100, 1024, 6), Permute(M, 100, 8, 6)], 40000)
