@@ -1545,7 +1545,10 @@ __global__ void __launch_bounds__(32 * kActRowLanes, 6)
     if (mine) atomicAdd(&s_seg, static_cast<unsigned long long>(mine));   // integers: the order does not matter
     __syncthreads();
     seg = s_seg < static_cast<unsigned long long>(rows) ? static_cast<int>(s_seg) : rows;
-    cnt = min(max(__ldg(counts + e), 0), rows - seg);
+    const int c = __ldg(counts + e);
+    cnt = min(max(c, 0), rows - seg);
+    // (alone, this pass is what reports a segment that would leave the buffers)
+    if (blockIdx.x == 0 && blockIdx.z == 0 && threadIdx.x == 0 && (c < 0 || c > cnt)) record_error(status, kDevErrIndex);
   }
   const bool gated = act == kActSwiglu;
   const int cols = gated ? N / 2 : N;

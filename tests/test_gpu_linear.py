@@ -291,3 +291,23 @@ def test_linear_on_another_stream_and_in_a_graph(M):
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(want, (y, z, dx, dw, db)))
     assert M.get_error(ws) == M.OK
+
+
+@pytest.mark.parametrize("rows,N,act", [(40, 64, "none"), (40, 64, "swiglu"), (2000, 4096, "gelu")])
+def test_a_bias_gradient_alone_reports_bad_counts(M, rows, N, act):
+    # only the activation's pass runs: it reports what the products report, and nothing where the counts fit
+    dy = torch.randn(rows, N // 2 if act == "swiglu" else N, device="cuda").to(BF)
+    z = None if act == "none" else torch.randn(rows, N, device="cuda").to(BF)
+    w = torch.zeros(4, N, 64, dtype=BF, device="cuda")
+    ws = M.new_workspace_linear(rows, N, 64, 4, act)
+    db = torch.empty(4, N, device="cuda")
+    n = rows // 4
+    bad = [[n, n, -1, 0], [n, n, n, 3 * n], [rows + 1, 0, 0, 0], [0, 0, 0, -7], [rows, 1, 0, 0], [2 ** 31 - 1, 2 ** 31 - 1, 7, 0]]
+    good = [[n // 2, 0, n, 1], [rows, 0, 0, 0], [0, 0, 0, rows], [0, 0, 0, 0], [rows - 1, 0, 0, 0]]
+    for counts, want in [(c, M.ERR_DEVICE_INDEX) for c in bad] + [(c, M.OK) for c in good]:
+        c = torch.tensor(counts, dtype=torch.int32, device="cuda")
+        M.linear_backward(dy, None, w, ws, dbias=db, act=act, z=z, expert_counts=c, align=8)
+        assert M.get_error(ws) == want, counts
+        # the same as with the products
+        M.linear_backward(dy, dy.new_zeros(rows, 64), w, ws, dw=torch.empty_like(w), act=act, z=z, expert_counts=c, align=8)
+        assert M.get_error(ws) == want, counts
