@@ -7,6 +7,8 @@
 // (the same as w_k (dw_k - sum_j w_j dw_j), since the weights add up to 1, but without its cancellation where one
 // weight is nearly 1)
 //   softmax:         dl_i = [i selected] g_i - p_i sum_j g_j     (renormalised: sum_j g_j = 0)
+//                         = (1 - p_i) g_i - p_i sum_{j != i} g_j  of a selected i: near p_i = 1 the first form subtracts two
+//                           nearly equal numbers, and 1 - p_i is there the other exponentials' share of the sum
 //   sqrt(softplus):  dl_k = g_k sigmoid(l_k) / (2 softplus(l_k)), zero elsewhere
 // so only the unnormalised softmax needs the whole row of logits.  The forward's own weights stand in
 // for the scores, so nothing divides by a sum that may underflow.  The selection itself (and with it
@@ -85,8 +87,9 @@ __global__ void __launch_bounds__(kGradWarps * 32) route_grad_kernel(const float
     g = id >= 0 ? wk * c : 0.f;
   }
   // p becomes the row's -p_e sum_j g_j (dense) or zeros
-  float total = 0.f, lmax = -INFINITY, sum = 0.f;
+  float total = 0.f, sum = 0.f, pk = 0.f, not_k = 1.f;      // pk, not_k: of the lane's selected expert, p and 1 - p
   if (dense) {
+    float lmax = -INFINITY;
     total = g;
 #pragma unroll
     for (int i = 0; i < PER; ++i) lmax = fmaxf(lmax, p[i]);
@@ -102,6 +105,17 @@ __global__ void __launch_bounds__(kGradWarps * 32) route_grad_kernel(const float
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    if (id >= 0) pk = expf(lk - lmax) / sum;
+    not_k = 1.f - pk;
+    if (__any_sync(0xffffffffu, pk > 0.5f)) {
+      // one selected expert has more than all others: its exponential is the only one that is 1
+      float rest = 0.f;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) rest += p[i] < 1.f ? p[i] : 0.f;
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) rest += __shfl_xor_sync(0xffffffffu, rest, off);
+      if (pk > 0.5f) not_k = rest / sum;
+    }
   }
 #pragma unroll
   for (int i = 0; i < PER; i += V) {
@@ -127,7 +141,7 @@ __global__ void __launch_bounds__(kGradWarps * 32) route_grad_kernel(const float
     }
   }
   // an expert named twice gets both terms, from its first slot
-  float mine = 0.f;
+  float mine = 0.f, others = 0.f;
   bool first = id >= 0;
   for (int k = 0; k < K; ++k) {
     const int ik = __shfl_sync(0xffffffffu, id, k);
@@ -135,6 +149,8 @@ __global__ void __launch_bounds__(kGradWarps * 32) route_grad_kernel(const float
     if (ik == id) {
       mine += gk;
       if (k < lane) first = false;
+    } else {
+      others += gk;
     }
   }
   __syncwarp();                                     // the row is written before its selected entries
@@ -143,7 +159,7 @@ __global__ void __launch_bounds__(kGradWarps * 32) route_grad_kernel(const float
     if (!softmax)
       v = 0.5f * mine * sigmoid_over_softplus(lk);
     else if (dense)
-      v = mine - (expf(lk - lmax) / sum) * total;
+      v = not_k * mine - pk * others;
     orow[id] = T::from_f(v);
   }
 }

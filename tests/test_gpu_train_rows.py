@@ -296,6 +296,53 @@ def test_route_gradient(M, fn, renorm, T, E, K, dt):
     R.check(out, ref, bound + R.half_step(dt) * ref.abs() * 1.01 + R.tiny(dt), "dlogits")
 
 
+@pytest.mark.parametrize("T,E,K,dt", [(64, 256, 6, FP), (64, 64, 8, BF), (64, 33, 5, FP), (64, 5, 5, FP), (64, 1024, 32, HF),
+                                      (64, 256, 1, FP)])
+def test_route_gradient_of_one_likely_expert(M, T, E, K, dt):
+    # softmax weights as they are, one logit 4 to 67 above the rest: a selected expert's gradient is
+    # w_k ((1 - p_k) dw_k - sum of the other w_j dw_j), held to the magnitudes of these terms, which are as small as 1 - p_k
+    g = torch.Generator().manual_seed(T + E + K)
+    logits = torch.randn(T, E, generator=g)
+    top = torch.randint(0, E, (T, 1), generator=g)
+    logits.scatter_(1, top, torch.arange(T)[:, None] + 4.0)
+    keys = torch.rand(T, E, generator=g)
+    keys[: T - 8].scatter_(1, top[: T - 8], 2.0)             # (in the last rows it may be left out)
+    ids = keys.topk(K, 1).indices.to(torch.int32)
+    w = R.route_weights(logits, ids, "softmax", False)
+    dw = torch.randn(T, K, generator=g)
+    p = torch.softmax(logits.double(), 1)
+    x = torch.exp(logits.double() - logits.double().amax(1, keepdim=True))
+    rest = torch.stack([x[:, :e].sum(1) + x[:, e + 1:].sum(1) for e in range(E)], 1) / x.sum(1, keepdim=True)   # 1 - p
+    q = rest.gather(1, ids.long())
+    terms = w * dw.double()
+    others = torch.stack([terms[:, :k].sum(1) + terms[:, k + 1:].sum(1) for k in range(K)], 1)
+    others_abs = torch.stack([terms[:, :k].abs().sum(1) + terms[:, k + 1:].abs().sum(1) for k in range(K)], 1)
+    ref = (-p * terms.sum(1, keepdim=True)).scatter(1, ids.long(), terms * q - w * others)
+    mag = (p * terms.abs().sum(1, keepdim=True)).scatter(1, ids.long(), terms.abs() * q + w * others_abs)
+    ws = M.new_workspace_rows(T, K, E)
+    out = torch.full((T, E), float("nan"), dtype=dt, device="cuda")
+    M.route_backward(logits.cuda(), ids.cuda(), w.float().cuda(), dw.cuda(), "softmax", False, out, ws)
+    assert M.get_error(ws) == M.OK
+    # sums of up to E terms, exponentials whose argument is off by |l| half steps, about 64 roundings in all; below
+    # the smallest normal number, whole steps of it
+    bound = mag * (E + 64 + 2 * logits.abs().max()) * R.U32 + 2.0 ** -126
+    R.check(out, ref, bound + R.half_step(dt) * ref.abs() * 1.01 + R.tiny(dt), "dlogits")
+
+
+def test_route_gradient_of_equal_logits(M):
+    # several largest logits: none of them is left out of 1 - p
+    logits = torch.tensor([[3.0, 3.0, -40.0, 3.0], [0.0, 0.0, 0.0, 0.0], [50.0, 50.0, 0.0, 49.0]])
+    ids = torch.tensor([[0, 3], [2, 1], [1, 3]], dtype=torch.int32)
+    w = R.route_weights(logits, ids, "softmax", False).float()
+    dw = torch.tensor([[1.0, -2.0], [0.5, 0.25], [-1.0, 3.0]])
+    ws = M.new_workspace_rows(3, 2, 4)
+    out = torch.empty(3, 4, device="cuda")
+    M.route_backward(logits.cuda(), ids.cuda(), w.cuda(), dw.cuda(), "softmax", False, out, ws)
+    ref = R.route_grad(logits, ids, dw, "softmax", False)
+    scale = torch.softmax(logits.double(), 1) * 4
+    R.check(out, ref, scale * (64 + 100) * R.U32 + 1e-30, "dlogits")
+
+
 def test_route_gradient_of_underflowing_scores(M):
     # logits so low that every sqrt(softplus) score underflows in the formula s'(l) = sigmoid / (2 s): the
     # gradient of the normalised weights is still w_k (dw_k - c) / 2; masked experts (-inf) get none
