@@ -311,3 +311,158 @@ def test_a_bias_gradient_alone_reports_bad_counts(M, rows, N, act):
         # the same as with the products
         M.linear_backward(dy, dy.new_zeros(rows, 64), w, ws, dw=torch.empty_like(w), act=act, z=z, expert_counts=c, align=8)
         assert M.get_error(ws) == want, counts
+
+
+@pytest.mark.parametrize("dt", [BF, HF])
+@pytest.mark.parametrize("rows,counts,align,N,K", [
+    (1, None, 0, 4096, 1000), (7, None, 0, 16, 8), (200, None, 0, 4096, 2048), (300, None, 0, 528, 328), (129, None, 0, 272, 4096),
+    (4109, None, 0, 2064, 1544), (2500, None, 0, 4096, 64), (0, [3, 0, 130, 1], 16, 144, 200), (0, [20, 0, 9], 64, 4096, 72),
+    (0, [1500, 0, 2, 1], 1, 176, 1032), (0, [700, 3, 90, 513, 256, 31], 32, 2064, 1544),
+    (0, [310, 200, 0, 513, 256, 333, 640, 301], 16, 4096, 9640)])
+def test_a_residual_in_place(M, dt, rows, counts, align, N, K):
+    # the residual may be the output itself: the bits are those of a residual of its own
+    E = len(counts) if counts else 0
+    rows = rows or sum(-(-c // align) * align for c in counts) + 3
+    g = torch.Generator(device="cuda").manual_seed(rows + N)
+    rand = lambda *s: torch.randn(*s, generator=g, device="cuda").to(dt)
+    x, w = rand(rows, K), rand(*((E, N, K) if E else (N, K))) * K ** -0.5
+    kw = dict(expert_counts=torch.tensor(counts, dtype=torch.int32, device="cuda") if E else None, align=align)
+    for act in ("none", "silu", "gelu", "swiglu"):
+        cols = N // 2 if act == "swiglu" else N
+        ws = M.new_workspace_linear(rows, N, K, E, act)
+        res, z = rand(rows, cols), torch.empty(rows, N, dtype=dt, device="cuda")
+        apart, same = res.clone(), res.clone()
+        M.linear(x, w, apart, ws, act=act, residual=res, z=z, **kw)
+        M.linear(x, w, same, ws, act=act, residual=same, z=z, **kw)
+        assert torch.equal(apart, same), act
+        assert not torch.equal(apart, res)
+        dres, dy = rand(rows, K), rand(rows, cols)
+        dx, dsame = dres.clone(), dres.clone()
+        zz = None if act == "none" else z
+        M.linear_backward(dy, None, w, ws, dx=dx, act=act, z=zz, dx_residual=dres, **kw)
+        M.linear_backward(dy, None, w, ws, dx=dsame, act=act, z=zz, dx_residual=dsame, **kw)
+        assert torch.equal(dx, dsame), act
+        assert M.get_error(ws) == M.OK
+
+
+def sample(rows, n=300):
+    return [slice(0, n), slice(rows // 2, rows // 2 + n), slice(rows - n, rows)]
+
+
+@pytest.mark.parametrize("act", ["none", "swiglu"])
+def test_outputs_beyond_32_bit_offsets(M, act):
+    # y, z, the residual and dx with more than 2^31 elements
+    rows, N, K, dt = 270_003, 8192, 64, BF
+    g = torch.Generator(device="cuda").manual_seed(1)
+    rand = lambda *s: torch.randn(*s, generator=g, device="cuda", dtype=dt)
+    cols = N // 2 if act == "swiglu" else N
+    x, w, bias, res = rand(rows, K), rand(N, K) * K ** -0.5, torch.randn(N, generator=g, device="cuda"), rand(rows, cols)
+    ws = M.new_workspace_linear(rows, N, K, 0, "none")
+    y, z = torch.empty(rows, cols, dtype=dt, device="cuda"), torch.empty(rows, N, dtype=dt, device="cuda")
+    M.linear(x, w, y, ws, bias=bias, act=act, residual=res, z=z)
+    for s in sample(rows):
+        yr, ey, zr, ez = R.linear(x[s], w, bias, act, res[s], dt)
+        R.check(y[s], yr.cpu(), ey.cpu(), "y")
+        R.check(z[s], zr.cpu(), ez.cpu(), "z")
+    assert M.get_error(ws) == M.OK
+
+
+def test_input_and_weight_gradients_beyond_32_bit_offsets(M):
+    rows, N, K, dt = 270_003, 64, 8192, BF
+    g = torch.Generator(device="cuda").manual_seed(2)
+    rand = lambda *s: torch.randn(*s, generator=g, device="cuda", dtype=dt)
+    x, w, dy = rand(rows, K), rand(N, K), rand(rows, N)
+    ws = M.new_workspace_linear(rows, N, K)
+    dx, dw, db = torch.empty_like(x), torch.empty_like(w), torch.empty(N, device="cuda")
+    M.linear_backward(dy, x, w, ws, dx=dx, dw=dw, dbias=db, dx_residual=x)
+    for s in sample(rows):
+        (a, ea), _, _ = R.linear_grad(dy[s], x[s], w, None, "none", x[s], dt)
+        R.check(dx[s], a.cpu(), ea.cpu(), "dx")
+    ref, bound = torch.zeros(N, K, dtype=R.F64, device="cuda"), torch.zeros(N, K, dtype=R.F64, device="cuda")
+    for r in range(0, rows, 30_000):
+        d, v = dy[r:r + 30_000].double(), x[r:r + 30_000].double()
+        ref += d.t() @ v
+        bound += d.abs().t() @ v.abs()
+    h = R.half_step(dt)
+    bound *= R.mma_err(rows)
+    R.check(dw, ref.cpu(), (bound + h * (ref.abs() + bound) + R.tiny(dt)).cpu(), "dw")
+    assert M.get_error(ws) == M.OK
+
+
+def test_expert_weights_beyond_32_bit_offsets(M):
+    E, N, K, dt = 40, 8192, 6656, BF                    # 2.18e9 weights
+    counts = [0] * E
+    counts[0], counts[1], counts[E - 2], counts[E - 1] = 70, 300, 1, 200
+    rows = sum(-(-c // 8) * 8 for c in counts)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    rand = lambda *s: torch.randn(*s, generator=g, device="cuda", dtype=dt)
+    x, w, bias, dy = rand(rows, K), rand(E, N, K), torch.randn(E, N, generator=g, device="cuda"), rand(rows, N)
+    w *= K ** -0.5
+    kw = dict(expert_counts=torch.tensor(counts, dtype=torch.int32, device="cuda"), align=8)
+    ws = M.new_workspace_linear(rows, N, K, E)
+    y, dx = torch.zeros(rows, N, dtype=dt, device="cuda"), torch.zeros(rows, K, dtype=dt, device="cuda")
+    dw, db = torch.full_like(w, 3), torch.empty(E, N, device="cuda")
+    M.linear(x, w, y, ws, bias=bias, **kw)
+    M.linear_backward(dy, x, w, ws, dx=dx, dw=dw, dbias=db, **kw)
+    assert M.get_error(ws) == M.OK
+    for e, r, c in R.segments(counts, 8, rows):
+        s = slice(r, r + c)
+        if c == 0:
+            assert (dw[e] == 0).all() and (db[e] == 0).all()
+            continue
+        yr, ey, _, _ = R.linear(x[s], w[e], bias[e], "none", None, dt)
+        R.check(y[s], yr.cpu(), ey.cpu(), f"y of expert {e}")
+        (a, ea), (b, eb), (v, ev) = R.linear_grad(dy[s], x[s], w[e], None, "none", None, dt)
+        for got, ref, bound, n in ((dx[s], a, ea, "dx"), (dw[e], b, eb, "dw"), (db[e], v, ev, "dbias")):
+            R.check(got, ref.cpu(), bound.cpu(), f"{n} of expert {e}")
+
+
+@pytest.mark.parametrize("counts,align,N,K,act", [
+    ([20, 0, 9], 16, 64, 4096, "silu"), ([33, 1, 0, 64, 500, 7, 0, 2], 8, 320, 1400, "swiglu"), ([1500, 0, 2, 1], 1, 176, 1032, "relu"),
+    ([500, 610, 0, 433, 256, 512, 1, 300, 470, 555, 128, 390], 32, 1536, 648, "gelu"),
+    ([310, 200, 0, 513, 256, 333, 640, 301], 16, 4096, 9640, "swiglu"), ([4109], 1, 2064, 1544, "none")])
+def test_experts_in_fp16(M, counts, align, N, K, act):
+    E, dt = len(counts), HF
+    rows = sum(-(-c // align) * align for c in counts)
+    g = torch.Generator(device="cuda").manual_seed(rows + N)
+    rand = lambda *s: torch.randn(*s, generator=g, device="cuda")
+    cols = N // 2 if act == "swiglu" else N
+    x, w, bias, res = rand(rows, K).to(dt), (rand(E, N, K) * K ** -0.5).to(dt), rand(E, N), rand(rows, cols).to(dt)
+    dy, dres = rand(rows, cols).to(dt), rand(rows, K).to(dt)
+    live = torch.zeros(rows, dtype=torch.bool, device="cuda")
+    for _, r, c in R.segments(counts, align, rows):
+        live[r:r + c] = True
+    for t in (x, res, dy, dres):
+        t[~live] = float("nan")
+    kw = dict(act=act, expert_counts=torch.tensor(counts, dtype=torch.int32, device="cuda"), align=align)
+    ws = M.new_workspace_linear(rows, N, K, E, act)
+    y, z = torch.empty(rows, cols, dtype=dt, device="cuda"), torch.zeros(rows, N, dtype=dt, device="cuda")
+    M.linear(x, w, y, ws, bias=bias, residual=res, z=z, **kw)
+    dx, dw, db = torch.empty(rows, K, dtype=dt, device="cuda"), torch.empty_like(w), torch.empty(E, N, device="cuda")
+    M.linear_backward(dy, x, w, ws, dx=dx, dw=dw, dbias=db, z=None if act == "none" else z, dx_residual=dres, **kw)
+    assert M.get_error(ws) == M.OK
+    for e, r, c in R.segments(counts, align, rows):
+        s = slice(r, r + c)
+        yr, ey, zr, ez = R.linear(x[s], w[e], bias[e], act, res[s], dt)
+        R.check(y[s], yr.cpu(), ey.cpu(), f"y of expert {e}")
+        R.check(z[s], zr.cpu(), ez.cpu(), f"z of expert {e}")
+        (a, ea), (b, eb), (v, ev) = R.linear_grad(dy[s], x[s], w[e], z[s], act, dres[s], dt)
+        for got, ref, bound, n in ((dx[s], a, ea, "dx"), (dw[e], b, eb, "dw"), (db[e], v, ev, "dbias")):
+            R.check(got, ref.cpu(), bound.cpu(), f"{n} of expert {e}")
+
+
+def test_range_of_dz(M):
+    # dz is an operand of the products in the rows' type: past its range it is infinite, the bias' sum (in fp32) is not
+    N, K = 64, 64
+    z = torch.ones(8, N)
+    dy = torch.full((8, N // 2), 400.0)
+    z[:, N // 2:] = 400.0
+    w = torch.full((N, K), 2.0 ** -12)
+    for dt, finite in ((HF, False), (BF, True)):
+        ws = M.new_workspace_linear(8, N, K, 0, "swiglu")
+        dx, db = torch.empty(8, K, dtype=dt, device="cuda"), torch.empty(N, device="cuda")
+        M.linear_backward(dy.to(dt).cuda(), None, w.to(dt).cuda(), ws, dx=dx, dbias=db, act="swiglu", z=z.to(dt).cuda())
+        assert bool(torch.isfinite(dx).all()) == finite
+        s = 1 / (1 + 2.718281828459045 ** -1)
+        ref = torch.cat([torch.full((N // 2,), 8 * 160000.0 * (s + s * (1 - s))), torch.full((N // 2,), 8 * 400.0 * s)]).double()
+        R.check(db, ref, 2.0 ** -16 * ref, "dbias")

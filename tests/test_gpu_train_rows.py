@@ -186,6 +186,31 @@ def test_rows_at_any_alignment(M, dt, T, H, off, gap):
     assert M.get_error(ws) == M.OK
 
 
+@pytest.mark.parametrize("dt", [BF, HF, FP])
+@pytest.mark.parametrize("T,H,off,gap", [(70, 1, 1, 0), (70, 7, 3, 1), (70, 9, 0, 0), (70, 64, 0, 1), (70, 261, 7, 2), (3, 23, 1, 1),
+                                         (700, 1027, 1, 0), (70, 256, 0, 0)])
+def test_combine_gradient_over_the_rows_themselves(M, dt, T, H, off, gap):
+    # dy_perm may be y_perm, whatever the rows' alignment; padding rows and what is between rows stay
+    E, K, align = 6, 4, 8
+    ids, w = routing(T, E, K, H)
+    inv, _ = R.positions(ids, E, align)
+    inv[0, 1] = -1
+    U = M.msum_upper(T, K, E, align)
+    g = torch.Generator().manual_seed(H + off)
+    y, d = (torch.randn(r, H, generator=g).to(dt) for r in (U, T))
+    _, dd = at(d, off + 1, H + gap)
+    _, yd = at(y, off, H + gap)
+    ws = M.new_workspace_rows(T, K, E)
+    flat, dy = at(y, off, H + gap)
+    dw, dw2 = torch.empty(T, K, device="cuda"), torch.empty(T, K, device="cuda")
+    M.combine_backward(dd, yd, inv.cuda(), w.cuda(), dy, dw, ws)
+    flat2, both = at(y, off, H + gap)
+    M.combine_backward(dd, both, inv.cuda(), w.cuda(), both, dw2, ws)
+    assert torch.equal(dw, dw2) and torch.equal(dy, both)
+    assert int(flat2.isnan().sum()) == flat2.numel() - U * H
+    assert M.get_error(ws) == M.OK
+
+
 def test_combine_gradient_against_differences(M):
     # fp32 rows: the directional derivative of <c, combine(y, w)> by central differences of the kernel itself.
     # The function is linear in y and in w, so the difference has no truncation error, only rounding.
