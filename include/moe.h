@@ -485,7 +485,8 @@ moe_status moe_forward_batched_i8(const uint16_t* hidden, const float* w_gate, c
  * gradient of moe_combine_backward goes by the rows' 16-byte alignment).
  * Sorted buffers have U rows (moe_msum_upper, or E * max_tokens for the BatchedExperts layout); padding
  * rows never count and are never written.
- * ws: a workspace whose first 256 bytes hold the device status word, zero-filled once before first use.
+ * ws: a workspace whose first 256 bytes hold the device status word, zero-filled once before first use.  Calls that
+ * overlap, on other streams or host threads, take a workspace each.
  * ------------------------------------------------------------------------------------ */
 typedef enum { MOE_BF16 = 0, MOE_F16 = 1, MOE_F32 = 2 } moe_dtype;
 typedef struct {
@@ -562,7 +563,7 @@ moe_status moe_linear(moe_dtype dt, moe_rows x, const void* w, const float* bias
                       const int32_t* expert_counts, int rows, int N, int K, int E, int align, moe_rows y, moe_rows z,
                       void* ws, size_t ws_bytes, void* stream);
 
-/* Gradients of moe_linear: with dz = dy * act'(z), rounded to the rows' type,
+/* Gradients of moe_linear: with dz = dy * act'(z), rounded to the rows' type (fp16: infinite above 65504),
  *   dx = dz @ w + dx_residual;  dw[e] = dz_e^T @ x_e;  dbias[e] = sum over e's rows of dz before its rounding.
  * dx, dw ([N, K] or [E, N, K], contiguous) and dbias ([N] or [E, N] fp32) are optional, one at least; w is
  * read for dx, x for dw, z (as moe_linear wrote it) for act other than NONE.  dx_residual may be dx itself.

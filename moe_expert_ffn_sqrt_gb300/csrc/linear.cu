@@ -721,13 +721,14 @@ __global__ void __launch_bounds__(kLinMaxE) expert_maps_kernel(const __grid_cons
 // weight gradients) a slab takes 750.  8192^3 bf16 597 us (1.84
 // PFLOP/s, 97% of the measured rate of library products); 4096^3 82 us (1.68; 256 tiles on 76 pairs leave 16% of the
 // last round empty, and the tensor core is busy for 86% of the SMs' active cycles); 4096 x 7168 over 2048 with bias and
-// residual 79 us; 12288 rows of 32 experts, 4096 x 7168, SwiGLU 490 to 590 us by the box's power limit, 16% of it for
+// residual 73 us, 82 under the power limit (1705 MHz instead of 2070); 12288 rows of 32 experts, 4096 x 7168, SwiGLU 490 to 590 us by the box's power limit, 16% of it for
 // the rows that fill their tiles up.
 // Tried and not kept: tiles claimed from a counter instead of dealt out (both gradients of the 32 experts 585 -> 607 us);
 // two pieces per epilogue warp in turn (within 2% either way); pieces of two warps as one copy of 128-byte rows
 // (16384 x 4096 over 64 36 -> 41 us); the last round's dense tiles in halves (1 to 4%, lost in the noise).
 // With sums below about 512 terms the epilogue is the longest way, 500 cycles a piece: 16384 x 4096 outputs over 64
-// 34.6 us, with a residual 74, SiLU 54, GELU 82 (with two warps per quarter 36, 84, 60 and 86).
+// 34.6 us, with a residual 74, SiLU 54, GELU 82 (with two warps per quarter 36, 84, 60 and 86; experts'
+// products over long sums are 1% faster with two).
 // mapa: map of the operand of the output's columns (w, in the weight gradient x), mapsb: of its rows, mapo: of the
 // output, 32 x 32 pieces.  emaps: expert e's maps at 2e and 2e + 1 (see expert_maps_kernel), or null.
 template <int MODE>
@@ -1500,10 +1501,12 @@ cudaError_t launch_linear_dw(const LinearShape& p, RowsView dz, RowsView x, uint
 }
 
 // ------------------------------------------------------------------------------------------
-// dz = dy * act'(z) and the bias gradient's partial sums: thread = 8 columns, walking the rows
-// s, s + S, ... of its expert (dense: all rows); CTA = 32 column groups x 8 rows.  Memory bounds it: SiLU,
-// 16384 x 7168, 705 MB in 113 us (93% of a plain copy's rate; with four CTAs per SM instead of six 147, two rows of a
-// thread at a time 152); 4096 x 2048 16 us with the bias' second launch, GELU 19.
+// dz = dy * act'(z), rounded to 16 bits since it is an operand of both products (at most 2^-8 of a value in bf16, 2^-11
+// in fp16, where it is infinite past 65504), and the bias gradient's partial sums, of values before that rounding:
+// thread = 8 columns, walking the rows s, s + S, ... of its expert (dense: all rows); CTA = 32 column groups x 8 rows.
+// Memory bounds it where rows are many: SiLU, 16384 x 7168, 705 MB in 113 us (93% of a plain copy's rate; with four CTAs
+// per SM instead of six 147, two rows of a thread at a time 152).  4096 x 2048 with the bias' second launch 15 us of
+// 7.5 for the bytes, GELU 19, no activation 8.7 of 2.5: a thread has one row's loads on their way, and the launch.
 
 namespace {
 

@@ -13,9 +13,9 @@
 // so only the unnormalised softmax needs the whole row of logits.  The forward's own weights stand in
 // for the scores, so nothing divides by a sum that may underflow.  The selection itself (and with it
 // e_score_correction_bias) has no gradient.
-// One warp per token, 16-byte accesses where E is a multiple of four; the [T, E] write (and the logits' read, where
-// needed) bounds it.  16384 tokens, 256 experts, K = 6, fp32: 8.6 us (34.7 MB, 4.0 TB/s), renormalised 4.5 us
-// (18.4 MB, 4.1 TB/s); a few tokens 1.5 us, the launch.
+// One warp per token, 16-byte accesses where E is a multiple of four.  16384 tokens, K = 6, fp32, from HBM: 64, 256 and
+// 512 experts 7.0, 10.1 and 14.7 us (9.6, 35 and 68 MB), renormalised 4.7, 6.2 and 8.2: the bytes at 7 TB/s behind about
+// 5 us (4) of one token's loads, reductions and stores after one another; a few tokens 1.7 us, the launch.
 #include "kernels.h"
 #include "rows.cuh"
 
