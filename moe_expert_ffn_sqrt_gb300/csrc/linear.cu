@@ -221,6 +221,9 @@ __device__ __forceinline__ float2 lin_unpack(uint32_t w, int f16) {
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
 
+// Zero below v = -87.3, where the value's magnitude is below 1e-36: __fdividef gives 0 for a divisor past 2^126.  (Every
+// other bf16 or fp16 value is within half a step of it.  With e^-|v|, whose divisor stays below 2, 16384 x 4096 gated
+// outputs over 64 take 75 us instead of 71, and the gradients' pass 2.5% more.)
 __device__ __forceinline__ float lin_silu(float v) { return __fdividef(v, 1.f + __expf(-v)); }
 // Phi(-a), the normal distribution's tail, for 0 <= a <= 30, and e^(-a^2 / 2): Phi(-a) e^(a^2 / 2) is smooth in
 // t = 1 / (1 + 0.36 a) and vanishes with it, so t times a polynomial of degree 6 in t, fitted for the least relative
