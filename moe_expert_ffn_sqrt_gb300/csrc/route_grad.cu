@@ -109,6 +109,8 @@ __global__ void __launch_bounds__(kGradWarps * 32) route_grad_kernel(const float
     not_k = 1.f - pk;
     if (__any_sync(0xffffffffu, pk > 0.5f)) {
       // one selected expert has more than all others: its exponential is the only one that is 1
+      // (a second pass over the row for such tokens alone: with 256 experts 10.1 us, 10.6 where every token is one; leaving
+      // one largest term out of every row's sum from the start 10.6 always)
       float rest = 0.f;
 #pragma unroll
       for (int i = 0; i < PER; ++i) rest += p[i] < 1.f ? p[i] : 0.f;
