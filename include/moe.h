@@ -59,7 +59,8 @@ typedef enum {
   MOE_ERR_DEVICE_CHECK = 7   /* a kernel's own bounds / alignment check failed; the access was skipped */
 } moe_status;
 
-typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SQRT_SOFTPLUS = 1 } moe_score_fn;
+/* SIGMOID: moe_select and its backward only. */
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SQRT_SOFTPLUS = 1, MOE_SCORE_SIGMOID = 2 } moe_score_fn;
 
 /* Weight formats (CUDA tag page teaser: MXFP4 vs NVFP4, chosen by moe_quant_algo; note
  * "INT8 高吞吐/低延迟 EP 代码梳理" §2, §3.1: INT8 with channel-wise weights).
@@ -572,6 +573,93 @@ moe_status moe_linear_backward(moe_dtype dt, moe_rows dy, moe_rows x, const void
                                const int32_t* expert_counts, int rows, int N, int K, int E, int align,
                                moe_rows dx_residual, moe_rows dx, void* dw, float* dbias, void* ws, size_t ws_bytes,
                                void* stream);
+
+/* --------------------------------------------------------------------------------------
+ * Around the layer: the norm in front of it, routing from logits by groups of experts, and activations kept for the
+ * backward pass in 8 bits.  Like the training operators they have no counterpart in the method's description.
+ * Matrices are moe_rows, as there; outputs do not overlap inputs or one another unless a comment says so.
+ *
+ * Rows in 8 bits (moe_rows8): E4M3 codes and one UE8M0 scale per 128 columns, in moe_route's x_q / x_sf rule: per
+ * group the smallest 2^e, e in [-127, 127], with amax <= 448 * 2^e (e = 0 when amax = 0), codes rounded to the nearest.
+ * amax is taken over the group's finite values; an infinity or NaN gets the NaN code.  The last group may be shorter.
+ * With ldq = H and lds = H/128, H a multiple of 128, they are moe_permute's x_q and x_sf.
+ * ------------------------------------------------------------------------------------ */
+typedef struct {
+  uint8_t* q;             /* code of (r, c) at q[r * ldq + c]         */
+  uint8_t* sf;            /* its scale at sf[r * lds + c / 128]       */
+  int64_t ldq, lds;       /* ldq >= columns, lds >= ceil(columns/128) */
+} moe_rows8;
+
+/* Root-mean-square norm of a stream of rows, after the addition of what the last block put out:
+ *   sum = x + residual (rounded to type dt);   y = sum / sqrt(mean(sum^2) + eps) * weight,   y8 = y in 8 bits.
+ * x [T, H]; residual, sum, y, y8 [T, H] are optional, one output at least; weight [H] fp32, 16-byte aligned.  The norm
+ * is of the rounded sum, stored or not; y and y8 are each rounded once from fp32.  sum and y may be x or residual
+ * themselves (not both the same one).  1 <= H <= 2^24, eps >= 0. */
+moe_status moe_rms_norm(moe_dtype dt, moe_rows x, moe_rows residual, const float* weight, float eps, int T, int H,
+                        moe_rows sum, moe_rows y, moe_rows8 y8, void* stream);
+
+/* Workspace bytes of moe_rms_norm_backward. */
+moe_status moe_workspace_size_norm(int T, int H, size_t* bytes);
+
+/* Gradients of moe_rms_norm with respect to sum (x and residual have the same) and weight.  x: the forward's sum (its
+ * x where there was no residual).  dsum [T, H] (optional): the gradient that reaches sum on its other way, added to dx.
+ * dx [T, H] and dweight [H] (fp32, 16-byte aligned) are optional, one at least.  dx may be dy, x or dsum itself.  No
+ * rows: dweight is zero.  Sums over rows are taken in a fixed order. */
+moe_status moe_rms_norm_backward(moe_dtype dt, moe_rows dy, moe_rows x, const float* weight, float eps, moe_rows dsum,
+                                 int T, int H, moe_rows dx, float* dweight, void* ws, size_t ws_bytes, void* stream);
+
+/* How moe_select chooses: experts come in n_groups groups of E / n_groups neighbours (1 to 32 groups); a group is worth
+ * the sum of its group_best (1 or 2) largest keys; a token may use its topk_groups best groups. */
+typedef struct {
+  moe_score_fn fn;
+  int n_groups, topk_groups, group_best;
+  int renormalize;        /* weights divided by their sum */
+  float scale;            /* and times this (finite, not 0) */
+} moe_select_rule;
+
+/* Routing from logits [T, E] of type dt (moe_route's logits_out, or a product's output):
+ *   s = fn(logits);  key = s + e_score_bias (fp32 [E], optional)
+ *   topk_ids [T, K] int32 out: the K largest keys among the experts of the token's groups, descending
+ *   topk_w   [T, K] fp32 out: scale * s of them (renormalize: / the sum of the K scores; all 0 where that is 0)
+ * Ties go to the lower group and expert id.  Keys are compared as 64-bit evaluations give them (without a bias: by the
+ * logits themselves), whatever the kernel's own arithmetic; a NaN key counts as -infinity, a logit of -infinity (an
+ * expert that is masked out) has score 0 under every fn, so ids are valid and different in any case.
+ * E <= 1024, K <= 32 and K <= topk_groups * E / n_groups. */
+moe_status moe_select(moe_dtype dt, moe_rows logits, const float* e_score_bias, int T, int E, int K, moe_select_rule rule,
+                      int32_t* topk_ids, float* topk_w, void* stream);
+
+/* Gradient of moe_select's weights with respect to its logits, as moe_route_backward: dlogits [T, E] of type grad_dt
+ * (any for fp32 logits, else that of the logits) from dtopk_w [T, K], with topk_ids and topk_w as moe_select wrote them
+ * for the same fn, renormalize and scale. */
+moe_status moe_select_backward(moe_dtype dt, moe_rows logits, const int32_t* topk_ids, const float* topk_w,
+                               const float* dtopk_w, int T, int E, int K, moe_score_fn fn, int renormalize, float scale,
+                               moe_dtype grad_dt, moe_rows dlogits, void* ws, size_t ws_bytes, void* stream);
+
+/* x [rows, cols] of type dt to 8 bits.  expert_counts NULL and E = 0: every row; else the rows of the experts' segments
+ * alone (as in moe_linear; ws then takes the status, 256 bytes, and may be NULL otherwise). */
+moe_status moe_pack_rows8(moe_dtype dt, moe_rows x, const int32_t* expert_counts, int rows, int cols, int E, int align,
+                          moe_rows8 x8, void* ws, size_t ws_bytes, void* stream);
+
+/* And back: x[r] = the values of row r of x8, or with x_ids [rows] of its row x_ids[r] / x_div, x8 then having x_rows
+ * rows (token rows for moe_permute's sorted_token_ids and x_div = K).  Values are exact but for those past dt's largest,
+ * which take it.  An id outside [0, x_rows * x_div) on a row that is wanted records MOE_ERR_DEVICE_INDEX, and the row
+ * becomes zero.  ws (256 bytes) is needed with x_ids or expert_counts. */
+moe_status moe_unpack_rows8(moe_dtype dt, moe_rows8 x8, const int32_t* x_ids, int x_div, int x_rows,
+                            const int32_t* expert_counts, int rows, int cols, int E, int align, moe_rows x, void* ws,
+                            size_t ws_bytes, void* stream);
+
+/* Workspace bytes of moe_linear_backward8; it starts on a 256-byte boundary. */
+moe_status moe_workspace_size_linear8(int rows, int N, int K, int E, moe_act act, size_t* bytes);
+
+/* moe_linear_backward with x, z or both kept in 8 bits: x or x8 for dw, z or z8 for act other than NONE (the other one
+ * of a pair left out).  x_ids, x_div, x_rows: as in moe_unpack_rows8, so that the experts' rows need not be kept, only
+ * the tokens' (x8 the rows that moe_rms_norm wrote, x_ids moe_dispatch's sorted_token_ids, x_div its K).  The results are
+ * moe_linear_backward's for the unpacked rows, bit for bit. */
+moe_status moe_linear_backward8(moe_dtype dt, moe_rows dy, moe_rows x, moe_rows8 x8, const int32_t* x_ids, int x_div,
+                                int x_rows, const void* w, moe_rows z, moe_rows8 z8, moe_act act,
+                                const int32_t* expert_counts, int rows, int N, int K, int E, int align,
+                                moe_rows dx_residual, moe_rows dx, void* dw, float* dbias, void* ws, size_t ws_bytes,
+                                void* stream);
 
 /* Self-test of the device failure path (no counterpart in the method's description): launches one
  * bounded wait that nothing can satisfy, through the primitives the hot path uses.  mode 0: a

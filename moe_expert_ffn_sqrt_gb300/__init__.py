@@ -13,9 +13,9 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libmoe.so")
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_CUDA, ERR_DEVICE_INDEX, ERR_TIMEOUT, ERR_DEVICE_CHECK = range(8)
-SCORE_SOFTMAX, SCORE_SQRT_SOFTPLUS = 0, 1
+SCORE_SOFTMAX, SCORE_SQRT_SOFTPLUS, SCORE_SIGMOID = 0, 1, 2
 W_MXFP4, W_NVFP4, W_INT8, W_INT8_B256 = 0, 1, 2, 3
-SCORE_FNS = {"softmax": SCORE_SOFTMAX, "sqrt_softplus": SCORE_SQRT_SOFTPLUS}
+SCORE_FNS = {"softmax": SCORE_SOFTMAX, "sqrt_softplus": SCORE_SQRT_SOFTPLUS, "sigmoid": SCORE_SIGMOID}   # sigmoid: select
 WFMTS = {"mxfp4": W_MXFP4, "nvfp4": W_NVFP4, "int8": W_INT8, "int8b": W_INT8_B256}
 I8_FMTS = (W_INT8, W_INT8_B256)
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
@@ -38,6 +38,18 @@ class _Rows(ctypes.Structure):
 
 
 _NO_ROWS = _Rows(None, 0)
+
+
+class _Rows8(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("sf", ctypes.c_void_p), ("ldq", ctypes.c_int64), ("lds", ctypes.c_int64)]
+
+
+_NO_ROWS8 = _Rows8(None, None, 0, 0)
+
+
+class _SelectRule(ctypes.Structure):
+    _fields_ = [("fn", ctypes.c_int), ("n_groups", ctypes.c_int), ("topk_groups", ctypes.c_int), ("group_best", ctypes.c_int),
+                ("renormalize", ctypes.c_int), ("scale", ctypes.c_float)]
 
 
 _lib = None
@@ -142,6 +154,25 @@ def lib():
         L.moe_linear.argtypes = [I, R, P, P, R, I, P, I, I, I, I, I, R, R, P, Z, P]
         L.moe_linear_backward.restype = S
         L.moe_linear_backward.argtypes = [I, R, R, P, R, I, P, I, I, I, I, I, R, R, P, P, P, Z, P]
+        R8, F = _Rows8, ctypes.c_float
+        L.moe_rms_norm.restype = S
+        L.moe_rms_norm.argtypes = [I, R, R, P, F, I, I, R, R, R8, P]
+        L.moe_workspace_size_norm.restype = S
+        L.moe_workspace_size_norm.argtypes = [I, I, ctypes.POINTER(Z)]
+        L.moe_rms_norm_backward.restype = S
+        L.moe_rms_norm_backward.argtypes = [I, R, R, P, F, R, I, I, R, P, P, Z, P]
+        L.moe_select.restype = S
+        L.moe_select.argtypes = [I, R, P, I, I, I, _SelectRule, P, P, P]
+        L.moe_select_backward.restype = S
+        L.moe_select_backward.argtypes = [I, R, P, P, P, I, I, I, I, I, F, I, R, P, Z, P]
+        L.moe_pack_rows8.restype = S
+        L.moe_pack_rows8.argtypes = [I, R, P, I, I, I, I, R8, P, Z, P]
+        L.moe_unpack_rows8.restype = S
+        L.moe_unpack_rows8.argtypes = [I, R8, P, I, I, P, I, I, I, I, R, P, Z, P]
+        L.moe_workspace_size_linear8.restype = S
+        L.moe_workspace_size_linear8.argtypes = [I, I, I, I, I, ctypes.POINTER(Z)]
+        L.moe_linear_backward8.restype = S
+        L.moe_linear_backward8.argtypes = [I, R, R, R8, P, I, I, P, R, R8, I, P, I, I, I, I, I, R, R, P, P, P, Z, P]
         L.moe_get_error.restype = S
         L.moe_get_error.argtypes = [P, P, ctypes.POINTER(ctypes.c_int)]
         L.moe_status_str.restype = ctypes.c_char_p
@@ -744,6 +775,154 @@ def linear_backward(dy, x, w, ws, dx=None, dw=None, dbias=None, act="none", z=No
                                      _rows(dx_residual, dt, (rows, K), "dx_residual"), _rows(dx, dt, (rows, K), "dx"),
                                      _full(dw, dt, w.shape, "dw"), _full(dbias, torch.float32, w.shape[:-1], "dbias"),
                                      _space(ws), ws.numel(), _stream()), "moe_linear_backward")
+
+
+# ------------------------------------------------------------------ around the layer
+
+def _at_home(*tensors):
+    """The calls run on the current device's stream: every tensor has to be there."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
+
+
+def _rows8(pair, rows, cols, name):
+    """A pair (codes [rows, cols], scales [rows, ceil(cols / 128)]) of uint8 matrices.  None: not given."""
+    if pair is None:
+        return _NO_ROWS8
+    q, sf = pair
+    a = _rows(q, torch.uint8, (rows, cols), name)
+    b = _rows(sf, torch.uint8, (rows, (cols + 127) // 128), name + " scales")
+    return _Rows8(a.ptr, b.ptr, a.ld, b.ld)
+
+
+def new_rows8(rows, cols, device="cuda"):
+    """Room for [rows, cols] in 8 bits: (codes, scales)."""
+    return (torch.empty(rows, cols, dtype=torch.uint8, device=device),
+            torch.empty(rows, (cols + 127) // 128, dtype=torch.uint8, device=device))
+
+
+def rms_norm(x, weight, eps, residual=None, sum_out=None, y=None, y8=None):
+    """sum_out = x + residual; y and y8 (a pair, see new_rows8) = its root-mean-square norm times weight [H] fp32.
+    residual and each output are optional, one output at least; sum_out and y may be x or residual themselves."""
+    TH = T, H = x.shape
+    dt = x.dtype
+    _at_home(x, residual, weight, sum_out, y, *(y8 or ()))
+    _check(lib().moe_rms_norm(_dtype(x, "x"), _rows(x, dt, TH, "x"), _rows(residual, dt, TH, "residual"),
+                              _full(weight, torch.float32, (H,), "weight"), eps, T, H, _rows(sum_out, dt, TH, "sum_out"),
+                              _rows(y, dt, TH, "y"), _rows8(y8, T, H, "y8"), _stream()), "moe_rms_norm")
+
+
+def workspace_size_norm(T, H):
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_workspace_size_norm(T, H, ctypes.byref(n)), "moe_workspace_size_norm")
+    return int(n.value)
+
+
+def new_workspace_norm(T, H, device="cuda"):
+    """A zero-filled workspace for rms_norm_backward."""
+    return torch.zeros(workspace_size_norm(T, H), dtype=torch.uint8, device=device)
+
+
+def rms_norm_backward(dy, x, weight, eps, dx, ws, dweight=None, dsum=None):
+    """Gradients of rms_norm with respect to its sum (x here: rms_norm's sum_out, or its x) and weight; dsum is added to
+    dx.  dx may be dy, x or dsum itself; dx or dweight may be None."""
+    TH = T, H = dy.shape
+    dt = dy.dtype
+    _at_home(dy, x, weight, dx, ws, dweight, dsum)
+    _check(lib().moe_rms_norm_backward(_dtype(dy, "dy"), _rows(dy, dt, TH, "dy"), _rows(x, dt, TH, "x"),
+                                       _full(weight, torch.float32, (H,), "weight"), eps, _rows(dsum, dt, TH, "dsum"), T, H,
+                                       _rows(dx, dt, TH, "dx"), _full(dweight, torch.float32, (H,), "dweight"), _space(ws),
+                                       ws.numel(), _stream()), "moe_rms_norm_backward")
+
+
+def select(logits, topk_ids, topk_w, score_fn, e_score_bias=None, n_groups=1, topk_groups=1, group_best=2, renormalize=True,
+           scale=1.0):
+    """topk_ids, topk_w [T, K] from logits [T, E] (bf16, fp16 or fp32): the K largest score + bias among the topk_groups
+    best of n_groups groups of experts (by the sum of their group_best largest), weights scaled (and normalised)."""
+    TK = T, K = topk_ids.shape
+    E, dt = logits.shape[1], logits.dtype
+    _at_home(logits, topk_ids, topk_w, e_score_bias)
+    rule = _SelectRule(SCORE_FNS.get(score_fn, score_fn), n_groups, topk_groups, group_best, int(renormalize), scale)
+    _check(lib().moe_select(_dtype(logits, "logits"), _rows(logits, dt, (T, E), "logits"),
+                            _full(e_score_bias, torch.float32, (E,), "e_score_bias"), T, E, K, rule,
+                            _full(topk_ids, torch.int32, TK, "topk_ids"), _full(topk_w, torch.float32, TK, "topk_w"),
+                            _stream()), "moe_select")
+
+
+def select_backward(logits, topk_ids, topk_w, dtopk_w, dlogits, ws, score_fn, renormalize=True, scale=1.0):
+    """dlogits [T, E] (any type for fp32 logits, else theirs) from dtopk_w, for select's topk_ids and topk_w.
+    ws: as for route_backward."""
+    TK = T, K = topk_ids.shape
+    E = logits.shape[1]
+    _at_home(logits, topk_ids, topk_w, dtopk_w, dlogits, ws)
+    _check(lib().moe_select_backward(_dtype(logits, "logits"), _rows(logits, logits.dtype, (T, E), "logits"),
+                                     _full(topk_ids, torch.int32, TK, "topk_ids"), _full(topk_w, torch.float32, TK, "topk_w"),
+                                     _full(dtopk_w, torch.float32, TK, "dtopk_w"), T, E, K,
+                                     SCORE_FNS.get(score_fn, score_fn), int(renormalize), scale, _dtype(dlogits, "dlogits"),
+                                     _rows(dlogits, dlogits.dtype, (T, E), "dlogits"), _space(ws), ws.numel(), _stream()),
+           "moe_select_backward")
+
+
+def _experts(counts):
+    if counts is not None and not counts.numel():
+        raise ValueError("expert_counts is empty")
+    return 0 if counts is None else counts.shape[0]
+
+
+def _ws_opt(ws):
+    return (None, 0) if ws is None else (_space(ws), ws.numel())
+
+
+def pack_rows8(x, x8, expert_counts=None, align=0, ws=None):
+    """x [rows, cols] to 8 bits (x8: a pair, see new_rows8).  With expert_counts [E] the rows of the experts' segments
+    alone; ws (256 bytes, zero-filled) then takes the status."""
+    rows, cols = x.shape
+    E = _experts(expert_counts)
+    _at_home(x, expert_counts, ws, *x8)
+    _check(lib().moe_pack_rows8(_dtype(x, "x"), _rows(x, x.dtype, (rows, cols), "x"),
+                                _full(expert_counts, torch.int32, (E,), "expert_counts"), rows, cols, E, align,
+                                _rows8(x8, rows, cols, "x8"), *_ws_opt(ws), _stream()), "moe_pack_rows8")
+
+
+def unpack_rows8(x8, x, x_ids=None, x_div=1, expert_counts=None, align=0, ws=None):
+    """The values of x8 into x [rows, cols]; with x_ids [rows], row r from row x_ids[r] // x_div of x8."""
+    rows, cols = x.shape
+    E = _experts(expert_counts)
+    src = rows if x_ids is None else x8[0].shape[0]
+    _at_home(x, x_ids, expert_counts, ws, *x8)
+    _check(lib().moe_unpack_rows8(_dtype(x, "x"), _rows8(x8, src, cols, "x8"), _full(x_ids, torch.int32, (rows,), "x_ids"),
+                                  x_div, src, _full(expert_counts, torch.int32, (E,), "expert_counts"), rows, cols, E, align,
+                                  _rows(x, x.dtype, (rows, cols), "x"), *_ws_opt(ws), _stream()), "moe_unpack_rows8")
+
+
+def workspace_size_linear8(rows, N, K, E=0, act="none"):
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_workspace_size_linear8(rows, N, K, E, ACTS.get(act, act), ctypes.byref(n)), "moe_workspace_size_linear8")
+    return int(n.value)
+
+
+def new_workspace_linear8(rows, N, K, E=0, act="none", device="cuda"):
+    """A zero-filled workspace for linear_backward8 (and linear, linear_backward)."""
+    return torch.zeros(workspace_size_linear8(rows, N, K, E, act), dtype=torch.uint8, device=device)
+
+
+def linear_backward8(dy, w, ws, x=None, x8=None, z=None, z8=None, x_ids=None, x_div=1, dx=None, dw=None, dbias=None,
+                     act="none", dx_residual=None, expert_counts=None, align=0):
+    """linear_backward with x and z each in 16 bits or in 8 (pairs x8, z8).  With x_ids [rows] row r of x is row
+    x_ids[r] // x_div of x8: token rows through dispatch's sorted_token_ids and K."""
+    rows, N, K, E, act, cols = _linear_dims(dy, w, act, expert_counts)
+    dt = dy.dtype
+    src = rows if x_ids is None or x8 is None else x8[0].shape[0]
+    _at_home(dy, w, ws, x, z, x_ids, dx, dw, dbias, dx_residual, expert_counts, *(x8 or ()), *(z8 or ()))
+    _check(lib().moe_linear_backward8(_dtype(dy, "dy"), _rows(dy, dt, (rows, cols), "dy"), _rows(x, dt, (rows, K), "x"),
+                                      _rows8(x8, src, K, "x8"), _full(x_ids, torch.int32, (rows,), "x_ids"), x_div, src,
+                                      _ptr(w, dt, "w"), _rows(z, dt, (rows, N), "z"), _rows8(z8, rows, N, "z8"), act,
+                                      _full(expert_counts, torch.int32, (E,), "expert_counts"), rows, N, K, E, align,
+                                      _rows(dx_residual, dt, (rows, K), "dx_residual"), _rows(dx, dt, (rows, K), "dx"),
+                                      _full(dw, dt, w.shape, "dw"), _full(dbias, torch.float32, w.shape[:-1], "dbias"),
+                                      _space(ws), ws.numel(), _stream()), "moe_linear_backward8")
 
 
 def selftest_wait_timeout(ws, mode):

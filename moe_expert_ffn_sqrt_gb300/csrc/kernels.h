@@ -200,6 +200,35 @@ struct RowsView {
   long long ld;
 };
 
+// Rows in 8 bits: E4M3 codes from q + r * ldq on, UE8M0 scales of 128 columns each from sf + r * lds on (q null: not given).
+struct Rows8View {
+  uint8_t *q, *sf;
+  long long ldq, lds;
+};
+
+// norm.cu: sum = x (+ res), y and y8 = its norm times w (each optional).
+cudaError_t launch_norm(int dt, RowsView x, RowsView res, const float* w, float eps, int T, int H, RowsView sum, RowsView y,
+                        Rows8View y8, cudaStream_t stream);
+// Gradients of the norm of x: dx (+ dsum; optional) and dw [H] (optional).
+size_t norm_scratch_bytes(int T, int H);
+cudaError_t launch_norm_grad(int dt, RowsView dy, RowsView x, const float* w, float eps, RowsView dsum, int T, int H,
+                             RowsView dx, float* dw, void* scratch, cudaStream_t stream);
+
+// rows8.cu: rows of type dt to 8 bits and back (counts null: all rows, else the experts' segments).  Unpacked row r is
+// row r of x, or with ids row ids[r] / div of its src_rows rows.
+cudaError_t launch_pack_rows8(int dt, RowsView x, const int32_t* counts, int rows, int cols, int E, int align, Rows8View out,
+                              uint32_t* status, cudaStream_t stream);
+cudaError_t launch_unpack_rows8(int dt, Rows8View x, const int32_t* ids, int div, int src_rows, const int32_t* counts,
+                                int rows, int cols, int E, int align, RowsView out, uint32_t* status, cudaStream_t stream);
+
+// select.cu: experts of a token from its logits (ldt: their type).
+struct SelectRule {
+  int fn, groups, topk_groups, best, renorm;
+  float scale;
+};
+cudaError_t launch_select(int ldt, RowsView logits, const float* bias, int T, int E, int K, const SelectRule& rule,
+                          int32_t* ids, float* w, cudaStream_t stream);
+
 // train_rows.cu: rows of T tokens to and from U sorted rows through inv [T, K] (-1: dropped pair).
 cudaError_t launch_scatter_rows(int dt, RowsView x, const int32_t* inv, int T, int K, int H, int U, RowsView out,
                                 uint32_t* status, cudaStream_t stream);
@@ -215,9 +244,10 @@ cudaError_t launch_sum_rows(int dt, RowsView y, const int32_t* inv, const float*
 cudaError_t launch_combine_grad(int dt, RowsView dout, RowsView y, const int32_t* inv, const float* w, int T, int K,
                                 int H, int U, RowsView dy, float* dw, uint32_t* status, cudaStream_t stream);
 
-// route_grad.cu (dt: type of out [T, E])
-cudaError_t launch_route_grad(int dt, const float* logits, const int32_t* ids, const float* w, const float* dw, int T,
-                              int E, int K, int softmax, int renorm, void* out, uint32_t* status, cudaStream_t stream);
+// route_grad.cu (fn: moe_score_fn; ldt, dt: types of logits and out [T, E], ldt kF32 or dt; weights times scale)
+cudaError_t launch_route_grad(int ldt, RowsView logits, const int32_t* ids, const float* w, const float* dw, int T, int E,
+                              int K, int fn, int renorm, float scale, int dt, RowsView out, uint32_t* status,
+                              cudaStream_t stream);
 
 // linear.cu: products of `rows` rows with w [N, K] (counts null), or of E experts' row segments (counts
 // [E], segments padded to `align` rows inside buffers of `rows` rows) with w [E, N, K].
@@ -234,10 +264,11 @@ cudaError_t launch_linear_dx(const LinearShape& p, RowsView dz, const uint16_t* 
                              uint32_t* status, cudaStream_t stream);
 cudaError_t launch_linear_dw(const LinearShape& p, RowsView dz, RowsView x, uint16_t* dw, void* maps, uint32_t* status,
                              cudaStream_t stream);
-// dz = dy * act'(z) (act none: not written) and, with db, the bias gradient (part: E * linear_bias_slices * N floats).
+// dz = dy * act'(z) (act none: not written), z in 8 bits where z8 is given, and, with db, the bias gradient (part:
+// E * linear_bias_slices * N floats).
 int linear_bias_slices(int rows, int N, int E, int act);
-cudaError_t launch_act_grad(const LinearShape& p, RowsView dy, RowsView z, int act, RowsView dz, float* part, float* db,
-                            uint32_t* status, cudaStream_t stream);
+cudaError_t launch_act_grad(const LinearShape& p, RowsView dy, RowsView z, Rows8View z8, int act, RowsView dz, float* part,
+                            float* db, uint32_t* status, cudaStream_t stream);
 
 // Lets a kernel use up to `bytes` of dynamic shared memory, once per device (`done`: a bit per device).  The limit is
 // the function's, not the launch's, so it is the most that any call needs: one that went by the call's own size could be

@@ -35,8 +35,10 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "kernels.h"
-#include "rows.cuh"
+#include "rows8.cuh"
 
 namespace moe {
 
@@ -1528,34 +1530,46 @@ __device__ __forceinline__ float gelu_grad(float v) {
   return v < 0.f ? tail - vphi : 1.f - tail + vphi;
 }
 
-template <class T>
+// Eight values of z, kept in the rows' type or in 8 bits (codes in whole words; the same values as unpacked ones).
+template <class T, bool Z8>
+struct ZRows {
+  const uint16_t* z;
+  const uint8_t *q, *sf;
+  long long ld, ldsf;
+  int words;
+  __device__ __forceinline__ Pack<T> get(long long row, int c) const {
+    if constexpr (!Z8) {
+      return load_pack<T>(z + row * ld + c);
+    } else {
+      uint32_t w[2];
+      load_codes8<8>(q + row * ld + c, w, 8, words);
+      const float s = scale8(__ldg(sf + row * ldsf + c / kGroup8));
+      Pack<T> p;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float v[4];
+        values8(w[i], s, v);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) p.v[4 * i + j] = from_value8<T>(v[j]);
+      }
+      return p;
+    }
+  }
+};
+
+template <class T, bool Z8>
 __global__ void __launch_bounds__(32 * kActRowLanes, 6)
-    act_grad_kernel(const uint16_t* __restrict__ dy, long long lddy, const uint16_t* __restrict__ z, long long ldz, int act,
+    act_grad_kernel(const uint16_t* __restrict__ dy, long long lddy, const ZRows<T, Z8> z, int act,
                     const int32_t* __restrict__ counts, int E, int align, int rows, int N, uint16_t* __restrict__ dz,
                     long long lddz, float* __restrict__ part, int S, uint32_t* status) {
-  __shared__ unsigned long long s_seg;
   __shared__ float red[kActRowLanes][2][32 * 8 + 8];
   const int lane = threadIdx.x & 31, rl = threadIdx.x >> 5;
   const int e = blockIdx.y;
   grid_dependency_wait();
   grid_launch_dependents();
-  int cnt = rows, seg = 0;
-  if (counts) {
-    if (threadIdx.x == 0) s_seg = 0;
-    __syncthreads();
-    int mine = 0;
-    for (int i = threadIdx.x; i < e; i += blockDim.x) {
-      const int c = min(max(__ldg(counts + i), 0), rows);
-      mine = min(mine + (c + align - 1) / align * align, rows);
-    }
-    if (mine) atomicAdd(&s_seg, static_cast<unsigned long long>(mine));   // integers: the order does not matter
-    __syncthreads();
-    seg = s_seg < static_cast<unsigned long long>(rows) ? static_cast<int>(s_seg) : rows;
-    const int c = __ldg(counts + e);
-    cnt = min(max(c, 0), rows - seg);
-    // (alone, this pass is what reports a segment that would leave the buffers)
-    if (blockIdx.x == 0 && blockIdx.z == 0 && threadIdx.x == 0 && (c < 0 || c > cnt)) record_error(status, kDevErrIndex);
-  }
+  // (alone, this pass is what reports a segment that would leave the buffers)
+  int cnt, seg;
+  expert_segment(counts, e, align, rows, blockIdx.x == 0 && blockIdx.z == 0, seg, cnt, status);
   const bool gated = act == kActSwiglu;
   const int cols = gated ? N / 2 : N;
   const int c = (blockIdx.x * 32 + lane) * 8;
@@ -1568,7 +1582,7 @@ __global__ void __launch_bounds__(32 * kActRowLanes, 6)
       const Pack<T> g = load_pack<T>(dy + row * lddy + c);
       Pack<T> o, o2;
       if (gated) {
-        const Pack<T> a = load_pack<T>(z + row * ldz + c), b = load_pack<T>(z + row * ldz + cols + c);
+        const Pack<T> a = z.get(row, c), b = z.get(row, cols + c);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           float s;
@@ -1585,7 +1599,7 @@ __global__ void __launch_bounds__(32 * kActRowLanes, 6)
 #pragma unroll
         for (int i = 0; i < 8; ++i) acc[0][i] += g.f(i);
       } else {
-        const Pack<T> a = load_pack<T>(z + row * ldz + c);
+        const Pack<T> a = z.get(row, c);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const float v = a.f(i);
@@ -1648,8 +1662,8 @@ int linear_bias_slices(int rows, int N, int E, int act) {
   return static_cast<int>(s < 1 ? 1 : (s > 64 ? 64 : s));
 }
 
-cudaError_t launch_act_grad(const LinearShape& p, RowsView dy, RowsView z, int act, RowsView dz, float* part, float* db,
-                            uint32_t* status, cudaStream_t stream) {
+cudaError_t launch_act_grad(const LinearShape& p, RowsView dy, RowsView z, Rows8View z8, int act, RowsView dz, float* part,
+                            float* db, uint32_t* status, cudaStream_t stream) {
   const int E = p.counts ? p.E : 1;
   // with the experts' padding known, the rows that are likely there; never more slices than the workspace holds
   const long long live = p.counts ? p.rows - static_cast<long long>(E) * (p.align - 1) : p.rows;
@@ -1658,11 +1672,21 @@ cudaError_t launch_act_grad(const LinearShape& p, RowsView dy, RowsView z, int a
   const int cols = act == kActSwiglu ? p.N / 2 : p.N;
   const dim3 grid((cols + 255) / 256, E, S);
   float* pp = !db ? nullptr : S == 1 ? db : part;
-  const auto kernel = p.f16 ? act_grad_kernel<F16Elem> : act_grad_kernel<Bf16Elem>;
-  const cudaError_t err =
-      launch_pdl(kernel, grid, dim3(32 * kActRowLanes), 0, stream, static_cast<const uint16_t*>(dy.ptr), dy.ld,
-                 static_cast<const uint16_t*>(z.ptr), z.ld, act, p.counts, E, p.align, p.rows, p.N,
-                 static_cast<uint16_t*>(dz.ptr), dz.ld, pp, S, status);
+  const auto run = [&](auto type, auto kept8) {
+    using T = decltype(type);
+    constexpr bool Z8 = decltype(kept8)::value;
+    ZRows<T, Z8> zr{};
+    zr.z = static_cast<const uint16_t*>(z.ptr);
+    zr.ld = Z8 ? z8.ldq : z.ld;
+    zr.q = z8.q;
+    zr.sf = z8.sf;
+    zr.ldsf = z8.lds;
+    zr.words = codes_aligned(z8, p.rows, 8);
+    return launch_pdl(act_grad_kernel<T, Z8>, grid, dim3(32 * kActRowLanes), 0, stream, static_cast<const uint16_t*>(dy.ptr),
+                      dy.ld, zr, act, p.counts, E, p.align, p.rows, p.N, static_cast<uint16_t*>(dz.ptr), dz.ld, pp, S, status);
+  };
+  const cudaError_t err = z8.q ? (p.f16 ? run(F16Elem{}, std::true_type{}) : run(Bf16Elem{}, std::true_type{}))
+                               : (p.f16 ? run(F16Elem{}, std::false_type{}) : run(Bf16Elem{}, std::false_type{}));
   if (err != cudaSuccess || !db || S == 1) return err;
   const long long total = static_cast<long long>(E) * p.N;
   return launch_pdl(bias_sum_kernel, dim3(static_cast<int>((total + 255) / 256)), dim3(256), 0, stream,

@@ -1,15 +1,16 @@
 // Gradient of the routing weights with respect to the gate logits (the scoring of moe_route:
 // page "DeepSeek V4 MegaMoE Kernel 深度解析", 经典 MoE 的计算过程 / 第一步：路由).
 //
-// With s = softmax(l) or sqrt(softplus(l)), w_k = s_k of the K selected experts (divided by their sum
-// when renormalised) and dw = dL/dw:
-//   g_k = s_k dL/ds_k = w_k sum_j w_j (dw_k - dw_j)   renormalised,   w_k dw_k   otherwise
-// (the same as w_k (dw_k - sum_j w_j dw_j), since the weights add up to 1, but without its cancellation where one
-// weight is nearly 1)
+// With s = softmax(l), sqrt(softplus(l)) or sigmoid(l), w_k = c s_k of the K selected experts (divided by their sum
+// when renormalised; c = 1 for moe_route's weights) and dw = dL/dw:
+//   g_k = s_k dL/ds_k = w_k sum_j w_j / c (dw_k - dw_j)   renormalised,   w_k dw_k   otherwise
+// (the same as w_k (dw_k - sum_j w_j dw_j / c), since the weights add up to c, but without its cancellation where one
+// weight is nearly c)
 //   softmax:         dl_i = [i selected] g_i - p_i sum_j g_j     (renormalised: sum_j g_j = 0)
 //                         = (1 - p_i) g_i - p_i sum_{j != i} g_j  of a selected i: near p_i = 1 the first form subtracts two
 //                           nearly equal numbers, and 1 - p_i is there the other exponentials' share of the sum
 //   sqrt(softplus):  dl_k = g_k sigmoid(l_k) / (2 softplus(l_k)), zero elsewhere
+//   sigmoid:         dl_k = g_k (1 - s_k) = g_k sigmoid(-l_k), zero elsewhere
 // so only the unnormalised softmax needs the whole row of logits.  The forward's own weights stand in
 // for the scores, so nothing divides by a sum that may underflow.  The selection itself (and with it
 // e_score_correction_bias) has no gradient.
@@ -35,35 +36,45 @@ __device__ __forceinline__ float sigmoid_over_softplus(float l) {
 
 // Value i of a lane is expert V * lane + 32 * V * (i / V) + i % V: V = 4 where rows are whole groups of four
 // (16-byte accesses), else 1.  PER: values per lane.
-template <class T, int PER, int V>
-__global__ void __launch_bounds__(kGradWarps * 32) route_grad_kernel(const float* __restrict__ logits,
+// L: type of the logits.
+template <class T, class L, int PER, int V>
+__global__ void __launch_bounds__(kGradWarps * 32) route_grad_kernel(const typename L::raw* __restrict__ logits, long long ldl,
                                                                      const int32_t* __restrict__ ids,
                                                                      const float* __restrict__ w,
                                                                      const float* __restrict__ dw, int T_, int E, int K,
-                                                                     int softmax, int renorm,
-                                                                     typename T::raw* __restrict__ out,
+                                                                     int fn, int renorm, float over_scale,
+                                                                     typename T::raw* __restrict__ out, long long ldo,
                                                                      uint32_t* status) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int t = blockIdx.x * kGradWarps + warp;
   grid_dependency_wait();
   grid_launch_dependents();
   if (t >= T_) return;
-  const float* lrow = logits + static_cast<size_t>(t) * E;
-  typename T::raw* orow = out + static_cast<size_t>(t) * E;
+  const bool softmax = fn == 0;
+  const typename L::raw* lrow = logits + t * ldl;
+  typename T::raw* orow = out + t * ldo;
   const bool dense = softmax && !renorm;
   float p[PER];
 #pragma unroll
   for (int i = 0; i < PER; i += V) {
     const int e = V * lane + 32 * i;
     if constexpr (V == 4) {
-      float4 q = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-      if (dense && e < E) q = __ldg(reinterpret_cast<const float4*>(lrow + e));
-      p[i] = q.x;
-      p[i + 1] = q.y;
-      p[i + 2] = q.z;
-      p[i + 3] = q.w;
+      typename L::raw q[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) p[i + j] = -INFINITY;
+      if (dense && e < E) {
+        if constexpr (sizeof(q) == 16) {
+          const uint4 u = __ldg(reinterpret_cast<const uint4*>(lrow + e));
+          memcpy(q, &u, 16);
+        } else {
+          const uint2 u = __ldg(reinterpret_cast<const uint2*>(lrow + e));
+          memcpy(q, &u, 8);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) p[i + j] = L::to_f(q[j]);
+      }
     } else {
-      p[i] = dense && e < E ? __ldg(lrow + e) : -INFINITY;
+      p[i] = dense && e < E ? L::to_f(__ldg(lrow + e)) : -INFINITY;
     }
   }
   int id = -1;
@@ -77,14 +88,14 @@ __global__ void __launch_bounds__(kGradWarps * 32) route_grad_kernel(const float
       id = -1;
       wk = dk = 0.f;
     } else if (dense || !softmax) {
-      lk = __ldg(lrow + id);
+      lk = L::to_f(__ldg(lrow + id));
     }
   }
   float g = wk * dk;
   if (renorm) {
     float c = 0.f;
     for (int j = 0; j < K; ++j) c = fmaf(__shfl_sync(0xffffffffu, wk, j), dk - __shfl_sync(0xffffffffu, dk, j), c);
-    g = id >= 0 ? wk * c : 0.f;
+    g = id >= 0 ? wk * (c * over_scale) : 0.f;
   }
   // p becomes the row's -p_e sum_j g_j (dense) or zeros
   float total = 0.f, sum = 0.f, pk = 0.f, not_k = 1.f;      // pk, not_k: of the lane's selected expert, p and 1 - p
@@ -100,12 +111,13 @@ __global__ void __launch_bounds__(kGradWarps * 32) route_grad_kernel(const float
     }
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      p[i] = expf(p[i] - lmax);
+      p[i] = p[i] == -INFINITY ? 0.f : expf(p[i] - lmax);       // (a row of nothing else: no probability at all)
       sum += V * lane + 32 * (i / V * V) + i % V < E ? p[i] : 0.f;
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    if (id >= 0) pk = expf(lk - lmax) / sum;
+    if (lmax == -INFINITY) sum = 1.f;
+    if (id >= 0 && lk != -INFINITY) pk = expf(lk - lmax) / sum;
     not_k = 1.f - pk;
     if (__any_sync(0xffffffffu, pk > 0.5f)) {
       // one selected expert has more than all others: its exponential is the only one that is 1
@@ -158,44 +170,67 @@ __global__ void __launch_bounds__(kGradWarps * 32) route_grad_kernel(const float
   __syncwarp();                                     // the row is written before its selected entries
   if (first) {
     float v = mine;
-    if (!softmax)
+    if (fn == 1)
       v = 0.5f * mine * sigmoid_over_softplus(lk);
+    else if (fn == 2)
+      v = mine / (1.f + expf(lk));
     else if (dense)
       v = not_k * mine - pk * others;
     orow[id] = T::from_f(v);
   }
 }
 
-template <class T, int PER, int V>
-cudaError_t route_grad_launch(const float* logits, const int32_t* ids, const float* w, const float* dw, int T_, int E, int K,
-                              int softmax, int renorm, void* out, uint32_t* status, cudaStream_t stream) {
-  return launch_pdl(route_grad_kernel<T, PER, V>, dim3((T_ + kGradWarps - 1) / kGradWarps), dim3(kGradWarps * 32), 0, stream,
-                    logits, ids, w, dw, T_, E, K, softmax, renorm, static_cast<typename T::raw*>(out), status);
+struct GradArgs {
+  const void* logits;
+  long long ldl;
+  const int32_t* ids;
+  const float *w, *dw;
+  int T, E, K, fn, renorm;
+  float over_scale;
+  void* out;
+  long long ldo;
+  uint32_t* status;
+};
+
+template <class T, class L, int PER, int V>
+cudaError_t route_grad_launch(const GradArgs& a, cudaStream_t stream) {
+  return launch_pdl(route_grad_kernel<T, L, PER, V>, dim3((a.T + kGradWarps - 1) / kGradWarps), dim3(kGradWarps * 32), 0,
+                    stream, static_cast<const typename L::raw*>(a.logits), a.ldl, a.ids, a.w, a.dw, a.T, a.E, a.K, a.fn,
+                    a.renorm, a.over_scale, static_cast<typename T::raw*>(a.out), a.ldo, a.status);
 }
 
-template <class T>
-cudaError_t route_grad_by_size(const float* l, const int32_t* i, const float* w, const float* d, int T_, int E, int K, int s,
-                               int r, void* o, uint32_t* st, cudaStream_t q) {
-  const int per = (E + 31) / 32;
-  if (E % 4 == 0) {
-    if (per <= 4) return route_grad_launch<T, 4, 4>(l, i, w, d, T_, E, K, s, r, o, st, q);
-    if (per <= 8) return route_grad_launch<T, 8, 4>(l, i, w, d, T_, E, K, s, r, o, st, q);
-    if (per <= 16) return route_grad_launch<T, 16, 4>(l, i, w, d, T_, E, K, s, r, o, st, q);
-    return route_grad_launch<T, 32, 4>(l, i, w, d, T_, E, K, s, r, o, st, q);
+// Four logits (and gradients) at a time where every row starts on a boundary of four.
+template <class T, class L>
+cudaError_t route_grad_by_size(const GradArgs& a, cudaStream_t q) {
+  const int per = (a.E + 31) / 32;
+  const auto fours = [&](const void* p, long long ld, size_t size) {
+    return reinterpret_cast<uintptr_t>(p) % (4 * size) == 0 && (a.T <= 1 || ld % 4 == 0);
+  };
+  if (a.E % 4 == 0 && fours(a.logits, a.ldl, sizeof(typename L::raw)) && fours(a.out, a.ldo, sizeof(typename T::raw))) {
+    if (per <= 4) return route_grad_launch<T, L, 4, 4>(a, q);
+    if (per <= 8) return route_grad_launch<T, L, 8, 4>(a, q);
+    if (per <= 16) return route_grad_launch<T, L, 16, 4>(a, q);
+    return route_grad_launch<T, L, 32, 4>(a, q);
   }
-  if (per <= 4) return route_grad_launch<T, 4, 1>(l, i, w, d, T_, E, K, s, r, o, st, q);
-  if (per <= 16) return route_grad_launch<T, 16, 1>(l, i, w, d, T_, E, K, s, r, o, st, q);
-  return route_grad_launch<T, 32, 1>(l, i, w, d, T_, E, K, s, r, o, st, q);
+  if (per <= 4) return route_grad_launch<T, L, 4, 1>(a, q);
+  if (per <= 16) return route_grad_launch<T, L, 16, 1>(a, q);
+  return route_grad_launch<T, L, 32, 1>(a, q);
 }
 
 }  // namespace
 
-cudaError_t launch_route_grad(int dt, const float* logits, const int32_t* ids, const float* w, const float* dw, int T,
-                              int E, int K, int softmax, int renorm, void* out, uint32_t* status, cudaStream_t stream) {
+cudaError_t launch_route_grad(int ldt, RowsView logits, const int32_t* ids, const float* w, const float* dw, int T, int E,
+                              int K, int fn, int renorm, float scale, int dt, RowsView out, uint32_t* status,
+                              cudaStream_t stream) {
   if (T == 0) return cudaSuccess;
-  if (dt == kBf16) return route_grad_by_size<Bf16Elem>(logits, ids, w, dw, T, E, K, softmax, renorm, out, status, stream);
-  if (dt == kF16) return route_grad_by_size<F16Elem>(logits, ids, w, dw, T, E, K, softmax, renorm, out, status, stream);
-  return route_grad_by_size<F32Elem>(logits, ids, w, dw, T, E, K, softmax, renorm, out, status, stream);
+  const GradArgs a{logits.ptr, logits.ld, ids, w, dw, T, E, K, fn, renorm, 1.f / scale, out.ptr, out.ld, status};
+  if (ldt == kF32) {
+    if (dt == kBf16) return route_grad_by_size<Bf16Elem, F32Elem>(a, stream);
+    if (dt == kF16) return route_grad_by_size<F16Elem, F32Elem>(a, stream);
+    return route_grad_by_size<F32Elem, F32Elem>(a, stream);
+  }
+  if (dt == kBf16) return route_grad_by_size<Bf16Elem, Bf16Elem>(a, stream);
+  return route_grad_by_size<F16Elem, F16Elem>(a, stream);
 }
 
 }  // namespace moe

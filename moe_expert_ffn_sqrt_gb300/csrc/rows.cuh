@@ -105,4 +105,27 @@ __device__ __forceinline__ void store_part(typename T::raw* p, const Pack<T>& r,
     if (i >= from && i < to) p[i] = r.v[i];
 }
 
+// Expert e's rows in buffers of `rows` rows: cnt rows from row seg on (counts null: all of them).  Called by the whole
+// CTA; where `report`, a segment that would leave the buffers is recorded; it is cut in any case.
+__device__ __forceinline__ void expert_segment(const int32_t* counts, int e, int align, int rows, bool report, int& seg,
+                                               int& cnt, uint32_t* status) {
+  __shared__ unsigned long long s_seg;
+  seg = 0;
+  cnt = rows;
+  if (!counts) return;
+  if (threadIdx.x == 0) s_seg = 0;
+  __syncthreads();
+  int mine = 0;
+  for (int i = threadIdx.x; i < e; i += blockDim.x) {
+    const int c = min(max(__ldg(counts + i), 0), rows);
+    mine = min(mine + (c + align - 1) / align * align, rows);
+  }
+  if (mine) atomicAdd(&s_seg, static_cast<unsigned long long>(mine));   // integers: the order does not matter
+  __syncthreads();
+  seg = s_seg < static_cast<unsigned long long>(rows) ? static_cast<int>(s_seg) : rows;
+  const int c = __ldg(counts + e);
+  cnt = min(max(c, 0), rows - seg);
+  if (report && threadIdx.x == 0 && (c < 0 || c > cnt)) record_error(status, kDevErrIndex);
+}
+
 }  // namespace moe

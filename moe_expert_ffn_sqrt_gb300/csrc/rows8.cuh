@@ -1,0 +1,122 @@
+// Rows held in 8 bits: E4M3 codes with one UE8M0 scale per 128 columns, by the rule of moe_route's x_q and x_sf
+// (page "DeepSeek V4 MegaMoE Kernel 深度解析", 二 阶段 3: amax -> UE8M0 -> E4M3).
+//
+// Per group of 128 columns (the last one may be shorter) the scale is the smallest 2^e, e in [-127, 127], with
+// amax <= 448 * 2^e over the group's finite values (e = 0 where amax = 0); a value's code is v / 2^e rounded to the
+// nearest of E4M3 (ties to even, off by at most 2^-4 of the value, 2^-10 * 2^e below 2^-6 * 2^e).  An infinity or NaN
+// gets the NaN code: a conversion that saturated would pass an overflow on as a number.
+#pragma once
+#include <cuda_fp8.h>
+
+#include "rows.cuh"
+
+namespace moe {
+
+constexpr int kGroup8 = 128;
+__host__ __device__ __forceinline__ int groups8(int cols) { return (cols + kGroup8 - 1) / kGroup8; }
+
+// max |v| as far as it is finite (NaN compares false)
+__device__ __forceinline__ float finite_abs(float v) {
+  const float a = fabsf(v);
+  return a <= 3.402823466e38f ? a : 0.f;
+}
+__device__ __forceinline__ uint32_t code8x2(float a, float b, float inv) {
+  a = fabsf(a) <= 3.402823466e38f ? a * inv : __int_as_float(0x7fc00000);
+  b = fabsf(b) <= 3.402823466e38f ? b * inv : __int_as_float(0x7fc00000);
+  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+}
+
+// max over the lanes that hold a group: N columns per lane
+template <int N>
+__device__ __forceinline__ float group_max(float m) {
+#pragma unroll
+  for (int d = kGroup8 / N / 2; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  return m;
+}
+
+// Codes of N values (4 or 8) into N / 4 words.
+template <int N>
+__device__ __forceinline__ void codes8(const float (&v)[N], float inv, uint32_t (&w)[N / 4]) {
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i)
+    w[i] = code8x2(v[4 * i], v[4 * i + 1], inv) | (code8x2(v[4 * i + 2], v[4 * i + 3], inv) << 16);
+}
+
+// The first `n` of N codes to q (whole words where `words`: q on an N-byte boundary).
+template <int N>
+__device__ __forceinline__ void store_codes8(uint8_t* q, const uint32_t (&w)[N / 4], int n, bool words) {
+  if (words && n >= N) {
+    if constexpr (N == 8)
+      *reinterpret_cast<uint2*>(q) = make_uint2(w[0], w[1]);
+    else
+      *reinterpret_cast<uint32_t*>(q) = w[0];
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (i < n) q[i] = static_cast<uint8_t>(w[i / 4] >> (8 * (i % 4)));
+}
+
+// 2^(s - 127) of a scale byte (255, which no call here writes, is UE8M0's NaN).
+__device__ __forceinline__ float scale8(uint32_t s) {
+  return s == 255 ? __int_as_float(0x7fc00000) : s ? __uint_as_float(s << 23) : __uint_as_float(0x00400000u);
+}
+
+// Values of 4 codes.  Two codes to fp16 at a time is exact; so is the product with a power of two within fp32's range.
+__device__ __forceinline__ void values8(uint32_t w, float scale, float (&v)[4]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w >> (16 * i)), __NV_E4M3);
+    const float2 f = __half22float2(__half2(h));
+    v[2 * i] = f.x * scale;
+    v[2 * i + 1] = f.y * scale;
+  }
+}
+
+// A value of the 8-bit rows in type T: exact but for magnitudes past T's largest, which take it (a value of T whose
+// code rounded up to the next power of two: 65536 of fp16, 2^128 of bf16 and fp32).
+template <class T>
+__device__ __forceinline__ typename T::raw from_value8(float v);
+template <>
+__device__ __forceinline__ uint16_t from_value8<F16Elem>(float v) {
+  return F16Elem::from_f(fabsf(v) > 65504.f ? copysignf(65504.f, v) : v);
+}
+template <>
+__device__ __forceinline__ uint16_t from_value8<Bf16Elem>(float v) {
+  return Bf16Elem::from_f(isinf(v) ? copysignf(3.3895314e38f, v) : v);
+}
+template <>
+__device__ __forceinline__ float from_value8<F32Elem>(float v) {
+  return isinf(v) ? copysignf(3.402823466e38f, v) : v;
+}
+
+// N codes from q on (whole words where `words`); zeros past the first n.
+template <int N>
+__device__ __forceinline__ void load_codes8(const uint8_t* q, uint32_t (&w)[N / 4], int n, bool words) {
+  if (words && n >= N) {
+    if constexpr (N == 8) {
+      const uint2 u = *reinterpret_cast<const uint2*>(q);
+      w[0] = u.x;
+      w[1] = u.y;
+    } else {
+      w[0] = *reinterpret_cast<const uint32_t*>(q);
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i) w[i] = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (i < n) w[i / 4] |= static_cast<uint32_t>(q[i]) << (8 * (i % 4));
+}
+
+// Every row of a matrix on a 16-byte boundary (not given: true).
+inline bool rows_aligned(const RowsView& m, int rows, int dt) {
+  return !m.ptr || (reinterpret_cast<uintptr_t>(m.ptr) % 16 == 0 && (rows <= 1 || m.ld * dtype_bytes(dt) % 16 == 0));
+}
+// Every row's codes on an n-byte boundary.
+inline bool codes_aligned(const Rows8View& m, int rows, int n) {
+  return reinterpret_cast<uintptr_t>(m.q) % n == 0 && (rows <= 1 || m.ldq % n == 0);
+}
+
+}  // namespace moe

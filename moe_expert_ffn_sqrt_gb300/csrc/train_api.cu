@@ -1,5 +1,7 @@
-// C ABI of the training operators (declarations and contracts in include/moe.h): host-side checks,
-// workspace layout, and launches on the caller's stream.
+// C ABI of the training operators and of those in front of the layer (declarations and contracts in include/moe.h):
+// host-side checks, workspace layout, and launches on the caller's stream.
+#include <cmath>
+
 #include "../../include/moe.h"
 #include "kernels.h"
 
@@ -27,6 +29,21 @@ bool opt_rows_ok(const moe_rows& m, int cols, moe_dtype dt) { return !m.ptr || r
 bool rows16_ok(const moe_rows& m, int cols) { return rows_ok(m, cols, MOE_BF16) && m.ld % 8 == 0 && aligned(m.ptr, 16); }
 bool opt_rows16_ok(const moe_rows& m, int cols) { return !m.ptr || rows16_ok(m, cols); }
 
+// Rows of `cols` columns in 8 bits.
+bool rows8_ok(const moe_rows8& m, int cols) {
+  const int64_t groups = (static_cast<int64_t>(cols) + 127) / 128;
+  return m.q && m.sf && m.ldq >= cols && m.ldq <= kMaxLd && m.lds >= groups && m.lds <= kMaxLd;
+}
+bool opt_rows8_ok(const moe_rows8& m, int cols) { return (!m.q && !m.sf) || rows8_ok(m, cols); }
+inline Rows8View view8(const moe_rows8& m) {
+  return Rows8View{m.q, m.sf, static_cast<long long>(m.ldq), static_cast<long long>(m.lds)};
+}
+
+bool norm_dims_ok(int T, int H, float eps) { return T >= 0 && H >= 1 && H <= (1 << 24) && eps >= 0.f && std::isfinite(eps); }
+
+bool fn_ok(moe_score_fn fn) { return fn == MOE_SCORE_SOFTMAX || fn == MOE_SCORE_SQRT_SOFTPLUS || fn == MOE_SCORE_SIGMOID; }
+bool scale_ok(float s) { return std::isfinite(s) && std::isfinite(1.f / s); }
+
 // T tokens to K sorted rows each, of H columns, in buffers of U rows.
 bool sorted_dims_ok(int T, int K, int H, int U) {
   return T >= 0 && K >= 1 && K <= 32 && H >= 1 && U >= 0 && static_cast<long long>(T) * K <= 0x7fffffff;
@@ -36,6 +53,7 @@ bool pow2_align(int a) { return a >= 1 && a <= 256 && (a & (a - 1)) == 0; }
 
 struct LinearWs {
   size_t maps = 0, dz = 0, part = 0, total = 0;
+  size_t x = 0, total8 = 0;                    // with room for x unpacked from 8 bits
 };
 
 bool linear_dims_ok(int rows, int N, int K, int E, int act) {
@@ -46,7 +64,7 @@ bool linear_dims_ok(int rows, int N, int K, int E, int act) {
   return rows <= (1 << 28) && N <= (1 << 24) && K <= (1 << 24);
 }
 
-LinearWs linear_layout(int rows, int N, int E, int act) {
+LinearWs linear_layout(int rows, int N, int K, int E, int act) {
   LinearWs w;
   size_t off = kAlign;                         // [0, 256): status word
   w.maps = off;
@@ -56,6 +74,8 @@ LinearWs linear_layout(int rows, int N, int E, int act) {
   w.part = off;
   off = up(off + static_cast<size_t>(E > 0 ? E : 1) * linear_bias_slices(rows, N, E, act) * N * 4);
   w.total = off;
+  w.x = off;
+  w.total8 = up(off + static_cast<size_t>(rows) * K * 2);
   return w;
 }
 
@@ -152,13 +172,13 @@ moe_status moe_route_backward(const float* logits, const int32_t* topk_ids, cons
   if (!logits || !topk_ids || !topk_w || !dtopk_w || !dlogits) return MOE_ERR_INVALID_ARG;
   if (!aligned(logits, 16) || !aligned(dlogits, 16)) return MOE_ERR_INVALID_ARG;
   if (!ws || ws_bytes < kAlign) return MOE_ERR_WORKSPACE;
-  return cuda_status(launch_route_grad(dt, logits, topk_ids, topk_w, dtopk_w, T, E, K, fn == MOE_SCORE_SOFTMAX,
-                                       renormalize != 0, dlogits, status_of(ws), S(stream)));
+  return cuda_status(launch_route_grad(kF32, RowsView{const_cast<float*>(logits), E}, topk_ids, topk_w, dtopk_w, T, E, K, fn,
+                                       renormalize != 0, 1.f, dt, RowsView{dlogits, E}, status_of(ws), S(stream)));
 }
 
 moe_status moe_workspace_size_linear(int rows, int N, int K, int E, moe_act act, size_t* bytes) {
   if (!bytes || !linear_dims_ok(rows, N, K, E, act)) return MOE_ERR_INVALID_ARG;
-  *bytes = linear_layout(rows, N, E, act).total;
+  *bytes = linear_layout(rows, N, K, E, act).total;
   return MOE_OK;
 }
 
@@ -178,13 +198,23 @@ moe_status moe_linear(moe_dtype dt, moe_rows x, const void* w, const float* bias
                                    static_cast<char*>(ws) + kAlign, status_of(ws), S(stream)));
 }
 
-moe_status moe_linear_backward(moe_dtype dt, moe_rows dy, moe_rows x, const void* w, moe_rows z, moe_act act,
-                               const int32_t* expert_counts, int rows, int N, int K, int E, int align,
-                               moe_rows dx_residual, moe_rows dx, void* dw, float* dbias, void* ws, size_t ws_bytes,
-                               void* stream) {
+}  // extern "C"
+
+// moe_linear_backward and moe_linear_backward8: x and z each in 16 bits or in 8 (x8's rows those of x, or through ids).
+struct Kept8 {
+  moe_rows8 x, z;
+  const int32_t* ids;
+  int div, src_rows;
+};
+
+static moe_status linear_backward(moe_dtype dt, moe_rows dy, moe_rows x, const void* w, moe_rows z, const Kept8* k8,
+                                  moe_act act, const int32_t* expert_counts, int rows, int N, int K, int E, int align,
+                                  moe_rows dx_residual, moe_rows dx, void* dw, float* dbias, void* ws, size_t ws_bytes,
+                                  void* stream) {
   const moe_status st = linear_common(dt, expert_counts, rows, N, K, E, align, act, ws);
   if (st != MOE_OK) return st;
   const int cols = act == MOE_ACT_SWIGLU ? N / 2 : N;
+  const bool x8 = k8 && k8->x.q, z8 = k8 && k8->z.q;
   if (!dx.ptr && !dw && !dbias && rows > 0) return MOE_ERR_INVALID_ARG;
   if ((dw && !aligned(dw, 16)) || (dbias && !aligned(dbias, 16))) return MOE_ERR_INVALID_ARG;
   const int En = E > 0 ? E : 1;
@@ -193,28 +223,150 @@ moe_status moe_linear_backward(moe_dtype dt, moe_rows dy, moe_rows x, const void
     if (dbias && cudaMemsetAsync(dbias, 0, static_cast<size_t>(En) * N * 4, S(stream)) != cudaSuccess) return MOE_ERR_CUDA;
     return MOE_OK;
   }
-  if (!rows16_ok(dy, cols) || (act != MOE_ACT_NONE ? !rows16_ok(z, N) : z.ptr != nullptr)) return MOE_ERR_INVALID_ARG;
+  if (!rows16_ok(dy, cols)) return MOE_ERR_INVALID_ARG;
+  if (act == MOE_ACT_NONE ? z.ptr || z8 : z8 ? z.ptr || !rows8_ok(k8->z, N) : !rows16_ok(z, N)) return MOE_ERR_INVALID_ARG;
   if (dx.ptr && (!rows16_ok(dx, K) || !w || !aligned(w, 16))) return MOE_ERR_INVALID_ARG;
   if (!opt_rows16_ok(dx_residual, K) || (dx_residual.ptr && !dx.ptr)) return MOE_ERR_INVALID_ARG;
-  if (dw && !rows16_ok(x, K)) return MOE_ERR_INVALID_ARG;
-  const LinearWs L = linear_layout(rows, N, E, act);
-  if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
+  if (dw && (x8 ? x.ptr || !rows8_ok(k8->x, K) : !rows16_ok(x, K))) return MOE_ERR_INVALID_ARG;
+  const LinearWs L = linear_layout(rows, N, K, E, act);
+  if (ws_bytes < (x8 && dw ? L.total8 : L.total)) return MOE_ERR_WORKSPACE;
   const LinearShape p = linear_shape(dt, expert_counts, rows, N, K, E, align);
   char* base = static_cast<char*>(ws);
-  RowsView dz = view(dy);
+  RowsView dz = view(dy), xv = view(x);
   if (act != MOE_ACT_NONE) dz = RowsView{base + L.dz, N};
   if (act != MOE_ACT_NONE || dbias) {
-    if (launch_act_grad(p, view(dy), view(z), act, dz, reinterpret_cast<float*>(base + L.part), dbias, status_of(ws),
-                        S(stream)) != cudaSuccess)
+    if (launch_act_grad(p, view(dy), view(z), z8 ? view8(k8->z) : Rows8View{}, act, dz,
+                        reinterpret_cast<float*>(base + L.part), dbias, status_of(ws), S(stream)) != cudaSuccess)
       return MOE_ERR_CUDA;
   }
   if (dx.ptr && launch_linear_dx(p, dz, static_cast<const uint16_t*>(w), view(dx_residual), view(dx),
                                  base + L.maps, status_of(ws),
                                  S(stream)) != cudaSuccess)
     return MOE_ERR_CUDA;
-  if (dw && launch_linear_dw(p, dz, view(x), static_cast<uint16_t*>(dw), base + L.maps, status_of(ws), S(stream)) != cudaSuccess)
+  if (x8 && dw) {
+    xv = RowsView{base + L.x, K};
+    if (launch_unpack_rows8(dt, view8(k8->x), k8->ids, k8->div, k8->src_rows, expert_counts, rows, K, E, align, xv,
+                            status_of(ws), S(stream)) != cudaSuccess)
+      return MOE_ERR_CUDA;
+  }
+  if (dw && launch_linear_dw(p, dz, xv, static_cast<uint16_t*>(dw), base + L.maps, status_of(ws), S(stream)) != cudaSuccess)
     return MOE_ERR_CUDA;
   return MOE_OK;
+}
+
+extern "C" {
+
+moe_status moe_linear_backward(moe_dtype dt, moe_rows dy, moe_rows x, const void* w, moe_rows z, moe_act act,
+                               const int32_t* expert_counts, int rows, int N, int K, int E, int align,
+                               moe_rows dx_residual, moe_rows dx, void* dw, float* dbias, void* ws, size_t ws_bytes,
+                               void* stream) {
+  return linear_backward(dt, dy, x, w, z, nullptr, act, expert_counts, rows, N, K, E, align, dx_residual, dx, dw, dbias, ws,
+                         ws_bytes, stream);
+}
+
+moe_status moe_workspace_size_linear8(int rows, int N, int K, int E, moe_act act, size_t* bytes) {
+  if (!bytes || !linear_dims_ok(rows, N, K, E, act)) return MOE_ERR_INVALID_ARG;
+  *bytes = linear_layout(rows, N, K, E, act).total8;
+  return MOE_OK;
+}
+
+moe_status moe_linear_backward8(moe_dtype dt, moe_rows dy, moe_rows x, moe_rows8 x8, const int32_t* x_ids, int x_div,
+                                int x_rows, const void* w, moe_rows z, moe_rows8 z8, moe_act act,
+                                const int32_t* expert_counts, int rows, int N, int K, int E, int align,
+                                moe_rows dx_residual, moe_rows dx, void* dw, float* dbias, void* ws, size_t ws_bytes,
+                                void* stream) {
+  if (x_ids && (!x8.q || x_div < 1 || x_rows < 0)) return MOE_ERR_INVALID_ARG;
+  if (!opt_rows8_ok(x8, K) || !opt_rows8_ok(z8, N)) return MOE_ERR_INVALID_ARG;
+  const Kept8 k8{x8, z8, x_ids, x_ids ? x_div : 1, x_ids ? x_rows : rows};
+  return linear_backward(dt, dy, x, w, z, &k8, act, expert_counts, rows, N, K, E, align, dx_residual, dx, dw, dbias, ws,
+                         ws_bytes, stream);
+}
+
+moe_status moe_pack_rows8(moe_dtype dt, moe_rows x, const int32_t* expert_counts, int rows, int cols, int E, int align,
+                          moe_rows8 x8, void* ws, size_t ws_bytes, void* stream) {
+  if (!dtype_ok(dt) || rows < 0 || cols < 1 || cols > (1 << 24)) return MOE_ERR_INVALID_ARG;
+  if (E < 0 || E > kLinearMaxExperts || (E > 0) != (expert_counts != nullptr) || (E > 0 && !pow2_align(align)))
+    return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return MOE_OK;
+  if (!rows_ok(x, cols, dt) || !rows8_ok(x8, cols)) return MOE_ERR_INVALID_ARG;
+  if (expert_counts && (!ws || ws_bytes < kAlign)) return MOE_ERR_WORKSPACE;
+  return cuda_status(launch_pack_rows8(dt, view(x), expert_counts, rows, cols, E, align, view8(x8), status_of(ws), S(stream)));
+}
+
+moe_status moe_unpack_rows8(moe_dtype dt, moe_rows8 x8, const int32_t* x_ids, int x_div, int x_rows,
+                            const int32_t* expert_counts, int rows, int cols, int E, int align, moe_rows x, void* ws,
+                            size_t ws_bytes, void* stream) {
+  if (!dtype_ok(dt) || rows < 0 || cols < 1 || cols > (1 << 24)) return MOE_ERR_INVALID_ARG;
+  if (E < 0 || E > kLinearMaxExperts || (E > 0) != (expert_counts != nullptr) || (E > 0 && !pow2_align(align)))
+    return MOE_ERR_INVALID_ARG;
+  if (x_ids && (x_div < 1 || x_rows < 0)) return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return MOE_OK;
+  if (!rows_ok(x, cols, dt) || !rows8_ok(x8, cols)) return MOE_ERR_INVALID_ARG;
+  if ((expert_counts || x_ids) && (!ws || ws_bytes < kAlign)) return MOE_ERR_WORKSPACE;
+  return cuda_status(launch_unpack_rows8(dt, view8(x8), x_ids, x_div, x_rows, expert_counts, rows, cols, E, align, view(x),
+                                         status_of(ws), S(stream)));
+}
+
+moe_status moe_rms_norm(moe_dtype dt, moe_rows x, moe_rows residual, const float* weight, float eps, int T, int H,
+                        moe_rows sum, moe_rows y, moe_rows8 y8, void* stream) {
+  if (!dtype_ok(dt) || !norm_dims_ok(T, H, eps)) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (!rows_ok(x, H, dt) || !opt_rows_ok(residual, H, dt) || !opt_rows_ok(sum, H, dt) || !opt_rows_ok(y, H, dt))
+    return MOE_ERR_INVALID_ARG;
+  if (!opt_rows8_ok(y8, H) || (!sum.ptr && !y.ptr && !y8.q)) return MOE_ERR_INVALID_ARG;
+  if (!weight || !aligned(weight, 16)) return MOE_ERR_INVALID_ARG;
+  return cuda_status(launch_norm(dt, view(x), view(residual), weight, eps, T, H, view(sum), view(y), view8(y8), S(stream)));
+}
+
+moe_status moe_workspace_size_norm(int T, int H, size_t* bytes) {
+  if (!bytes || !norm_dims_ok(T, H, 0.f)) return MOE_ERR_INVALID_ARG;
+  *bytes = up(kAlign + norm_scratch_bytes(T, H));
+  return MOE_OK;
+}
+
+moe_status moe_rms_norm_backward(moe_dtype dt, moe_rows dy, moe_rows x, const float* weight, float eps, moe_rows dsum,
+                                 int T, int H, moe_rows dx, float* dweight, void* ws, size_t ws_bytes, void* stream) {
+  if (!dtype_ok(dt) || !norm_dims_ok(T, H, eps)) return MOE_ERR_INVALID_ARG;
+  if (!dx.ptr && !dweight && T > 0) return MOE_ERR_INVALID_ARG;
+  if (dweight && !aligned(dweight, 16)) return MOE_ERR_INVALID_ARG;
+  if (T == 0) {
+    if (dweight && cudaMemsetAsync(dweight, 0, static_cast<size_t>(H) * 4, S(stream)) != cudaSuccess) return MOE_ERR_CUDA;
+    return MOE_OK;
+  }
+  if (!rows_ok(dy, H, dt) || !rows_ok(x, H, dt) || !opt_rows_ok(dsum, H, dt) || !opt_rows_ok(dx, H, dt) ||
+      (dsum.ptr && !dx.ptr))
+    return MOE_ERR_INVALID_ARG;
+  if (!weight || !aligned(weight, 16)) return MOE_ERR_INVALID_ARG;
+  if (!ws || !aligned(ws, 16) || ws_bytes < up(kAlign + norm_scratch_bytes(T, H))) return MOE_ERR_WORKSPACE;
+  return cuda_status(launch_norm_grad(dt, view(dy), view(x), weight, eps, view(dsum), T, H, view(dx), dweight,
+                                      static_cast<char*>(ws) + kAlign, S(stream)));
+}
+
+moe_status moe_select(moe_dtype dt, moe_rows logits, const float* e_score_bias, int T, int E, int K, moe_select_rule rule,
+                      int32_t* topk_ids, float* topk_w, void* stream) {
+  if (!dtype_ok(dt) || !sorted_dims_ok(T, K, 1, 0) || E < 1 || E > 1024 || !fn_ok(rule.fn)) return MOE_ERR_INVALID_ARG;
+  if (rule.n_groups < 1 || rule.n_groups > 32 || E % rule.n_groups || rule.topk_groups < 1 ||
+      rule.topk_groups > rule.n_groups || rule.group_best < 1 || rule.group_best > 2 || !scale_ok(rule.scale))
+    return MOE_ERR_INVALID_ARG;
+  if (K > rule.topk_groups * (E / rule.n_groups)) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (!rows_ok(logits, E, dt) || !topk_ids || !topk_w) return MOE_ERR_INVALID_ARG;
+  const SelectRule r{rule.fn, rule.n_groups, rule.topk_groups, rule.group_best, rule.renormalize != 0, rule.scale};
+  return cuda_status(launch_select(dt, view(logits), e_score_bias, T, E, K, r, topk_ids, topk_w, S(stream)));
+}
+
+moe_status moe_select_backward(moe_dtype dt, moe_rows logits, const int32_t* topk_ids, const float* topk_w,
+                               const float* dtopk_w, int T, int E, int K, moe_score_fn fn, int renormalize, float scale,
+                               moe_dtype grad_dt, moe_rows dlogits, void* ws, size_t ws_bytes, void* stream) {
+  if (!dtype_ok(dt) || !dtype_ok(grad_dt) || !sorted_dims_ok(T, K, 1, 0) || E < 1 || E > 1024 || K > E)
+    return MOE_ERR_INVALID_ARG;
+  if (!fn_ok(fn) || !scale_ok(scale)) return MOE_ERR_INVALID_ARG;
+  if (dt != MOE_F32 && grad_dt != dt) return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (!rows_ok(logits, E, dt) || !topk_ids || !topk_w || !dtopk_w || !rows_ok(dlogits, E, grad_dt)) return MOE_ERR_INVALID_ARG;
+  if (!ws || ws_bytes < kAlign) return MOE_ERR_WORKSPACE;
+  return cuda_status(launch_route_grad(dt, view(logits), topk_ids, topk_w, dtopk_w, T, E, K, fn, renormalize != 0, scale,
+                                       grad_dt, view(dlogits), status_of(ws), S(stream)));
 }
 
 }  // extern "C"
