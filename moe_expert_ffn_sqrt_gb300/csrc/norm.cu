@@ -5,6 +5,8 @@
 //   g_i = dy_i w_i:   dx_i = r g_i - s_i r^3 mean(s g) + dsum_i;   dw_i = sum over rows of dy_i s_i r
 // Both are taken in fp32; each output is rounded once, the 8-bit rows (rows8.cuh) from the fp32 y.  One pass over a
 // row gives both of the backward's sums (s^2 and s g), so nothing but s is kept from the forward.
+#include <type_traits>
+
 #include "rows8.cuh"
 
 namespace moe {
@@ -19,7 +21,7 @@ struct NormArgs {
   const float* w;
   uint8_t *q, *sf;
   long long ldx, ldr, lds, ldy, ldq, ldsf;
-  float eps;
+  float eps, over_h;          // over_h: 1 / H
   int T, H;
   int q_words;                // codes in whole words
 };
@@ -44,6 +46,64 @@ __device__ __forceinline__ void block_sum(float (&v)[K], float (*sh)[K]) {
     for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], d);
 }
 
+// A pack as words: two 16-bit values are taken out of and put into a word at a time.  (As an array of 16-bit values the
+// compiler gives each a register of its own.)
+template <class T>
+struct Words {
+  static constexpr int N = Pack<T>::N;
+  uint32_t w[4];
+  __device__ __forceinline__ Words() : w{0, 0, 0, 0} {}
+  __device__ __forceinline__ Words(const Pack<T>& p) { memcpy(w, &p, 16); }
+  __device__ __forceinline__ operator Pack<T>() const {
+    Pack<T> p;
+    memcpy(&p, w, 16);
+    return p;
+  }
+  __device__ __forceinline__ float f(int j) const {
+    if constexpr (N == 4) return __uint_as_float(w[j]);
+    else if constexpr (std::is_same<T, Bf16Elem>::value)
+      return __uint_as_float(j & 1 ? w[j / 2] & 0xFFFF0000u : w[j / 2] << 16);
+    else {
+      const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w[j / 2]));
+      return j & 1 ? v.y : v.x;
+    }
+  }
+  // values j and j + 1, j even
+  __device__ __forceinline__ void set2(int j, float a, float b) {
+    if constexpr (N == 4) {
+      w[j] = __float_as_uint(a);
+      w[j + 1] = __float_as_uint(b);
+    } else if constexpr (std::is_same<T, Bf16Elem>::value) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+      w[j / 2] = *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+      const __half2 h = __floats2half2_rn(a, b);
+      w[j / 2] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+  }
+  // Each value plus o's, rounded to T.  (Two 16-bit values at a time, with one rounding; a sum in fp32 first would round to
+  // the same: it is exact unless the smaller value is below 2^-13 of the larger, which then stays what it is.)
+  __device__ __forceinline__ void add(const Words& o) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (N == 4) {
+        w[i] = __float_as_uint(__uint_as_float(w[i]) + __uint_as_float(o.w[i]));
+      } else if constexpr (std::is_same<T, Bf16Elem>::value) {
+        const __nv_bfloat162 h = __hadd2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]), *reinterpret_cast<const __nv_bfloat162*>(&o.w[i]));
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+      } else {
+        const __half2 h = __hadd2(*reinterpret_cast<const __half2*>(&w[i]), *reinterpret_cast<const __half2*>(&o.w[i]));
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+    }
+  }
+  // After this the compiler has the words alone: without it, it holds the values over a reduction, in twice the registers.
+  __device__ __forceinline__ void keep() {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) asm volatile("" : "+r"(w[i]));
+  }
+};
+
 // A matrix of rows of H columns.  AL: every row on a 16-byte boundary and H in whole packs.
 template <class T>
 struct Mat {
@@ -54,10 +114,16 @@ struct Mat {
       : lo(static_cast<raw*>(const_cast<void*>(p))), hi(lo + (rows - 1) * l + H), ld(l) {}
   // columns [c, c + N) of a row; zeros past its end
   template <bool AL>
-  __device__ __forceinline__ Pack<T> get(long long row, int c, int H) const {
+  __device__ __forceinline__ Words<T> get(long long row, int c, int H) const {
     const raw* p = lo + row * ld + c;
     if constexpr (AL) {
-      return load_pack<T>(p);
+      const uint4 u = *reinterpret_cast<const uint4*>(p);
+      Words<T> v;
+      v.w[0] = u.x;
+      v.w[1] = u.y;
+      v.w[2] = u.z;
+      v.w[3] = u.w;
+      return v;
     } else {
       ShiftedPack<T> s;
       s.load(p, lo, hi);
@@ -68,43 +134,187 @@ struct Mat {
       return v;
     }
   }
-  template <bool AL>
-  __device__ __forceinline__ void put(long long row, int c, int H, const Pack<T>& v) const {
-    raw* p = lo + row * ld + c;
-    if constexpr (AL) {
-      store_pack<T>(p, v);
-    } else {
-#pragma unroll
-      for (int i = 0; i < Pack<T>::N; ++i)
-        if (c + i < H) p[i] = v.v[i];
+};
+
+// Row pointers of the outputs (null: not wanted).
+template <class T>
+struct RowOut {
+  typename T::raw *sum, *y;
+  uint8_t *q, *sf;
+  __device__ __forceinline__ RowOut(const NormArgs& a, long long t)
+      : sum(static_cast<typename T::raw*>(a.sum)), y(static_cast<typename T::raw*>(a.y)), q(a.q), sf(a.sf) {
+    on(a, t);
+  }
+  __device__ __forceinline__ void on(const NormArgs& a, long long rows) {
+    if (sum) sum += rows * a.lds;
+    if (y) y += rows * a.ldy;
+    if (q) {
+      q += rows * a.ldq;
+      sf += rows * a.ldsf;
     }
   }
 };
-
-// One CTA per row.
 template <class T, bool AL>
-__global__ void __launch_bounds__(kNormThreads) norm_kernel(const NormArgs a) {
+__device__ __forceinline__ void put_words(typename T::raw* p, int left, const Words<T>& words) {
+  if constexpr (AL) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(words.w[0], words.w[1], words.w[2], words.w[3]);
+  } else {
+    const Pack<T> v = words;
+#pragma unroll
+    for (int i = 0; i < Pack<T>::N; ++i)
+      if (i < left) p[i] = v.v[i];
+  }
+}
+
+// The outputs of N values of y from column c of a row on (called by all lanes of a group of 128 columns).
+template <class T, bool AL>
+__device__ __forceinline__ void norm_out(const NormArgs& a, const RowOut<T>& row, int c, const float (&v)[Pack<T>::N]) {
+  constexpr int N = Pack<T>::N;
+  if (row.y && c < a.H) {
+    Words<T> o;
+#pragma unroll
+    for (int j = 0; j < N; j += 2) o.set2(j, v[j], v[j + 1]);
+    put_words<T, AL>(row.y + c, a.H - c, o);
+  }
+  if (row.q) {
+    uint32_t q[N / 4];
+    const uint32_t scale = encode8<N>(v, q);
+    if (c < a.H) {
+      store_codes8<N>(row.q + c, q, a.H - c, a.q_words);
+      if (c % kGroup8 == 0) row.sf[c / kGroup8] = static_cast<uint8_t>(scale);
+    }
+  }
+}
+
+// A row's packs over the threads that share it: pack i of thread `tid` is tid + i * threads.  A warp per row (WARP) or
+// the CTA; the CTA's sums meet in two buffers in turn, so that one barrier a row is enough.
+template <bool WARP, int K>
+__device__ __forceinline__ void row_sum(float (&v)[K], float (*sh)[32][K], int& turn) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1)
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], d);
+  if constexpr (!WARP) {
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, warps = blockDim.x / 32;
+    if (lane == 0)
+#pragma unroll
+      for (int k = 0; k < K; ++k) sh[turn][warp][k] = v[k];
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] = lane < warps ? sh[turn][lane][k] : 0.f;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+#pragma unroll
+      for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], d);
+    turn ^= 1;
+  }
+}
+
+// The thread's part of w (zeros past the row's end).
+template <class T, bool AL, int PER>
+__device__ __forceinline__ void weights(float (&w)[PER][Pack<T>::N], const float* g, int tid, int threads, int H) {
+  constexpr int N = Pack<T>::N;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int c = (tid + i * threads) * N;
+    if constexpr (AL) {
+#pragma unroll
+      for (int j = 0; j < N; j += 4) {
+        const float4 f = c < H ? __ldg(reinterpret_cast<const float4*>(g + c + j)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        w[i][j] = f.x;
+        w[i][j + 1] = f.y;
+        w[i][j + 2] = f.z;
+        w[i][j + 3] = f.w;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < N; ++j) w[i][j] = c + j < H ? __ldg(g + c + j) : 0.f;
+    }
+  }
+}
+
+// Rows in registers, PER packs a thread, NT threads at most, MIN CTAs per SM.  AHEAD: the next row's loads are on their way
+// while this one is worked on, and w stays in registers.
+template <class T, bool AL, int PER, bool WARP, int NT, int MIN, bool AHEAD>
+__global__ void __launch_bounds__(NT, MIN) norm_kernel(const NormArgs a) {
+  constexpr int N = Pack<T>::N;
+  __shared__ float sh[2][32][1];
+  const int H = a.H, threads = WARP ? 32 : blockDim.x, tid = WARP ? threadIdx.x % 32 : threadIdx.x;
+  const int rows = WARP ? blockDim.x / 32 : 1;            // rows of a CTA at a time
+  const long long step = static_cast<long long>(gridDim.x) * rows;
+  long long t = static_cast<long long>(blockIdx.x) * rows + (WARP ? threadIdx.x / 32 : 0);
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const Mat<T> x(a.x, a.ldx, a.T, H), r(a.res, a.ldr, a.T, H);
+  RowOut<T> out(a, t);
+  Words<T> px[PER], pr[PER];
+  auto fetch = [&](long long row) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int c = (tid + i * threads) * N;
+      px[i] = pr[i] = Words<T>{};
+      if (c < H && row < a.T) {
+        px[i] = x.template get<AL>(row, c, H);
+        if (a.res) pr[i] = r.template get<AL>(row, c, H);
+      }
+    }
+  };
+  if (AHEAD) fetch(t);
+  float w[PER][N];
+  weights<T, AL, PER>(w, a.w, tid, threads, H);
+  int turn = 0;
+  for (; t < a.T; t += step, out.on(a, step)) {
+    if (!AHEAD) fetch(t);
+    Words<T> p[PER];
+    float ss[1] = {0.f};
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int c = (tid + i * threads) * N;
+      p[i] = px[i];
+      if (a.res) p[i].add(pr[i]);
+      p[i].keep();
+      if (out.sum && c < H) put_words<T, AL>(out.sum + c, H - c, p[i]);
+#pragma unroll
+      for (int j = 0; j < N; ++j) ss[0] = fmaf(p[i].f(j), p[i].f(j), ss[0]);
+    }
+    if (AHEAD) fetch(t + step);
+    row_sum<WARP, 1>(ss, sh, turn);
+    if (!AHEAD) weights<T, AL, PER>(w, a.w, tid, threads, H);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) p[i].keep();
+    const float rs = rsqrtf(ss[0] * a.over_h + a.eps);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int c = (tid + i * threads) * N;
+      float v[N];
+#pragma unroll
+      for (int j = 0; j < N; ++j) v[j] = p[i].f(j) * rs * w[i][j];
+      norm_out<T, AL>(a, out, c, v);
+    }
+  }
+}
+
+// Rows too wide for registers: one CTA per row, which is read twice.
+template <class T, bool AL>
+__global__ void __launch_bounds__(kNormThreads) norm_wide_kernel(const NormArgs a) {
   constexpr int N = Pack<T>::N;
   __shared__ float sh[32][1];
   grid_dependency_wait();
   grid_launch_dependents();
   const long long t = blockIdx.x;
   const int H = a.H;
-  const Mat<T> x(a.x, a.ldx, a.T, H), r(a.res, a.ldr, a.T, H), s(a.sum, a.lds, a.T, H), y(a.y, a.ldy, a.T, H);
+  const Mat<T> x(a.x, a.ldx, a.T, H), r(a.res, a.ldr, a.T, H), s(a.sum, a.lds, a.T, H);
+  const RowOut<T> out(a, t);
   float ss[1] = {0.f};
   for (int c = threadIdx.x * N; c < H; c += kNormThreads * N) {
-    Pack<T> p = x.template get<AL>(t, c, H);
-    if (a.res) {
-      const Pack<T> q = r.template get<AL>(t, c, H);
-#pragma unroll
-      for (int i = 0; i < N; ++i) p.set(i, p.f(i) + q.f(i));
-    }
-    if (a.sum) s.template put<AL>(t, c, H, p);
+    Words<T> p = x.template get<AL>(t, c, H);
+    if (a.res) p.add(r.template get<AL>(t, c, H));
+    if (a.sum) put_words<T, AL>(out.sum + c, H - c, p);
 #pragma unroll
     for (int i = 0; i < N; ++i) ss[0] = fmaf(p.f(i), p.f(i), ss[0]);
   }
   block_sum<1>(ss, sh);
-  const float rs = rsqrtf(ss[0] / H + a.eps);
+  const float rs = rsqrtf(ss[0] * a.over_h + a.eps);
   const int whole = groups8(H) * kGroup8;      // (a group's lanes meet in group_max)
   for (int c0 = 0; c0 < whole; c0 += kNormThreads * N) {
     const int c = c0 + threadIdx.x * N;
@@ -112,37 +322,207 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const NormArgs a) {
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = 0.f;
     if (c < H) {
-      Pack<T> p;
+      Words<T> p;
       if (a.sum) {
         p = s.template get<AL>(t, c, H);
       } else {
         p = x.template get<AL>(t, c, H);
-        if (a.res) {
-          const Pack<T> q = r.template get<AL>(t, c, H);
-#pragma unroll
-          for (int i = 0; i < N; ++i) p.set(i, p.f(i) + q.f(i));
-        }
+        if (a.res) p.add(r.template get<AL>(t, c, H));
       }
 #pragma unroll
       for (int i = 0; i < N; ++i)
         if (AL || c + i < H) v[i] = p.f(i) * rs * __ldg(a.w + c + i);
-      if (a.y) {
+    }
+    norm_out<T, AL>(a, out, c, v);
+  }
+}
+
+// ------------------------------------------------------------------------------------------
+// Many rows on 16-byte boundaries: rows arrive in a ring of S shared-memory stages by bulk copies, and G groups of threads
+// take them in turn (row k of the CTA's is in stage k % S and group k % G's), each into registers, so that a group's
+// reductions run under the copies and the others' work.  One CTA per SM.
+// S is a multiple of G: then a stage is always the same group's, which has seen its last row arrive before it waits for the
+// next one.  (A group that waited for a row whose stage's last row, another group's, had not arrived yet would take the
+// barrier's older phase for the one it wants: copies of different rows may arrive in any order.)
+
+constexpr int kRingStages = 16, kRingGroups = 8;
+constexpr int kRingThreads = 960, kRingGradThreads = 608;       // of all groups, at most
+constexpr int kRingWarps = 30, kRingGradWarps = 16;             // of a group, at most
+constexpr int kRingBytes = 223 * 1024;                          // stages and w
+constexpr int kRingSmem = kRingBytes + 128;
+// Stages, if that makes enough of them: two a group in the backward, one (but two in all) in the forward.  What arrives much
+// ahead of the other SMs' rows costs the memory its locality: 16384 x 7168 with residual, two groups, 2 stages 160 us, 4 of
+// them 183; the backward of 8192 x 7168 (one group) 1 stage 95 us, 2 stages 75, 4 79.
+constexpr int kRingAhead = 60 * 1024;
+constexpr int kRingPer = 2;                                     // packs a thread
+
+struct Ring {
+  int G, threads, S;          // groups, threads of a group, stages
+};
+
+struct RingState {
+  uint64_t full[kRingStages], empty[kRingStages], w_full;
+};
+
+// The loading warp: `in` (n of them) hold rows of `bytes` bytes.
+template <int MOST>
+__device__ __forceinline__ void ring_load(const Ring& R, RingState& st, uint32_t smem, const void* const (&in)[MOST],
+                                          const long long (&ld)[MOST], int T, uint32_t bytes, const float* w, uint32_t wbytes) {
+  int n = 0;
 #pragma unroll
-        for (int i = 0; i < N; ++i) p.set(i, v[i]);
-        y.template put<AL>(t, c, H, p);
+  for (int i = 0; i < MOST; ++i) n += in[i] != nullptr;
+  mbar_arrive_expect_tx(smem_u32(&st.w_full), wbytes);
+  bulk_load(smem, w, wbytes, smem_u32(&st.w_full));
+  smem += wbytes;
+  int s = 0;
+  uint32_t ph = 0;
+  for (long long t = blockIdx.x; t < T; t += gridDim.x) {
+    // (a wait that runs out ends the copies; the groups' own waits for them then run out too)
+    if (!mbar_wait(smem_u32(&st.empty[s]), ph ^ 1, nullptr)) return;
+    const uint32_t bar = smem_u32(&st.full[s]);
+    mbar_arrive_expect_tx(bar, n * bytes);
+    uint32_t to = smem + s * n * bytes;
+#pragma unroll
+    for (int i = 0; i < MOST; ++i)
+      if (in[i]) {
+        bulk_load(to, static_cast<const uint8_t*>(in[i]) + t * ld[i], bytes, bar);
+        to += bytes;
+      }
+    if (++s == R.S) {
+      s = 0;
+      ph ^= 1;
+    }
+  }
+}
+
+__device__ __forceinline__ void ring_init(const Ring& R, RingState& st) {
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < R.S; ++s) {
+      mbar_init(smem_u32(&st.full[s]), 1);
+      mbar_init(smem_u32(&st.empty[s]), R.threads / 32);
+    }
+    mbar_init(smem_u32(&st.w_full), 1);
+    fence_barrier_init();
+  }
+}
+
+// A group's place in the ring: its k-th row's stage and the parity to wait for.
+struct RingPlace {
+  int s;
+  uint32_t ph;
+  __device__ __forceinline__ RingPlace(int k, int S) : s(k % S), ph((k / S) & 1) {}
+  __device__ __forceinline__ void on(int n, int S) {
+    s += n;
+    while (s >= S) {
+      s -= S;
+      ph ^= 1;
+    }
+  }
+};
+
+template <class T>
+__device__ __forceinline__ Words<T> shared_words(uint32_t addr) {
+  Words<T> v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.w[0]), "=r"(v.w[1]), "=r"(v.w[2]), "=r"(v.w[3])
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 shared_float4(uint32_t addr) {
+  float4 f;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(f.x), "=f"(f.y), "=f"(f.z), "=f"(f.w) : "r"(addr));
+  return f;
+}
+
+// Sum over a group of up to W warps of K values per thread, in a fixed order (sh: zeros where there is no warp); false: some thread's
+// `ok` was.
+template <int K, int W>
+__device__ __forceinline__ bool group_sum(float (&v)[K], float (*sh)[W], int group, int threads, int warp, int lane, bool ok) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1)
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], d);
+  if (lane == 0)
+#pragma unroll
+    for (int k = 0; k < K; ++k) sh[k][warp] = v[k];
+  ok = named_barrier_and(1 + group, threads, ok);
+#pragma unroll
+  for (int k = 0; k < K; ++k) v[k] = sh[k][lane % W];
+#pragma unroll
+  for (int d = W / 2; d > 0; d >>= 1)
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], d);
+  return ok;
+}
+
+template <class T>
+__global__ void __launch_bounds__(kRingThreads + 32, 1) norm_ring_kernel(const NormArgs a, const Ring R) {
+  constexpr int N = Pack<T>::N, PER = kRingPer;
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  __shared__ RingState st;
+  __shared__ __align__(16) float sh[kRingGroups][2][1][32];
+  const int H = a.H, lane = threadIdx.x % 32, group = threadIdx.x / R.threads, tid = threadIdx.x - group * R.threads;
+  const uint32_t smem = (smem_u32(smem_raw) + 127) & ~127u, bytes = H * 16 / N, wbytes = H * 4;
+  ring_init(R, st);
+  for (int i = threadIdx.x; i < kRingGroups * 2 * 32; i += blockDim.x) (&sh[0][0][0][0])[i] = 0.f;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  __syncthreads();
+  if (group == R.G) {
+    if (lane == 0) {
+      const void* in[2] = {a.x, a.res};
+      const long long ld[2] = {a.ldx * (16 / N), a.ldr * (16 / N)};
+      ring_load(R, st, smem, in, ld, a.T, bytes, a.w, wbytes);
+    }
+    return;
+  }
+  const uint32_t stage0 = smem + wbytes, stage = (a.res ? 2 : 1) * bytes;
+  bool ok = mbar_wait(smem_u32(&st.w_full), 0, nullptr);
+  RingPlace at(group, R.S);
+  int turn = 0;
+  const int first = blockIdx.x + group * gridDim.x, step = R.G * gridDim.x;
+  RowOut<T> out(a, first);
+  for (long long t = first; t < a.T; t += step, out.on(a, step), at.on(R.G, R.S), turn ^= 1) {
+    ok = mbar_wait(smem_u32(&st.full[at.s]), at.ph, nullptr) && ok;
+    const uint32_t from = stage0 + at.s * stage;
+    Words<T> p[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int c = (tid + i * R.threads) * N;
+      p[i] = Words<T>{};
+      if (c < H) {
+        p[i] = shared_words<T>(from + c * (16 / N));
+        if (a.res) p[i].add(shared_words<T>(from + bytes + c * (16 / N)));
       }
     }
-    if (a.q) {
-      float m = 0.f;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&st.empty[at.s]));
+    float ss[1] = {0.f};
 #pragma unroll
-      for (int i = 0; i < N; ++i) m = fmaxf(m, finite_abs(v[i]));
-      const int e = ue8m0_exponent(group_max<N>(m));
-      if (c < H) {
-        uint32_t w[N / 4];
-        codes8<N>(v, pow2_neg(e), w);
-        store_codes8<N>(a.q + t * a.ldq + c, w, H - c, a.q_words);
-        if (c % kGroup8 == 0) a.sf[t * a.ldsf + c / kGroup8] = static_cast<uint8_t>(e + 127);
+    for (int i = 0; i < PER; ++i) {
+      const int c = (tid + i * R.threads) * N;
+      if (out.sum && c < H) put_words<T, true>(out.sum + c, N, p[i]);
+#pragma unroll
+      for (int j = 0; j < N; ++j) ss[0] = fmaf(p[i].f(j), p[i].f(j), ss[0]);
+      p[i].keep();
+    }
+    ok = group_sum(ss, sh[group][turn], group, R.threads, tid / 32, lane, ok);
+    if (!ok) return;
+    const float rs = rsqrtf(ss[0] * a.over_h + a.eps);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int c = (tid + i * R.threads) * N;
+      float v[N];
+#pragma unroll
+      for (int j = 0; j < N; j += 4) {
+        const float4 w = c < H ? shared_float4(smem + (c + j) * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+        v[j] = p[i].f(j) * rs * w.x;
+        v[j + 1] = p[i].f(j + 1) * rs * w.y;
+        v[j + 2] = p[i].f(j + 2) * rs * w.z;
+        v[j + 3] = p[i].f(j + 3) * rs * w.w;
       }
+      norm_out<T, true>(a, out, c, v);
     }
   }
 }
@@ -153,22 +533,241 @@ struct NormGradArgs {
   const float* w;
   float *rs, *part;           // [T], [S, H]
   long long lddy, ldx, lddsum, lddx;
-  float eps;
+  float eps, over_h;
   int T, H;
 };
 
+// Rows in registers, as norm_kernel; a thread adds its columns' part of dw up over its rows (w: a CTA's sums to `part`).
+template <class T, bool AL, int PER, bool WARP, int NT, int MIN, bool AHEAD>
+__global__ void __launch_bounds__(NT, MIN) norm_grad_kernel(const NormGradArgs a) {
+  constexpr int N = Pack<T>::N;
+  __shared__ float sh[2][32][2];
+  __shared__ float meet[WARP ? NT / 32 : 1][WARP ? 32 * PER * N + 4 : 1];
+  const int H = a.H, threads = WARP ? 32 : blockDim.x, tid = WARP ? threadIdx.x % 32 : threadIdx.x;
+  const int rows = WARP ? blockDim.x / 32 : 1;
+  const long long step = static_cast<long long>(gridDim.x) * rows;
+  long long t = static_cast<long long>(blockIdx.x) * rows + (WARP ? threadIdx.x / 32 : 0);
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const Mat<T> dy(a.dy, a.lddy, a.T, H), x(a.x, a.ldx, a.T, H), ds(a.dsum, a.lddsum, a.T, H);
+  typename T::raw* dx = static_cast<typename T::raw*>(a.dx) + t * a.lddx;
+  Words<T> px[PER], pd[PER], pu[PER];
+  auto fetch = [&](long long row) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int c = (tid + i * threads) * N;
+      px[i] = pd[i] = pu[i] = Words<T>{};
+      if (c < H && row < a.T) {
+        px[i] = x.template get<AL>(row, c, H);
+        pd[i] = dy.template get<AL>(row, c, H);
+        if (a.dsum) pu[i] = ds.template get<AL>(row, c, H);
+      }
+    }
+  };
+  if (AHEAD) fetch(t);
+  float w[PER][N], acc[PER][N];
+  weights<T, AL, PER>(w, a.w, tid, threads, H);
+#pragma unroll
+  for (int i = 0; i < PER; ++i)
+#pragma unroll
+    for (int j = 0; j < N; ++j) acc[i][j] = 0.f;
+  int turn = 0;
+  for (; t < a.T; t += step, dx += step * a.lddx) {
+    if (!AHEAD) {
+      fetch(t);
+      weights<T, AL, PER>(w, a.w, tid, threads, H);
+    }
+    Words<T> p[PER], d[PER], u[PER];
+    float m[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      p[i] = px[i];
+      d[i] = pd[i];
+      u[i] = pu[i];
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        m[0] = fmaf(p[i].f(j), p[i].f(j), m[0]);
+        m[1] = fmaf(p[i].f(j), d[i].f(j) * w[i][j], m[1]);
+      }
+    }
+    if (AHEAD) fetch(t + step);
+    row_sum<WARP, 2>(m, sh, turn);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      p[i].keep();
+      d[i].keep();
+      u[i].keep();
+    }
+    const float rs = rsqrtf(m[0] * a.over_h + a.eps), k = m[1] * a.over_h * rs * rs;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int c = (tid + i * threads) * N;
+      Words<T> o;
+      float v[N];
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        acc[i][j] = fmaf(d[i].f(j), p[i].f(j) * rs, acc[i][j]);
+        v[j] = (d[i].f(j) * w[i][j] - p[i].f(j) * k) * rs;
+        if (a.dsum) v[j] += u[i].f(j);
+      }
+#pragma unroll
+      for (int j = 0; j < N; j += 2) o.set2(j, v[j], v[j + 1]);
+      if (a.dx && c < H) put_words<T, AL>(dx + c, H - c, o);
+    }
+  }
+  if (!a.part) return;
+  float* out = a.part + static_cast<size_t>(blockIdx.x) * H;
+  if constexpr (WARP) {
+    float* mine = meet[threadIdx.x / 32];
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+#pragma unroll
+      for (int j = 0; j < N; ++j) mine[(tid + i * 32) * N + j] = acc[i][j];
+    __syncthreads();
+    for (int c = threadIdx.x; c < H; c += blockDim.x) {
+      float v = 0.f;
+      for (int k = 0; k < rows; ++k) v += meet[k][c];
+      out[c] = v;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int c = (tid + i * threads) * N;
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        if (c + j < H) out[c + j] = acc[i][j];
+    }
+  }
+}
+
+// (the rows' sums and their use as in norm_ring_kernel)
+template <class T>
+__global__ void __launch_bounds__(kRingGradThreads + 32, 1) norm_grad_ring_kernel(const NormGradArgs a, const Ring R) {
+  constexpr int N = Pack<T>::N, PER = kRingPer;
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  __shared__ RingState st;
+  __shared__ __align__(16) float sh[kRingGroups][2][2][kRingGradWarps];
+  const int H = a.H, lane = threadIdx.x % 32, group = threadIdx.x / R.threads, tid = threadIdx.x - group * R.threads;
+  const uint32_t smem = (smem_u32(smem_raw) + 127) & ~127u, bytes = H * 16 / N, wbytes = H * 4;
+  ring_init(R, st);
+  for (int i = threadIdx.x; i < kRingGroups * 2 * 2 * kRingGradWarps; i += blockDim.x) (&sh[0][0][0][0])[i] = 0.f;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  __syncthreads();
+  if (group == R.G) {
+    if (lane == 0) {
+      const void* in[3] = {a.x, a.dy, a.dsum};
+      const long long ld[3] = {a.ldx * (16 / N), a.lddy * (16 / N), a.lddsum * (16 / N)};
+      ring_load(R, st, smem, in, ld, a.T, bytes, a.w, wbytes);
+    }
+    return;
+  }
+  const uint32_t stage0 = smem + wbytes, stage = (a.dsum ? 3 : 2) * bytes;
+  bool ok = mbar_wait(smem_u32(&st.w_full), 0, nullptr);
+  float acc[PER][N];
+#pragma unroll
+  for (int i = 0; i < PER; ++i)
+#pragma unroll
+    for (int j = 0; j < N; ++j) acc[i][j] = 0.f;
+  RingPlace at(group, R.S);
+  int turn = 0;
+  const int first = blockIdx.x + group * gridDim.x, step = R.G * gridDim.x;
+  typename T::raw* dx = static_cast<typename T::raw*>(a.dx) + first * a.lddx;
+  for (long long t = first; t < a.T; t += step, dx += step * a.lddx, at.on(R.G, R.S), turn ^= 1) {
+    ok = mbar_wait(smem_u32(&st.full[at.s]), at.ph, nullptr) && ok;
+    const uint32_t from = stage0 + at.s * stage;
+    Words<T> p[PER], d[PER], u[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int c = (tid + i * R.threads) * N;
+      p[i] = d[i] = u[i] = Words<T>{};
+      if (c < H) {
+        p[i] = shared_words<T>(from + c * (16 / N));
+        d[i] = shared_words<T>(from + bytes + c * (16 / N));
+        if (a.dsum) u[i] = shared_words<T>(from + 2 * bytes + c * (16 / N));
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&st.empty[at.s]));
+    float m[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int c = (tid + i * R.threads) * N;
+#pragma unroll
+      for (int j = 0; j < N; j += 4) {
+        const float4 w = c < H ? shared_float4(smem + (c + j) * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+        const float wj[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          m[0] = fmaf(p[i].f(j + k), p[i].f(j + k), m[0]);
+          m[1] = fmaf(p[i].f(j + k), d[i].f(j + k) * wj[k], m[1]);
+        }
+      }
+      p[i].keep();
+      d[i].keep();
+      u[i].keep();
+    }
+    ok = group_sum(m, sh[group][turn], group, R.threads, tid / 32, lane, ok);
+    if (!ok) break;
+    const float rs = rsqrtf(m[0] * a.over_h + a.eps), k = m[1] * a.over_h * rs * rs;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int c = (tid + i * R.threads) * N;
+      Words<T> o;
+#pragma unroll
+      for (int j = 0; j < N; j += 4) {
+        const float4 w = c < H ? shared_float4(smem + (c + j) * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+        const float wj[4] = {w.x, w.y, w.z, w.w};
+        float v[4];
+#pragma unroll
+        for (int l = 0; l < 4; ++l) {
+          const float f = p[i].f(j + l), g = d[i].f(j + l);
+          acc[i][j + l] = fmaf(g, f * rs, acc[i][j + l]);
+          v[l] = (g * wj[l] - f * k) * rs;
+          if (a.dsum) v[l] += u[i].f(j + l);
+        }
+        o.set2(j, v[0], v[1]);
+        o.set2(j + 2, v[2], v[3]);
+      }
+      if (a.dx && c < H) put_words<T, true>(dx + c, N, o);
+    }
+  }
+  if (!a.part) return;
+  // the groups' sums meet where the stages were: every group has taken its last row out of them
+  const int all = R.G * R.threads;
+  named_barrier(15, all);
+  float* meet = reinterpret_cast<float*>(smem_raw + (stage0 - smem_u32(smem_raw)));
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int c = (tid + i * R.threads) * N;
+    if (c < H)
+#pragma unroll
+      for (int j = 0; j < N; j += 4)
+        *reinterpret_cast<float4*>(meet + static_cast<size_t>(group) * H + c + j) = make_float4(acc[i][j], acc[i][j + 1], acc[i][j + 2], acc[i][j + 3]);
+  }
+  named_barrier(15, all);
+  for (int c = threadIdx.x * 4; c < H; c += all * 4) {
+    float4 v = *reinterpret_cast<const float4*>(meet + c);
+    for (int k = 1; k < R.G; ++k) {
+      const float4 o = *reinterpret_cast<const float4*>(meet + static_cast<size_t>(k) * H + c);
+      v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
+    }
+    *reinterpret_cast<float4*>(a.part + static_cast<size_t>(blockIdx.x) * H + c) = v;
+  }
+}
+
 template <class T, bool AL>
-__global__ void __launch_bounds__(kNormThreads) norm_grad_kernel(const NormGradArgs a) {
+__global__ void __launch_bounds__(kNormThreads) norm_grad_wide_kernel(const NormGradArgs a) {
   constexpr int N = Pack<T>::N;
   __shared__ float sh[32][2];
   grid_dependency_wait();
   grid_launch_dependents();
   const long long t = blockIdx.x;
   const int H = a.H;
-  const Mat<T> dy(a.dy, a.lddy, a.T, H), x(a.x, a.ldx, a.T, H), ds(a.dsum, a.lddsum, a.T, H), dx(a.dx, a.lddx, a.T, H);
+  const Mat<T> dy(a.dy, a.lddy, a.T, H), x(a.x, a.ldx, a.T, H), ds(a.dsum, a.lddsum, a.T, H);
   float m[2] = {0.f, 0.f};
   for (int c = threadIdx.x * N; c < H; c += kNormThreads * N) {
-    const Pack<T> p = x.template get<AL>(t, c, H), d = dy.template get<AL>(t, c, H);
+    const Words<T> p = x.template get<AL>(t, c, H), d = dy.template get<AL>(t, c, H);
 #pragma unroll
     for (int i = 0; i < N; ++i)
       if (AL || c + i < H) {
@@ -177,27 +776,29 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_kernel(const NormGradA
       }
   }
   block_sum<2>(m, sh);
-  const float rs = rsqrtf(m[0] / H + a.eps), k = m[1] / H * rs * rs;
+  const float rs = rsqrtf(m[0] * a.over_h + a.eps), k = m[1] * a.over_h * rs * rs;
   if (threadIdx.x == 0) a.rs[t] = rs;
   if (!a.dx) return;
   for (int c = threadIdx.x * N; c < H; c += kNormThreads * N) {
-    const Pack<T> p = x.template get<AL>(t, c, H), d = dy.template get<AL>(t, c, H);
-    Pack<T> o, u;
+    const Words<T> p = x.template get<AL>(t, c, H), d = dy.template get<AL>(t, c, H);
+    Words<T> o, u;
     if (a.dsum) u = ds.template get<AL>(t, c, H);
+    float v[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      float v = 0.f;
-      if (AL || c + i < H) v = (d.f(i) * __ldg(a.w + c + i) - p.f(i) * k) * rs;
-      if (a.dsum) v += u.f(i);
-      o.set(i, v);
+      v[i] = 0.f;
+      if (AL || c + i < H) v[i] = (d.f(i) * __ldg(a.w + c + i) - p.f(i) * k) * rs;
+      if (a.dsum) v[i] += u.f(i);
     }
-    dx.template put<AL>(t, c, H, o);
+#pragma unroll
+    for (int i = 0; i < N; i += 2) o.set2(i, v[i], v[i + 1]);
+    put_words<T, AL>(static_cast<typename T::raw*>(a.dx) + t * a.lddx + c, H - c, o);
   }
 }
 
 // Partial sums of dw over rows blockIdx.y, + gridDim.y, ...; thread = column.
 template <class T>
-__global__ void __launch_bounds__(256) norm_dw_kernel(const NormGradArgs a) {
+__global__ void __launch_bounds__(256) norm_dw_wide_kernel(const NormGradArgs a) {
   using raw = typename T::raw;
   grid_dependency_wait();
   grid_launch_dependents();
@@ -210,40 +811,163 @@ __global__ void __launch_bounds__(256) norm_dw_kernel(const NormGradArgs a) {
   a.part[static_cast<size_t>(blockIdx.y) * a.H + c] = s;
 }
 
-__global__ void __launch_bounds__(256) norm_dw_sum_kernel(const float* __restrict__ part, int S, int H, float* __restrict__ dw) {
+// dw from its S partial sums: a CTA has 32 columns, each of its 32 warps every 32nd slice.
+__global__ void __launch_bounds__(1024) norm_dw_sum_kernel(const float* __restrict__ part, int S, int H, float* __restrict__ dw) {
+  __shared__ float sh[32][33];
   grid_dependency_wait();
   grid_launch_dependents();
-  const int c = blockIdx.x * 256 + threadIdx.x;
-  if (c >= H) return;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, c = blockIdx.x * 32 + lane;
   float s = 0.f;
-  for (int k = 0; k < S; ++k) s += part[static_cast<size_t>(k) * H + c];
-  dw[c] = s;
-}
-
-template <class T>
-cudaError_t norm_launch(const NormArgs& a, bool al, cudaStream_t stream) {
-  return launch_pdl(al ? norm_kernel<T, true> : norm_kernel<T, false>, dim3(a.T), dim3(kNormThreads), 0, stream, a);
-}
-
-int norm_slices(int T) { return T < 64 ? (T < 1 ? 1 : T) : 64; }
-
-// The gradient of w first: dx may take the place of what it reads.
-template <class T>
-cudaError_t norm_grad_launch(NormGradArgs a, bool al, float* dw, cudaStream_t stream) {
-  const auto kernel = al ? norm_grad_kernel<T, true> : norm_grad_kernel<T, false>;
-  void* dx = a.dx;
-  if (dw) {
-    a.dx = nullptr;
-    cudaError_t err = launch_pdl(kernel, dim3(a.T), dim3(kNormThreads), 0, stream, a);
-    if (err != cudaSuccess) return err;
-    const int S = norm_slices(a.T), blocks = (a.H + 255) / 256;
-    err = launch_pdl(norm_dw_kernel<T>, dim3(blocks, S), dim3(256), 0, stream, a);
-    if (err != cudaSuccess) return err;
-    err = launch_pdl(norm_dw_sum_kernel, dim3(blocks), dim3(256), 0, stream, static_cast<const float*>(a.part), S, a.H, dw);
-    if (err != cudaSuccess) return err;
+  if (c < H) {
+#pragma unroll 5
+    for (int k = warp; k < S; k += 32) s += part[static_cast<size_t>(k) * H + c];
   }
-  a.dx = dx;
-  return dx ? launch_pdl(kernel, dim3(a.T), dim3(kNormThreads), 0, stream, a) : cudaSuccess;
+  sh[warp][lane] = s;
+  __syncthreads();
+  s = sh[lane][warp];
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+  if (lane == 0 && blockIdx.x * 32 + warp < H) dw[blockIdx.x * 32 + warp] = s;
+}
+
+// How rows of `packs` packs run: a warp each with one or a few packs a lane; CTAs of up to 512 threads with two packs;
+// CTAs of up to 1024 threads with one pack (few rows, each over as many threads as it can fill) or with two; or by the
+// kernels for wide rows.
+enum NormPlanKind { kWarpOne, kWarpMore, kCta, kCtaFew, kCtaMost, kWide, kRing };
+struct NormPlan {
+  NormPlanKind kind;
+  int threads, grid;
+  Ring ring;
+};
+// most: packs that a warp takes; resident: CTAs of 512 threads per SM; ring_threads, ring_warps, ring_stages: threads of
+// the ring's kernels and warps of a group at most, and a group's stages at least; inputs: rows of a stage (0: rows that are not on 16-byte boundaries).
+NormPlan norm_plan(int T, int H, int dt, int most, int resident, int ring_threads, int ring_warps, int ring_stages, int inputs) {
+  const int packs = static_cast<int>((static_cast<long long>(H) * dtype_bytes(dt) + 15) / 16), sms = num_sms();
+  NormPlan p{kWide, kNormThreads, T, Ring{1, 0, 0}};
+  if (packs <= 32 || (packs <= most && T >= 2 * sms)) {
+    p.kind = packs <= 32 ? kWarpOne : kWarpMore;
+    const int warps = T >= 16 * sms ? 8 : T >= 8 * sms ? 4 : T >= 4 * sms ? 2 : 1;       // (few rows: over all SMs)
+    p.threads = 32 * warps;
+    const int ctas = (T + warps - 1) / warps, all = sms * 16 * resident / warps;
+    p.grid = ctas < all ? ctas : all;
+    return p;
+  }
+  if (inputs && packs <= kRingPer * 32 * ring_warps && T > sms) {
+    p.ring.threads = ((packs + kRingPer - 1) / kRingPer + 31) / 32 * 32;
+    const int stage = inputs * packs * 16, fit = (kRingBytes - H * 4) / stage;
+    int G = ring_threads / p.ring.threads;
+    if (G > kRingGroups) G = kRingGroups;
+    if (G > fit) G = fit;
+    if (G > 0) {
+      int S = kRingAhead / stage;
+      if (S < ring_stages * G) S = ring_stages * G;
+      if (S < 2) S = 2;
+      if (S > fit) S = fit;
+      if (S > kRingStages) S = kRingStages;
+      p.kind = kRing;
+      p.ring.G = G;
+      p.ring.S = S / G * G;
+      p.threads = G * p.ring.threads + 32;
+      p.grid = sms;
+      return p;
+    }
+  }
+  int per = 2;
+  if (packs <= 1024 && T <= sms) {
+    p.kind = kCtaFew;
+    per = resident = 1;
+  } else if (packs <= 1024) {
+    p.kind = kCta;
+  } else if (packs <= 2048) {
+    p.kind = kCtaMost;
+    resident = 1;
+  } else {
+    return p;
+  }
+  p.threads = ((packs + per - 1) / per + 31) / 32 * 32;
+  if (p.kind == kCta) resident = resident * 512 / p.threads;
+  const int all = sms * resident;
+  p.grid = T < all ? T : all;
+  return p;
+}
+NormPlan norm_forward_plan(int T, int H, int dt, int inputs) {
+  return norm_plan(T, H, dt, 128, 2, kRingThreads, kRingWarps, 1, inputs);
+}
+NormPlan norm_grad_plan(int T, int H, int dt, int inputs) {
+  return norm_plan(T, H, dt, 64, 1, kRingGradThreads, kRingGradWarps, 2, inputs);
+}
+
+template <class K, class A>
+cudaError_t ring_launch(K kernel, const A& a, const NormPlan& p, std::atomic<unsigned long long>& done, cudaStream_t stream) {
+  const cudaError_t err = allow_smem(reinterpret_cast<const void*>(kernel), kRingSmem, done);
+  if (err != cudaSuccess) return err;
+  return launch_pdl(kernel, dim3(p.grid), dim3(p.threads), kRingSmem, stream, a, p.ring);
+}
+
+template <class T, bool AL>
+cudaError_t norm_launch(const NormArgs& a, const NormPlan& p, cudaStream_t stream) {
+  const auto go = [&](auto kernel) { return launch_pdl(kernel, dim3(p.grid), dim3(p.threads), 0, stream, a); };
+  if constexpr (AL) {
+    static std::atomic<unsigned long long> done{0};
+    if (p.kind == kRing) return ring_launch(norm_ring_kernel<T>, a, p, done, stream);
+  }
+  switch (p.kind) {
+    case kWarpOne: return go(norm_kernel<T, AL, 1, true, 256, 4, true>);
+    case kWarpMore: return go(norm_kernel<T, AL, 4, true, 256, 2, true>);
+    case kCta:                                          // (with rows on 16-byte boundaries the ring's)
+      if constexpr (!AL) return go(norm_kernel<T, AL, 2, false, 512, 2, true>);
+      return cudaErrorInvalidValue;
+    case kCtaFew: return go(norm_kernel<T, AL, 1, false, 1024, 1, false>);
+    case kCtaMost: return go(norm_kernel<T, AL, 2, false, 1024, 1, false>);
+    default: return go(norm_wide_kernel<T, AL>);
+  }
+}
+
+int norm_slices(int T) { return T < 64 ? (T < 1 ? 1 : T) : 64; }      // of the wide rows' kernels
+
+template <class T, bool AL>
+cudaError_t norm_grad_launch(NormGradArgs a, const NormPlan& p, float* dw, cudaStream_t stream) {
+  cudaError_t err;
+  int slices = p.grid;
+  if (p.kind == kRing) {
+    if (!dw) a.part = nullptr;
+    err = cudaErrorInvalidValue;
+    if constexpr (AL) {
+      static std::atomic<unsigned long long> done{0};
+      err = ring_launch(norm_grad_ring_kernel<T>, a, p, done, stream);
+    }
+  } else if (p.kind == kWide) {
+    // the gradient of w first: dx may take the place of what it reads
+    slices = norm_slices(a.T);
+    void* dx = a.dx;
+    if (dw) {
+      a.dx = nullptr;
+      err = launch_pdl(norm_grad_wide_kernel<T, AL>, dim3(a.T), dim3(kNormThreads), 0, stream, a);
+      if (err != cudaSuccess) return err;
+      err = launch_pdl(norm_dw_wide_kernel<T>, dim3((a.H + 255) / 256, slices), dim3(256), 0, stream, a);
+      if (err != cudaSuccess) return err;
+    }
+    a.dx = dx;
+    err = dx ? launch_pdl(norm_grad_wide_kernel<T, AL>, dim3(a.T), dim3(kNormThreads), 0, stream, a) : cudaSuccess;
+  } else {
+    if (!dw) a.part = nullptr;
+    else if (slices == 1) a.part = dw;
+    const auto go = [&](auto kernel) { return launch_pdl(kernel, dim3(p.grid), dim3(p.threads), 0, stream, a); };
+    switch (p.kind) {
+      case kWarpOne: err = go(norm_grad_kernel<T, AL, 1, true, 256, 2, true>); break;
+      case kWarpMore: err = go(norm_grad_kernel<T, AL, 2, true, 256, 2, true>); break;
+      case kCta:
+        err = cudaErrorInvalidValue;
+        if constexpr (!AL) err = go(norm_grad_kernel<T, AL, 2, false, 512, 1, true>);
+        break;
+      case kCtaFew: err = go(norm_grad_kernel<T, AL, 1, false, 1024, 1, false>); break;
+      default: err = go(norm_grad_kernel<T, AL, 2, false, 1024, 1, false>); break;
+    }
+    if (slices == 1) return err;
+  }
+  if (err != cudaSuccess || !dw) return err;
+  return launch_pdl(norm_dw_sum_kernel, dim3((a.H + 31) / 32), dim3(1024), 0, stream, static_cast<const float*>(a.part), slices,
+                    a.H, dw);
 }
 
 }  // namespace
@@ -265,19 +989,30 @@ cudaError_t launch_norm(int dt, RowsView x, RowsView res, const float* w, float 
   a.ldq = y8.ldq;
   a.ldsf = y8.lds;
   a.eps = eps;
+  a.over_h = 1.f / static_cast<float>(H);
   a.T = T;
   a.H = H;
   const int n = static_cast<int>(16 / dtype_bytes(dt));
   a.q_words = codes_aligned(y8, T, n);
   const bool al = H % n == 0 && rows_aligned(x, T, dt) && rows_aligned(res, T, dt) && rows_aligned(sum, T, dt) &&
                   rows_aligned(y, T, dt);
-  if (dt == kBf16) return norm_launch<Bf16Elem>(a, al, stream);
-  if (dt == kF16) return norm_launch<F16Elem>(a, al, stream);
-  return norm_launch<F32Elem>(a, al, stream);
+  const NormPlan p = norm_forward_plan(T, H, dt, al ? 1 + (res.ptr != nullptr) : 0);
+  if (dt == kBf16) return al ? norm_launch<Bf16Elem, true>(a, p, stream) : norm_launch<Bf16Elem, false>(a, p, stream);
+  if (dt == kF16) return al ? norm_launch<F16Elem, true>(a, p, stream) : norm_launch<F16Elem, false>(a, p, stream);
+  return al ? norm_launch<F32Elem, true>(a, p, stream) : norm_launch<F32Elem, false>(a, p, stream);
 }
 
+// The wide rows' reciprocal roots [T], then the partial sums of dw.  The types' plans differ: room for any.
 size_t norm_scratch_bytes(int T, int H) {
-  return (static_cast<size_t>(T) * 4 + 255) / 256 * 256 + static_cast<size_t>(norm_slices(T)) * H * 4;
+  size_t slices = 1;
+  for (int dt = kBf16; dt <= kF32; ++dt) {
+    for (int inputs = 0; inputs <= 3; inputs += 3) {
+      const NormPlan p = norm_grad_plan(T, H, dt, inputs);
+      const size_t n = static_cast<size_t>(p.kind == kWide ? norm_slices(T) : p.grid);
+      if (n > slices) slices = n;
+    }
+  }
+  return (static_cast<size_t>(T) * 4 + 255) / 256 * 256 + slices * H * 4;
 }
 
 cudaError_t launch_norm_grad(int dt, RowsView dy, RowsView x, const float* w, float eps, RowsView dsum, int T, int H,
@@ -295,14 +1030,16 @@ cudaError_t launch_norm_grad(int dt, RowsView dy, RowsView x, const float* w, fl
   a.lddsum = dsum.ld;
   a.lddx = dx.ld;
   a.eps = eps;
+  a.over_h = 1.f / static_cast<float>(H);
   a.T = T;
   a.H = H;
   const int n = static_cast<int>(16 / dtype_bytes(dt));
   const bool al = H % n == 0 && rows_aligned(dy, T, dt) && rows_aligned(x, T, dt) && rows_aligned(dsum, T, dt) &&
                   rows_aligned(dx, T, dt);
-  if (dt == kBf16) return norm_grad_launch<Bf16Elem>(a, al, dw, stream);
-  if (dt == kF16) return norm_grad_launch<F16Elem>(a, al, dw, stream);
-  return norm_grad_launch<F32Elem>(a, al, dw, stream);
+  const NormPlan p = norm_grad_plan(T, H, dt, al ? 2 + (dsum.ptr != nullptr) : 0);
+  if (dt == kBf16) return al ? norm_grad_launch<Bf16Elem, true>(a, p, dw, stream) : norm_grad_launch<Bf16Elem, false>(a, p, dw, stream);
+  if (dt == kF16) return al ? norm_grad_launch<F16Elem, true>(a, p, dw, stream) : norm_grad_launch<F16Elem, false>(a, p, dw, stream);
+  return al ? norm_grad_launch<F32Elem, true>(a, p, dw, stream) : norm_grad_launch<F32Elem, false>(a, p, dw, stream);
 }
 
 }  // namespace moe

@@ -50,15 +50,11 @@ __global__ void __launch_bounds__(kRows8Threads) pack_rows8_kernel(const Rows8Ar
       for (int i = 0; i < N; ++i)
         if (AL || c + i < a.cols) v[i] = p.f(i);
     }
-    float m = 0.f;
-#pragma unroll
-    for (int i = 0; i < N; ++i) m = fmaxf(m, finite_abs(v[i]));
-    const int e = ue8m0_exponent(group_max<N>(m));
+    uint32_t w[N / 4];
+    const uint32_t scale = encode8<N>(v, w);
     if (live) {
-      uint32_t w[N / 4];
-      codes8<N>(v, pow2_neg(e), w);
       store_codes8<N>(a.q + row * a.ldq + c, w, a.cols - c, a.words);
-      if (lane == 0) a.sf[row * a.ldsf + g] = static_cast<uint8_t>(e + 127);
+      if (lane == 0) a.sf[row * a.ldsf + g] = static_cast<uint8_t>(scale);
     }
   }
 }

@@ -15,17 +15,6 @@ namespace moe {
 constexpr int kGroup8 = 128;
 __host__ __device__ __forceinline__ int groups8(int cols) { return (cols + kGroup8 - 1) / kGroup8; }
 
-// max |v| as far as it is finite (NaN compares false)
-__device__ __forceinline__ float finite_abs(float v) {
-  const float a = fabsf(v);
-  return a <= 3.402823466e38f ? a : 0.f;
-}
-__device__ __forceinline__ uint32_t code8x2(float a, float b, float inv) {
-  a = fabsf(a) <= 3.402823466e38f ? a * inv : __int_as_float(0x7fc00000);
-  b = fabsf(b) <= 3.402823466e38f ? b * inv : __int_as_float(0x7fc00000);
-  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-}
-
 // max over the lanes that hold a group: N columns per lane
 template <int N>
 __device__ __forceinline__ float group_max(float m) {
@@ -34,12 +23,40 @@ __device__ __forceinline__ float group_max(float m) {
   return m;
 }
 
-// Codes of N values (4 or 8) into N / 4 words.
+// Codes (N / 4 words) and scale byte of a group's values, N (4 or 8) in each of its 128 / N lanes; called by whole warps.
+// The maximum skips NaN by itself, and a NaN's conversion is the NaN code: only an infinity, which shows in the maximum,
+// takes another look.  For amax = (1 + m / 2^23) 2^(x - 127) the exponent is x - 135, one more where m > 0x600000 (448 is
+// 1.75 * 2^8); it is at most 120, so that 2^-e is a normal number.
 template <int N>
-__device__ __forceinline__ void codes8(const float (&v)[N], float inv, uint32_t (&w)[N / 4]) {
+__device__ __forceinline__ uint32_t encode8(const float (&value)[N], uint32_t (&w)[N / 4]) {
+  float v[N], m = 0.f;
 #pragma unroll
-  for (int i = 0; i < N / 4; ++i)
-    w[i] = code8x2(v[4 * i], v[4 * i + 1], inv) | (code8x2(v[4 * i + 2], v[4 * i + 3], inv) << 16);
+  for (int i = 0; i < N; ++i) {
+    v[i] = value[i];
+    m = fmaxf(m, fabsf(v[i]));
+  }
+  m = group_max<N>(m);
+  if (__any_sync(0xffffffffu, m == INFINITY)) {
+    m = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (fabsf(v[i]) == INFINITY) v[i] = __int_as_float(0x7fc00000);
+      m = fmaxf(m, fabsf(v[i]));
+    }
+    m = group_max<N>(m);
+  }
+  const uint32_t b = __float_as_uint(m);
+  uint32_t s = (b + 0x1FFFFFu) >> 23;                    // e + 135
+  s = s > 8 ? s - 8 : 0;                                 // e + 127
+  if (b == 0) s = 127;
+  const float inv = __uint_as_float((254 - s) << 23);
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * i] * inv, v[4 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * i + 2] * inv, v[4 * i + 3] * inv), __NV_SATFINITE, __NV_E4M3);
+    w[i] = lo | (hi << 16);
+  }
+  return s;
 }
 
 // The first `n` of N codes to q (whole words where `words`: q on an N-byte boundary).

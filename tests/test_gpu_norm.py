@@ -77,14 +77,21 @@ def test_norm(M, T, H, dt, extra):
                     assert torch.equal(v[0], y8[0][:, :H]) and torch.equal(v[1], y8[1])
                 else:
                     assert torch.equal(v, (so if k == "sum_out" else yo)[:, :H])
-    # in place: the stream into x or into the residual, y over the other
+    # in place: the stream into x or into the residual, y over the other.  (A row's sum is taken in an order that goes by
+    # the rows' alignment, so y's last bits may differ from those of rows with a pitch: the same bits are asked of a call
+    # out of place on rows like these.)
+    xc, rc = xd.clone(), rd.clone()
+    so, yo = torch.empty_like(xc), torch.empty_like(xc)
+    M.rms_norm(xc, wd, EPS, residual=rc, sum_out=so, y=yo)
+    assert torch.equal(so.cpu().to(A.F64), s)
+    R.check(yo, y, bound, "y of contiguous rows")
     for a, b in ((0, 1), (1, 0)):
         buf = [xd.clone(), rd.clone()]
         M.rms_norm(buf[0], wd, EPS, residual=buf[1], sum_out=buf[a], y=buf[b])
-        assert torch.equal(buf[a], so[:, :H]) and torch.equal(buf[b], yo[:, :H])
+        assert torch.equal(buf[a], so) and torch.equal(buf[b], yo)
     buf = xd.clone()
-    M.rms_norm(buf, wd, EPS, residual=rd, y=buf)
-    assert torch.equal(buf, yo[:, :H])
+    M.rms_norm(buf, wd, EPS, residual=rc, y=buf)
+    assert torch.equal(buf, yo)
 
 
 @pytest.mark.parametrize("T,H,dt,extra", CASES)
@@ -102,20 +109,24 @@ def test_norm_gradients(M, T, H, dt, extra):
         R.check(out[:, :H], dx, ex, "dx")
         R.check(dwo, dw, ew, "dweight")
         assert (out[:, H:] == SENTINEL).all()
-        # either alone, and again: the same bits
+        # either alone; and again, on contiguous rows: the same bits (their order goes by the rows' alignment)
         o2, w2 = torch.empty_like(xd), torch.empty_like(dwo)
         M.rms_norm_backward(dyd, xd, wd, EPS, o2, ws, dsum=dd)
         M.rms_norm_backward(dyd, xd, wd, EPS, None, ws, dweight=w2)
         R.check(o2, dx, ex, "dx alone")
         R.check(w2, dw, ew, "dweight alone")
-        o3, w3 = torch.empty_like(o2), torch.empty_like(w2)
-        M.rms_norm_backward(dyd, xd, wd, EPS, o3, ws, dweight=w3, dsum=dd)
-        assert torch.equal(o3, out[:, :H]) and torch.equal(w3, dwo)
+        full = [t if t is None else t.clone() for t in (dyd, xd, dd)]
+        o3, w3, o4, w4 = (f(v) for f in (torch.empty_like,) for v in (full[0], w2, full[0], w2))
+        for o, v in ((o3, w3), (o4, w4)):
+            M.rms_norm_backward(full[0], full[1], wd, EPS, o, ws, dweight=v, dsum=full[2])
+        R.check(o3, dx, ex, "dx of contiguous rows")
+        R.check(w3, dw, ew, "dweight of contiguous rows")
+        assert torch.equal(o3, o4) and torch.equal(w3, w4)
     # in place of each input
     for k in range(3):
         buf = [dyd.clone(), xd.clone(), dsd.clone()]
         M.rms_norm_backward(buf[0], buf[1], wd, EPS, buf[k], ws, dweight=w2, dsum=buf[2])
-        assert torch.equal(buf[k], out[:, :H]) and torch.equal(w2, dwo)
+        assert torch.equal(buf[k], o3) and torch.equal(w2, w3)
     assert M.get_error(ws) == M.OK
 
 
