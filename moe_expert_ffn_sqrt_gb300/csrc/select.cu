@@ -7,11 +7,15 @@
 // NaN keys count as -infinity, so the ids are valid and different whatever the logits hold.
 //
 // One warp per token.  Its lanes are split over the groups, L = 2^i <= 32 / groups to each; a lane holds experts
-// V (sub + L i) .. + V - 1 of its group, V = 4 where rows and groups are whole fours (one load each).
+// V (sub + L i) .. + V - 1 of its group, V = 4 where rows and groups are whole fours (one load each).  The K + 1 largest of
+// the lanes' largest two keys give a bound that the K + 1 largest keys reach; the few keys that do (in shared memory, one to
+// a lane) are ranked by comparing all of them.  Where more than 32 do (many equal keys), K + 1 rounds of a maximum over the
+// warp instead.
 //
-// The choice does not depend on how a score is evaluated: a key in fp32 is off by a known bound, and a token where two
-// keys (or groups) that decide are closer than that is done again in 64 bits.  Two experts of equal logit and bias are
-// an exact tie and need no second look; without a bias keys go by the logits themselves, which all scores rise with.
+// The choice does not depend on how a score is evaluated: a key in fp32 is off by a known bound, and where two keys (or
+// groups) that decide are closer than that, the keys that are near are evaluated in 64 bits, one to a lane.  Two experts of
+// equal logit and bias are an exact tie and need no second look; without a bias keys go by the logits themselves, which all
+// scores rise with.
 #include "rows.cuh"
 
 namespace moe {
@@ -20,13 +24,15 @@ namespace {
 
 constexpr int kSelectWarps = 8;
 constexpr unsigned kAll = 0xffffffffu;
+constexpr int kNone = 0x7fffffff;
 
 struct SelectArgs {
-  const void* logits;
-  long long ld;
+  const uint8_t* logits;      // rows of type dt, row_bytes apart
+  long long row_bytes;
+  int dt;
   const float* bias;
   int T, E, K;
-  int G, KG, best, fn, renorm;
+  int G, KG, best, renorm;
   int per_group, L, log_l;    // experts per group, lanes per group
   float scale;
   int32_t* ids;
@@ -39,24 +45,30 @@ __device__ __forceinline__ uint32_t ordered(float k) {
   return static_cast<uint32_t>(u) ^ (static_cast<uint32_t>(u >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float from_ordered(uint32_t o) { return __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o); }
+// 0 for what is not finite
+__device__ __forceinline__ float size_of(float f) {
+  const float a = fabsf(f);
+  return a <= 3.402823466e38f ? a : 0.f;
+}
 
-// Scores; softmax of a row: lmax its largest logit, sum its exponentials' (a row of -infinities has scores of 0).
+// Scores (FN: moe_score_fn); softmax of a row: lmax its largest logit, sum its exponentials' (a masked expert, a logit of
+// -infinity, has 0, in a row of nothing else too).
+template <int FN>
 struct Scores {
-  int fn;
   float lmax, sum;
   __device__ __forceinline__ float operator()(float l) const {
-    if (fn == 0) return l == -INFINITY ? 0.f : expf(l - lmax) / sum;
-    if (fn == 1) return sqrtf(fmaxf(l, 0.f) + log1pf(expf(-fabsf(l))));
+    if (FN == 0) return l == -INFINITY ? 0.f : expf(l - lmax) / sum;
+    if (FN == 1) return sqrtf(fmaxf(l, 0.f) + log1pf(expf(-fabsf(l))));
     return 1.f / (1.f + expf(-l));
   }
 };
 // The same, for keys: fast exponentials and divisions for softmax (over: 1 / sum) and sigmoid.
+template <int FN>
 struct FastScores {
-  int fn;
   float lmax, over;
   __device__ __forceinline__ float operator()(float l) const {
-    if (fn == 0) return l == -INFINITY ? 0.f : __expf(l - lmax) * over;
-    if (fn == 1) return sqrtf(fmaxf(l, 0.f) + log1pf(expf(-fabsf(l))));
+    if (FN == 0) return l == -INFINITY ? 0.f : __expf(l - lmax) * over;
+    if (FN == 1) return sqrtf(fmaxf(l, 0.f) + log1pf(expf(-fabsf(l))));
     return __fdividef(1.f, 1.f + __expf(-l));
   }
   // How far the difference of two scores may be off at most.  __expf(x) is within 2 + 1.2 |x| steps of 2^-23, the division
@@ -65,36 +77,68 @@ struct FastScores {
   // + 5 additions.  Square root, logarithm: accurate ones, eight steps.  (Scores below 2^-126 come out as 0.)
   template <int PER>
   __device__ __forceinline__ float apart() const {
-    const float steps = fn == 0 ? PER + 16.f : fn == 1 ? 16.f : 16.f + 4.f * fmaxf(-lmax, 0.f);
+    const float steps = FN == 0 ? PER + 16.f : FN == 1 ? 16.f : 16.f + 4.f * fmaxf(-lmax, 0.f);
     return (*this)(lmax) * (steps * 0x1p-23f) + 0x1p-120f;
   }
 };
+template <int FN>
 struct Scores64 {
-  int fn;
   double lmax, sum;
   __device__ __forceinline__ double operator()(double l) const {
-    if (fn == 0) return l == -INFINITY ? 0. : exp(l - lmax) / sum;
-    if (fn == 1) return sqrt(fmax(l, 0.) + log1p(exp(-fabs(l))));
+    if (FN == 0) return l == -INFINITY ? 0. : exp(l - lmax) / sum;
+    if (FN == 1) return sqrt(fmax(l, 0.) + log1p(exp(-fabs(l))));
     return 1. / (1. + exp(-l));
   }
 };
 
-// A token's experts in 64 bits: lane k gets the k-th (the others what was there).
-template <class T, int PER>
-__device__ __noinline__ int select_exact(const SelectArgs& a, const typename T::raw* row, int id) {
-  const int lane = threadIdx.x % 32, g = lane / a.L, sub = lane % a.L;
-  Scores64 score{a.fn, -INFINITY, 0.};
-  double key[PER];
-  if (a.fn == 0) {
-    float m = -INFINITY;
-    for (int e = lane; e < a.E; e += 32) m = fmaxf(m, T::to_f(row[e]));
+__device__ __forceinline__ float logit(const SelectArgs& a, const uint8_t* row, int e) {
+  if (a.dt == kF32) return __ldg(reinterpret_cast<const float*>(row) + e);
+  const uint16_t u = __ldg(reinterpret_cast<const uint16_t*>(row) + e);
+  return a.dt == kBf16 ? Bf16Elem::to_f(u) : F16Elem::to_f(u);
+}
+// V logits from expert e on (zeros where there are none).
+template <int V>
+__device__ __forceinline__ void logits(const SelectArgs& a, const uint8_t* row, int e, bool there, float (&v)[V]) {
+  if constexpr (V == 1) {
+    v[0] = there ? logit(a, row, e) : 0.f;
+  } else if (a.dt == kF32) {
+    const float4 f = there ? __ldg(reinterpret_cast<const float4*>(row) + e / 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+    v[0] = f.x;
+    v[1] = f.y;
+    v[2] = f.z;
+    v[3] = f.w;
+  } else {
+    const uint2 u = there ? __ldg(reinterpret_cast<const uint2*>(row) + e / 4) : make_uint2(0, 0);
+    const uint16_t r[4] = {static_cast<uint16_t>(u.x), static_cast<uint16_t>(u.x >> 16), static_cast<uint16_t>(u.y),
+                           static_cast<uint16_t>(u.y >> 16)};
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, d));
-    score.lmax = m;
-    for (int e = lane; e < a.E; e += 32) score.sum += exp(static_cast<double>(T::to_f(row[e])) - score.lmax);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) score.sum += __shfl_xor_sync(kAll, score.sum, d);
+    for (int j = 0; j < 4; ++j) v[j] = a.dt == kBf16 ? Bf16Elem::to_f(r[j]) : F16Elem::to_f(r[j]);
   }
+}
+
+// Scores of the row in 64 bits (softmax: its largest logit and sum).
+template <int FN>
+__device__ __forceinline__ Scores64<FN> scores64(const SelectArgs& a, const uint8_t* row, float lmax) {
+  Scores64<FN> s{lmax, 0.};
+  if (FN == 0) {
+    for (int e = threadIdx.x % 32; e < a.E; e += 32) {
+      const float l = logit(a, row, e);
+      if (l != -INFINITY) s.sum += exp(static_cast<double>(l) - s.lmax);
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) s.sum += __shfl_xor_sync(kAll, s.sum, d);
+  }
+  return s;
+}
+__device__ __forceinline__ double clean(double k) { return k == k ? k : -INFINITY; }
+
+// A token's experts all in 64 bits, K rounds: lane k gets the k-th (the others what was there).  For rows where many keys
+// are near one another.
+template <int FN, int PER>
+__device__ __noinline__ int select_all64(const SelectArgs& a, const uint8_t* row, float lmax, int id) {
+  const int lane = threadIdx.x % 32, g = lane >> a.log_l, sub = lane & (a.L - 1);
+  const Scores64<FN> score = scores64<FN>(a, row, lmax);
+  double key[PER];
   double k1 = -INFINITY, k2 = -INFINITY;
   int n = 0;
   for (int i = 0; i < PER; ++i) {
@@ -102,10 +146,8 @@ __device__ __noinline__ int select_exact(const SelectArgs& a, const typename T::
     key[i] = -INFINITY;
     if (g < a.G && r < a.per_group) {
       const int e = g * a.per_group + r;
-      const double s = score(T::to_f(row[e]));
-      double k = a.bias ? s + a.bias[e] : s;
-      if (!(k == k)) k = -INFINITY;
-      key[i] = a.bias ? k : static_cast<double>(from_ordered(ordered(T::to_f(row[e]))));
+      const double l = logit(a, row, e), s = score(l), k = clean(a.bias ? s + a.bias[e] : s);
+      key[i] = a.bias ? k : clean(l);
       if (k > k1) {
         k2 = k1;
         k1 = k;
@@ -123,11 +165,10 @@ __device__ __noinline__ int select_exact(const SelectArgs& a, const typename T::
       k1 = fmax(k1, o1);
       k2 = fmax(lo, hi2);
     }
-    double mine = a.best == 2 && a.per_group > 1 ? k1 + k2 : k1;
-    if (!(mine == mine)) mine = -INFINITY;
+    const double mine = clean(a.best == 2 && a.per_group > 1 ? k1 + k2 : k1);
     int rank = 0;
     for (int h = 0; h < a.G; ++h) {
-      const double o = __shfl_sync(kAll, mine, h * a.L);
+      const double o = __shfl_sync(kAll, mine, h << a.log_l);
       rank += o > mine || (o == mine && h < g);
     }
     open = open && rank < a.KG;
@@ -135,7 +176,7 @@ __device__ __noinline__ int select_exact(const SelectArgs& a, const typename T::
   unsigned long long taken = 0;
   for (int k = 0; k < a.K; ++k) {
     double bk = 0.;
-    int be = 0x7fffffff, bi = -1;
+    int be = kNone, bi = -1;
     for (int i = 0; open && i < n; ++i)
       if (!(taken >> i & 1) && (bi < 0 || key[i] > bk)) {
         bk = key[i];
@@ -147,7 +188,7 @@ __device__ __noinline__ int select_exact(const SelectArgs& a, const typename T::
     for (int d = 16; d > 0; d >>= 1) {
       const double ok = __shfl_xor_sync(kAll, bk, d);
       const int oe = __shfl_xor_sync(kAll, be, d);
-      if (oe != 0x7fffffff && (be == 0x7fffffff || ok > bk || (ok == bk && oe < be))) {
+      if (oe != kNone && (be == kNone || ok > bk || (ok == bk && oe < be))) {
         bk = ok;
         be = oe;
       }
@@ -158,41 +199,13 @@ __device__ __noinline__ int select_exact(const SelectArgs& a, const typename T::
   return id;
 }
 
-// V values from p on (zeros where there are none).
-template <class T, int V>
-__device__ __forceinline__ void load_values(const typename T::raw* p, bool there, float (&v)[V]) {
-  if constexpr (V == 4) {
-    typename T::raw r[4];
-    if constexpr (sizeof(r) == 16) {
-      const uint4 u = there ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0, 0, 0, 0);
-      memcpy(r, &u, 16);
-    } else {
-      const uint2 u = there ? __ldg(reinterpret_cast<const uint2*>(p)) : make_uint2(0, 0);
-      memcpy(r, &u, 8);
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = T::to_f(r[j]);
-  } else {
-    v[0] = there ? T::to_f(__ldg(p)) : 0.f;
-  }
-}
-
-// A lane's largest two keys (0: none) and where they are.
-struct Top2 {
-  uint32_t k1, k2;
-  int i1, i2;
-  __device__ __forceinline__ void add(uint32_t k, int i) {
-    const bool first = k > k1, second = k > k2;
-    k2 = first ? k1 : second ? k : k2;
-    i2 = first ? i1 : second ? i : i2;
-    k1 = first ? k : k1;
-    i1 = first ? i : i1;
-  }
-};
-
-template <class T, int PER, int V>
+template <int FN, int PER, int V>
 __global__ void __launch_bounds__(kSelectWarps * 32) select_kernel(const SelectArgs a) {
-  const int lane = threadIdx.x % 32, g = lane >> a.log_l, sub = lane & (a.L - 1);
+  __shared__ int s_id[kSelectWarps][34];               // experts that are near, then the chosen ones in order
+  __shared__ uint32_t s_key[kSelectWarps][34];
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g = lane >> a.log_l, sub = lane & (a.L - 1);
+  int* ids = s_id[warp];
+  uint32_t* keys = s_key[warp];
   grid_dependency_wait();
   grid_launch_dependents();
   const bool used = g < a.G;
@@ -206,25 +219,25 @@ __global__ void __launch_bounds__(kSelectWarps * 32) select_kernel(const SelectA
 #pragma unroll
     for (int j = 0; j < V; ++j) bias[i + j] = there ? __ldg(a.bias + e0 + at(i) + j) : 0.f;
   }
-  for (long long t = static_cast<long long>(blockIdx.x) * kSelectWarps + threadIdx.x / 32; t < a.T; t += gridDim.x * kSelectWarps) {
-    const typename T::raw* row = static_cast<const typename T::raw*>(a.logits) + t * a.ld;
+  for (long long t = static_cast<long long>(blockIdx.x) * kSelectWarps + warp; t < a.T; t += gridDim.x * kSelectWarps) {
+    const uint8_t* row = a.logits + t * a.row_bytes;
     float v[PER];
-#pragma unroll
-    for (int i = 0; i < PER; i += V) {
-      float f[V];
-      load_values<T, V>(row + e0 + at(i), used && at(i) < a.per_group, f);
-#pragma unroll
-      for (int j = 0; j < V; ++j) v[i + j] = f[j];
-    }
     uint32_t key[PER], top = 0;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      key[i] = used && at(i) < a.per_group ? ordered(v[i]) : 0;
-      top = max(top, key[i]);
+    for (int i = 0; i < PER; i += V) {
+      const bool there = used && at(i) < a.per_group;
+      float f[V];
+      logits<V>(a, row, e0 + at(i), there, f);
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        v[i + j] = f[j];
+        key[i + j] = there ? ordered(f[j]) : 0;
+        top = max(top, key[i + j]);
+      }
     }
     const float lmax = from_ordered(__reduce_max_sync(kAll, top));
     float sum = 1.f;
-    if (a.fn == 0) {
+    if (FN == 0) {
       sum = 0.f;
 #pragma unroll
       for (int i = 0; i < PER; ++i)
@@ -232,43 +245,66 @@ __global__ void __launch_bounds__(kSelectWarps * 32) select_kernel(const SelectA
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
     }
-    const FastScores fast{a.fn, lmax, 1.f / sum};
+    const FastScores<FN> fast{lmax, 1.f / sum};
     const float near = fast.template apart<PER>();
     if (a.bias) {
 #pragma unroll
       for (int i = 0; i < PER; ++i)
         if (key[i]) key[i] = ordered(fast(v[i]) + bias[i]);
     }
-    Top2 head{0, 0, 0, 0};
+    uint32_t k1 = 0, k2 = 0;            // the lane's largest two keys
 #pragma unroll
-    for (int i = 0; i < PER; ++i) head.add(key[i], i);
-    bool unsure = false;
-    int left = 0;                     // the lane's experts that may still be taken
+    for (int i = 0; i < PER; ++i) {
+      k2 = max(k2, min(k1, key[i]));
+      k1 = max(k1, key[i]);
+    }
+    // Experts of keys >= bound into ids (and keys), 32 of them at most; returns how many there are.
+    const auto collect = [&](uint32_t bound) {
+      int c = 0;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) left += key[i] != 0;
+      for (int i = 0; i < PER; ++i) {
+        const bool is = key[i] && key[i] >= bound;
+        const unsigned m = __ballot_sync(kAll, is);
+        if (m) {
+          const int p = c + __popc(m & ((1u << lane) - 1));
+          if (is && p < 32) {
+            ids[p] = e0 + at(i);
+            keys[p] = key[i];
+          }
+          c += __popc(m);
+        }
+      }
+      __syncwarp();
+      return c;
+    };
+    const auto key64 = [&](const Scores64<FN>& score, int e) {
+      const double s = score(logit(a, row, e));
+      return clean(a.bias ? s + __ldg(a.bias + e) : s);
+    };
+    bool all64 = false;                 // too many keys are near one another
     if (a.KG < a.G) {
-      uint32_t k1 = head.k1, k2 = head.k2;
+      uint32_t g1 = k1, g2 = k2;
       for (int d = 1; d < a.L; d <<= 1) {
-        const uint32_t o1 = __shfl_xor_sync(kAll, k1, d), o2 = __shfl_xor_sync(kAll, k2, d);
-        k2 = max(min(k1, o1), max(k2, o2));
-        k1 = max(k1, o1);
+        const uint32_t o1 = __shfl_xor_sync(kAll, g1, d), o2 = __shfl_xor_sync(kAll, g2, d);
+        g2 = max(min(g1, o1), max(g2, o2));
+        g1 = max(g1, o1);
       }
       // what the group is worth, and how far that may be off: two scores and additions
-      float worth = -INFINITY, size = 0.f;
+      const bool two = a.best == 2 && g2;
+      float worth = -INFINITY, size = 0.f, f2 = 0.f;
       if (used) {
-        const float f1 = from_ordered(k1), f2 = from_ordered(k2);
-        worth = a.bias ? f1 : fast(f1);
-        size = fabsf(worth);
-        if (a.best == 2 && k2) {
+        f2 = from_ordered(two ? g2 : g1);
+        worth = a.bias ? from_ordered(g1) : fast(from_ordered(g1));
+        size = size_of(worth);
+        if (two) {
           const float w2 = a.bias ? f2 : fast(f2);
           worth += w2;
-          size += fabsf(w2);
+          size += size_of(w2);
         }
-        size = size <= 3e38f ? size : 0.f;       // (an infinite worth is exact)
       }
       uint32_t mine = used && sub == 0 ? ordered(worth) : 0;
       const float tol = 2.f * near + __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(size))) * 0x1p-21f;
-      unsigned open = 0;
+      unsigned open = 0;                // by the lanes with sub = 0
       float last = 0.f;
       for (int k = 0; k < a.KG; ++k) {
         const uint32_t best = __reduce_max_sync(kAll, mine);
@@ -277,54 +313,155 @@ __global__ void __launch_bounds__(kSelectWarps * 32) select_kernel(const SelectA
         if (lane == who) mine = 0;
         last = from_ordered(best);
       }
-      unsure = last - from_ordered(__reduce_max_sync(kAll, mine)) <= tol;
+      const float next = from_ordered(__reduce_max_sync(kAll, mine));
+      if (last - next <= tol) {
+        // groups that are surely in, and those that may be: the latter in 64 bits, from their experts that may be among
+        // the best two
+        const bool in = used && worth - next > tol, maybe = used && !in && !(last - worth > tol);
+        const uint32_t bound = !maybe ? 0xffffffffu : a.bias ? ordered(f2 - tol) : two ? g2 : g1;
+        int c = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          const bool is = maybe && key[i] >= bound;
+          const unsigned m = __ballot_sync(kAll, is);
+          const int p = c + __popc(m & ((1u << lane) - 1));
+          if (is && p < 32) ids[p] = e0 + at(i);
+          c += __popc(m);
+        }
+        __syncwarp();
+        all64 = c > 32;
+        if (!all64) {
+          const Scores64<FN> score = scores64<FN>(a, row, lmax);
+          const int e = lane < c ? ids[lane] : 0;
+          const double k = lane < c ? key64(score, e) : 0.;
+          const int of = lane < c ? e / a.per_group : -1;
+          double b1 = -INFINITY, b2 = -INFINITY;
+          for (int r = 0; r < c; ++r) {
+            const double o = __shfl_sync(kAll, k, r);
+            if (__shfl_sync(kAll, of, r) != g) continue;
+            if (o > b1) {
+              b2 = b1;
+              b1 = o;
+            } else if (o > b2) {
+              b2 = o;
+            }
+          }
+          const double exact = clean(two ? b1 + b2 : b1);
+          const unsigned may = __ballot_sync(kAll, maybe && sub == 0);
+          open = __ballot_sync(kAll, in && sub == 0);
+          const int places = a.KG - __popc(open);
+          int rank = 0;
+          for (unsigned m = may; m; m &= m - 1) {
+            const int h = __ffs(m) - 1;
+            const double o = __shfl_sync(kAll, exact, h);
+            rank += o > exact || (o == exact && h < (lane & ~(a.L - 1)));
+          }
+          open |= __ballot_sync(kAll, maybe && sub == 0 && rank < places);
+        }
+        __syncwarp();
+      }
       if (!(open >> (g << a.log_l) & 1)) {
-        head = Top2{0, 0, 0, 0};
-        left = 0;
+        k1 = k2 = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) key[i] = 0;
       }
     }
-    // lane k keeps the k-th largest key; every lane ends with the first that is left out (key 0 where there is none)
-    int id = 0, won = 0;
-    uint32_t mk = 0, best = 0;
-    unsigned long long taken = 0;
-    for (int k = 0; k <= a.K; ++k) {
-      best = __reduce_max_sync(kAll, head.k1);
-      const int e = head.k1 == best ? e0 + at(head.i1) : 0x7fffffff;
-      won = static_cast<int>(__reduce_min_sync(kAll, static_cast<uint32_t>(e)));
-      if (lane == k) {
-        id = won;
-        mk = best;
+    int id = 0;
+    if (!all64) {
+      // the K + 1 largest of the lanes' largest two keys (fewer: every key) are a bound for the K + 1 largest keys
+      uint32_t bound = 0;
+      for (int k = 0; k <= a.K; ++k) {
+        bound = __reduce_max_sync(kAll, k1);
+        if (bound == 0) break;
+        const int who = __ffs(__ballot_sync(kAll, k1 == bound)) - 1;
+        if (lane == who) {
+          k1 = k2;
+          k2 = 0;
+        }
       }
-      if (e == won && best) {
-        taken |= 1ull << head.i1;
-        --left;
-        head.k1 = head.k2;
-        head.i1 = head.i2;
-        head.k2 = 0;
-        if (head.k1 == 0 && left > 0) {
+      int c = collect(bound);
+      if (c <= 32) {
+        const int e = lane < c ? ids[lane] : kNone;
+        const uint32_t k = lane < c ? keys[lane] : 0;
+        int rank = 0;
+        for (int r = 0; r < c; ++r) {
+          const uint32_t o = __shfl_sync(kAll, k, r);
+          const int oe = __shfl_sync(kAll, e, r);
+          rank += o > k || (o == k && oe < e);
+        }
+        __syncwarp();
+        if (lane < c && rank <= a.K) {
+          ids[rank] = e;
+          keys[rank] = k;
+        }
+        if (lane == 0 && c <= a.K) keys[a.K] = 0;
+      } else {
+        __syncwarp();
+        for (int k = 0; k <= a.K; ++k) {
+          uint32_t b = 0;
+          int bi = 0;
 #pragma unroll
           for (int i = 0; i < PER; ++i)
-            if (!(taken >> i & 1)) head.add(key[i], i);
+            if (key[i] > b) {
+              b = key[i];
+              bi = i;
+            }
+          const uint32_t best = __reduce_max_sync(kAll, b);
+          const int e = b == best && best ? e0 + at(bi) : kNone;
+          const int won = static_cast<int>(__reduce_min_sync(kAll, static_cast<uint32_t>(e)));
+          if (lane == 0) {
+            ids[k] = won;
+            keys[k] = best;
+          }
+          if (e == won && best) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+              if (i == bi) key[i] = 0;
+          }
+        }
+      }
+      __syncwarp();
+      if (lane < a.K) id = ids[lane];
+      if (a.bias) {
+        bool unsure = false;
+        const uint32_t nk = lane < a.K ? keys[lane + 1] : 0;
+        const float f = from_ordered(lane < a.K ? keys[lane] : 1);
+        if (nk != 0) {
+          const int ne = ids[lane + 1];
+          const float nf = from_ordered(nk);
+          if (f - nf <= near + (size_of(f) + size_of(nf)) * 0x1p-23f)
+            unsure = logit(a, row, id) != logit(a, row, ne) || __ldg(a.bias + id) != __ldg(a.bias + ne);
+        }
+        if (__any_sync(kAll, unsure)) {
+          // every key that may be among the K largest, in 64 bits
+          const float kth = __shfl_sync(kAll, f, a.K - 1);
+          const uint32_t low = ordered(kth - (near + size_of(kth) * 0x1p-21f));
+          __syncwarp();
+          all64 = c > 32;               // (the rounds have used the keys up)
+          if (!all64) c = collect(low);
+          all64 = all64 || c > 32;
+          if (!all64) {
+            const Scores64<FN> score = scores64<FN>(a, row, lmax);
+            const int e = lane < c ? ids[lane] : kNone;
+            const double k = lane < c ? key64(score, e) : -INFINITY;
+            int rank = 0;
+            for (int r = 0; r < c; ++r) {
+              const double o = __shfl_sync(kAll, k, r);
+              const int oe = __shfl_sync(kAll, e, r);
+              rank += o > k || (o == k && oe < e);
+            }
+            __syncwarp();
+            if (lane < c && rank < a.K) ids[rank] = e;
+            __syncwarp();
+            if (lane < a.K) id = ids[lane];
+          }
         }
       }
     }
-    if (a.bias) {
-      uint32_t nk = __shfl_down_sync(kAll, mk, 1);
-      int nid = __shfl_down_sync(kAll, id, 1);
-      if (lane == a.K - 1) {
-        nk = best;
-        nid = won;
-      }
-      if (lane < a.K && nk != 0) {
-        const float f = from_ordered(mk), nf = from_ordered(nk);
-        const float tol = near + (fminf(fabsf(f), 3e38f) + fminf(fabsf(nf), 3e38f)) * 0x1p-23f;
-        if (f - nf <= tol)
-          unsure = unsure || T::to_f(row[id]) != T::to_f(row[nid]) || __ldg(a.bias + id) != __ldg(a.bias + nid);
-      }
-    }
-    if (__any_sync(kAll, unsure)) id = select_exact<T, PER>(a, row, id);
-    const Scores score{a.fn, lmax, sum};
-    float s = lane < a.K ? score(T::to_f(row[id])) : 0.f;
+    if (all64) id = select_all64<FN, PER>(a, row, lmax, id);
+    __syncwarp();
+    const Scores<FN> score{lmax, sum};
+    float s = lane < a.K ? score(logit(a, row, id)) : 0.f;
     if (a.renorm) {
       float all = s;
 #pragma unroll
@@ -338,28 +475,28 @@ __global__ void __launch_bounds__(kSelectWarps * 32) select_kernel(const SelectA
   }
 }
 
-template <class T, int PER, int V>
+template <int FN, int PER, int V>
 cudaError_t select_launch(const SelectArgs& a, cudaStream_t stream) {
   const long long ctas = (static_cast<long long>(a.T) + kSelectWarps - 1) / kSelectWarps, most = 8LL * num_sms();
-  return launch_pdl(select_kernel<T, PER, V>, dim3(static_cast<unsigned>(ctas < most ? ctas : most)), dim3(kSelectWarps * 32), 0,
+  return launch_pdl(select_kernel<FN, PER, V>, dim3(static_cast<unsigned>(ctas < most ? ctas : most)), dim3(kSelectWarps * 32), 0,
                     stream, a);
 }
 
-template <class T>
+template <int FN>
 cudaError_t select_by_size(const SelectArgs& a, cudaStream_t stream) {
-  const size_t four = 4 * sizeof(typename T::raw);
-  if (a.per_group % 4 == 0 && reinterpret_cast<uintptr_t>(a.logits) % four == 0 && (a.T <= 1 || a.ld % 4 == 0)) {
+  const size_t four = 4 * dtype_bytes(a.dt);
+  if (a.per_group % 4 == 0 && reinterpret_cast<uintptr_t>(a.logits) % four == 0 && (a.T <= 1 || a.row_bytes % four == 0)) {
     const int per = (a.per_group + 4 * a.L - 1) / (4 * a.L) * 4;
-    if (per <= 4) return select_launch<T, 4, 4>(a, stream);
-    if (per <= 8) return select_launch<T, 8, 4>(a, stream);
-    if (per <= 16) return select_launch<T, 16, 4>(a, stream);
-    if (per <= 32) return select_launch<T, 32, 4>(a, stream);
-    return select_launch<T, 64, 4>(a, stream);
+    if (per <= 8) return select_launch<FN, 8, 4>(a, stream);
+    if (per <= 16) return select_launch<FN, 16, 4>(a, stream);
+    if (per <= 32) return select_launch<FN, 32, 4>(a, stream);
+    return select_launch<FN, 64, 4>(a, stream);
   }
   const int per = (a.per_group + a.L - 1) / a.L;
-  if (per <= 8) return select_launch<T, 8, 1>(a, stream);
-  if (per <= 32) return select_launch<T, 32, 1>(a, stream);
-  return select_launch<T, 64, 1>(a, stream);
+  if (per <= 8) return select_launch<FN, 8, 1>(a, stream);
+  if (per <= 16) return select_launch<FN, 16, 1>(a, stream);
+  if (per <= 32) return select_launch<FN, 32, 1>(a, stream);
+  return select_launch<FN, 64, 1>(a, stream);
 }
 
 }  // namespace
@@ -367,8 +504,9 @@ cudaError_t select_by_size(const SelectArgs& a, cudaStream_t stream) {
 cudaError_t launch_select(int ldt, RowsView logits, const float* bias, int T, int E, int K, const SelectRule& rule,
                           int32_t* ids, float* w, cudaStream_t stream) {
   SelectArgs a{};
-  a.logits = logits.ptr;
-  a.ld = logits.ld;
+  a.logits = static_cast<const uint8_t*>(logits.ptr);
+  a.row_bytes = logits.ld * static_cast<long long>(dtype_bytes(ldt));
+  a.dt = ldt;
   a.bias = bias;
   a.T = T;
   a.E = E;
@@ -377,7 +515,6 @@ cudaError_t launch_select(int ldt, RowsView logits, const float* bias, int T, in
   a.G = rule.topk_groups < rule.groups ? rule.groups : 1;     // all groups used: one group of all experts
   if (a.G == 1) a.KG = 1;
   a.best = rule.best;
-  a.fn = rule.fn;
   a.renorm = rule.renorm;
   a.scale = rule.scale;
   a.per_group = E / a.G;
@@ -386,9 +523,9 @@ cudaError_t launch_select(int ldt, RowsView logits, const float* bias, int T, in
   a.L = 1 << a.log_l;
   a.ids = ids;
   a.w = w;
-  if (ldt == kBf16) return select_by_size<Bf16Elem>(a, stream);
-  if (ldt == kF16) return select_by_size<F16Elem>(a, stream);
-  return select_by_size<F32Elem>(a, stream);
+  if (rule.fn == 0) return select_by_size<0>(a, stream);
+  if (rule.fn == 1) return select_by_size<1>(a, stream);
+  return select_by_size<2>(a, stream);
 }
 
 }  // namespace moe
