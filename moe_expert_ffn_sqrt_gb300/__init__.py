@@ -53,6 +53,18 @@ class _SelectRule(ctypes.Structure):
 
 
 _lib = None
+_fast = None
+
+
+def _load_native():
+    """The calls around the layer with their arguments marshalled in C++ (raises if it was not built)."""
+    global _fast
+    if _fast is None:
+        lib()
+        from . import _native as n
+        n.bind(LIB_PATH)
+        _fast = n
+    return _fast
 
 
 def lib():
@@ -779,6 +791,9 @@ def linear_backward(dy, x, w, ws, dx=None, dw=None, dbias=None, act="none", z=No
 
 # ------------------------------------------------------------------ around the layer
 
+# The checks of these calls' arguments run in C++ (csrc/native.cpp), which answers None where one fails; what follows in each
+# of them then says why.
+
 def _at_home(*tensors):
     """The calls run on the current device's stream: every tensor has to be there."""
     dev = torch.cuda.current_device()
@@ -806,6 +821,11 @@ def new_rows8(rows, cols, device="cuda"):
 def rms_norm(x, weight, eps, residual=None, sum_out=None, y=None, y8=None):
     """sum_out = x + residual; y and y8 (a pair, see new_rows8) = its root-mean-square norm times weight [H] fp32.
     residual and each output are optional, one output at least; sum_out and y may be x or residual themselves."""
+    status = (_fast or _load_native()).rms_norm(x, weight, eps, residual, sum_out, y, y8)
+    if status == 0:
+        return
+    if status is not None:
+        raise MoeError(status, "moe_rms_norm")
     TH = T, H = x.shape
     dt = x.dtype
     _at_home(x, residual, weight, sum_out, y, *(y8 or ()))
@@ -828,6 +848,11 @@ def new_workspace_norm(T, H, device="cuda"):
 def rms_norm_backward(dy, x, weight, eps, dx, ws, dweight=None, dsum=None):
     """Gradients of rms_norm with respect to its sum (x here: rms_norm's sum_out, or its x) and weight; dsum is added to
     dx.  dx may be dy, x or dsum itself; dx or dweight may be None."""
+    status = (_fast or _load_native()).rms_norm_backward(dy, x, weight, eps, dx, ws, dweight, dsum)
+    if status == 0:
+        return
+    if status is not None:
+        raise MoeError(status, "moe_rms_norm_backward")
     TH = T, H = dy.shape
     dt = dy.dtype
     _at_home(dy, x, weight, dx, ws, dweight, dsum)
@@ -841,10 +866,17 @@ def select(logits, topk_ids, topk_w, score_fn, e_score_bias=None, n_groups=1, to
            scale=1.0):
     """topk_ids, topk_w [T, K] from logits [T, E] (bf16, fp16 or fp32): the K largest score + bias among the topk_groups
     best of n_groups groups of experts (by the sum of their group_best largest), weights scaled (and normalised)."""
+    fn = SCORE_FNS.get(score_fn, score_fn)
+    status = (_fast or _load_native()).select(logits, topk_ids, topk_w, e_score_bias, fn, n_groups, topk_groups, group_best,
+                                                renormalize, scale)
+    if status == 0:
+        return
+    if status is not None:
+        raise MoeError(status, "moe_select")
     TK = T, K = topk_ids.shape
     E, dt = logits.shape[1], logits.dtype
     _at_home(logits, topk_ids, topk_w, e_score_bias)
-    rule = _SelectRule(SCORE_FNS.get(score_fn, score_fn), n_groups, topk_groups, group_best, int(renormalize), scale)
+    rule = _SelectRule(fn, n_groups, topk_groups, group_best, int(renormalize), scale)
     _check(lib().moe_select(_dtype(logits, "logits"), _rows(logits, dt, (T, E), "logits"),
                             _full(e_score_bias, torch.float32, (E,), "e_score_bias"), T, E, K, rule,
                             _full(topk_ids, torch.int32, TK, "topk_ids"), _full(topk_w, torch.float32, TK, "topk_w"),
@@ -854,13 +886,19 @@ def select(logits, topk_ids, topk_w, score_fn, e_score_bias=None, n_groups=1, to
 def select_backward(logits, topk_ids, topk_w, dtopk_w, dlogits, ws, score_fn, renormalize=True, scale=1.0):
     """dlogits [T, E] (any type for fp32 logits, else theirs) from dtopk_w, for select's topk_ids and topk_w.
     ws: as for route_backward."""
+    fn = SCORE_FNS.get(score_fn, score_fn)
+    status = (_fast or _load_native()).select_backward(logits, topk_ids, topk_w, dtopk_w, dlogits, ws, fn, renormalize, scale)
+    if status == 0:
+        return
+    if status is not None:
+        raise MoeError(status, "moe_select_backward")
     TK = T, K = topk_ids.shape
     E = logits.shape[1]
     _at_home(logits, topk_ids, topk_w, dtopk_w, dlogits, ws)
     _check(lib().moe_select_backward(_dtype(logits, "logits"), _rows(logits, logits.dtype, (T, E), "logits"),
                                      _full(topk_ids, torch.int32, TK, "topk_ids"), _full(topk_w, torch.float32, TK, "topk_w"),
                                      _full(dtopk_w, torch.float32, TK, "dtopk_w"), T, E, K,
-                                     SCORE_FNS.get(score_fn, score_fn), int(renormalize), scale, _dtype(dlogits, "dlogits"),
+                                     fn, int(renormalize), scale, _dtype(dlogits, "dlogits"),
                                      _rows(dlogits, dlogits.dtype, (T, E), "dlogits"), _space(ws), ws.numel(), _stream()),
            "moe_select_backward")
 
@@ -878,6 +916,11 @@ def _ws_opt(ws):
 def pack_rows8(x, x8, expert_counts=None, align=0, ws=None):
     """x [rows, cols] to 8 bits (x8: a pair, see new_rows8).  With expert_counts [E] the rows of the experts' segments
     alone; ws (256 bytes, zero-filled) then takes the status."""
+    status = (_fast or _load_native()).pack_rows8(x, x8, expert_counts, align, ws)
+    if status == 0:
+        return
+    if status is not None:
+        raise MoeError(status, "moe_pack_rows8")
     rows, cols = x.shape
     E = _experts(expert_counts)
     _at_home(x, expert_counts, ws, *x8)
@@ -912,6 +955,13 @@ def linear_backward8(dy, w, ws, x=None, x8=None, z=None, z8=None, x_ids=None, x_
                      act="none", dx_residual=None, expert_counts=None, align=0):
     """linear_backward with x and z each in 16 bits or in 8 (pairs x8, z8).  With x_ids [rows] row r of x is row
     x_ids[r] // x_div of x8: token rows through dispatch's sorted_token_ids and K."""
+    act = ACTS.get(act, act)
+    status = (_fast or _load_native()).linear_backward8(dy, w, ws, x, x8, z, z8, x_ids, x_div, dx, dw, dbias, act, dx_residual,
+                                                          expert_counts, align)
+    if status == 0:
+        return
+    if status is not None:
+        raise MoeError(status, "moe_linear_backward8")
     rows, N, K, E, act, cols = _linear_dims(dy, w, act, expert_counts)
     dt = dy.dtype
     src = rows if x_ids is None or x8 is None else x8[0].shape[0]
