@@ -5,8 +5,6 @@
 //   g_i = dy_i w_i:   dx_i = r g_i - s_i r^3 mean(s g) + dsum_i;   dw_i = sum over rows of dy_i s_i r
 // Both are taken in fp32; each output is rounded once, the 8-bit rows (rows8.cuh) from the fp32 y.  One pass over a
 // row gives both of the backward's sums (s^2 and s g), so nothing but s is kept from the forward.
-#include <type_traits>
-
 #include "rows8.cuh"
 
 namespace moe {
@@ -45,64 +43,6 @@ __device__ __forceinline__ void block_sum(float (&v)[K], float (*sh)[K]) {
 #pragma unroll
     for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], d);
 }
-
-// A pack as words: two 16-bit values are taken out of and put into a word at a time.  (As an array of 16-bit values the
-// compiler gives each a register of its own.)
-template <class T>
-struct Words {
-  static constexpr int N = Pack<T>::N;
-  uint32_t w[4];
-  __device__ __forceinline__ Words() : w{0, 0, 0, 0} {}
-  __device__ __forceinline__ Words(const Pack<T>& p) { memcpy(w, &p, 16); }
-  __device__ __forceinline__ operator Pack<T>() const {
-    Pack<T> p;
-    memcpy(&p, w, 16);
-    return p;
-  }
-  __device__ __forceinline__ float f(int j) const {
-    if constexpr (N == 4) return __uint_as_float(w[j]);
-    else if constexpr (std::is_same<T, Bf16Elem>::value)
-      return __uint_as_float(j & 1 ? w[j / 2] & 0xFFFF0000u : w[j / 2] << 16);
-    else {
-      const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w[j / 2]));
-      return j & 1 ? v.y : v.x;
-    }
-  }
-  // values j and j + 1, j even
-  __device__ __forceinline__ void set2(int j, float a, float b) {
-    if constexpr (N == 4) {
-      w[j] = __float_as_uint(a);
-      w[j + 1] = __float_as_uint(b);
-    } else if constexpr (std::is_same<T, Bf16Elem>::value) {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-      w[j / 2] = *reinterpret_cast<const uint32_t*>(&h);
-    } else {
-      const __half2 h = __floats2half2_rn(a, b);
-      w[j / 2] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-  }
-  // Each value plus o's, rounded to T.  (Two 16-bit values at a time, with one rounding; a sum in fp32 first would round to
-  // the same: it is exact unless the smaller value is below 2^-13 of the larger, which then stays what it is.)
-  __device__ __forceinline__ void add(const Words& o) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (N == 4) {
-        w[i] = __float_as_uint(__uint_as_float(w[i]) + __uint_as_float(o.w[i]));
-      } else if constexpr (std::is_same<T, Bf16Elem>::value) {
-        const __nv_bfloat162 h = __hadd2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]), *reinterpret_cast<const __nv_bfloat162*>(&o.w[i]));
-        w[i] = *reinterpret_cast<const uint32_t*>(&h);
-      } else {
-        const __half2 h = __hadd2(*reinterpret_cast<const __half2*>(&w[i]), *reinterpret_cast<const __half2*>(&o.w[i]));
-        w[i] = *reinterpret_cast<const uint32_t*>(&h);
-      }
-    }
-  }
-  // After this the compiler has the words alone: without it, it holds the values over a reduction, in twice the registers.
-  __device__ __forceinline__ void keep() {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) asm volatile("" : "+r"(w[i]));
-  }
-};
 
 // A matrix of rows of H columns.  AL: every row on a 16-byte boundary and H in whole packs.
 template <class T>

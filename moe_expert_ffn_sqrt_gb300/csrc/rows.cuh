@@ -4,6 +4,7 @@
 #include <cuda_fp16.h>
 
 #include <cstring>
+#include <type_traits>
 
 #include "kernels.h"
 
@@ -104,6 +105,65 @@ __device__ __forceinline__ void store_part(typename T::raw* p, const Pack<T>& r,
   for (int i = 0; i < Pack<T>::N; ++i)
     if (i >= from && i < to) p[i] = r.v[i];
 }
+
+// A pack as words: two 16-bit values are taken out of and put into a word at a time.  (As an array of 16-bit values the
+// compiler gives each a register of its own.)
+template <class T>
+struct Words {
+  static constexpr int N = Pack<T>::N;
+  uint32_t w[4];
+  __device__ __forceinline__ Words() : w{0, 0, 0, 0} {}
+  __device__ __forceinline__ Words(const uint4& u) : w{u.x, u.y, u.z, u.w} {}
+  __device__ __forceinline__ Words(const Pack<T>& p) { memcpy(w, &p, 16); }
+  __device__ __forceinline__ operator Pack<T>() const {
+    Pack<T> p;
+    memcpy(&p, w, 16);
+    return p;
+  }
+  __device__ __forceinline__ float f(int j) const {
+    if constexpr (N == 4) return __uint_as_float(w[j]);
+    else if constexpr (std::is_same<T, Bf16Elem>::value)
+      return __uint_as_float(j & 1 ? w[j / 2] & 0xFFFF0000u : w[j / 2] << 16);
+    else {
+      const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w[j / 2]));
+      return j & 1 ? v.y : v.x;
+    }
+  }
+  // values j and j + 1, j even
+  __device__ __forceinline__ void set2(int j, float a, float b) {
+    if constexpr (N == 4) {
+      w[j] = __float_as_uint(a);
+      w[j + 1] = __float_as_uint(b);
+    } else if constexpr (std::is_same<T, Bf16Elem>::value) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+      w[j / 2] = *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+      const __half2 h = __floats2half2_rn(a, b);
+      w[j / 2] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+  }
+  // Each value plus o's, rounded to T.  (Two 16-bit values at a time, with one rounding; a sum in fp32 first would round to
+  // the same: it is exact unless the smaller value is below 2^-13 of the larger, which then stays what it is.)
+  __device__ __forceinline__ void add(const Words& o) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (N == 4) {
+        w[i] = __float_as_uint(__uint_as_float(w[i]) + __uint_as_float(o.w[i]));
+      } else if constexpr (std::is_same<T, Bf16Elem>::value) {
+        const __nv_bfloat162 h = __hadd2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]), *reinterpret_cast<const __nv_bfloat162*>(&o.w[i]));
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+      } else {
+        const __half2 h = __hadd2(*reinterpret_cast<const __half2*>(&w[i]), *reinterpret_cast<const __half2*>(&o.w[i]));
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+    }
+  }
+  // After this the compiler has the words alone: without it, it holds the values over a reduction, in twice the registers.
+  __device__ __forceinline__ void keep() {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) asm volatile("" : "+r"(w[i]));
+  }
+};
 
 // Expert e's rows in buffers of `rows` rows: cnt rows from row seg on (counts null: all of them).  Called by the whole
 // CTA; where `report`, a segment that would leave the buffers is recorded; it is cut in any case.

@@ -5,7 +5,7 @@ namespace moe {
 
 namespace {
 
-constexpr int kRows8Threads = 256;
+constexpr int kRows8Threads = 256, kRows8Ctas = 8;
 
 struct Rows8Args {
   const void* x;              // packed from
@@ -18,91 +18,109 @@ struct Rows8Args {
   uint32_t* status;
 };
 
+// A thread has the same columns of every rows-th row (a group of 128 columns to 16 lanes, fp32 32): `lanes` threads a row,
+// of which a CTA has several where `lanes` is less than its threads; blockIdx.z: which `lanes` packs of the row.
 template <class T, bool AL>
-__global__ void __launch_bounds__(kRows8Threads) pack_rows8_kernel(const Rows8Args a) {
-  using raw = typename T::raw;
-  constexpr int N = Pack<T>::N, kLanes = kGroup8 / N, kPer = kRows8Threads / kLanes;
-  grid_dependency_wait();
-  grid_launch_dependents();
-  int seg, cnt;
-  expert_segment(a.counts, blockIdx.y, a.align, a.rows, blockIdx.x == 0, seg, cnt, a.status);
-  const int groups = groups8(a.cols), lane = threadIdx.x % kLanes;
-  const raw* lo = static_cast<const raw*>(a.x);
-  const raw* hi = lo + (a.rows - 1) * a.ldx + a.cols;
-  const long long units = static_cast<long long>(cnt) * groups, step = static_cast<long long>(gridDim.x) * kPer;
-  for (long long u0 = static_cast<long long>(blockIdx.x) * kPer; u0 < units; u0 += step) {
-    const long long u = u0 + threadIdx.x / kLanes, row = seg + u / groups;
-    const int g = static_cast<int>(u % groups), c = g * kGroup8 + lane * N;
-    const bool live = u < units && c < a.cols;
-    float v[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = 0.f;
-    if (live) {
-      Pack<T> p;
-      if constexpr (AL) {
-        p = load_pack<T>(lo + row * a.ldx + c);
-      } else {
-        ShiftedPack<T> s;
-        s.load(lo + row * a.ldx + c, lo, hi);
-        p = s.get();
-      }
-#pragma unroll
-      for (int i = 0; i < N; ++i)
-        if (AL || c + i < a.cols) v[i] = p.f(i);
-    }
-    uint32_t w[N / 4];
-    const uint32_t scale = encode8<N>(v, w);
-    if (live) {
-      store_codes8<N>(a.q + row * a.ldq + c, w, a.cols - c, a.words);
-      if (lane == 0) a.sf[row * a.ldsf + g] = static_cast<uint8_t>(scale);
-    }
-  }
-}
-
-// Row r of the output is row r of the codes, or row ids[r] / div of them.
-template <class T, bool AL>
-__global__ void __launch_bounds__(kRows8Threads) unpack_rows8_kernel(const Rows8Args a) {
+__global__ void __launch_bounds__(kRows8Threads) pack_rows8_kernel(const Rows8Args a, int lanes) {
   using raw = typename T::raw;
   constexpr int N = Pack<T>::N;
   grid_dependency_wait();
   grid_launch_dependents();
   int seg, cnt;
-  expert_segment(a.counts, blockIdx.y, a.align, a.rows, blockIdx.x == 0, seg, cnt, a.status);
-  const int packs = (a.cols + N - 1) / N;
-  const long long units = static_cast<long long>(cnt) * packs, step = static_cast<long long>(gridDim.x) * kRows8Threads;
-  for (long long u = static_cast<long long>(blockIdx.x) * kRows8Threads + threadIdx.x; u < units; u += step) {
-    const long long row = seg + u / packs;
-    const int c = static_cast<int>(u % packs) * N;
-    long long src = row;
-    if (a.ids) {
-      const int id = __ldg(a.ids + row);
-      src = id >= 0 ? id / a.div : -1;
-      if (src >= a.src_rows) src = -1;
-      if (src < 0 && c == 0) record_error(a.status, kDevErrIndex);
+  expert_segment(a.counts, blockIdx.y, a.align, a.rows, blockIdx.x == 0 && blockIdx.z == 0, seg, cnt, a.status);
+  const int sub = threadIdx.x % lanes, c = (blockIdx.z * lanes + sub) * N, per = kRows8Threads / lanes;
+  const bool cols = c < a.cols;
+  const int step = gridDim.x * per;
+  const raw* lo = static_cast<const raw*>(a.x);
+  const raw* hi = lo + (a.rows - 1) * a.ldx + a.cols;
+  long long row = static_cast<long long>(blockIdx.x) * per;          // the CTA's first; every warp goes on as long as it does
+  const long long mine = seg + row + threadIdx.x / lanes;
+  const raw* x = lo + mine * a.ldx + c;
+  uint8_t* q = a.q + mine * a.ldq + c;
+  uint8_t* sf = a.sf + mine * a.ldsf + c / kGroup8;
+  int left = cnt - static_cast<int>(row < cnt ? row : cnt) - static_cast<int>(threadIdx.x) / lanes;     // rows from this one on
+  for (; row < cnt; row += step, left -= step) {
+    const bool live = cols && left > 0;
+    Words<T> p;
+    if (live) {
+      if constexpr (AL) {
+        p = Words<T>(*reinterpret_cast<const uint4*>(x));
+      } else {
+        ShiftedPack<T> s;
+        s.load(x, lo, hi);
+        p = Words<T>(s.get());
+      }
     }
+    float v[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = AL || c + i < a.cols ? p.f(i) : 0.f;
     uint32_t w[N / 4];
-#pragma unroll
-    for (int i = 0; i < N / 4; ++i) w[i] = 0;
-    float s = 1.f;
-    if (src >= 0) {
-      load_codes8<N>(a.q + src * a.ldq + c, w, a.cols - c, a.words);
-      s = scale8(a.sf[src * a.ldsf + c / kGroup8]);
+    const uint32_t scale = encode8<N>(v, w);
+    if (live) {
+      store_codes8<N>(q, w, a.cols - c, a.words);
+      if (c % kGroup8 == 0) *sf = static_cast<uint8_t>(scale);
     }
-    Pack<T> p;
+    x += step * a.ldx;
+    q += step * a.ldq;
+    sf += step * a.ldsf;
+  }
+}
+
+// Row r of the output is row r of the codes, or row ids[r] / div of them.  Threads as in the pack kernel; two rows' codes are
+// on their way together.
+template <class T, bool AL>
+__global__ void __launch_bounds__(kRows8Threads) unpack_rows8_kernel(const Rows8Args a, int lanes) {
+  using raw = typename T::raw;
+  constexpr int N = Pack<T>::N, kAhead = 2;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  int seg, cnt;
+  expert_segment(a.counts, blockIdx.y, a.align, a.rows, blockIdx.x == 0 && blockIdx.z == 0, seg, cnt, a.status);
+  const int sub = threadIdx.x % lanes, c = (blockIdx.z * lanes + sub) * N, per = kRows8Threads / lanes;
+  const int step = gridDim.x * per;
+  if (c >= a.cols) return;
+  const uint8_t *q = a.q + c, *sf = a.sf + c / kGroup8;
+  long long row = static_cast<long long>(blockIdx.x) * per + threadIdx.x / lanes;
+  raw* out = static_cast<raw*>(a.out) + (seg + row) * a.ldx + c;
+  for (; row < cnt; row += kAhead * step) {
+    uint32_t w[kAhead][N / 4], s[kAhead];
 #pragma unroll
-    for (int i = 0; i < N / 4; ++i) {
-      float v[4];
-      values8(w[i], s, v);
+    for (int k = 0; k < kAhead; ++k) {
+      long long src = seg + row + k * step;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) p.v[4 * i + j] = from_value8<T>(v[j]);
+      for (int i = 0; i < N / 4; ++i) w[k][i] = 0;
+      s[k] = 127;
+      if (row + k * step >= cnt) continue;
+      if (a.ids) {
+        const int id = __ldg(a.ids + src);
+        src = id >= 0 ? static_cast<unsigned>(id) / static_cast<unsigned>(a.div) : -1;
+        if (src >= a.src_rows) src = -1;
+        if (src < 0) {
+          if (c == 0) record_error(a.status, kDevErrIndex);
+          continue;
+        }
+      }
+      load_codes8<N>(q + src * a.ldq, w[k], a.cols - c, a.words);
+      s[k] = sf[src * a.ldsf];
     }
-    raw* o = static_cast<raw*>(a.out) + row * a.ldx + c;
-    if constexpr (AL) {
-      store_pack<T>(o, p);
-    } else {
 #pragma unroll
-      for (int i = 0; i < N; ++i)
-        if (c + i < a.cols) o[i] = p.v[i];
+    for (int k = 0; k < kAhead; ++k) {
+      float v[N];
+      decode8<T, N>(w[k], s[k], v);
+      Words<T> p;
+#pragma unroll
+      for (int i = 0; i < N; i += 2) p.set2(i, v[i], v[i + 1]);
+      if (row + k * step < cnt) {
+        if constexpr (AL) {
+          *reinterpret_cast<uint4*>(out) = make_uint4(p.w[0], p.w[1], p.w[2], p.w[3]);
+        } else {
+          const Pack<T> o = p;
+#pragma unroll
+          for (int i = 0; i < N; ++i)
+            if (c + i < a.cols) out[i] = o.v[i];
+        }
+      }
+      out += step * a.ldx;
     }
   }
 }
@@ -124,25 +142,27 @@ Rows8Args rows8_args(RowsView x, const Rows8View& m, const int32_t* counts, int 
   return a;
 }
 
-// CTAs per segment: `units` in all at `per` a CTA, sixteen CTAs per SM at most.
-dim3 rows8_grid(long long units, int per, int E) {
-  long long n = (units + per - 1) / per;
-  const long long most = (16LL * num_sms() + E - 1) / E;
-  if (n > most) n = most;
-  return dim3(static_cast<unsigned>(n < 1 ? 1 : n), static_cast<unsigned>(E));
+// Threads per row: the most (of 256, 128, ..) that leave at most an eighth of a row's last round idle; least: a group's.
+template <class T, class K>
+cudaError_t rows8_launch(K kernel, const Rows8Args& a, int E, cudaStream_t stream) {
+  const int packs = (a.cols + Pack<T>::N - 1) / Pack<T>::N, least = kGroup8 / Pack<T>::N;
+  int lanes = kRows8Threads;
+  while (lanes > least && (packs + lanes - 1) / lanes * lanes - packs > packs / 8) lanes /= 2;
+  const int z = (packs + lanes - 1) / lanes, per = kRows8Threads / lanes;
+  const long long blocks = (static_cast<long long>(a.rows) + per - 1) / per;
+  long long most = static_cast<long long>(kRows8Ctas) * num_sms() / (static_cast<long long>(z) * E);
+  if (most < 1) most = 1;
+  return launch_pdl(kernel,
+                    dim3(static_cast<unsigned>(blocks < most ? blocks : most), static_cast<unsigned>(E), static_cast<unsigned>(z)),
+                    dim3(kRows8Threads), 0, stream, a, lanes);
 }
-
 template <class T>
 cudaError_t pack_launch(const Rows8Args& a, bool al, int E, cudaStream_t stream) {
-  constexpr int per = kRows8Threads / (kGroup8 / Pack<T>::N);
-  return launch_pdl(al ? pack_rows8_kernel<T, true> : pack_rows8_kernel<T, false>,
-                    rows8_grid(static_cast<long long>(a.rows) * groups8(a.cols), per, E), dim3(kRows8Threads), 0, stream, a);
+  return rows8_launch<T>(al ? pack_rows8_kernel<T, true> : pack_rows8_kernel<T, false>, a, E, stream);
 }
 template <class T>
 cudaError_t unpack_launch(const Rows8Args& a, bool al, int E, cudaStream_t stream) {
-  return launch_pdl(al ? unpack_rows8_kernel<T, true> : unpack_rows8_kernel<T, false>,
-                    rows8_grid(static_cast<long long>(a.rows) * ((a.cols + Pack<T>::N - 1) / Pack<T>::N), kRows8Threads, E),
-                    dim3(kRows8Threads), 0, stream, a);
+  return rows8_launch<T>(al ? unpack_rows8_kernel<T, true> : unpack_rows8_kernel<T, false>, a, E, stream);
 }
 
 }  // namespace

@@ -74,38 +74,50 @@ __device__ __forceinline__ void store_codes8(uint8_t* q, const uint32_t (&w)[N /
     if (i < n) q[i] = static_cast<uint8_t>(w[i / 4] >> (8 * (i % 4)));
 }
 
-// 2^(s - 127) of a scale byte (255, which no call here writes, is UE8M0's NaN).
-__device__ __forceinline__ float scale8(uint32_t s) {
-  return s == 255 ? __int_as_float(0x7fc00000) : s ? __uint_as_float(s << 23) : __uint_as_float(0x00400000u);
-}
-
-// Values of 4 codes.  Two codes to fp16 at a time is exact; so is the product with a power of two within fp32's range.
-__device__ __forceinline__ void values8(uint32_t w, float scale, float (&v)[4]) {
+// Values (as T holds them, in fp32) of N codes with scale byte s.  Two codes to fp16 at a time is exact, so is the product
+// with 2^(s - 127) within fp32's range, and T holds a value of its own type's rows exactly but where a code rounded up to
+// the next power of two past T's largest, which then stands for it (65536 of fp16, 2^128 of bf16 and fp32); only scales
+// from kLimit on can reach that.  (s = 255, which no call here writes, is UE8M0's NaN.)
+template <class T, int N>
+__device__ __forceinline__ void decode8(const uint32_t (&w)[N / 4], uint32_t s, float (&v)[N]) {
+  constexpr bool kHalf = std::is_same<T, F16Elem>::value;
+  constexpr uint32_t kLimit = kHalf ? 135 : 247;           // 448 * 2^8 > 65504, 448 * 2^120 > 2^128
+  const float scale = __uint_as_float((s << 23) | (s ? 0u : 0x00400000u));
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w >> (16 * i)), __NV_E4M3);
+  for (int i = 0; i < N / 2; ++i) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w[i / 2] >> (16 * (i % 2))), __NV_E4M3);
     const float2 f = __half22float2(__half2(h));
     v[2 * i] = f.x * scale;
     v[2 * i + 1] = f.y * scale;
   }
+  if (s >= kLimit) {
+    const float most = kHalf ? 65504.f : std::is_same<T, Bf16Elem>::value ? 3.3895314e38f : 3.402823466e38f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (fabsf(v[i]) > most) v[i] = copysignf(most, v[i]);
+      if (s == 255) v[i] = __int_as_float(0x7fc00000);
+    }
+  }
 }
 
-// A value of the 8-bit rows in type T: exact but for magnitudes past T's largest, which take it (a value of T whose
-// code rounded up to the next power of two: 65536 of fp16, 2^128 of bf16 and fp32).
+// The same of 8 codes, taken out one by one (the codes and the scale stay in three registers).
 template <class T>
-__device__ __forceinline__ typename T::raw from_value8(float v);
-template <>
-__device__ __forceinline__ uint16_t from_value8<F16Elem>(float v) {
-  return F16Elem::from_f(fabsf(v) > 65504.f ? copysignf(65504.f, v) : v);
-}
-template <>
-__device__ __forceinline__ uint16_t from_value8<Bf16Elem>(float v) {
-  return Bf16Elem::from_f(isinf(v) ? copysignf(3.3895314e38f, v) : v);
-}
-template <>
-__device__ __forceinline__ float from_value8<F32Elem>(float v) {
-  return isinf(v) ? copysignf(3.402823466e38f, v) : v;
-}
+struct Codes8 {
+  uint32_t w[2];
+  float scale;
+  __device__ __forceinline__ void set_scale(uint32_t s) {
+    scale = s == 255 ? __int_as_float(0x7fc00000) : __uint_as_float((s << 23) | (s ? 0u : 0x00400000u));
+  }
+  __device__ __forceinline__ float f(int i) const {
+    constexpr float most = std::is_same<T, F16Elem>::value ? 65504.f : 3.3895314e38f;
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w[i / 4] >> (16 * (i / 2 % 2))), __NV_E4M3);
+    const float2 p = __half22float2(__half2(h));
+    float v = (i % 2 ? p.y : p.x) * scale;
+    v = fabsf(v) > most ? copysignf(most, v) : v;
+    // (rows of other types may hold values that fp16 rounds)
+    return std::is_same<T, F16Elem>::value ? F16Elem::to_f(F16Elem::from_f(v)) : v;
+  }
+};
 
 // N codes from q on (whole words where `words`); zeros past the first n.
 template <int N>

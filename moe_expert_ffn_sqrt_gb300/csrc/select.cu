@@ -22,7 +22,7 @@ namespace moe {
 
 namespace {
 
-constexpr int kSelectWarps = 8;
+constexpr int kSelectWarps = 4, kSelectCtas = 8;       // of a CTA; CTAs per SM that are there at a time
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kNone = 0x7fffffff;
 
@@ -69,16 +69,20 @@ struct FastScores {
   __device__ __forceinline__ float operator()(float l) const {
     if (FN == 0) return l == -INFINITY ? 0.f : __expf(l - lmax) * over;
     if (FN == 1) return sqrtf(fmaxf(l, 0.f) + log1pf(expf(-fabsf(l))));
-    return __fdividef(1.f, 1.f + __expf(-l));
+    float e, s;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(l * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));
+    return s;
   }
-  // How far the difference of two scores may be off at most.  __expf(x) is within 2 + 1.2 |x| steps of 2^-23, the division
-  // within two.  Sigmoid: 1 / (1 + e^-l) is off by s (4.5 + 1.2 max(-l, 0)) 2^-23, which rises with l.  Softmax: the
-  // difference of two logits d adds |d| / 2 steps, all outweighed by e^-d: two steps of the largest score, and the sum's PER
-  // + 5 additions.  Square root, logarithm: accurate ones, eight steps.  (Scores below 2^-126 come out as 0.)
+  // How far the difference of two scores may be off at most.  Exponentials of x are within 2 + 1.5 |x| steps of 2^-23,
+  // reciprocals and products within one or two.  Sigmoid: 1 / (1 + e^-l) is off by s (5 + 1.5 max(-l, 0)) 2^-23, at most
+  // eight steps (s is below e^l).  Softmax: the difference of two logits d adds |d| / 2 steps, all outweighed by e^-d: two
+  // steps of the largest score, and the sum's PER + 5 additions.  Square root, logarithm: accurate ones, eight steps of the
+  // largest score.  (Scores below 2^-126 come out as 0.)
   template <int PER>
   __device__ __forceinline__ float apart() const {
-    const float steps = FN == 0 ? PER + 16.f : FN == 1 ? 16.f : 16.f + 4.f * fmaxf(-lmax, 0.f);
-    return (*this)(lmax) * (steps * 0x1p-23f) + 0x1p-120f;
+    if (FN == 2) return 0x1p-19f;
+    return (*this)(lmax) * ((FN == 0 ? PER + 16.f : 16.f) * 0x1p-23f) + 0x1p-120f;
   }
 };
 template <int FN>
@@ -200,12 +204,10 @@ __device__ __noinline__ int select_all64(const SelectArgs& a, const uint8_t* row
 }
 
 template <int FN, int PER, int V>
-__global__ void __launch_bounds__(kSelectWarps * 32) select_kernel(const SelectArgs a) {
-  __shared__ int s_id[kSelectWarps][34];               // experts that are near, then the chosen ones in order
-  __shared__ uint32_t s_key[kSelectWarps][34];
+__global__ void __launch_bounds__(kSelectWarps * 32, PER <= 8 ? kSelectCtas : 1) select_kernel(const SelectArgs a) {
+  __shared__ uint2 s_near[kSelectWarps][34];           // experts that are near (id, key), then the chosen ones in order
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g = lane >> a.log_l, sub = lane & (a.L - 1);
-  int* ids = s_id[warp];
-  uint32_t* keys = s_key[warp];
+  uint2* list = s_near[warp];
   grid_dependency_wait();
   grid_launch_dependents();
   const bool used = g < a.G;
@@ -231,12 +233,15 @@ __global__ void __launch_bounds__(kSelectWarps * 32) select_kernel(const SelectA
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         v[i + j] = f[j];
-        key[i + j] = there ? ordered(f[j]) : 0;
-        top = max(top, key[i + j]);
+        key[i + j] = there;
+        if (FN != 2 || !a.bias) {
+          if (there) key[i + j] = ordered(f[j]);
+          top = max(top, key[i + j]);
+        }
       }
     }
-    const float lmax = from_ordered(__reduce_max_sync(kAll, top));
-    float sum = 1.f;
+    float lmax = 0.f, sum = 1.f;
+    if (FN != 2) lmax = from_ordered(__reduce_max_sync(kAll, top));
     if (FN == 0) {
       sum = 0.f;
 #pragma unroll
@@ -258,22 +263,26 @@ __global__ void __launch_bounds__(kSelectWarps * 32) select_kernel(const SelectA
       k2 = max(k2, min(k1, key[i]));
       k1 = max(k1, key[i]);
     }
-    // Experts of keys >= bound into ids (and keys), 32 of them at most; returns how many there are.
-    const auto collect = [&](uint32_t bound) {
-      int c = 0;
+    // The lanes' experts with `is` into list, 32 of them at most; returns how many there are.
+    const auto collect = [&](auto is) {
+      int n = 0;
 #pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const bool is = key[i] && key[i] >= bound;
-        const unsigned m = __ballot_sync(kAll, is);
-        if (m) {
-          const int p = c + __popc(m & ((1u << lane) - 1));
-          if (is && p < 32) {
-            ids[p] = e0 + at(i);
-            keys[p] = key[i];
-          }
-          c += __popc(m);
-        }
+      for (int i = 0; i < PER; ++i) n += is(i);
+      int p = n;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(kAll, p, d);
+        if (lane >= d) p += o;
       }
+      const int c = __shfl_sync(kAll, p, 31);
+      p -= n;
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        {
+          const bool in = is(i);
+          if (in && p < 32) list[p] = make_uint2(e0 + at(i), key[i]);
+          p += in;
+        }
       __syncwarp();
       return c;
     };
@@ -305,34 +314,25 @@ __global__ void __launch_bounds__(kSelectWarps * 32) select_kernel(const SelectA
       uint32_t mine = used && sub == 0 ? ordered(worth) : 0;
       const float tol = 2.f * near + __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(size))) * 0x1p-21f;
       unsigned open = 0;                // by the lanes with sub = 0
-      float last = 0.f;
+      uint32_t kth = 0;
       for (int k = 0; k < a.KG; ++k) {
         const uint32_t best = __reduce_max_sync(kAll, mine);
         const int who = __ffs(__ballot_sync(kAll, mine == best)) - 1;      // the lowest group of equals
         open |= 1u << who;
         if (lane == who) mine = 0;
-        last = from_ordered(best);
+        kth = best;
       }
-      const float next = from_ordered(__reduce_max_sync(kAll, mine));
+      const float last = from_ordered(kth), next = from_ordered(__reduce_max_sync(kAll, mine));
       if (last - next <= tol) {
         // groups that are surely in, and those that may be: the latter in 64 bits, from their experts that may be among
         // the best two
         const bool in = used && worth - next > tol, maybe = used && !in && !(last - worth > tol);
         const uint32_t bound = !maybe ? 0xffffffffu : a.bias ? ordered(f2 - tol) : two ? g2 : g1;
-        int c = 0;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-          const bool is = maybe && key[i] >= bound;
-          const unsigned m = __ballot_sync(kAll, is);
-          const int p = c + __popc(m & ((1u << lane) - 1));
-          if (is && p < 32) ids[p] = e0 + at(i);
-          c += __popc(m);
-        }
-        __syncwarp();
+        const int c = collect([&](int i) { return maybe && key[i] >= bound; });
         all64 = c > 32;
         if (!all64) {
           const Scores64<FN> score = scores64<FN>(a, row, lmax);
-          const int e = lane < c ? ids[lane] : 0;
+          const int e = lane < c ? list[lane].x : 0;
           const double k = lane < c ? key64(score, e) : 0.;
           const int of = lane < c ? e / a.per_group : -1;
           double b1 = -INFINITY, b2 = -INFINITY;
@@ -372,29 +372,27 @@ __global__ void __launch_bounds__(kSelectWarps * 32) select_kernel(const SelectA
       uint32_t bound = 0;
       for (int k = 0; k <= a.K; ++k) {
         bound = __reduce_max_sync(kAll, k1);
-        if (bound == 0) break;
         const int who = __ffs(__ballot_sync(kAll, k1 == bound)) - 1;
         if (lane == who) {
           k1 = k2;
           k2 = 0;
         }
       }
-      int c = collect(bound);
+      bound = max(bound, 1u);
+      int c = collect([&](int i) { return key[i] >= bound; });
       if (c <= 32) {
-        const int e = lane < c ? ids[lane] : kNone;
-        const uint32_t k = lane < c ? keys[lane] : 0;
+        // the order of (key, lower id first) as one number
+        const uint2 m = lane < c ? list[lane] : make_uint2(0, 0);
+        const unsigned long long mine = static_cast<unsigned long long>(m.y) << 32 | ~m.x;
         int rank = 0;
+#pragma unroll 4
         for (int r = 0; r < c; ++r) {
-          const uint32_t o = __shfl_sync(kAll, k, r);
-          const int oe = __shfl_sync(kAll, e, r);
-          rank += o > k || (o == k && oe < e);
+          const uint2 o = list[r];
+          rank += (static_cast<unsigned long long>(o.y) << 32 | ~o.x) > mine;
         }
         __syncwarp();
-        if (lane < c && rank <= a.K) {
-          ids[rank] = e;
-          keys[rank] = k;
-        }
-        if (lane == 0 && c <= a.K) keys[a.K] = 0;
+        if (lane < c && rank <= a.K) list[rank] = m;
+        if (lane == 0 && c <= a.K) list[a.K].y = 0;
       } else {
         __syncwarp();
         for (int k = 0; k <= a.K; ++k) {
@@ -409,10 +407,7 @@ __global__ void __launch_bounds__(kSelectWarps * 32) select_kernel(const SelectA
           const uint32_t best = __reduce_max_sync(kAll, b);
           const int e = b == best && best ? e0 + at(bi) : kNone;
           const int won = static_cast<int>(__reduce_min_sync(kAll, static_cast<uint32_t>(e)));
-          if (lane == 0) {
-            ids[k] = won;
-            keys[k] = best;
-          }
+          if (lane == 0) list[k] = make_uint2(won, best);
           if (e == won && best) {
 #pragma unroll
             for (int i = 0; i < PER; ++i)
@@ -421,14 +416,15 @@ __global__ void __launch_bounds__(kSelectWarps * 32) select_kernel(const SelectA
         }
       }
       __syncwarp();
-      if (lane < a.K) id = ids[lane];
+      const uint2 own = lane < a.K ? list[lane] : make_uint2(0, 1);
+      id = own.x;
       if (a.bias) {
         bool unsure = false;
-        const uint32_t nk = lane < a.K ? keys[lane + 1] : 0;
-        const float f = from_ordered(lane < a.K ? keys[lane] : 1);
-        if (nk != 0) {
-          const int ne = ids[lane + 1];
-          const float nf = from_ordered(nk);
+        const uint2 after = lane < a.K ? list[lane + 1] : make_uint2(0, 0);
+        const float f = from_ordered(own.y);
+        if (after.y != 0) {
+          const int ne = after.x;
+          const float nf = from_ordered(after.y);
           if (f - nf <= near + (size_of(f) + size_of(nf)) * 0x1p-23f)
             unsure = logit(a, row, id) != logit(a, row, ne) || __ldg(a.bias + id) != __ldg(a.bias + ne);
         }
@@ -438,11 +434,11 @@ __global__ void __launch_bounds__(kSelectWarps * 32) select_kernel(const SelectA
           const uint32_t low = ordered(kth - (near + size_of(kth) * 0x1p-21f));
           __syncwarp();
           all64 = c > 32;               // (the rounds have used the keys up)
-          if (!all64) c = collect(low);
+          if (!all64) c = collect([&](int i) { return key[i] >= low; });
           all64 = all64 || c > 32;
           if (!all64) {
             const Scores64<FN> score = scores64<FN>(a, row, lmax);
-            const int e = lane < c ? ids[lane] : kNone;
+            const int e = lane < c ? list[lane].x : kNone;
             const double k = lane < c ? key64(score, e) : -INFINITY;
             int rank = 0;
             for (int r = 0; r < c; ++r) {
@@ -451,9 +447,9 @@ __global__ void __launch_bounds__(kSelectWarps * 32) select_kernel(const SelectA
               rank += o > k || (o == k && oe < e);
             }
             __syncwarp();
-            if (lane < c && rank < a.K) ids[rank] = e;
+            if (lane < c && rank < a.K) list[rank].x = e;
             __syncwarp();
-            if (lane < a.K) id = ids[lane];
+            if (lane < a.K) id = list[lane].x;
           }
         }
       }
@@ -477,9 +473,9 @@ __global__ void __launch_bounds__(kSelectWarps * 32) select_kernel(const SelectA
 
 template <int FN, int PER, int V>
 cudaError_t select_launch(const SelectArgs& a, cudaStream_t stream) {
-  const long long ctas = (static_cast<long long>(a.T) + kSelectWarps - 1) / kSelectWarps, most = 8LL * num_sms();
-  return launch_pdl(select_kernel<FN, PER, V>, dim3(static_cast<unsigned>(ctas < most ? ctas : most)), dim3(kSelectWarps * 32), 0,
-                    stream, a);
+  // (as many tokens to every warp that is there at a time: 16384 tokens 21.8 us instead of 19.4; a warp a token 22)
+  const int ctas = (a.T - 1) / kSelectWarps + 1, most = 2 * kSelectCtas * num_sms();
+  return launch_pdl(select_kernel<FN, PER, V>, dim3(ctas < most ? ctas : most), dim3(kSelectWarps * 32), 0, stream, a);
 }
 
 template <int FN>
