@@ -106,23 +106,33 @@ __device__ __forceinline__ void put_words(typename T::raw* p, int left, const Wo
   }
 }
 
-// The outputs of N values of y from column c of a row on (called by all lanes of a group of 128 columns).
+// The same by all lanes of a warp, whose packs follow one another (c may lie past the row's end).
+template <class T, bool AL>
+__device__ __forceinline__ void put_row(typename T::raw* row, int c, int H, const Words<T>& words) {
+  if constexpr (AL) {
+    if (c < H) put_words<T, true>(row + c, H - c, words);
+  } else {
+    const int lane = threadIdx.x % 32;
+    store_shifted<T>(row, c, H, words, lane == 0, lane == 31);
+  }
+}
+
+// The outputs of N values of y from column c of a row on (called by all lanes of a warp).
 template <class T, bool AL>
 __device__ __forceinline__ void norm_out(const NormArgs& a, const RowOut<T>& row, int c, const float (&v)[Pack<T>::N]) {
   constexpr int N = Pack<T>::N;
-  if (row.y && c < a.H) {
+  if (row.y) {
     Words<T> o;
 #pragma unroll
     for (int j = 0; j < N; j += 2) o.set2(j, v[j], v[j + 1]);
-    put_words<T, AL>(row.y + c, a.H - c, o);
+    put_row<T, AL>(row.y, c, a.H, o);
   }
   if (row.q) {
     uint32_t q[N / 4];
     const uint32_t scale = encode8<N>(v, q);
-    if (c < a.H) {
-      store_codes8<N>(row.q + c, q, a.H - c, a.q_words);
-      if (c % kGroup8 == 0) row.sf[c / kGroup8] = static_cast<uint8_t>(scale);
-    }
+    const int lane = threadIdx.x % 32;
+    store_row_codes8<N>(row.q, c, a.H, q, a.q_words, lane == 0, lane == 31);
+    if (c < a.H && c % kGroup8 == 0) row.sf[c / kGroup8] = static_cast<uint8_t>(scale);
   }
 }
 
@@ -213,7 +223,7 @@ __global__ void __launch_bounds__(NT, MIN) norm_kernel(const NormArgs a) {
       p[i] = px[i];
       if (a.res) p[i].add(pr[i]);
       p[i].keep();
-      if (out.sum && c < H) put_words<T, AL>(out.sum + c, H - c, p[i]);
+      if (out.sum) put_row<T, AL>(out.sum, c, H, p[i]);
 #pragma unroll
       for (int j = 0; j < N; ++j) ss[0] = fmaf(p[i].f(j), p[i].f(j), ss[0]);
     }
@@ -278,15 +288,18 @@ __global__ void __launch_bounds__(kNormThreads) norm_wide_kernel(const NormArgs 
 }
 
 // ------------------------------------------------------------------------------------------
-// Many rows on 16-byte boundaries: rows arrive in a ring of S shared-memory stages by bulk copies, and G groups of threads
+// Many rows: they arrive in a ring of S shared-memory stages by bulk copies, and G groups of threads
 // take them in turn (row k of the CTA's is in stage k % S and group k % G's), each into registers, so that a group's
 // reductions run under the copies and the others' work.  One CTA per SM.
 // S is a multiple of G: then a stage is always the same group's, which has seen its last row arrive before it waits for the
 // next one.  (A group that waited for a row whose stage's last row, another group's, had not arrived yet would take the
 // barrier's older phase for the one it wants: copies of different rows may arrive in any order.)
+// Rows that start anywhere (not AL) come with the ends of the 16-byte words that they begin and end in, and are shifted as
+// they are taken out; the few elements of a word that reaches out of the matrix are copied one by one.
 
 constexpr int kRingStages = 16, kRingGroups = 8;
-constexpr int kRingThreads = 960, kRingGradThreads = 608;       // of all groups, at most
+constexpr int kRingThreads = 960, kRingOddThreads = 608;        // of all groups, at most (odd: rows that start anywhere)
+constexpr int kRingGradThreads = 608;
 constexpr int kRingWarps = 30, kRingGradWarps = 16;             // of a group, at most
 constexpr int kRingBytes = 223 * 1024;                          // stages and w
 constexpr int kRingSmem = kRingBytes + 128;
@@ -304,30 +317,92 @@ struct RingState {
   uint64_t full[kRingStages], empty[kRingStages], w_full;
 };
 
-// The loading warp: `in` (n of them) hold rows of `bytes` bytes.
-template <int MOST>
+template <class E>
+__device__ __forceinline__ void copy_element(uint32_t to, uintptr_t from) {
+  if constexpr (sizeof(E) == 2)
+    asm volatile("st.shared.u16 [%0], %1;" ::"r"(to), "h"(*reinterpret_cast<const uint16_t*>(from)) : "memory");
+  else
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(to), "f"(*reinterpret_cast<const float*>(from)) : "memory");
+}
+
+// Bytes of a row's place in a stage (not AL: wherever in its first word it starts, and a word that a shift reads on).
+template <bool AL>
+__host__ __device__ __forceinline__ uint32_t ring_slot(uint32_t row_bytes) {
+  return AL ? row_bytes : (row_bytes + 15) / 16 * 16 + 32;
+}
+// Shared memory of w.
+__host__ __device__ __forceinline__ uint32_t ring_w_bytes(int H) { return static_cast<uint32_t>(H + 7) / 8 * 32; }
+
+// The loading thread: `in` hold rows of `bytes` bytes, ld bytes apart, of elements of type E.
+template <bool AL, class E, int MOST>
 __device__ __forceinline__ void ring_load(const Ring& R, RingState& st, uint32_t smem, const void* const (&in)[MOST],
-                                          const long long (&ld)[MOST], int T, uint32_t bytes, const float* w, uint32_t wbytes) {
+                                          const long long (&ld)[MOST], int T, uint32_t bytes, const float* w, int H) {
+  using U = uintptr_t;
+  const uint32_t wbytes = static_cast<uint32_t>(H) / 4 * 16;
+  for (int i = H / 4 * 4; i < (H + 7) / 8 * 8; ++i)      // the last values, and zeros to the end of a pack
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(smem + 4 * i), "f"(i < H ? __ldg(w + i) : 0.f) : "memory");
+  if (wbytes) {
+    mbar_arrive_expect_tx(smem_u32(&st.w_full), wbytes);
+    bulk_load(smem, w, wbytes, smem_u32(&st.w_full));
+  } else {
+    mbar_arrive(smem_u32(&st.w_full));
+  }
+  smem += ring_w_bytes(H);
+  const uint32_t slot = ring_slot<AL>(bytes);
   int n = 0;
 #pragma unroll
   for (int i = 0; i < MOST; ++i) n += in[i] != nullptr;
-  mbar_arrive_expect_tx(smem_u32(&st.w_full), wbytes);
-  bulk_load(smem, w, wbytes, smem_u32(&st.w_full));
-  smem += wbytes;
   int s = 0;
   uint32_t ph = 0;
   for (long long t = blockIdx.x; t < T; t += gridDim.x) {
     // (a wait that runs out ends the copies; the groups' own waits for them then run out too)
     if (!mbar_wait(smem_u32(&st.empty[s]), ph ^ 1, nullptr)) return;
     const uint32_t bar = smem_u32(&st.full[s]);
-    mbar_arrive_expect_tx(bar, n * bytes);
-    uint32_t to = smem + s * n * bytes;
+    const uint32_t stage = smem + s * n * slot;
+    if constexpr (AL) {
+      mbar_arrive_expect_tx(bar, n * bytes);
+      uint32_t to = stage;
 #pragma unroll
-    for (int i = 0; i < MOST; ++i)
-      if (in[i]) {
-        bulk_load(to, static_cast<const uint8_t*>(in[i]) + t * ld[i], bytes, bar);
-        to += bytes;
+      for (int i = 0; i < MOST; ++i)
+        if (in[i]) {
+          bulk_load(to, static_cast<const uint8_t*>(in[i]) + t * ld[i], bytes, bar);
+          to += slot;
+        }
+    } else {
+      U from[MOST];
+      uint32_t skip[MOST], size[MOST], all = 0, to = stage;
+#pragma unroll
+      for (int i = 0; i < MOST; ++i) {
+        size[i] = 0;
+        if (!in[i]) continue;
+        const U lo = reinterpret_cast<U>(in[i]), row = lo + static_cast<U>(t * ld[i]), end = row + bytes;
+        const U hi = lo + static_cast<U>((T - 1) * ld[i]) + bytes;
+        U a = row & ~U(15), b = (end + 15) & ~U(15);
+        skip[i] = 0;
+        if (a < lo) {                   // (the matrix' first row)
+          a += 16;
+          skip[i] = 16;
+          for (U e = row; e < a; e += sizeof(E)) copy_element<E>(to + static_cast<uint32_t>(e & 15), e);
+        }
+        if (b > hi) {                   // (its last one)
+          b -= 16;
+          for (U e = b; e < end; e += sizeof(E)) copy_element<E>(to + skip[i] + static_cast<uint32_t>(e - a), e);
+        }
+        from[i] = a;
+        size[i] = static_cast<uint32_t>(b - a);
+        all += size[i];
+        to += slot;
       }
+      if (t == 0 || t == T - 1) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");    // (elements copied one by one)
+      mbar_arrive_expect_tx(bar, all);
+      to = stage;
+#pragma unroll
+      for (int i = 0; i < MOST; ++i)
+        if (in[i]) {
+          if (size[i]) bulk_load(to + skip[i], reinterpret_cast<const void*>(from[i]), size[i], bar);
+          to += slot;
+        }
+    }
     if (++s == R.S) {
       s = 0;
       ph ^= 1;
@@ -369,6 +444,33 @@ __device__ __forceinline__ Words<T> shared_words(uint32_t addr) {
                : "memory");
   return v;
 }
+// Columns [c, c + N) of a row of H from its first element's place on (not AL: any place; zeros past the end).
+template <class T, bool AL>
+__device__ __forceinline__ Words<T> shared_row(uint32_t row, int c, int H) {
+  constexpr int N = Words<T>::N;
+  if constexpr (AL) {
+    return shared_words<T>(row + c * (16 / N));
+  } else {
+    const uint32_t p = row + c * (16 / N);
+    const Words<T> a = shared_words<T>(p & ~15u), b = shared_words<T>((p & ~15u) + 16);
+    ShiftedPack<T> s;
+    s.a = make_uint4(a.w[0], a.w[1], a.w[2], a.w[3]);
+    s.b = make_uint4(b.w[0], b.w[1], b.w[2], b.w[3]);
+    s.off = p & 15;
+    Pack<T> v = s.get();
+    if (c + N > H) {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (c + i >= H) v.v[i] = T::from_f(0.f);
+    }
+    return v;
+  }
+}
+// Where in its first word row t of a matrix starts.
+template <bool AL>
+__device__ __forceinline__ uint32_t ring_off(const void* p, long long row_bytes, long long t) {
+  return AL ? 0 : static_cast<uint32_t>((reinterpret_cast<uintptr_t>(p) + static_cast<uintptr_t>(t * row_bytes)) & 15);
+}
 __device__ __forceinline__ float4 shared_float4(uint32_t addr) {
   float4 f;
   asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(f.x), "=f"(f.y), "=f"(f.z), "=f"(f.w) : "r"(addr));
@@ -396,14 +498,14 @@ __device__ __forceinline__ bool group_sum(float (&v)[K], float (*sh)[W], int gro
   return ok;
 }
 
-template <class T>
-__global__ void __launch_bounds__(kRingThreads + 32, 1) norm_ring_kernel(const NormArgs a, const Ring R) {
+template <class T, bool AL>
+__global__ void __launch_bounds__((AL ? kRingThreads : kRingOddThreads) + 32, 1) norm_ring_kernel(const NormArgs a, const Ring R) {
   constexpr int N = Pack<T>::N, PER = kRingPer;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   __shared__ RingState st;
   __shared__ __align__(16) float sh[kRingGroups][2][1][32];
   const int H = a.H, lane = threadIdx.x % 32, group = threadIdx.x / R.threads, tid = threadIdx.x - group * R.threads;
-  const uint32_t smem = (smem_u32(smem_raw) + 127) & ~127u, bytes = H * 16 / N, wbytes = H * 4;
+  const uint32_t smem = (smem_u32(smem_raw) + 127) & ~127u, bytes = H * (16 / N), slot = ring_slot<AL>(bytes);
   ring_init(R, st);
   for (int i = threadIdx.x; i < kRingGroups * 2 * 32; i += blockDim.x) (&sh[0][0][0][0])[i] = 0.f;
   grid_dependency_wait();
@@ -413,11 +515,11 @@ __global__ void __launch_bounds__(kRingThreads + 32, 1) norm_ring_kernel(const N
     if (lane == 0) {
       const void* in[2] = {a.x, a.res};
       const long long ld[2] = {a.ldx * (16 / N), a.ldr * (16 / N)};
-      ring_load(R, st, smem, in, ld, a.T, bytes, a.w, wbytes);
+      ring_load<AL, typename T::raw>(R, st, smem, in, ld, a.T, bytes, a.w, H);
     }
     return;
   }
-  const uint32_t stage0 = smem + wbytes, stage = (a.res ? 2 : 1) * bytes;
+  const uint32_t stage0 = smem + ring_w_bytes(H), stage = (a.res ? 2 : 1) * slot;
   bool ok = mbar_wait(smem_u32(&st.w_full), 0, nullptr);
   RingPlace at(group, R.S);
   int turn = 0;
@@ -432,8 +534,8 @@ __global__ void __launch_bounds__(kRingThreads + 32, 1) norm_ring_kernel(const N
       const int c = (tid + i * R.threads) * N;
       p[i] = Words<T>{};
       if (c < H) {
-        p[i] = shared_words<T>(from + c * (16 / N));
-        if (a.res) p[i].add(shared_words<T>(from + bytes + c * (16 / N)));
+        p[i] = shared_row<T, AL>(from + ring_off<AL>(a.x, a.ldx * (16 / N), t), c, H);
+        if (a.res) p[i].add(shared_row<T, AL>(from + slot + ring_off<AL>(a.res, a.ldr * (16 / N), t), c, H));
       }
     }
     __syncwarp();
@@ -442,7 +544,7 @@ __global__ void __launch_bounds__(kRingThreads + 32, 1) norm_ring_kernel(const N
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const int c = (tid + i * R.threads) * N;
-      if (out.sum && c < H) put_words<T, true>(out.sum + c, N, p[i]);
+      if (out.sum) put_row<T, AL>(out.sum, c, H, p[i]);
 #pragma unroll
       for (int j = 0; j < N; ++j) ss[0] = fmaf(p[i].f(j), p[i].f(j), ss[0]);
       p[i].keep();
@@ -462,7 +564,7 @@ __global__ void __launch_bounds__(kRingThreads + 32, 1) norm_ring_kernel(const N
         v[j + 2] = p[i].f(j + 2) * rs * w.z;
         v[j + 3] = p[i].f(j + 3) * rs * w.w;
       }
-      norm_out<T, true>(a, out, c, v);
+      norm_out<T, AL>(a, out, c, v);
     }
   }
 }
@@ -552,7 +654,7 @@ __global__ void __launch_bounds__(NT, MIN) norm_grad_kernel(const NormGradArgs a
       }
 #pragma unroll
       for (int j = 0; j < N; j += 2) o.set2(j, v[j], v[j + 1]);
-      if (a.dx && c < H) put_words<T, AL>(dx + c, H - c, o);
+      if (a.dx) put_row<T, AL>(dx, c, H, o);
     }
   }
   if (!a.part) return;
@@ -581,14 +683,14 @@ __global__ void __launch_bounds__(NT, MIN) norm_grad_kernel(const NormGradArgs a
 }
 
 // (the rows' sums and their use as in norm_ring_kernel)
-template <class T>
+template <class T, bool AL>
 __global__ void __launch_bounds__(kRingGradThreads + 32, 1) norm_grad_ring_kernel(const NormGradArgs a, const Ring R) {
   constexpr int N = Pack<T>::N, PER = kRingPer;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   __shared__ RingState st;
   __shared__ __align__(16) float sh[kRingGroups][2][2][kRingGradWarps];
   const int H = a.H, lane = threadIdx.x % 32, group = threadIdx.x / R.threads, tid = threadIdx.x - group * R.threads;
-  const uint32_t smem = (smem_u32(smem_raw) + 127) & ~127u, bytes = H * 16 / N, wbytes = H * 4;
+  const uint32_t smem = (smem_u32(smem_raw) + 127) & ~127u, bytes = H * (16 / N), slot = ring_slot<AL>(bytes);
   ring_init(R, st);
   for (int i = threadIdx.x; i < kRingGroups * 2 * 2 * kRingGradWarps; i += blockDim.x) (&sh[0][0][0][0])[i] = 0.f;
   grid_dependency_wait();
@@ -598,11 +700,11 @@ __global__ void __launch_bounds__(kRingGradThreads + 32, 1) norm_grad_ring_kerne
     if (lane == 0) {
       const void* in[3] = {a.x, a.dy, a.dsum};
       const long long ld[3] = {a.ldx * (16 / N), a.lddy * (16 / N), a.lddsum * (16 / N)};
-      ring_load(R, st, smem, in, ld, a.T, bytes, a.w, wbytes);
+      ring_load<AL, typename T::raw>(R, st, smem, in, ld, a.T, bytes, a.w, H);
     }
     return;
   }
-  const uint32_t stage0 = smem + wbytes, stage = (a.dsum ? 3 : 2) * bytes;
+  const uint32_t stage0 = smem + ring_w_bytes(H), stage = (a.dsum ? 3 : 2) * slot;
   bool ok = mbar_wait(smem_u32(&st.w_full), 0, nullptr);
   float acc[PER][N];
 #pragma unroll
@@ -622,9 +724,9 @@ __global__ void __launch_bounds__(kRingGradThreads + 32, 1) norm_grad_ring_kerne
       const int c = (tid + i * R.threads) * N;
       p[i] = d[i] = u[i] = Words<T>{};
       if (c < H) {
-        p[i] = shared_words<T>(from + c * (16 / N));
-        d[i] = shared_words<T>(from + bytes + c * (16 / N));
-        if (a.dsum) u[i] = shared_words<T>(from + 2 * bytes + c * (16 / N));
+        p[i] = shared_row<T, AL>(from + ring_off<AL>(a.x, a.ldx * (16 / N), t), c, H);
+        d[i] = shared_row<T, AL>(from + slot + ring_off<AL>(a.dy, a.lddy * (16 / N), t), c, H);
+        if (a.dsum) u[i] = shared_row<T, AL>(from + 2 * slot + ring_off<AL>(a.dsum, a.lddsum * (16 / N), t), c, H);
       }
     }
     __syncwarp();
@@ -669,7 +771,7 @@ __global__ void __launch_bounds__(kRingGradThreads + 32, 1) norm_grad_ring_kerne
         o.set2(j, v[0], v[1]);
         o.set2(j + 2, v[2], v[3]);
       }
-      if (a.dx && c < H) put_words<T, true>(dx + c, N, o);
+      if (a.dx) put_row<T, AL>(dx, c, H, o);
     }
   }
   if (!a.part) return;
@@ -677,22 +779,20 @@ __global__ void __launch_bounds__(kRingGradThreads + 32, 1) norm_grad_ring_kerne
   const int all = R.G * R.threads;
   named_barrier(15, all);
   float* meet = reinterpret_cast<float*>(smem_raw + (stage0 - smem_u32(smem_raw)));
+  const int pitch = (H + 7) / 8 * 8;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int c = (tid + i * R.threads) * N;
     if (c < H)
 #pragma unroll
       for (int j = 0; j < N; j += 4)
-        *reinterpret_cast<float4*>(meet + static_cast<size_t>(group) * H + c + j) = make_float4(acc[i][j], acc[i][j + 1], acc[i][j + 2], acc[i][j + 3]);
+        *reinterpret_cast<float4*>(meet + group * pitch + c + j) = make_float4(acc[i][j], acc[i][j + 1], acc[i][j + 2], acc[i][j + 3]);
   }
   named_barrier(15, all);
-  for (int c = threadIdx.x * 4; c < H; c += all * 4) {
-    float4 v = *reinterpret_cast<const float4*>(meet + c);
-    for (int k = 1; k < R.G; ++k) {
-      const float4 o = *reinterpret_cast<const float4*>(meet + static_cast<size_t>(k) * H + c);
-      v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
-    }
-    *reinterpret_cast<float4*>(a.part + static_cast<size_t>(blockIdx.x) * H + c) = v;
+  for (int c = threadIdx.x; c < H; c += all) {
+    float v = meet[c];
+    for (int k = 1; k < R.G; ++k) v += meet[k * pitch + c];
+    a.part[static_cast<size_t>(blockIdx.x) * H + c] = v;
   }
 }
 
@@ -770,37 +870,47 @@ __global__ void __launch_bounds__(1024) norm_dw_sum_kernel(const float* __restri
   if (lane == 0 && blockIdx.x * 32 + warp < H) dw[blockIdx.x * 32 + warp] = s;
 }
 
-// How rows of `packs` packs run: a warp each with one or a few packs a lane; CTAs of up to 512 threads with two packs;
-// CTAs of up to 1024 threads with one pack (few rows, each over as many threads as it can fill) or with two; or by the
-// kernels for wide rows.
-enum NormPlanKind { kWarpOne, kWarpMore, kCta, kCtaFew, kCtaMost, kWide, kRing };
+// How rows of `packs` packs run: a warp each with one or a few packs a lane; many rows through the ring; few rows in CTAs of
+// up to 1024 threads with one pack a thread, each row over as many threads as it can fill, or with two; or by the kernels for
+// wide rows.
+enum NormPlanKind { kWarpOne, kWarpMore, kCtaFew, kCtaMost, kWide, kRing };
 struct NormPlan {
   NormPlanKind kind;
   int threads, grid;
   Ring ring;
 };
-// most: packs that a warp takes; resident: CTAs of 512 threads per SM; ring_threads, ring_warps, ring_stages: threads of
-// the ring's kernels and warps of a group at most, and a group's stages at least; inputs: rows of a stage (0: rows that are not on 16-byte boundaries).
-NormPlan norm_plan(int T, int H, int dt, int most, int resident, int ring_threads, int ring_warps, int ring_stages, int inputs) {
-  const int packs = static_cast<int>((static_cast<long long>(H) * dtype_bytes(dt) + 15) / 16), sms = num_sms();
+// What forward and backward differ in: packs that a warp takes, warps of short rows' CTAs per SM (by 16), the ring's threads,
+// warps of a group and a group's stages, and values that are few.
+struct NormLimits {
+  int warp_packs, resident, ring_threads, ring_warps, ring_stages, few;
+};
+// inputs: matrices of a row that are read; al: all rows on 16-byte boundaries and in whole packs.
+NormPlan norm_plan(int T, int H, int dt, const NormLimits& m, int inputs, bool al) {
+  const long long row_bytes = static_cast<long long>(H) * dtype_bytes(dt);
+  const int packs = static_cast<int>((row_bytes + 15) / 16), sms = num_sms();
   NormPlan p{kWide, kNormThreads, T, Ring{1, 0, 0}};
-  if (packs <= 32 || (packs <= most && T >= 2 * sms)) {
+  if (packs <= 32 || (al && packs <= m.warp_packs && T >= 2 * sms)) {
     p.kind = packs <= 32 ? kWarpOne : kWarpMore;
     const int warps = T >= 16 * sms ? 8 : T >= 8 * sms ? 4 : T >= 4 * sms ? 2 : 1;       // (few rows: over all SMs)
     p.threads = 32 * warps;
-    const int ctas = (T + warps - 1) / warps, all = sms * 16 * resident / warps;
+    const int ctas = (T + warps - 1) / warps, all = sms * 16 * m.resident / warps;
     p.grid = ctas < all ? ctas : all;
     return p;
   }
-  if (inputs && packs <= kRingPer * 32 * ring_warps && T > sms) {
+  // few rows: all at a time, a pack a thread (500 x 2048 bf16 3.0 us, through the ring 3.6; 333 x 1001 fp32 backward 5.4, 7.3;
+  // but 500 x 2048 backward, whose partial sums of dw are 4 MB then, 10.1, 6.5)
+  const int one = (packs + 31) / 32 * 32, at_once = one <= 1024 ? 1024 / one : 1;
+  const bool few = T <= sms || (T <= sms * (at_once < 4 ? at_once : 4) && static_cast<long long>(T) * H <= m.few);
+  if (packs <= kRingPer * 32 * m.ring_warps && !few) {
     p.ring.threads = ((packs + kRingPer - 1) / kRingPer + 31) / 32 * 32;
-    const int stage = inputs * packs * 16, fit = (kRingBytes - H * 4) / stage;
-    int G = ring_threads / p.ring.threads;
+    const int slot = static_cast<int>(al ? ring_slot<true>(row_bytes) : ring_slot<false>(row_bytes));
+    const int stage = inputs * slot, fit = (kRingBytes - static_cast<int>(ring_w_bytes(H))) / stage;
+    int G = m.ring_threads / p.ring.threads;
     if (G > kRingGroups) G = kRingGroups;
     if (G > fit) G = fit;
     if (G > 0) {
       int S = kRingAhead / stage;
-      if (S < ring_stages * G) S = ring_stages * G;
+      if (S < m.ring_stages * G) S = m.ring_stages * G;
       if (S < 2) S = 2;
       if (S > fit) S = fit;
       if (S > kRingStages) S = kRingStages;
@@ -812,29 +922,19 @@ NormPlan norm_plan(int T, int H, int dt, int most, int resident, int ring_thread
       return p;
     }
   }
-  int per = 2;
-  if (packs <= 1024 && T <= sms) {
-    p.kind = kCtaFew;
-    per = resident = 1;
-  } else if (packs <= 1024) {
-    p.kind = kCta;
-  } else if (packs <= 2048) {
-    p.kind = kCtaMost;
-    resident = 1;
-  } else {
-    return p;
-  }
+  const int per = packs <= 1024 ? 1 : 2;
+  if (packs > 2048) return p;
+  p.kind = per == 1 ? kCtaFew : kCtaMost;
   p.threads = ((packs + per - 1) / per + 31) / 32 * 32;
-  if (p.kind == kCta) resident = resident * 512 / p.threads;
-  const int all = sms * resident;
-  p.grid = T < all ? T : all;
+  p.grid = few || T < sms ? T : sms;
   return p;
 }
-NormPlan norm_forward_plan(int T, int H, int dt, int inputs) {
-  return norm_plan(T, H, dt, 128, 2, kRingThreads, kRingWarps, 1, inputs);
+NormPlan norm_forward_plan(int T, int H, int dt, int inputs, bool al) {
+  return norm_plan(T, H, dt, NormLimits{128, 2, al ? kRingThreads : kRingOddThreads, al ? kRingWarps : kRingOddThreads / 32, 1, 1 << 30},
+                   inputs, al);
 }
-NormPlan norm_grad_plan(int T, int H, int dt, int inputs) {
-  return norm_plan(T, H, dt, 64, 1, kRingGradThreads, kRingGradWarps, 2, inputs);
+NormPlan norm_grad_plan(int T, int H, int dt, int inputs, bool al) {
+  return norm_plan(T, H, dt, NormLimits{64, 1, kRingGradThreads, kRingGradWarps, 2, 400000}, inputs, al);
 }
 
 template <class K, class A>
@@ -846,16 +946,13 @@ cudaError_t ring_launch(K kernel, const A& a, const NormPlan& p, std::atomic<uns
 
 template <class T, bool AL>
 cudaError_t norm_launch(const NormArgs& a, const NormPlan& p, cudaStream_t stream) {
+  static std::atomic<unsigned long long> done{0};
   const auto go = [&](auto kernel) { return launch_pdl(kernel, dim3(p.grid), dim3(p.threads), 0, stream, a); };
-  if constexpr (AL) {
-    static std::atomic<unsigned long long> done{0};
-    if (p.kind == kRing) return ring_launch(norm_ring_kernel<T>, a, p, done, stream);
-  }
   switch (p.kind) {
-    case kWarpOne: return go(norm_kernel<T, AL, 1, true, 256, 4, true>);
-    case kWarpMore: return go(norm_kernel<T, AL, 4, true, 256, 2, true>);
-    case kCta:                                          // (with rows on 16-byte boundaries the ring's)
-      if constexpr (!AL) return go(norm_kernel<T, AL, 2, false, 512, 2, true>);
+    case kRing: return ring_launch(norm_ring_kernel<T, AL>, a, p, done, stream);
+    case kWarpOne: return go(norm_kernel<T, AL, 1, true, 256, AL ? 4 : 2, true>);
+    case kWarpMore:
+      if constexpr (AL) return go(norm_kernel<T, AL, 4, true, 256, 2, true>);
       return cudaErrorInvalidValue;
     case kCtaFew: return go(norm_kernel<T, AL, 1, false, 1024, 1, false>);
     case kCtaMost: return go(norm_kernel<T, AL, 2, false, 1024, 1, false>);
@@ -869,13 +966,10 @@ template <class T, bool AL>
 cudaError_t norm_grad_launch(NormGradArgs a, const NormPlan& p, float* dw, cudaStream_t stream) {
   cudaError_t err;
   int slices = p.grid;
+  static std::atomic<unsigned long long> done{0};
   if (p.kind == kRing) {
     if (!dw) a.part = nullptr;
-    err = cudaErrorInvalidValue;
-    if constexpr (AL) {
-      static std::atomic<unsigned long long> done{0};
-      err = ring_launch(norm_grad_ring_kernel<T>, a, p, done, stream);
-    }
+    err = ring_launch(norm_grad_ring_kernel<T, AL>, a, p, done, stream);
   } else if (p.kind == kWide) {
     // the gradient of w first: dx may take the place of what it reads
     slices = norm_slices(a.T);
@@ -895,10 +989,9 @@ cudaError_t norm_grad_launch(NormGradArgs a, const NormPlan& p, float* dw, cudaS
     const auto go = [&](auto kernel) { return launch_pdl(kernel, dim3(p.grid), dim3(p.threads), 0, stream, a); };
     switch (p.kind) {
       case kWarpOne: err = go(norm_grad_kernel<T, AL, 1, true, 256, 2, true>); break;
-      case kWarpMore: err = go(norm_grad_kernel<T, AL, 2, true, 256, 2, true>); break;
-      case kCta:
+      case kWarpMore:
         err = cudaErrorInvalidValue;
-        if constexpr (!AL) err = go(norm_grad_kernel<T, AL, 2, false, 512, 1, true>);
+        if constexpr (AL) err = go(norm_grad_kernel<T, AL, 2, true, 256, 2, true>);
         break;
       case kCtaFew: err = go(norm_grad_kernel<T, AL, 1, false, 1024, 1, false>); break;
       default: err = go(norm_grad_kernel<T, AL, 2, false, 1024, 1, false>); break;
@@ -936,18 +1029,18 @@ cudaError_t launch_norm(int dt, RowsView x, RowsView res, const float* w, float 
   a.q_words = codes_aligned(y8, T, n);
   const bool al = H % n == 0 && rows_aligned(x, T, dt) && rows_aligned(res, T, dt) && rows_aligned(sum, T, dt) &&
                   rows_aligned(y, T, dt);
-  const NormPlan p = norm_forward_plan(T, H, dt, al ? 1 + (res.ptr != nullptr) : 0);
+  const NormPlan p = norm_forward_plan(T, H, dt, 1 + (res.ptr != nullptr), al);
   if (dt == kBf16) return al ? norm_launch<Bf16Elem, true>(a, p, stream) : norm_launch<Bf16Elem, false>(a, p, stream);
   if (dt == kF16) return al ? norm_launch<F16Elem, true>(a, p, stream) : norm_launch<F16Elem, false>(a, p, stream);
   return al ? norm_launch<F32Elem, true>(a, p, stream) : norm_launch<F32Elem, false>(a, p, stream);
 }
 
-// The wide rows' reciprocal roots [T], then the partial sums of dw.  The types' plans differ: room for any.
+// The wide rows' reciprocal roots [T], then the partial sums of dw.  The plans differ by type and alignment: room for any.
 size_t norm_scratch_bytes(int T, int H) {
   size_t slices = 1;
   for (int dt = kBf16; dt <= kF32; ++dt) {
-    for (int inputs = 0; inputs <= 3; inputs += 3) {
-      const NormPlan p = norm_grad_plan(T, H, dt, inputs);
+    for (int k = 0; k < 4; ++k) {
+      const NormPlan p = norm_grad_plan(T, H, dt, 2 + k / 2, k % 2);
       const size_t n = static_cast<size_t>(p.kind == kWide ? norm_slices(T) : p.grid);
       if (n > slices) slices = n;
     }
@@ -976,7 +1069,7 @@ cudaError_t launch_norm_grad(int dt, RowsView dy, RowsView x, const float* w, fl
   const int n = static_cast<int>(16 / dtype_bytes(dt));
   const bool al = H % n == 0 && rows_aligned(dy, T, dt) && rows_aligned(x, T, dt) && rows_aligned(dsum, T, dt) &&
                   rows_aligned(dx, T, dt);
-  const NormPlan p = norm_grad_plan(T, H, dt, al ? 2 + (dsum.ptr != nullptr) : 0);
+  const NormPlan p = norm_grad_plan(T, H, dt, 2 + (dsum.ptr != nullptr), al);
   if (dt == kBf16) return al ? norm_grad_launch<Bf16Elem, true>(a, p, dw, stream) : norm_grad_launch<Bf16Elem, false>(a, p, dw, stream);
   if (dt == kF16) return al ? norm_grad_launch<F16Elem, true>(a, p, dw, stream) : norm_grad_launch<F16Elem, false>(a, p, dw, stream);
   return al ? norm_grad_launch<F32Elem, true>(a, p, dw, stream) : norm_grad_launch<F32Elem, false>(a, p, dw, stream);

@@ -36,7 +36,8 @@ __global__ void __launch_bounds__(kRows8Threads) pack_rows8_kernel(const Rows8Ar
   long long row = static_cast<long long>(blockIdx.x) * per;          // the CTA's first; every warp goes on as long as it does
   const long long mine = seg + row + threadIdx.x / lanes;
   const raw* x = lo + mine * a.ldx + c;
-  uint8_t* q = a.q + mine * a.ldq + c;
+  uint8_t* q = a.q + mine * a.ldq;
+  const bool first = threadIdx.x % 32 == 0 || sub == 0, last = threadIdx.x % 32 == 31 || sub == lanes - 1;
   uint8_t* sf = a.sf + mine * a.ldsf + c / kGroup8;
   int left = cnt - static_cast<int>(row < cnt ? row : cnt) - static_cast<int>(threadIdx.x) / lanes;     // rows from this one on
   for (; row < cnt; row += step, left -= step) {
@@ -56,10 +57,12 @@ __global__ void __launch_bounds__(kRows8Threads) pack_rows8_kernel(const Rows8Ar
     for (int i = 0; i < N; ++i) v[i] = AL || c + i < a.cols ? p.f(i) : 0.f;
     uint32_t w[N / 4];
     const uint32_t scale = encode8<N>(v, w);
-    if (live) {
-      store_codes8<N>(q, w, a.cols - c, a.words);
-      if (c % kGroup8 == 0) *sf = static_cast<uint8_t>(scale);
+    if constexpr (AL) {
+      if (live) store_codes8<N>(q + c, w, N, true);
+    } else {
+      store_row_codes8<N>(q, c, left > 0 ? a.cols : 0, w, a.words, first, last);
     }
+    if (live && c % kGroup8 == 0) *sf = static_cast<uint8_t>(scale);
     x += step * a.ldx;
     q += step * a.ldq;
     sf += step * a.ldsf;
@@ -78,19 +81,20 @@ __global__ void __launch_bounds__(kRows8Threads) unpack_rows8_kernel(const Rows8
   expert_segment(a.counts, blockIdx.y, a.align, a.rows, blockIdx.x == 0 && blockIdx.z == 0, seg, cnt, a.status);
   const int sub = threadIdx.x % lanes, c = (blockIdx.z * lanes + sub) * N, per = kRows8Threads / lanes;
   const int step = gridDim.x * per;
-  if (c >= a.cols) return;
+  const bool first = threadIdx.x % 32 == 0 || sub == 0, last = threadIdx.x % 32 == 31 || sub == lanes - 1;
   const uint8_t *q = a.q + c, *sf = a.sf + c / kGroup8;
-  long long row = static_cast<long long>(blockIdx.x) * per + threadIdx.x / lanes;
-  raw* out = static_cast<raw*>(a.out) + (seg + row) * a.ldx + c;
+  long long row = static_cast<long long>(blockIdx.x) * per;          // the CTA's first; every warp goes on as long as it does
+  const int mine = threadIdx.x / lanes;
+  raw* out = static_cast<raw*>(a.out) + (seg + row + mine) * a.ldx;
   for (; row < cnt; row += kAhead * step) {
     uint32_t w[kAhead][N / 4], s[kAhead];
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
-      long long src = seg + row + k * step;
+      long long src = seg + row + mine + k * step;
 #pragma unroll
       for (int i = 0; i < N / 4; ++i) w[k][i] = 0;
       s[k] = 127;
-      if (row + k * step >= cnt) continue;
+      if (c >= a.cols || row + mine + k * step >= cnt) continue;
       if (a.ids) {
         const int id = __ldg(a.ids + src);
         src = id >= 0 ? static_cast<unsigned>(id) / static_cast<unsigned>(a.div) : -1;
@@ -110,15 +114,11 @@ __global__ void __launch_bounds__(kRows8Threads) unpack_rows8_kernel(const Rows8
       Words<T> p;
 #pragma unroll
       for (int i = 0; i < N; i += 2) p.set2(i, v[i], v[i + 1]);
-      if (row + k * step < cnt) {
-        if constexpr (AL) {
-          *reinterpret_cast<uint4*>(out) = make_uint4(p.w[0], p.w[1], p.w[2], p.w[3]);
-        } else {
-          const Pack<T> o = p;
-#pragma unroll
-          for (int i = 0; i < N; ++i)
-            if (c + i < a.cols) out[i] = o.v[i];
-        }
+      const bool there = row + mine + k * step < cnt;
+      if constexpr (AL) {
+        if (there && c < a.cols) *reinterpret_cast<uint4*>(out + c) = make_uint4(p.w[0], p.w[1], p.w[2], p.w[3]);
+      } else {
+        store_shifted<T>(out, c, there ? a.cols : 0, p, first, last);
       }
       out += step * a.ldx;
     }
@@ -173,7 +173,7 @@ cudaError_t launch_pack_rows8(int dt, RowsView x, const int32_t* counts, int row
   const int n = static_cast<int>(16 / dtype_bytes(dt)), segs = counts ? E : 1;
   a.x = x.ptr;
   a.words = codes_aligned(out, rows, n);
-  const bool al = cols % n == 0 && rows_aligned(x, rows, dt);
+  const bool al = cols % n == 0 && rows_aligned(x, rows, dt) && a.words;
   if (dt == kBf16) return pack_launch<Bf16Elem>(a, al, segs, stream);
   if (dt == kF16) return pack_launch<F16Elem>(a, al, segs, stream);
   return pack_launch<F32Elem>(a, al, segs, stream);

@@ -74,6 +74,41 @@ __device__ __forceinline__ void store_codes8(uint8_t* q, const uint32_t (&w)[N /
     if (i < n) q[i] = static_cast<uint8_t>(w[i / 4] >> (8 * (i % 4)));
 }
 
+// A row's codes, N to a lane from column c on (c may lie past the row's end), called as store_shifted: where rows start on no
+// N-byte boundary (not `words`), a lane stores the aligned N bytes that end in its codes.
+template <int N>
+__device__ __forceinline__ void store_row_codes8(uint8_t* row, int c, int cols, const uint32_t (&w)[N / 4], bool words,
+                                                 bool first, bool last) {
+  if (words) {
+    if (c < cols) store_codes8<N>(row + c, w, cols - c, true);
+    return;
+  }
+  const int m = static_cast<int>(reinterpret_cast<uintptr_t>(row) & (N - 1));
+  uint32_t out[N / 4];
+  if constexpr (N == 8) {
+    const unsigned long long own = static_cast<unsigned long long>(w[1]) << 32 | w[0], prev = __shfl_up_sync(0xffffffffu, own, 1);
+    const unsigned long long o = m ? own << (8 * m) | prev >> (64 - 8 * m) : own;
+    out[0] = static_cast<uint32_t>(o);
+    out[1] = static_cast<uint32_t>(o >> 32);
+  } else {
+    const uint32_t prev = __shfl_up_sync(0xffffffffu, w[0], 1);
+    out[0] = m ? w[0] << (8 * m) | prev >> (32 - 8 * m) : w[0];
+  }
+  const int c0 = c - m;
+  if ((!first || m == 0) && c0 + N <= cols) {
+    store_codes8<N>(row + c0, out, N, true);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (c0 + i < cols && (!first || i >= m)) row[c0 + i] = static_cast<uint8_t>(out[i / 4] >> (8 * (i % 4)));
+  }
+  if (last && m) {
+#pragma unroll
+    for (int i = 1; i < N; ++i)
+      if (i >= N - m && c + i < cols) row[c + i] = static_cast<uint8_t>(w[i / 4] >> (8 * (i % 4)));
+  }
+}
+
 // Values (as T holds them, in fp32) of N codes with scale byte s.  Two codes to fp16 at a time is exact, so is the product
 // with 2^(s - 127) within fp32's range, and T holds a value of its own type's rows exactly but where a code rounded up to
 // the next power of two past T's largest, which then stands for it (65536 of fp16, 2^128 of bf16 and fp32); only scales
