@@ -313,7 +313,7 @@ moe_status moe_rms_norm(moe_dtype dt, moe_rows x, moe_rows residual, const float
   if (T == 0) return MOE_OK;
   if (!rows_ok(x, H, dt) || !opt_rows_ok(residual, H, dt) || !opt_rows_ok(sum, H, dt) || !opt_rows_ok(y, H, dt))
     return MOE_ERR_INVALID_ARG;
-  if (!opt_rows8_ok(y8, H) || (!sum.ptr && !y.ptr && !y8.q)) return MOE_ERR_INVALID_ARG;
+  if (!opt_rows8_ok(y8, H) || (!sum.ptr && !y.ptr && !y8.q) || (sum.ptr && sum.ptr == y.ptr)) return MOE_ERR_INVALID_ARG;
   if (!weight || !aligned(weight, 16)) return MOE_ERR_INVALID_ARG;
   return cuda_status(launch_norm(dt, view(x), view(residual), weight, eps, T, H, view(sum), view(y), view8(y8), S(stream)));
 }

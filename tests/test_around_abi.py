@@ -47,6 +47,7 @@ def test_norm_refusals(M):
     assert fwd(res=rows(M, 10)) == bad and fwd(s=rows(M, 10)) == bad and fwd(y=rows(M, 10)) == bad
     assert fwd(w=None) == bad and fwd(w=ODD) == bad
     assert fwd(y=none) == bad                                              # no output at all
+    assert fwd(s=rows(M, 200, 0x40000), y=rows(M, 200, 0x40000)) == bad    # two outputs in one place
     assert fwd(y8=rows8(M, 199, 2)) == bad and fwd(y8=rows8(M, 200, 1)) == bad
     assert fwd(y8=rows8(M, 200, 2, None)) == bad and fwd(y8=rows8(M, 200, 2, 0x10000, None)) == bad
     assert fwd(T=0, x=none) == M.OK

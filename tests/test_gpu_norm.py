@@ -51,6 +51,12 @@ CASES = [  # T, H, dtype, extra pitch
 ]
 
 
+# rows through the ring: groups of several sizes, rows that start anywhere, rows of more than 1024 packs, few rows at a time
+CASES += [(200, 7168, BF, 0), (160, 8192, BF, 0), (155, 15360, BF, 0), (400, 5001, FP, 0), (170, 4472, HF, 0), (700, 945, HF, 0),
+          (2500, 264, BF, 0), (620, 1001, FP, 3), (333, 2521, BF, 1), (1000, 4096, FP, 0), (5000, 72, FP, 0), (310, 1032, HF, 8),
+          (153, 9700, HF, 0), (153, 9733, BF, 0), (8, 7168, FP, 0), (9, 7168, BF, 0), (10, 7168, BF, 0)]
+
+
 @pytest.mark.parametrize("T,H,dt,extra", CASES)
 def test_norm(M, T, H, dt, extra):
     x, xd = mat(T, H, dt, T + H, extra)
@@ -164,6 +170,20 @@ def test_rows_of_zeros_and_what_is_not_finite(M):
     assert (y[4].float() - 1e-27).abs().max() < 1e-29
     M.rms_norm(x, w, 0.0, y=y)                    # no eps: 0 * inf
     assert torch.isnan(y[0]).all() and (y[1] == 1).all()
+
+
+def test_one_workspace_for_many_sizes(M):
+    """Calls of different sizes in turn on one workspace: what one leaves there does not reach the next."""
+    ws = M.new_workspace_norm(700, 945)
+    for T, H, dt in ((5, 300, BF), (700, 945, HF), (9, 512, FP), (1, 64, BF), (5, 300, BF), (300, 128, FP), (40, 600, BF)) * 2:
+        x, xd = mat(T, H, dt, T)
+        dy, dyd = mat(T, H, dt, T + 1)
+        w, wd = weight(H)
+        dw = torch.full((H,), float("nan"), device="cuda")
+        M.rms_norm_backward(dyd, xd, wd, EPS, None, ws, dweight=dw)
+        _, (ref, ew) = A.norm_grad(dy, x, w, EPS, None, dt)
+        R.check(dw, ref, ew, "dweight")
+    assert M.get_error(ws) == M.OK
 
 
 def test_no_rows(M):
