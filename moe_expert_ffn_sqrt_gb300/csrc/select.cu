@@ -16,6 +16,12 @@
 // groups) that decide are closer than that, the keys that are near are evaluated in 64 bits, one to a lane.  Two experts of
 // equal logit and bias are an exact tie and need no second look; without a bias keys go by the logits themselves, which all
 // scores rise with.
+//
+// 16384 tokens of 256 experts in 8 groups, 6 of them, sigmoid and bias: 19.4 us, of 2.6 for the bytes.  The instructions
+// bound it, about 900 a token, with the schedulers busy for 60% of the time (64 registers, 32 warps per SM; 80 registers
+// 20.9 us, five CTAs of 8 warps 21.4).  The second looks take 0.2 us of it.  K rounds of a maximum instead of the ranking
+// took 43 us.  8 tokens: 3.5 us, one warp's chain.  Where all experts' keys are alike (say a row of padding, a zero bias and
+// groups) the groups' order takes a 64-bit evaluation of every expert, some 10 us for the warps that have such tokens.
 #include "rows.cuh"
 
 namespace moe {
