@@ -61,7 +61,11 @@ def _load_native():
     global _fast
     if _fast is None:
         lib()
-        from . import _native as n
+        try:
+            from . import _native as n
+        except ImportError as e:
+            raise RuntimeError("_native.so was not built for this torch: build it with "
+                               "`python -m moe_expert_ffn_sqrt_gb300.build`") from e
         n.bind(LIB_PATH)
         _fast = n
     return _fast
