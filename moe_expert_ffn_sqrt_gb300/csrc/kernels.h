@@ -270,6 +270,14 @@ int linear_bias_slices(int rows, int N, int E, int act);
 cudaError_t launch_act_grad(const LinearShape& p, RowsView dy, RowsView z, Rows8View z8, int act, RowsView dz, float* part,
                             float* db, uint32_t* status, cudaStream_t stream);
 
+// CTAs along the rows of a kernel that takes `per` rows a CTA at a time in E segments and nz parts of columns: an average
+// segment's rows (of `rows` that are likely there) once over, eight CTAs per SM at most.
+inline unsigned row_blocks(long long rows, int E, int per, int nz) {
+  const long long blocks = (rows / E + per) / per, most = 8LL * num_sms() / (static_cast<long long>(nz) * E);
+  const long long n = blocks < most ? blocks : most;
+  return static_cast<unsigned>(n < 1 ? 1 : n);
+}
+
 // Lets a kernel use up to `bytes` of dynamic shared memory, once per device (`done`: a bit per device).  The limit is
 // the function's, not the launch's, so it is the most that any call needs: one that went by the call's own size could be
 // lowered by another host thread between this thread's setting it and its launch, which is then refused.

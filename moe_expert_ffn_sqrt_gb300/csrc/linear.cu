@@ -1549,7 +1549,8 @@ struct ZRows {
   }
 };
 
-// (Z8 with more registers and fewer CTAs: 4096 x 4096 SwiGLU gradients 283 us of the whole call, with six CTAs 295)
+// With a bias gradient.  (Z8 with more registers and fewer CTAs: 4096 x 4096 SwiGLU gradients 283 us of the whole call, with
+// six CTAs 295.)
 template <class T, bool Z8>
 __global__ void __launch_bounds__(32 * kActRowLanes, Z8 ? 4 : 6)
     act_grad_kernel(const uint16_t* __restrict__ dy, long long lddy, const ZRows<T, Z8> z, int act,
@@ -1612,7 +1613,6 @@ __global__ void __launch_bounds__(32 * kActRowLanes, Z8 ? 4 : 6)
       }
     }
   }
-  if (!part) return;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     red[rl][0][lane * 8 + i] = acc[0][i];
@@ -1626,6 +1626,66 @@ __global__ void __launch_bounds__(32 * kActRowLanes, Z8 ? 4 : 6)
 #pragma unroll
       for (int r = 0; r < kActRowLanes; ++r) s += red[r][h][threadIdx.x];
       part[(static_cast<size_t>(e) * S + blockIdx.z) * N + h * cols + col] = s;
+    }
+  }
+}
+
+// The same values without the bias gradient's sums: `lanes` threads to a row (fewer than a CTA's where rows are narrow), two
+// rows of a thread on their way together; blockIdx.x: which `lanes` groups of eight columns, so that neighbouring CTAs read
+// one row.  Beside act_grad_kernel, with the dx product of K = 64 behind both: 4096 x 2048 SiLU 17.3 us of 19.7 and GELU 21.2
+// of 26.7, 128 x 4096 SwiGLU 12.1 of 14.0, 16384 x 7168 SiLU 161.8 of 160.3 and GELU 178.6 of 183.8; from 8 bits, 6971 x 80
+// ReLU 4 of 17 and 7 experts of 288 columns 6 of 14 (a warp of act_grad_kernel takes 256 columns of one row).  With one row
+// at a time and six CTAs per SM the SiLU case of 16384 x 7168 is 174, with CTAs of one column group side by side 163.6.
+template <class T, bool Z8>
+__global__ void __launch_bounds__(256, 4)
+    act_grad_rows_kernel(const uint16_t* __restrict__ dy, long long lddy, const ZRows<T, Z8> z, int act,
+                         const int32_t* __restrict__ counts, int align, int rows, int N, uint16_t* __restrict__ dz,
+                         long long lddz, int lanes, uint32_t* status) {
+  constexpr int kAhead = 2;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  int cnt, seg;
+  expert_segment(counts, blockIdx.y, align, rows, blockIdx.x == 0 && blockIdx.z == 0, seg, cnt, status);
+  const bool gated = act == kActSwiglu;
+  const int cols = gated ? N / 2 : N;
+  const int c = (blockIdx.x * lanes + threadIdx.x % lanes) * 8, per = 256 / lanes, step = gridDim.z * per;
+  if (c >= cols) return;
+  for (long long r = static_cast<long long>(blockIdx.z) * per + threadIdx.x / lanes; r < cnt; r += kAhead * step) {
+    Pack<T> g[kAhead];
+    decltype(z.get(0, 0)) a[kAhead], b[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const long long row = seg + (r + k * step < cnt ? r + k * step : r);
+      g[k] = load_pack<T>(dy + row * lddy + c);
+      a[k] = z.get(row, c);
+      if (gated) b[k] = z.get(row, cols + c);
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      if (r + k * step >= cnt) break;
+      uint16_t* out = dz + (seg + r + k * step) * lddz + c;
+      Pack<T> o;
+      if (gated) {
+        Pack<T> o2;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float s;
+          const float d = silu_grad(a[k].f(i), s);
+          o.set(i, g[k].f(i) * b[k].f(i) * d);
+          o2.set(i, g[k].f(i) * s);
+        }
+        store_pack<T>(out + cols, o2);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float v = a[k].f(i);
+          float s;
+          o.set(i, act == kActRelu   ? (v > 0.f ? g[k].f(i) : 0.f)
+                   : act == kActSilu ? g[k].f(i) * silu_grad(v, s)
+                                     : g[k].f(i) * gelu_grad(v));
+        }
+      }
+      store_pack<T>(out, o);
     }
   }
 }
@@ -1664,7 +1724,7 @@ cudaError_t launch_act_grad(const LinearShape& p, RowsView dy, RowsView z, Rows8
   const int S = few < most ? few : most;
   const int cols = act == kActSwiglu ? p.N / 2 : p.N;
   const dim3 grid((cols + 255) / 256, E, S);
-  float* pp = !db ? nullptr : S == 1 ? db : part;
+  float* pp = S == 1 ? db : part;
   const auto run = [&](auto type, auto kept8) {
     using T = decltype(type);
     constexpr bool Z8 = decltype(kept8)::value;
@@ -1675,6 +1735,17 @@ cudaError_t launch_act_grad(const LinearShape& p, RowsView dy, RowsView z, Rows8
     zr.sf = z8.sf;
     zr.ldsf = z8.lds;
     zr.words = codes_aligned(z8, p.rows, 8);
+    if (!db) {
+      // threads per row: the most (of 256, 128, ..) that leave at most an eighth of a row's last round idle
+      const int packs = cols / 8;
+      int lanes = 256;
+      while (lanes > 8 && (packs + lanes - 1) / lanes * lanes - packs > packs / 8) lanes /= 2;
+      const int nz = (packs + lanes - 1) / lanes, per = 256 / lanes;
+      const unsigned nx = row_blocks(p.counts ? live : p.rows, E, per, nz);
+      return launch_pdl(act_grad_rows_kernel<T, Z8>, dim3(static_cast<unsigned>(nz), static_cast<unsigned>(E), nx), dim3(256), 0,
+                        stream, static_cast<const uint16_t*>(dy.ptr), dy.ld, zr, act, p.counts, p.align, p.rows, p.N,
+                        static_cast<uint16_t*>(dz.ptr), dz.ld, lanes, status);
+    }
     return launch_pdl(act_grad_kernel<T, Z8>, grid, dim3(32 * kActRowLanes), 0, stream, static_cast<const uint16_t*>(dy.ptr),
                       dy.ld, zr, act, p.counts, E, p.align, p.rows, p.N, static_cast<uint16_t*>(dz.ptr), dz.ld, pp, S, status);
   };

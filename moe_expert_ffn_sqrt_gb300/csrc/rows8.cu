@@ -11,7 +11,7 @@ namespace moe {
 
 namespace {
 
-constexpr int kRows8Threads = 256, kRows8Ctas = 8;
+constexpr int kRows8Threads = 256;
 
 struct Rows8Args {
   const void* x;              // packed from
@@ -155,11 +155,8 @@ cudaError_t rows8_launch(K kernel, const Rows8Args& a, int E, cudaStream_t strea
   int lanes = kRows8Threads;
   while (lanes > least && (packs + lanes - 1) / lanes * lanes - packs > packs / 8) lanes /= 2;
   const int z = (packs + lanes - 1) / lanes, per = kRows8Threads / lanes;
-  const long long blocks = (static_cast<long long>(a.rows) + per - 1) / per;
-  long long most = static_cast<long long>(kRows8Ctas) * num_sms() / (static_cast<long long>(z) * E);
-  if (most < 1) most = 1;
-  return launch_pdl(kernel,
-                    dim3(static_cast<unsigned>(blocks < most ? blocks : most), static_cast<unsigned>(E), static_cast<unsigned>(z)),
+  const long long live = a.counts ? a.rows - static_cast<long long>(E) * (a.align - 1) : a.rows;
+  return launch_pdl(kernel, dim3(row_blocks(live, E, per, z), static_cast<unsigned>(E), static_cast<unsigned>(z)),
                     dim3(kRows8Threads), 0, stream, a, lanes);
 }
 template <class T>
