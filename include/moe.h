@@ -644,8 +644,8 @@ moe_status moe_pack_rows8(moe_dtype dt, moe_rows x, const int32_t* expert_counts
                           moe_rows8 x8, void* ws, size_t ws_bytes, void* stream);
 
 /* And back: x[r] = the values of row r of x8, or with x_ids [rows] of its row x_ids[r] / x_div, x8 then having x_rows
- * rows (token rows for moe_permute's sorted_token_ids and x_div = K).  Values are exact but for those past dt's largest,
- * which take it.  An id outside [0, x_rows * x_div) on a row that is wanted records MOE_ERR_DEVICE_INDEX, and the row
+ * rows (token rows for moe_permute's sorted_token_ids and x_div = K).  Values past dt's largest take it, those below
+ * its smallest normal number are rounded to what dt has there, all others are exact.  An id outside [0, x_rows * x_div) on a row that is wanted records MOE_ERR_DEVICE_INDEX, and the row
  * becomes zero.  ws (256 bytes) is needed with x_ids or expert_counts. */
 moe_status moe_unpack_rows8(moe_dtype dt, moe_rows8 x8, const int32_t* x_ids, int x_div, int x_rows,
                             const int32_t* expert_counts, int rows, int cols, int E, int align, moe_rows x, void* ws,
@@ -657,7 +657,7 @@ moe_status moe_workspace_size_linear8(int rows, int N, int K, int E, moe_act act
 /* moe_linear_backward with x, z or both kept in 8 bits: x or x8 for dw, z or z8 for act other than NONE (the other one
  * of a pair left out).  x_ids, x_div, x_rows: as in moe_unpack_rows8, so that the experts' rows need not be kept, only
  * the tokens' (x8 the rows that moe_rms_norm wrote, x_ids moe_dispatch's sorted_token_ids, x_div its K).  The results are
- * moe_linear_backward's for the unpacked rows, bit for bit. */
+ * moe_linear_backward's for the unpacked rows, bit for bit (but for bf16 values of z below 2^-126, which are not rounded here). */
 moe_status moe_linear_backward8(moe_dtype dt, moe_rows dy, moe_rows x, moe_rows8 x8, const int32_t* x_ids, int x_div,
                                 int x_rows, const void* w, moe_rows z, moe_rows8 z8, moe_act act,
                                 const int32_t* expert_counts, int rows, int N, int K, int E, int align,

@@ -121,14 +121,15 @@ struct Args {
 
 // Runs a call's body: its status as a Python number, None where its arguments were not in order.
 template <class F>
-PyObject* run(Args&& x, F&& body) {
+PyObject* run(PyObject* const* a, Py_ssize_t n, Py_ssize_t want, F&& body) {
   try {
+    Args x(a, n, want);
     if (x.ok) {
       const int status = body(x);
       if (x.ok) return PyLong_FromLong(status);
     }
-  } catch (const std::exception&) {
-    // (a tensor without storage, say)
+  } catch (...) {
+    // (a tensor without storage, a machine without a GPU)
   }
   Py_RETURN_NONE;
 }
@@ -144,7 +145,7 @@ int enqueue(F&& call) {
 
 // x, weight, eps, residual, sum_out, y, y8
 PyObject* rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return run(Args(a, n, 7), [](Args& x) {
+  return run(a, n, 7, [](Args& x) {
     int T = 0, H = 0;
     x.shape(0, &T, &H);
     const moe_rows in = x.rows(0, T, H), res = x.rows(3, T, H), sum = x.rows(4, T, H), y = x.rows(5, T, H);
@@ -158,7 +159,7 @@ PyObject* rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 // dy, x, weight, eps, dx, ws, dweight, dsum
 PyObject* rms_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return run(Args(a, n, 8), [](Args& x) {
+  return run(a, n, 8, [](Args& x) {
     int T = 0, H = 0;
     size_t bytes;
     x.shape(0, &T, &H);
@@ -174,7 +175,7 @@ PyObject* rms_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 // logits, topk_ids, topk_w, e_score_bias, fn, n_groups, topk_groups, group_best, renormalize, scale
 PyObject* select(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return run(Args(a, n, 10), [](Args& x) {
+  return run(a, n, 10, [](Args& x) {
     int T = 0, E = 0;
     x.shape(0, &T, &E);
     const moe_rows logits = x.rows(0, T, E);
@@ -198,7 +199,7 @@ PyObject* select(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 // logits, topk_ids, topk_w, dtopk_w, dlogits, ws, fn, renormalize, scale
 PyObject* select_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return run(Args(a, n, 9), [](Args& x) {
+  return run(a, n, 9, [](Args& x) {
     int T = 0, E = 0;
     size_t bytes;
     x.shape(0, &T, &E);
@@ -225,7 +226,7 @@ PyObject* select_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 // x, x8, expert_counts, align, ws
 PyObject* pack_rows8(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return run(Args(a, n, 5), [](Args& x) {
+  return run(a, n, 5, [](Args& x) {
     int rows = 0, cols = 0, E = 0;
     size_t bytes;
     x.shape(0, &rows, &cols);
@@ -247,7 +248,7 @@ PyObject* pack_rows8(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 // dy, w, ws, x, x8, z, z8, x_ids, x_div, dx, dw, dbias, act, dx_residual, expert_counts, align
 PyObject* linear_backward8(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return run(Args(a, n, 16), [](Args& x) {
+  return run(a, n, 16, [](Args& x) {
     int rows = 0, cols = 0;
     size_t bytes;
     x.shape(0, &rows, &cols);

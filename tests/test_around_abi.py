@@ -140,6 +140,34 @@ def test_the_binding_checks_its_arguments(M):
 
 # ------------------------------------------------------------------------------------- the references
 
+CPU_CALLS = """
+import torch
+import moe_expert_ffn_sqrt_gb300 as M
+x, w, ws = torch.ones(4, 256, dtype=torch.bfloat16), torch.ones(256), torch.zeros(4096, dtype=torch.uint8)
+ids, tw, w2, q = torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2), torch.ones(256, 256, dtype=torch.bfloat16), M.new_rows8(4, 256, "cpu")
+for f in (lambda: M.rms_norm(x, w, 1e-6, y=x), lambda: M.rms_norm_backward(x, x, w, 1e-6, x, ws),
+          lambda: M.select(x, ids, tw, "sigmoid"), lambda: M.select_backward(x, ids, tw, tw, x, ws, "sigmoid"),
+          lambda: M.pack_rows8(x, q), lambda: M.unpack_rows8(q, x),
+          lambda: M.linear_backward8(x, w2, ws, x8=q, dw=w2)):
+    try:
+        f()
+    except Exception:
+        continue
+    raise SystemExit("not refused")
+print("refused all")
+"""
+
+
+def test_tensors_of_the_host_raise(M):
+    """Every call with tensors outside a GPU, on a machine without one too: an exception, and the process lives."""
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", CPU_CALLS], cwd=root, capture_output=True, text=True, timeout=300,
+                       env={**os.environ, "CUDA_VISIBLE_DEVICES": ""})
+    assert r.returncode == 0 and r.stdout.strip() == "refused all", r.stderr[-2000:]
+
+
 def test_reference_norm_gradient_against_differences():
     g = torch.Generator().manual_seed(5)
     x, d, c = (torch.randn(5, 12, generator=g, dtype=R.F64) for _ in range(3))
