@@ -318,7 +318,14 @@ __global__ void __launch_bounds__(kSelectWarps * 32, PER <= 8 ? kSelectCtas : 1)
         }
       }
       uint32_t mine = used && sub == 0 ? ordered(worth) : 0;
-      const float tol = 2.f * near + __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(size))) * 0x1p-21f;
+      // (a NaN logit is -infinity in the keys here, whose score is 0: where one may count, all groups take the second look)
+      bool nan = false;
+      if (!a.bias && __any_sync(kAll, f2 == -INFINITY)) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) nan = nan || v[i] != v[i];
+        nan = __any_sync(kAll, nan);
+      }
+      const float tol = nan ? INFINITY : 2.f * near + __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(size))) * 0x1p-21f;
       unsigned open = 0;                // by the lanes with sub = 0
       uint32_t kth = 0;
       for (int k = 0; k < a.KG; ++k) {
@@ -329,7 +336,7 @@ __global__ void __launch_bounds__(kSelectWarps * 32, PER <= 8 ? kSelectCtas : 1)
         kth = best;
       }
       const float last = from_ordered(kth), next = from_ordered(__reduce_max_sync(kAll, mine));
-      if (last - next <= tol) {
+      if (nan || last - next <= tol) {
         // groups that are surely in, and those that may be: the latter in 64 bits, from their experts that may be among
         // the best two
         const bool in = used && worth - next > tol, maybe = used && !in && !(last - worth > tol);

@@ -138,6 +138,33 @@ def test_nan_and_infinite_logits_give_valid_ids(M):
                 assert torch.isnan(w[1]).any()
 
 
+@pytest.mark.parametrize("fn", FNS)
+@pytest.mark.parametrize("E,G,KG,K,best", [(32, 8, 3, 6, 2), (32, 16, 4, 5, 2), (32, 16, 4, 5, 1), (12, 12, 5, 5, 2), (96, 6, 2, 8, 2),
+                                           (256, 8, 4, 6, 2), (512, 4, 2, 9, 1)])
+def test_nan_logits_without_a_bias_leave_their_groups_last(M, fn, E, G, KG, K, best):
+    """A NaN's key is -infinity in what its group is worth too, not the score 0 of a masked expert."""
+    g = torch.Generator().manual_seed(E + G)
+    l = torch.randn(64, E, generator=g)
+    l[torch.rand(64, E, generator=g) < torch.linspace(0, 1, 64)[:, None]] = float("nan")
+    ids, _ = run(M, l, None, K, fn, G=G, KG=KG, best=best)
+    ref, _ = A.select(l, None, K, fn, G, KG, best)
+    assert torch.equal(ids.cpu(), ref)
+
+
+@pytest.mark.parametrize("fn", FNS)
+def test_masked_groups_without_a_bias(M, fn):
+    """Groups whose logits are all -infinity score 0; equals go to the lower group and expert."""
+    g = torch.Generator().manual_seed(3)
+    l = torch.randn(40, 8, 8, generator=g)
+    l[torch.rand(40, 8, generator=g) < torch.linspace(0, 0.95, 40)[:, None]] = -INF
+    l = l.reshape(40, 64)
+    ids, _ = run(M, l, None, 7, fn, G=8, KG=3)
+    l64 = l.to(torch.float64)
+    l64[(l == -INF).all(1)] = 0          # (a row of nothing: every score 0, so are these)
+    ref, _ = A.select(l64, None, 7, fn, 8, 3)
+    assert torch.equal(ids.cpu(), ref)
+
+
 GRAD = [  # T, E, K, dtype, grad dtype, pitch
     (8, 256, 6, FP, FP, 0), (33, 64, 4, BF, BF, 0), (70, 100, 5, FP, BF, 4), (11, 7, 7, HF, HF, 1), (5, 1, 1, FP, FP, 0),
     (9, 1024, 32, FP, HF, 0), (100, 258, 3, BF, BF, 2), (40, 511, 8, FP, FP, 0), (300, 32, 2, HF, HF, 0),
