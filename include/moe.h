@@ -596,7 +596,7 @@ typedef struct {
  * is of the rounded sum, stored or not; y and y8 are each rounded once from fp32.  sum and y may be x or residual
  * themselves (not both the same one: refused).  1 <= H <= 2^24, eps >= 0.  The squares are added up in fp32: a row whose
  * sum of squares passes 3.4e38 comes out as zeros (its infinities as NaN), one whose sum is 0 needs an eps.  A row's sum is
- * taken in an order that goes by T, H and the rows' 16-byte alignment. */
+ * taken in an order that goes by T, H and the rows' 16-byte alignment.  (A bounded wait inside that runs out leaves NaN.) */
 moe_status moe_rms_norm(moe_dtype dt, moe_rows x, moe_rows residual, const float* weight, float eps, int T, int H,
                         moe_rows sum, moe_rows y, moe_rows8 y8, void* stream);
 
@@ -606,8 +606,9 @@ moe_status moe_workspace_size_norm(int T, int H, size_t* bytes);
 /* Gradients of moe_rms_norm with respect to sum (x and residual have the same) and weight.  x: the forward's sum (its
  * x where there was no residual).  dsum [T, H] (optional): the gradient that reaches sum on its other way, added to dx.
  * dx [T, H] and dweight [H] (fp32, 16-byte aligned) are optional, one at least.  dx may be dy, x or dsum itself.  No
- * rows: dweight is zero.  Sums over rows are taken in a fixed order (by T, H and alignment).  ws 16-byte aligned; calls that
- * may overlap, replays of captured ones among them, take a workspace each. */
+ * rows: dweight is zero.  Sums over rows are taken in a fixed order (by T, H and alignment).  ws 16-byte
+ * aligned, its first 256 bytes the status word, zero-filled once; calls that may overlap, replays of captured ones among
+ * them, take a workspace each. */
 moe_status moe_rms_norm_backward(moe_dtype dt, moe_rows dy, moe_rows x, const float* weight, float eps, moe_rows dsum,
                                  int T, int H, moe_rows dx, float* dweight, void* ws, size_t ws_bytes, void* stream);
 
@@ -645,8 +646,9 @@ moe_status moe_pack_rows8(moe_dtype dt, moe_rows x, const int32_t* expert_counts
 
 /* And back: x[r] = the values of row r of x8, or with x_ids [rows] of its row x_ids[r] / x_div, x8 then having x_rows
  * rows (token rows for moe_permute's sorted_token_ids and x_div = K).  Values past dt's largest take it, those below
- * its smallest normal number are rounded to what dt has there, all others are exact.  An id outside [0, x_rows * x_div) on a row that is wanted records MOE_ERR_DEVICE_INDEX, and the row
- * becomes zero.  ws (256 bytes) is needed with x_ids or expert_counts. */
+ * its smallest normal number are rounded to what dt has there, all others are exact.  An id outside [0, x_rows * x_div) on a
+ * row that is wanted records MOE_ERR_DEVICE_INDEX, and the row becomes zero.  ws (256 bytes) is needed with x_ids or
+ * expert_counts. */
 moe_status moe_unpack_rows8(moe_dtype dt, moe_rows8 x8, const int32_t* x_ids, int x_div, int x_rows,
                             const int32_t* expert_counts, int rows, int cols, int E, int align, moe_rows x, void* ws,
                             size_t ws_bytes, void* stream);
@@ -657,7 +659,8 @@ moe_status moe_workspace_size_linear8(int rows, int N, int K, int E, moe_act act
 /* moe_linear_backward with x, z or both kept in 8 bits: x or x8 for dw, z or z8 for act other than NONE (the other one
  * of a pair left out).  x_ids, x_div, x_rows: as in moe_unpack_rows8, so that the experts' rows need not be kept, only
  * the tokens' (x8 the rows that moe_rms_norm wrote, x_ids moe_dispatch's sorted_token_ids, x_div its K).  The results are
- * moe_linear_backward's for the unpacked rows, bit for bit (but for bf16 values of z below 2^-126, which are not rounded here). */
+ * moe_linear_backward's for the unpacked rows, bit for bit (but for bf16 values of z below 2^-126, which
+ * are not rounded here). */
 moe_status moe_linear_backward8(moe_dtype dt, moe_rows dy, moe_rows x, moe_rows8 x8, const int32_t* x_ids, int x_div,
                                 int x_rows, const void* w, moe_rows z, moe_rows8 z8, moe_act act,
                                 const int32_t* expert_counts, int rows, int N, int K, int E, int align,

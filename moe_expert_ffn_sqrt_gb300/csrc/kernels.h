@@ -212,7 +212,7 @@ cudaError_t launch_norm(int dt, RowsView x, RowsView res, const float* w, float 
 // Gradients of the norm of x: dx (+ dsum; optional) and dw [H] (optional).
 size_t norm_scratch_bytes(int T, int H);
 cudaError_t launch_norm_grad(int dt, RowsView dy, RowsView x, const float* w, float eps, RowsView dsum, int T, int H,
-                             RowsView dx, float* dw, void* scratch, cudaStream_t stream);
+                             RowsView dx, float* dw, void* scratch, uint32_t* status, cudaStream_t stream);
 
 // rows8.cu: rows of type dt to 8 bits and back (counts null: all rows, else the experts' segments).  Unpacked row r is
 // row r of x, or with ids row ids[r] / div of its src_rows rows.

@@ -341,10 +341,13 @@ __host__ __device__ __forceinline__ uint32_t ring_slot(uint32_t row_bytes) {
 // Shared memory of w.
 __host__ __device__ __forceinline__ uint32_t ring_w_bytes(int H) { return static_cast<uint32_t>(H + 7) / 8 * 32; }
 
-// The loading thread: `in` hold rows of `bytes` bytes, ld bytes apart, of elements of type E.
+// The loading thread, which stays until its copies are there or have had as long as a wait has (they would land in the shared
+// memory of whoever comes after the CTA); status: where a wait that runs out is recorded (null: nowhere).  `in` hold rows of
+// `bytes` bytes, ld bytes apart, of elements of type E.
 template <bool AL, class E, int MOST>
 __device__ __forceinline__ void ring_load(const Ring& R, RingState& st, uint32_t smem, const void* const (&in)[MOST],
-                                          const long long (&ld)[MOST], int T, uint32_t bytes, const float* w, int H) {
+                                          const long long (&ld)[MOST], int T, uint32_t bytes, const float* w, int H,
+                                          uint32_t* status) {
   using U = uintptr_t;
   const uint32_t wbytes = static_cast<uint32_t>(H) / 4 * 16;
   for (int i = H / 4 * 4; i < (H + 7) / 8 * 8; ++i)      // the last values, and zeros to the end of a pack
@@ -364,7 +367,7 @@ __device__ __forceinline__ void ring_load(const Ring& R, RingState& st, uint32_t
   uint32_t ph = 0;
   for (long long t = blockIdx.x; t < T; t += gridDim.x) {
     // (a wait that runs out ends the copies; the groups' own waits for them then run out too)
-    if (!mbar_wait(smem_u32(&st.empty[s]), ph ^ 1, nullptr)) return;
+    if (!mbar_wait(smem_u32(&st.empty[s]), ph ^ 1, status)) break;
     const uint32_t bar = smem_u32(&st.full[s]);
     const uint32_t stage = smem + s * n * slot;
     if constexpr (AL) {
@@ -416,6 +419,8 @@ __device__ __forceinline__ void ring_load(const Ring& R, RingState& st, uint32_t
       ph ^= 1;
     }
   }
+  mbar_wait(smem_u32(&st.w_full), 0, status);
+  for (int i = 0; i < R.S; ++i) mbar_wait(smem_u32(&st.full[i]), i < s ? ph : ph ^ 1, status);
 }
 
 __device__ __forceinline__ void ring_init(const Ring& R, RingState& st) {
@@ -523,7 +528,7 @@ __global__ void __launch_bounds__((AL ? kRingThreads : kRingOddThreads) + 32, 1)
     if (lane == 0) {
       const void* in[2] = {a.x, a.res};
       const long long ld[2] = {a.ldx * (16 / N), a.ldr * (16 / N)};
-      ring_load<AL, typename T::raw>(R, st, smem, in, ld, a.T, bytes, a.w, H);
+      ring_load<AL, typename T::raw>(R, st, smem, in, ld, a.T, bytes, a.w, H, nullptr);
     }
     return;
   }
@@ -558,7 +563,18 @@ __global__ void __launch_bounds__((AL ? kRingThreads : kRingOddThreads) + 32, 1)
       p[i].keep();
     }
     ok = group_sum(ss, sh[group][turn], group, R.threads, tid / 32, lane, ok);
-    if (!ok) return;
+    if (!ok) {                          // there is no workspace for a status: the group's rows become NaN
+      for (; t < a.T; t += step, out.on(a, step))
+        for (int c = tid; c < H; c += R.threads) {
+          if (out.sum) out.sum[c] = T::from_f(NAN);
+          if (out.y) out.y[c] = T::from_f(NAN);
+          if (out.q) {
+            out.q[c] = 0x7f;
+            if (c % kGroup8 == 0) out.sf[c / kGroup8] = 255;
+          }
+        }
+      return;
+    }
     const float rs = rsqrtf(ss[0] * a.over_h + a.eps);
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
@@ -585,6 +601,7 @@ struct NormGradArgs {
   long long lddy, ldx, lddsum, lddx;
   float eps, over_h;
   int T, H;
+  uint32_t* status;
 };
 
 // Rows in registers, as norm_kernel; a thread adds its columns' part of dw up over its rows (w: a CTA's sums to `part`).
@@ -708,12 +725,12 @@ __global__ void __launch_bounds__(kRingGradThreads + 32, 1) norm_grad_ring_kerne
     if (lane == 0) {
       const void* in[3] = {a.x, a.dy, a.dsum};
       const long long ld[3] = {a.ldx * (16 / N), a.lddy * (16 / N), a.lddsum * (16 / N)};
-      ring_load<AL, typename T::raw>(R, st, smem, in, ld, a.T, bytes, a.w, H);
+      ring_load<AL, typename T::raw>(R, st, smem, in, ld, a.T, bytes, a.w, H, a.status);
     }
     return;
   }
   const uint32_t stage0 = smem + ring_w_bytes(H), stage = (a.dsum ? 3 : 2) * slot;
-  bool ok = mbar_wait(smem_u32(&st.w_full), 0, nullptr);
+  bool ok = mbar_wait(smem_u32(&st.w_full), 0, a.status);
   float acc[PER][N];
 #pragma unroll
   for (int i = 0; i < PER; ++i)
@@ -724,7 +741,7 @@ __global__ void __launch_bounds__(kRingGradThreads + 32, 1) norm_grad_ring_kerne
   const int first = blockIdx.x + group * gridDim.x, step = R.G * gridDim.x;
   typename T::raw* dx = static_cast<typename T::raw*>(a.dx) + first * a.lddx;
   for (long long t = first; t < a.T; t += step, dx += step * a.lddx, at.on(R.G, R.S), turn ^= 1) {
-    ok = mbar_wait(smem_u32(&st.full[at.s]), at.ph, nullptr) && ok;
+    ok = mbar_wait(smem_u32(&st.full[at.s]), at.ph, a.status) && ok;
     const uint32_t from = stage0 + at.s * stage;
     Words<T> p[PER], d[PER], u[PER];
 #pragma unroll
@@ -901,7 +918,7 @@ NormPlan norm_plan(int T, int H, int dt, const NormLimits& m, int inputs, bool a
     p.kind = packs <= 32 ? kWarpOne : kWarpMore;
     const int warps = T >= 16 * sms ? 8 : T >= 8 * sms ? 4 : T >= 4 * sms ? 2 : 1;       // (few rows: over all SMs)
     p.threads = 32 * warps;
-    const int ctas = (T + warps - 1) / warps, all = sms * 16 * m.resident / warps;
+    const int ctas = (T - 1) / warps + 1, all = sms * 16 * m.resident / warps;
     p.grid = ctas < all ? ctas : all;
     return p;
   }
@@ -1057,8 +1074,9 @@ size_t norm_scratch_bytes(int T, int H) {
 }
 
 cudaError_t launch_norm_grad(int dt, RowsView dy, RowsView x, const float* w, float eps, RowsView dsum, int T, int H,
-                             RowsView dx, float* dw, void* scratch, cudaStream_t stream) {
+                             RowsView dx, float* dw, void* scratch, uint32_t* status, cudaStream_t stream) {
   NormGradArgs a{};
+  a.status = status;
   a.dy = dy.ptr;
   a.x = x.ptr;
   a.dsum = dsum.ptr;

@@ -194,7 +194,7 @@ struct GradArgs {
 
 template <class T, class L, int PER, int V>
 cudaError_t route_grad_launch(const GradArgs& a, cudaStream_t stream) {
-  return launch_pdl(route_grad_kernel<T, L, PER, V>, dim3((a.T + kGradWarps - 1) / kGradWarps), dim3(kGradWarps * 32), 0,
+  return launch_pdl(route_grad_kernel<T, L, PER, V>, dim3((a.T - 1) / kGradWarps + 1), dim3(kGradWarps * 32), 0,
                     stream, static_cast<const typename L::raw*>(a.logits), a.ldl, a.ids, a.w, a.dw, a.T, a.E, a.K, a.fn,
                     a.renorm, a.over_scale, static_cast<typename T::raw*>(a.out), a.ldo, a.status);
 }

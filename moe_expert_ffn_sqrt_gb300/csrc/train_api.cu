@@ -339,7 +339,7 @@ moe_status moe_rms_norm_backward(moe_dtype dt, moe_rows dy, moe_rows x, const fl
   if (!weight || !aligned(weight, 16)) return MOE_ERR_INVALID_ARG;
   if (!ws || !aligned(ws, 16) || ws_bytes < up(kAlign + norm_scratch_bytes(T, H))) return MOE_ERR_WORKSPACE;
   return cuda_status(launch_norm_grad(dt, view(dy), view(x), weight, eps, view(dsum), T, H, view(dx), dweight,
-                                      static_cast<char*>(ws) + kAlign, S(stream)));
+                                      static_cast<char*>(ws) + kAlign, status_of(ws), S(stream)));
 }
 
 moe_status moe_select(moe_dtype dt, moe_rows logits, const float* e_score_bias, int T, int E, int K, moe_select_rule rule,
