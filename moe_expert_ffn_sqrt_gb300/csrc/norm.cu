@@ -10,7 +10,7 @@
 // 8-bit outputs, 1.06 GB in 160 us (98% of a plain copy's rate); without residual 104 us (83%: about 170 instructions a
 // pack); gradients of 8192 x 7168 with dsum 75 us (93%), 4 us of it the launch that adds the CTAs' parts of dw up.  8192 x
 // 4096 fp32 88 us (95%), 16384 x 2048 bf16 49 (91%), its gradients 43 (92%).  Rows that start on no 16-byte boundary are
-// bound by the shifts' instructions: 9000 x 6001 bf16 204 us of 72, 1450 x 2521 fp16 12 of 4.  A row of 7168 alone takes 2.9
+// bound by the shifts' instructions: 9000 x 6001 bf16 208 us of 72, 1450 x 2521 fp16 17 of 5.  A row of 7168 alone takes 2.9
 // us: launch, one load, the reduction's two steps, the stores.  (Reading each row twice, from L1 and L2 the second time:
 // 205 us and, the gradients, 266; a row in registers with the next one's loads ahead, two CTAs of 448 threads: 243, 151.)
 #include "rows8.cuh"
@@ -305,7 +305,10 @@ __global__ void __launch_bounds__(kNormThreads) norm_wide_kernel(const NormArgs 
 // Rows that start anywhere (not AL) come with the ends of the 16-byte words that they begin and end in, and are shifted as
 // they are taken out; the few elements of a word that reaches out of the matrix are copied one by one.
 
-constexpr int kRingStages = 16, kRingGroups = 8;
+// Groups of several warps, at most (15 barriers there are; 8: 4000 x 1001 bf16 17.4 us instead of 15.9, 14: 2000 x 700 fp32
+// 5.9 instead of 5.6).  Groups of one warp (ONE) need none, and there are as many as have their stages: with 8 of them
+// 20000 x 300 bf16 56 us and its gradients 38 instead of 31.5 and 30.7.  (A warp per row without the ring 102 and 48.)
+constexpr int kRingStages = 32, kRingGroups = 9;
 constexpr int kRingThreads = 960, kRingOddThreads = 608;        // of all groups, at most (odd: rows that start anywhere)
 constexpr int kRingGradThreads = 608;
 constexpr int kRingWarps = 30, kRingGradWarps = 16;             // of a group, at most
@@ -341,86 +344,115 @@ __host__ __device__ __forceinline__ uint32_t ring_slot(uint32_t row_bytes) {
 // Shared memory of w.
 __host__ __device__ __forceinline__ uint32_t ring_w_bytes(int H) { return static_cast<uint32_t>(H + 7) / 8 * 32; }
 
-// The loading thread, which stays until its copies are there or have had as long as a wait has (they would land in the shared
-// memory of whoever comes after the CTA); status: where a wait that runs out is recorded (null: nowhere).  `in` hold rows of
-// `bytes` bytes, ld bytes apart, of elements of type E.
+// Whether the phase with the given parity is over (asked only, where mbar_wait may put the thread to sleep).
+__device__ __forceinline__ bool mbar_over(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{ .reg .pred p; mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+               : "=r"(ok)
+               : "r"(bar), "r"(parity)
+               : "memory");
+  return ok != 0;
+}
+
+// Copies one row of the MOST matrices `in` (null: not there) of rows of `bytes` bytes, ld bytes apart, of elements of type E
+// to a stage, to arrive on bar.
+template <bool AL, class E, int MOST>
+__device__ __forceinline__ void ring_row(long long t, uint32_t stage, uint32_t bar, const void* const (&in)[MOST],
+                                         const long long (&ld)[MOST], int n, int T, uint32_t bytes, uint32_t slot) {
+  using U = uintptr_t;
+  uint32_t to = stage;
+  if constexpr (AL) {
+    mbar_arrive_expect_tx(bar, n * bytes);
+#pragma unroll
+    for (int i = 0; i < MOST; ++i)
+      if (in[i]) {
+        bulk_load(to, static_cast<const uint8_t*>(in[i]) + t * ld[i], bytes, bar);
+        to += slot;
+      }
+  } else {
+    U from[MOST];
+    uint32_t skip[MOST], size[MOST], all = 0;
+#pragma unroll
+    for (int i = 0; i < MOST; ++i) {
+      size[i] = 0;
+      if (!in[i]) continue;
+      const U lo = reinterpret_cast<U>(in[i]), row = lo + static_cast<U>(t * ld[i]), end = row + bytes;
+      const U hi = lo + static_cast<U>((T - 1) * ld[i]) + bytes;
+      U a = row & ~U(15), b = (end + 15) & ~U(15);
+      skip[i] = 0;
+      if (a < lo) {                   // (the matrix' first row)
+        a += 16;
+        skip[i] = 16;
+        for (U e = row; e < a; e += sizeof(E)) copy_element<E>(to + static_cast<uint32_t>(e & 15), e);
+      }
+      if (b > hi) {                   // (its last one)
+        b -= 16;
+        for (U e = b; e < end; e += sizeof(E)) copy_element<E>(to + skip[i] + static_cast<uint32_t>(e - a), e);
+      }
+      from[i] = a;
+      size[i] = static_cast<uint32_t>(b - a);
+      all += size[i];
+      to += slot;
+    }
+    if (t == 0 || t == T - 1) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");    // (elements copied one by one)
+    mbar_arrive_expect_tx(bar, all);
+    to = stage;
+#pragma unroll
+    for (int i = 0; i < MOST; ++i)
+      if (in[i]) {
+        if (size[i]) bulk_load(to + skip[i], reinterpret_cast<const void*>(from[i]), size[i], bar);
+        to += slot;
+      }
+  }
+}
+
+// The loading warp: lane s refills stage s whenever it is empty (one lane for all of them: gradients of 20000 x
+// 300 bf16 81 us instead of 38, of 9887 x 544 fp16 26 instead of 16, 8192 x 4096 fp32 to 8 bits alone 66 instead of 68).  It stays until its copies are there or have had as long as a wait has (they would land in the shared memory of
+// whoever comes after the CTA); status: where a wait that runs out is recorded (null: nowhere).
 template <bool AL, class E, int MOST>
 __device__ __forceinline__ void ring_load(const Ring& R, RingState& st, uint32_t smem, const void* const (&in)[MOST],
                                           const long long (&ld)[MOST], int T, uint32_t bytes, const float* w, int H,
                                           uint32_t* status) {
-  using U = uintptr_t;
-  const uint32_t wbytes = static_cast<uint32_t>(H) / 4 * 16;
-  for (int i = H / 4 * 4; i < (H + 7) / 8 * 8; ++i)      // the last values, and zeros to the end of a pack
-    asm volatile("st.shared.f32 [%0], %1;" ::"r"(smem + 4 * i), "f"(i < H ? __ldg(w + i) : 0.f) : "memory");
-  if (wbytes) {
-    mbar_arrive_expect_tx(smem_u32(&st.w_full), wbytes);
-    bulk_load(smem, w, wbytes, smem_u32(&st.w_full));
-  } else {
-    mbar_arrive(smem_u32(&st.w_full));
+  const int lane = threadIdx.x % 32;
+  if (lane == 0) {
+    const uint32_t wbytes = static_cast<uint32_t>(H) / 4 * 16;
+    for (int i = H / 4 * 4; i < (H + 7) / 8 * 8; ++i)      // the last values, and zeros to the end of a pack
+      asm volatile("st.shared.f32 [%0], %1;" ::"r"(smem + 4 * i), "f"(i < H ? __ldg(w + i) : 0.f) : "memory");
+    if (wbytes) {
+      mbar_arrive_expect_tx(smem_u32(&st.w_full), wbytes);
+      bulk_load(smem, w, wbytes, smem_u32(&st.w_full));
+    } else {
+      mbar_arrive(smem_u32(&st.w_full));
+    }
   }
-  smem += ring_w_bytes(H);
-  const uint32_t slot = ring_slot<AL>(bytes);
   int n = 0;
 #pragma unroll
   for (int i = 0; i < MOST; ++i) n += in[i] != nullptr;
-  int s = 0;
+  const uint32_t slot = ring_slot<AL>(bytes), stage = smem + ring_w_bytes(H) + lane * n * slot;
+  const int mine = lane < R.S ? lane : 0;
+  const uint32_t full = smem_u32(&st.full[mine]), empty = smem_u32(&st.empty[mine]);
+  long long t = lane < R.S ? blockIdx.x + static_cast<long long>(lane) * gridDim.x : T;
   uint32_t ph = 0;
-  for (long long t = blockIdx.x; t < T; t += gridDim.x) {
-    // (a wait that runs out ends the copies; the groups' own waits for them then run out too)
-    if (!mbar_wait(smem_u32(&st.empty[s]), ph ^ 1, status)) break;
-    const uint32_t bar = smem_u32(&st.full[s]);
-    const uint32_t stage = smem + s * n * slot;
-    if constexpr (AL) {
-      mbar_arrive_expect_tx(bar, n * bytes);
-      uint32_t to = stage;
-#pragma unroll
-      for (int i = 0; i < MOST; ++i)
-        if (in[i]) {
-          bulk_load(to, static_cast<const uint8_t*>(in[i]) + t * ld[i], bytes, bar);
-          to += slot;
-        }
-    } else {
-      U from[MOST];
-      uint32_t skip[MOST], size[MOST], all = 0, to = stage;
-#pragma unroll
-      for (int i = 0; i < MOST; ++i) {
-        size[i] = 0;
-        if (!in[i]) continue;
-        const U lo = reinterpret_cast<U>(in[i]), row = lo + static_cast<U>(t * ld[i]), end = row + bytes;
-        const U hi = lo + static_cast<U>((T - 1) * ld[i]) + bytes;
-        U a = row & ~U(15), b = (end + 15) & ~U(15);
-        skip[i] = 0;
-        if (a < lo) {                   // (the matrix' first row)
-          a += 16;
-          skip[i] = 16;
-          for (U e = row; e < a; e += sizeof(E)) copy_element<E>(to + static_cast<uint32_t>(e & 15), e);
-        }
-        if (b > hi) {                   // (its last one)
-          b -= 16;
-          for (U e = b; e < end; e += sizeof(E)) copy_element<E>(to + skip[i] + static_cast<uint32_t>(e - a), e);
-        }
-        from[i] = a;
-        size[i] = static_cast<uint32_t>(b - a);
-        all += size[i];
-        to += slot;
-      }
-      if (t == 0 || t == T - 1) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");    // (elements copied one by one)
-      mbar_arrive_expect_tx(bar, all);
-      to = stage;
-#pragma unroll
-      for (int i = 0; i < MOST; ++i)
-        if (in[i]) {
-          if (size[i]) bulk_load(to + skip[i], reinterpret_cast<const void*>(from[i]), size[i], bar);
-          to += slot;
-        }
-    }
-    if (++s == R.S) {
-      s = 0;
+  long long since = clock64();
+  while (__any_sync(0xffffffffu, t < T)) {
+    const bool go = t < T && mbar_over(empty, ph ^ 1);
+    if (go) {
+      ring_row<AL, E, MOST>(t, stage, full, in, ld, n, T, bytes, slot);
+      t += static_cast<long long>(R.S) * gridDim.x;
       ph ^= 1;
     }
+    // (a wait that runs out ends the copies; the groups' own waits for them then run out too)
+    if (__any_sync(0xffffffffu, go)) {
+      since = clock64();
+    } else if (__any_sync(0xffffffffu, clock64() - since > kWaitBudgetCycles)) {
+      record_error(status, kDevErrTimeout);
+      break;
+    } else {
+      __nanosleep(100);
+    }
   }
-  mbar_wait(smem_u32(&st.w_full), 0, status);
-  for (int i = 0; i < R.S; ++i) mbar_wait(smem_u32(&st.full[i]), i < s ? ph : ph ^ 1, status);
+  if (lane == 0) mbar_wait(smem_u32(&st.w_full), 0, status);
+  if (lane < R.S) mbar_wait(full, ph ^ 1, status);
 }
 
 __device__ __forceinline__ void ring_init(const Ring& R, RingState& st) {
@@ -492,12 +524,13 @@ __device__ __forceinline__ float4 shared_float4(uint32_t addr) {
 
 // Sum over a group of up to W warps of K values per thread, in a fixed order (sh: zeros where there is no warp); false: some thread's
 // `ok` was.
-template <int K, int W>
+template <int K, int W, bool ONE>
 __device__ __forceinline__ bool group_sum(float (&v)[K], float (*sh)[W], int group, int threads, int warp, int lane, bool ok) {
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1)
 #pragma unroll
     for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], d);
+  if constexpr (ONE) return __all_sync(0xffffffffu, ok);
   if (lane == 0)
 #pragma unroll
     for (int k = 0; k < K; ++k) sh[k][warp] = v[k];
@@ -511,13 +544,14 @@ __device__ __forceinline__ bool group_sum(float (&v)[K], float (*sh)[W], int gro
   return ok;
 }
 
-template <class T, bool AL>
+template <class T, bool AL, bool ONE>
 __global__ void __launch_bounds__((AL ? kRingThreads : kRingOddThreads) + 32, 1) norm_ring_kernel(const NormArgs a, const Ring R) {
   constexpr int N = Pack<T>::N, PER = kRingPer;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   __shared__ RingState st;
   __shared__ __align__(16) float sh[kRingGroups][2][1][32];
-  const int H = a.H, lane = threadIdx.x % 32, group = threadIdx.x / R.threads, tid = threadIdx.x - group * R.threads;
+  const int H = a.H, threads = ONE ? 32 : R.threads, lane = threadIdx.x % 32, group = threadIdx.x / threads;
+  const int tid = threadIdx.x - group * threads;
   const uint32_t smem = (smem_u32(smem_raw) + 127) & ~127u, bytes = H * (16 / N), slot = ring_slot<AL>(bytes);
   ring_init(R, st);
   for (int i = threadIdx.x; i < kRingGroups * 2 * 32; i += blockDim.x) (&sh[0][0][0][0])[i] = 0.f;
@@ -525,11 +559,9 @@ __global__ void __launch_bounds__((AL ? kRingThreads : kRingOddThreads) + 32, 1)
   grid_launch_dependents();
   __syncthreads();
   if (group == R.G) {
-    if (lane == 0) {
-      const void* in[2] = {a.x, a.res};
-      const long long ld[2] = {a.ldx * (16 / N), a.ldr * (16 / N)};
-      ring_load<AL, typename T::raw>(R, st, smem, in, ld, a.T, bytes, a.w, H, nullptr);
-    }
+    const void* in[2] = {a.x, a.res};
+    const long long ld[2] = {a.ldx * (16 / N), a.ldr * (16 / N)};
+    ring_load<AL, typename T::raw>(R, st, smem, in, ld, a.T, bytes, a.w, H, nullptr);
     return;
   }
   const uint32_t stage0 = smem + ring_w_bytes(H), stage = (a.res ? 2 : 1) * slot;
@@ -544,7 +576,7 @@ __global__ void __launch_bounds__((AL ? kRingThreads : kRingOddThreads) + 32, 1)
     Words<T> p[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      const int c = (tid + i * R.threads) * N;
+      const int c = (tid + i * threads) * N;
       p[i] = Words<T>{};
       if (c < H) {
         p[i] = shared_row<T, AL>(from + ring_off<AL>(a.x, a.ldx * (16 / N), t), c, H);
@@ -556,16 +588,16 @@ __global__ void __launch_bounds__((AL ? kRingThreads : kRingOddThreads) + 32, 1)
     float ss[1] = {0.f};
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      const int c = (tid + i * R.threads) * N;
+      const int c = (tid + i * threads) * N;
       if (out.sum) put_row<T, AL>(out.sum, c, H, p[i]);
 #pragma unroll
       for (int j = 0; j < N; ++j) ss[0] = fmaf(p[i].f(j), p[i].f(j), ss[0]);
       p[i].keep();
     }
-    ok = group_sum(ss, sh[group][turn], group, R.threads, tid / 32, lane, ok);
+    ok = group_sum<1, 32, ONE>(ss, sh[ONE ? 0 : group][turn], group, threads, tid / 32, lane, ok);
     if (!ok) {                          // there is no workspace for a status: the group's rows become NaN
       for (; t < a.T; t += step, out.on(a, step))
-        for (int c = tid; c < H; c += R.threads) {
+        for (int c = tid; c < H; c += threads) {
           if (out.sum) out.sum[c] = T::from_f(NAN);
           if (out.y) out.y[c] = T::from_f(NAN);
           if (out.q) {
@@ -578,7 +610,7 @@ __global__ void __launch_bounds__((AL ? kRingThreads : kRingOddThreads) + 32, 1)
     const float rs = rsqrtf(ss[0] * a.over_h + a.eps);
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      const int c = (tid + i * R.threads) * N;
+      const int c = (tid + i * threads) * N;
       float v[N];
 #pragma unroll
       for (int j = 0; j < N; j += 4) {
@@ -708,13 +740,14 @@ __global__ void __launch_bounds__(NT, MIN) norm_grad_kernel(const NormGradArgs a
 }
 
 // (the rows' sums and their use as in norm_ring_kernel)
-template <class T, bool AL>
+template <class T, bool AL, bool ONE>
 __global__ void __launch_bounds__(kRingGradThreads + 32, 1) norm_grad_ring_kernel(const NormGradArgs a, const Ring R) {
   constexpr int N = Pack<T>::N, PER = kRingPer;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   __shared__ RingState st;
   __shared__ __align__(16) float sh[kRingGroups][2][2][kRingGradWarps];
-  const int H = a.H, lane = threadIdx.x % 32, group = threadIdx.x / R.threads, tid = threadIdx.x - group * R.threads;
+  const int H = a.H, threads = ONE ? 32 : R.threads, lane = threadIdx.x % 32, group = threadIdx.x / threads;
+  const int tid = threadIdx.x - group * threads;
   const uint32_t smem = (smem_u32(smem_raw) + 127) & ~127u, bytes = H * (16 / N), slot = ring_slot<AL>(bytes);
   ring_init(R, st);
   for (int i = threadIdx.x; i < kRingGroups * 2 * 2 * kRingGradWarps; i += blockDim.x) (&sh[0][0][0][0])[i] = 0.f;
@@ -722,11 +755,9 @@ __global__ void __launch_bounds__(kRingGradThreads + 32, 1) norm_grad_ring_kerne
   grid_launch_dependents();
   __syncthreads();
   if (group == R.G) {
-    if (lane == 0) {
-      const void* in[3] = {a.x, a.dy, a.dsum};
-      const long long ld[3] = {a.ldx * (16 / N), a.lddy * (16 / N), a.lddsum * (16 / N)};
-      ring_load<AL, typename T::raw>(R, st, smem, in, ld, a.T, bytes, a.w, H, a.status);
-    }
+    const void* in[3] = {a.x, a.dy, a.dsum};
+    const long long ld[3] = {a.ldx * (16 / N), a.lddy * (16 / N), a.lddsum * (16 / N)};
+    ring_load<AL, typename T::raw>(R, st, smem, in, ld, a.T, bytes, a.w, H, a.status);
     return;
   }
   const uint32_t stage0 = smem + ring_w_bytes(H), stage = (a.dsum ? 3 : 2) * slot;
@@ -746,7 +777,7 @@ __global__ void __launch_bounds__(kRingGradThreads + 32, 1) norm_grad_ring_kerne
     Words<T> p[PER], d[PER], u[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      const int c = (tid + i * R.threads) * N;
+      const int c = (tid + i * threads) * N;
       p[i] = d[i] = u[i] = Words<T>{};
       if (c < H) {
         p[i] = shared_row<T, AL>(from + ring_off<AL>(a.x, a.ldx * (16 / N), t), c, H);
@@ -759,7 +790,7 @@ __global__ void __launch_bounds__(kRingGradThreads + 32, 1) norm_grad_ring_kerne
     float m[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      const int c = (tid + i * R.threads) * N;
+      const int c = (tid + i * threads) * N;
 #pragma unroll
       for (int j = 0; j < N; j += 4) {
         const float4 w = c < H ? shared_float4(smem + (c + j) * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -774,12 +805,12 @@ __global__ void __launch_bounds__(kRingGradThreads + 32, 1) norm_grad_ring_kerne
       d[i].keep();
       u[i].keep();
     }
-    ok = group_sum(m, sh[group][turn], group, R.threads, tid / 32, lane, ok);
+    ok = group_sum<2, kRingGradWarps, ONE>(m, sh[ONE ? 0 : group][turn], group, threads, tid / 32, lane, ok);
     if (!ok) break;
     const float rs = rsqrtf(m[0] * a.over_h + a.eps), k = m[1] * a.over_h * rs * rs;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      const int c = (tid + i * R.threads) * N;
+      const int c = (tid + i * threads) * N;
       Words<T> o;
 #pragma unroll
       for (int j = 0; j < N; j += 4) {
@@ -801,13 +832,13 @@ __global__ void __launch_bounds__(kRingGradThreads + 32, 1) norm_grad_ring_kerne
   }
   if (!a.part) return;
   // the groups' sums meet where the stages were: every group has taken its last row out of them
-  const int all = R.G * R.threads;
+  const int all = R.G * threads;
   named_barrier(15, all);
   float* meet = reinterpret_cast<float*>(smem_raw + (stage0 - smem_u32(smem_raw)));
   const int pitch = (H + 7) / 8 * 8;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const int c = (tid + i * R.threads) * N;
+    const int c = (tid + i * threads) * N;
     if (c < H)
 #pragma unroll
       for (int j = 0; j < N; j += 4)
@@ -898,7 +929,7 @@ __global__ void __launch_bounds__(1024) norm_dw_sum_kernel(const float* __restri
 // How rows of `packs` packs run: a warp each with one or a few packs a lane; many rows through the ring; few rows in CTAs of
 // up to 1024 threads with one pack a thread, each row over as many threads as it can fill, or with two; or by the kernels for
 // wide rows.
-enum NormPlanKind { kWarpOne, kWarpMore, kCtaFew, kCtaMost, kWide, kRing };
+enum NormPlanKind { kWarpOne, kWarpMore, kCtaFew, kCtaMost, kWide, kRing, kRingOne };
 struct NormPlan {
   NormPlanKind kind;
   int threads, grid;
@@ -931,7 +962,9 @@ NormPlan norm_plan(int T, int H, int dt, const NormLimits& m, int inputs, bool a
     const int slot = static_cast<int>(al ? ring_slot<true>(row_bytes) : ring_slot<false>(row_bytes));
     const int stage = inputs * slot, fit = (kRingBytes - static_cast<int>(ring_w_bytes(H))) / stage;
     int G = m.ring_threads / p.ring.threads;
-    if (G > kRingGroups) G = kRingGroups;
+    const bool one = !al && p.ring.threads == 32;
+    const int most = one ? kRingStages / m.ring_stages : kRingGroups;
+    if (G > most) G = most;
     if (G > fit) G = fit;
     if (G > 0) {
       int S = kRingAhead / stage;
@@ -939,7 +972,7 @@ NormPlan norm_plan(int T, int H, int dt, const NormLimits& m, int inputs, bool a
       if (S < 2) S = 2;
       if (S > fit) S = fit;
       if (S > kRingStages) S = kRingStages;
-      p.kind = kRing;
+      p.kind = one ? kRingOne : kRing;
       p.ring.G = G;
       p.ring.S = S / G * G;
       p.threads = G * p.ring.threads + 32;
@@ -974,7 +1007,13 @@ cudaError_t norm_launch(const NormArgs& a, const NormPlan& p, cudaStream_t strea
   static std::atomic<unsigned long long> done{0};
   const auto go = [&](auto kernel) { return launch_pdl(kernel, dim3(p.grid), dim3(p.threads), 0, stream, a); };
   switch (p.kind) {
-    case kRing: return ring_launch(norm_ring_kernel<T, AL>, a, p, done, stream);
+    case kRing: return ring_launch(norm_ring_kernel<T, AL, false>, a, p, done, stream);
+    case kRingOne:
+      if constexpr (!AL) {
+        static std::atomic<unsigned long long> done_one{0};
+        return ring_launch(norm_ring_kernel<T, AL, true>, a, p, done_one, stream);
+      }
+      return cudaErrorInvalidValue;
     case kWarpOne: return go(norm_kernel<T, AL, 1, true, 256, AL ? 4 : 2, true>);
     case kWarpMore:
       if constexpr (AL) return go(norm_kernel<T, AL, 4, true, 256, 2, true>);
@@ -992,9 +1031,17 @@ cudaError_t norm_grad_launch(NormGradArgs a, const NormPlan& p, float* dw, cudaS
   cudaError_t err;
   int slices = p.grid;
   static std::atomic<unsigned long long> done{0};
-  if (p.kind == kRing) {
+  if (p.kind == kRing || p.kind == kRingOne) {
     if (!dw) a.part = nullptr;
-    err = ring_launch(norm_grad_ring_kernel<T, AL>, a, p, done, stream);
+    if (p.kind == kRing) {
+      err = ring_launch(norm_grad_ring_kernel<T, AL, false>, a, p, done, stream);
+    } else {
+      err = cudaErrorInvalidValue;
+      if constexpr (!AL) {
+        static std::atomic<unsigned long long> done_one{0};
+        err = ring_launch(norm_grad_ring_kernel<T, AL, true>, a, p, done_one, stream);
+      }
+    }
   } else if (p.kind == kWide) {
     // the gradient of w first: dx may take the place of what it reads
     slices = norm_slices(a.T);

@@ -55,6 +55,9 @@ CASES = [  # T, H, dtype, extra pitch
 CASES += [(200, 7168, BF, 0), (160, 8192, BF, 0), (155, 15360, BF, 0), (400, 5001, FP, 0), (170, 4472, HF, 0), (700, 945, HF, 0),
           (2500, 264, BF, 0), (620, 1001, FP, 3), (333, 2521, BF, 1), (1000, 4096, FP, 0), (5000, 72, FP, 0), (310, 1032, HF, 8),
           (153, 9700, HF, 0), (153, 9733, BF, 0), (8, 7168, FP, 0), (9, 7168, BF, 0), (10, 7168, BF, 0)]
+# many short rows that start anywhere: groups of one warp, and of two
+CASES += [(700, 155, FP, 0), (3000, 300, BF, 0), (6500, 301, HF, 1), (5000, 265, BF, 0), (800, 509, HF, 0), (900, 254, FP, 2),
+          (4000, 545, HF, 0), (640, 257, FP, 0)]
 
 
 @pytest.mark.parametrize("T,H,dt,extra", CASES)
