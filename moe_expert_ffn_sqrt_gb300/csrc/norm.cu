@@ -309,7 +309,8 @@ __global__ void __launch_bounds__(kNormThreads) norm_wide_kernel(const NormArgs 
 // 5.9 instead of 5.6).  Groups of one warp (ONE) need none, and there are as many as have their stages: with 8 of them
 // 20000 x 300 bf16 56 us and its gradients 38 instead of 31.5 and 30.7.  (A warp per row without the ring 102 and 48.)
 constexpr int kRingStages = 32, kRingGroups = 9;
-constexpr int kRingThreads = 960, kRingOddThreads = 608;        // of all groups, at most (odd: rows that start anywhere)
+// Threads of all groups, at most.
+constexpr int ring_threads(bool al) { return al ? 960 : 608; }
 constexpr int kRingGradThreads = 608;
 constexpr int kRingWarps = 30, kRingGradWarps = 16;             // of a group, at most
 constexpr int kRingBytes = 223 * 1024;                          // stages and w
@@ -318,10 +319,16 @@ constexpr int kRingSmem = kRingBytes + 128;
 // ahead of the other SMs' rows costs the memory its locality: 16384 x 7168 with residual, two groups, 2 stages 160 us, 4 of
 // them 183; the backward of 8192 x 7168 (one group) 1 stage 95 us, 2 stages 75, 4 79.
 constexpr int kRingAhead = 60 * 1024;
-constexpr int kRingPer = 2;                                     // packs a thread
+// Packs a thread; the forward takes four where a row has more than kRingWide and its instructions are the bound (one input, or
+// rows that start anywhere), since a row's reduction costs the same for twice the packs: 8192 x 4096 fp32 to 8 bits alone
+// 44.8 us instead of 68, 9000 x 6001 bf16 167 instead of 208, but 16384 x 7168 bf16 with residual 191 instead of 159.  From 320 to
+// 440 packs either is as fast (2801 odd bf16 columns 32.5 and 33.9, 3501 fp16 40.9 and 40.3), at 256 four are slower (16.3,
+// 14.2).  Three where they make one warp of a group of two: 9887 x 545 fp16 36 us, so 25.8.
+constexpr int kRingPer = 2, kRingWide = 512;
 
 struct Ring {
   int G, threads, S;          // groups, threads of a group, stages
+  int per;                    // packs of a thread
 };
 
 struct RingState {
@@ -544,9 +551,9 @@ __device__ __forceinline__ bool group_sum(float (&v)[K], float (*sh)[W], int gro
   return ok;
 }
 
-template <class T, bool AL, bool ONE>
-__global__ void __launch_bounds__((AL ? kRingThreads : kRingOddThreads) + 32, 1) norm_ring_kernel(const NormArgs a, const Ring R) {
-  constexpr int N = Pack<T>::N, PER = kRingPer;
+template <class T, bool AL, bool ONE, int PER>
+__global__ void __launch_bounds__(ring_threads(AL) + 32, 1) norm_ring_kernel(const NormArgs a, const Ring R) {
+  constexpr int N = Pack<T>::N;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   __shared__ RingState st;
   __shared__ __align__(16) float sh[kRingGroups][2][1][32];
@@ -938,13 +945,13 @@ struct NormPlan {
 // What forward and backward differ in: packs that a warp takes, warps of short rows' CTAs per SM (by 16), the ring's threads,
 // warps of a group and a group's stages, and values that are few.
 struct NormLimits {
-  int warp_packs, resident, ring_threads, ring_warps, ring_stages, few;
+  int warp_packs, resident, ring_per, ring_threads, ring_warps, ring_stages, few;
 };
 // inputs: matrices of a row that are read; al: all rows on 16-byte boundaries and in whole packs.
 NormPlan norm_plan(int T, int H, int dt, const NormLimits& m, int inputs, bool al) {
   const long long row_bytes = static_cast<long long>(H) * dtype_bytes(dt);
   const int packs = static_cast<int>((row_bytes + 15) / 16), sms = num_sms();
-  NormPlan p{kWide, kNormThreads, T, Ring{1, 0, 0}};
+  NormPlan p{kWide, kNormThreads, T, Ring{1, 0, 0, kRingPer}};
   if (packs <= 32 || (al && packs <= m.warp_packs && T >= 2 * sms)) {
     p.kind = packs <= 32 ? kWarpOne : kWarpMore;
     const int warps = T >= 16 * sms ? 8 : T >= 8 * sms ? 4 : T >= 4 * sms ? 2 : 1;       // (few rows: over all SMs)
@@ -957,8 +964,9 @@ NormPlan norm_plan(int T, int H, int dt, const NormLimits& m, int inputs, bool a
   // but 500 x 2048 backward, whose partial sums of dw are 4 MB then, 10.1, 6.5)
   const int one = (packs + 31) / 32 * 32, at_once = one <= 1024 ? 1024 / one : 1;
   const bool few = T <= sms || (T <= sms * (at_once < 4 ? at_once : 4) && static_cast<long long>(T) * H <= m.few);
-  if (packs <= kRingPer * 32 * m.ring_warps && !few) {
-    p.ring.threads = ((packs + kRingPer - 1) / kRingPer + 31) / 32 * 32;
+  if (packs <= m.ring_per * 32 * m.ring_warps && !few) {
+    p.ring.per = m.ring_per;
+    p.ring.threads = ((packs + m.ring_per - 1) / m.ring_per + 31) / 32 * 32;
     const int slot = static_cast<int>(al ? ring_slot<true>(row_bytes) : ring_slot<false>(row_bytes));
     const int stage = inputs * slot, fit = (kRingBytes - static_cast<int>(ring_w_bytes(H))) / stage;
     int G = m.ring_threads / p.ring.threads;
@@ -966,7 +974,7 @@ NormPlan norm_plan(int T, int H, int dt, const NormLimits& m, int inputs, bool a
     const int most = one ? kRingStages / m.ring_stages : kRingGroups;
     if (G > most) G = most;
     if (G > fit) G = fit;
-    if (G > 0) {
+    if (G > 0 && fit > 1) {
       int S = kRingAhead / stage;
       if (S < m.ring_stages * G) S = m.ring_stages * G;
       if (S < 2) S = 2;
@@ -988,11 +996,13 @@ NormPlan norm_plan(int T, int H, int dt, const NormLimits& m, int inputs, bool a
   return p;
 }
 NormPlan norm_forward_plan(int T, int H, int dt, int inputs, bool al) {
-  return norm_plan(T, H, dt, NormLimits{128, 2, al ? kRingThreads : kRingOddThreads, al ? kRingWarps : kRingOddThreads / 32, 1, 1 << 30},
-                   inputs, al);
+  const int packs = static_cast<int>((static_cast<long long>(H) * dtype_bytes(dt) + 15) / 16);
+  const int per = packs > kRingWide && (inputs == 1 || !al) ? 4 : !al && packs > 64 && packs <= 96 ? 3 : kRingPer;
+  const int threads = ring_threads(al), warps = threads / 32;
+  return norm_plan(T, H, dt, NormLimits{128, 2, per, threads, warps < kRingWarps ? warps : kRingWarps, 1, 1 << 30}, inputs, al);
 }
 NormPlan norm_grad_plan(int T, int H, int dt, int inputs, bool al) {
-  return norm_plan(T, H, dt, NormLimits{64, 1, kRingGradThreads, kRingGradWarps, 2, 400000}, inputs, al);
+  return norm_plan(T, H, dt, NormLimits{64, 1, kRingPer, kRingGradThreads, kRingGradWarps, 2, 400000}, inputs, al);
 }
 
 template <class K, class A>
@@ -1002,18 +1012,27 @@ cudaError_t ring_launch(K kernel, const A& a, const NormPlan& p, std::atomic<uns
   return launch_pdl(kernel, dim3(p.grid), dim3(p.threads), kRingSmem, stream, a, p.ring);
 }
 
+template <class T, bool AL, bool ONE, int PER>
+cudaError_t norm_ring_launch(const NormArgs& a, const NormPlan& p, cudaStream_t stream) {
+  static std::atomic<unsigned long long> done{0};
+  return ring_launch(norm_ring_kernel<T, AL, ONE, PER>, a, p, done, stream);
+}
+template <class T, bool AL>
+cudaError_t norm_ring_launch(const NormArgs& a, const NormPlan& p, cudaStream_t stream) {
+  if constexpr (!AL) {
+    if (p.kind == kRingOne)
+      return p.ring.per == 2 ? norm_ring_launch<T, AL, true, 2>(a, p, stream) : norm_ring_launch<T, AL, true, 3>(a, p, stream);
+  }
+  return p.ring.per == 2 ? norm_ring_launch<T, AL, false, 2>(a, p, stream) : norm_ring_launch<T, AL, false, 4>(a, p, stream);
+}
+
 template <class T, bool AL>
 cudaError_t norm_launch(const NormArgs& a, const NormPlan& p, cudaStream_t stream) {
   static std::atomic<unsigned long long> done{0};
   const auto go = [&](auto kernel) { return launch_pdl(kernel, dim3(p.grid), dim3(p.threads), 0, stream, a); };
   switch (p.kind) {
-    case kRing: return ring_launch(norm_ring_kernel<T, AL, false>, a, p, done, stream);
-    case kRingOne:
-      if constexpr (!AL) {
-        static std::atomic<unsigned long long> done_one{0};
-        return ring_launch(norm_ring_kernel<T, AL, true>, a, p, done_one, stream);
-      }
-      return cudaErrorInvalidValue;
+    case kRing:
+    case kRingOne: return norm_ring_launch<T, AL>(a, p, stream);
     case kWarpOne: return go(norm_kernel<T, AL, 1, true, 256, AL ? 4 : 2, true>);
     case kWarpMore:
       if constexpr (AL) return go(norm_kernel<T, AL, 4, true, 256, 2, true>);
