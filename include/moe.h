@@ -596,7 +596,8 @@ typedef struct {
  * is of the rounded sum, stored or not; y and y8 are each rounded once from fp32.  sum and y may be x or residual
  * themselves (not both the same one: refused).  1 <= H <= 2^24, eps >= 0.  The squares are added up in fp32: a row whose
  * sum of squares passes 3.4e38 comes out as zeros (its infinities as NaN), one whose sum is 0 needs an eps.  A row's sum is
- * taken in an order that goes by T, H and the rows' 16-byte alignment.  (A bounded wait inside that runs out leaves NaN.) */
+ * taken in an order that goes by dt, T, H, the rows' 16-byte alignment and whether there is a residual, not by the outputs.
+ * (A bounded wait inside that runs out leaves NaN.) */
 moe_status moe_rms_norm(moe_dtype dt, moe_rows x, moe_rows residual, const float* weight, float eps, int T, int H,
                         moe_rows sum, moe_rows y, moe_rows8 y8, void* stream);
 

@@ -7,10 +7,10 @@
 // row gives both of the backward's sums (s^2 and s g), so nothing but s is kept from the forward.
 //
 // HBM bounds them where rows are many: each value is read and written once.  16384 x 7168 bf16 with residual, 16-bit and
-// 8-bit outputs, 1.06 GB in 160 us (98% of a plain copy's rate); without residual 104 us (83%: about 170 instructions a
-// pack); gradients of 8192 x 7168 with dsum 75 us (93%), 4 us of it the launch that adds the CTAs' parts of dw up.  8192 x
+// 8-bit outputs, 1.06 GB in 160 us (98% of a plain copy's rate); without residual 114 us (76%: about 170 instructions a
+// pack); gradients of 8192 x 7168 with dsum 75.5 us (92%), 4 us of it the launch that adds the CTAs' parts of dw up.  8192 x
 // 4096 fp32 88 us (95%), 16384 x 2048 bf16 49 (91%), its gradients 43 (92%).  Rows that start on no 16-byte boundary are
-// bound by the shifts' instructions: 9000 x 6001 bf16 208 us of 72, 1450 x 2521 fp16 17 of 5.  A row of 7168 alone takes 2.9
+// bound by the shifts' instructions: 9000 x 6001 bf16 167 us of 72, 1450 x 2521 fp16 17 of 5.  A row of 7168 alone takes 2.9
 // us: launch, one load, the reduction's two steps, the stores.  (Reading each row twice, from L1 and L2 the second time:
 // 205 us and, the gradients, 266; a row in registers with the next one's loads ahead, two CTAs of 448 threads: 243, 151.)
 #include "rows8.cuh"
@@ -319,11 +319,12 @@ constexpr int kRingSmem = kRingBytes + 128;
 // ahead of the other SMs' rows costs the memory its locality: 16384 x 7168 with residual, two groups, 2 stages 160 us, 4 of
 // them 183; the backward of 8192 x 7168 (one group) 1 stage 95 us, 2 stages 75, 4 79.
 constexpr int kRingAhead = 60 * 1024;
-// Packs a thread; the forward takes four where a row has more than kRingWide and its instructions are the bound (one input, or
-// rows that start anywhere), since a row's reduction costs the same for twice the packs: 8192 x 4096 fp32 to 8 bits alone
-// 44.8 us instead of 68, 9000 x 6001 bf16 167 instead of 208, but 16384 x 7168 bf16 with residual 191 instead of 159.  From 320 to
-// 440 packs either is as fast (2801 odd bf16 columns 32.5 and 33.9, 3501 fp16 40.9 and 40.3), at 256 four are slower (16.3,
-// 14.2).  Three where they make one warp of a group of two: 9887 x 545 fp16 36 us, so 25.8.
+// Packs a thread; the forward takes four where a row has more than kRingWide and its instructions are the bound (fp32 without
+// residual, rows that start anywhere), since a row's reduction costs the same for twice the packs: 8192 x 4096 fp32 to 8 bits
+// alone 44.8 us instead of 68 and to fp32 44.6 of 47.7 (with residual 95 of 88), 9000 x 6001 bf16 167 instead of 208.  In 16
+// bits on boundaries they do not fit the 64 registers: 16384 x 7168 to 8 bits alone 100 us of 110, but to bf16 84 of 75 and
+// with residual 191 of 159.  From 320 to 440 packs either is as fast (2801 odd bf16 columns 33.9 with four, 32.5; 3501 fp16
+// 40.3, 40.9).  Three where they make one warp of a group of two: 9887 x 545 fp16 36 us, so 25.8.
 constexpr int kRingPer = 2, kRingWide = 512;
 
 struct Ring {
@@ -997,7 +998,7 @@ NormPlan norm_plan(int T, int H, int dt, const NormLimits& m, int inputs, bool a
 }
 NormPlan norm_forward_plan(int T, int H, int dt, int inputs, bool al) {
   const int packs = static_cast<int>((static_cast<long long>(H) * dtype_bytes(dt) + 15) / 16);
-  const int per = packs > kRingWide && (inputs == 1 || !al) ? 4 : !al && packs > 64 && packs <= 96 ? 3 : kRingPer;
+  const int per = packs > kRingWide && (!al || (inputs == 1 && dt == kF32)) ? 4 : !al && packs > 64 && packs <= 96 ? 3 : kRingPer;
   const int threads = ring_threads(al), warps = threads / 32;
   return norm_plan(T, H, dt, NormLimits{128, 2, per, threads, warps < kRingWarps ? warps : kRingWarps, 1, 1 << 30}, inputs, al);
 }
@@ -1023,7 +1024,10 @@ cudaError_t norm_ring_launch(const NormArgs& a, const NormPlan& p, cudaStream_t 
     if (p.kind == kRingOne)
       return p.ring.per == 2 ? norm_ring_launch<T, AL, true, 2>(a, p, stream) : norm_ring_launch<T, AL, true, 3>(a, p, stream);
   }
-  return p.ring.per == 2 ? norm_ring_launch<T, AL, false, 2>(a, p, stream) : norm_ring_launch<T, AL, false, 4>(a, p, stream);
+  if constexpr (!AL || Pack<T>::N == 4) {
+    if (p.ring.per == 4) return norm_ring_launch<T, AL, false, 4>(a, p, stream);
+  }
+  return norm_ring_launch<T, AL, false, 2>(a, p, stream);
 }
 
 template <class T, bool AL>
