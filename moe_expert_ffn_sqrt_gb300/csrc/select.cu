@@ -14,8 +14,8 @@
 //
 // The choice does not depend on how a score is evaluated: a key in fp32 is off by a known bound, and where two keys (or
 // groups) that decide are closer than that, the keys that are near are evaluated in 64 bits, one to a lane.  Two experts of
-// equal logit and bias are an exact tie and need no second look; without a bias keys go by the logits themselves, which all
-// scores rise with.
+// equal logit and bias are an exact tie and need no second look, unless they are the last one in and the first one out and a
+// third, other key is near them.  Without a bias keys go by the logits themselves, which all scores rise with.
 //
 // 16384 tokens of 256 experts in 8 groups, 6 of them, sigmoid and bias: 19.4 us, of 2.6 for the bytes.  The instructions
 // bound it, about 900 a token, with the schedulers busy for 60% of the time (64 registers, 32 warps per SM; 80 registers
@@ -432,37 +432,54 @@ __global__ void __launch_bounds__(kSelectWarps * 32, PER <= 8 ? kSelectCtas : 1)
       const uint2 own = lane < a.K ? list[lane] : make_uint2(0, 1);
       id = own.x;
       if (a.bias) {
-        bool unsure = false;
+        bool unsure = false, tie = false;
         const uint2 after = lane < a.K ? list[lane + 1] : make_uint2(0, 0);
         const float f = from_ordered(own.y);
         if (after.y != 0) {
           const int ne = after.x;
           const float nf = from_ordered(after.y);
-          if (f - nf <= near + (size_of(f) + size_of(nf)) * 0x1p-23f)
+          if (f - nf <= near + (size_of(f) + size_of(nf)) * 0x1p-23f) {
             unsure = logit(a, row, id) != logit(a, row, ne) || __ldg(a.bias + id) != __ldg(a.bias + ne);
+            tie = !unsure && lane == a.K - 1;
+          }
         }
-        if (__any_sync(kAll, unsure)) {
-          // every key that may be among the K largest, in 64 bits
+        if (__any_sync(kAll, unsure || tie)) {
           const float kth = __shfl_sync(kAll, f, a.K - 1);
           const uint32_t low = ordered(kth - (near + size_of(kth) * 0x1p-21f));
-          __syncwarp();
-          all64 = c > 32;               // (the rounds have used the keys up)
-          if (!all64) c = collect([&](int i) { return key[i] >= low; });
-          all64 = all64 || c > 32;
-          if (!all64) {
-            const Scores64<FN> score = scores64<FN>(a, row, lmax);
-            const int e = lane < c ? list[lane].x : kNone;
-            const double k = lane < c ? key64(score, e) : -INFINITY;
-            int rank = 0;
-            for (int r = 0; r < c; ++r) {
-              const double o = __shfl_sync(kAll, k, r);
-              const int oe = __shfl_sync(kAll, e, r);
-              rank += o > k || (o == k && oe < e);
+          if (!__any_sync(kAll, unsure)) {
+            // the last one in and the first one out are equals: a key behind the two may be near them, and larger
+            const uint32_t high = __shfl_sync(kAll, own.y, a.K - 1);
+            const int last = __shfl_sync(kAll, id, a.K - 1);
+            const float l = logit(a, row, last), b = __ldg(a.bias + last);
+            unsigned long long alike = 0;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) alike |= static_cast<unsigned long long>(key[i] >= low && key[i] <= high) << i;
+            for (; alike && !unsure; alike &= alike - 1) {
+              const int e = e0 + at(__ffsll(alike) - 1);
+              unsure = logit(a, row, e) != l || __ldg(a.bias + e) != b;
             }
+          }
+          if (__any_sync(kAll, unsure)) {
+            // every key that may be among the K largest, in 64 bits
             __syncwarp();
-            if (lane < c && rank < a.K) list[rank].x = e;
-            __syncwarp();
-            if (lane < a.K) id = list[lane].x;
+            all64 = c > 32;             // (the rounds have used the keys up)
+            if (!all64) c = collect([&](int i) { return key[i] >= low; });
+            all64 = all64 || c > 32;
+            if (!all64) {
+              const Scores64<FN> score = scores64<FN>(a, row, lmax);
+              const int e = lane < c ? list[lane].x : kNone;
+              const double k = lane < c ? key64(score, e) : -INFINITY;
+              int rank = 0;
+              for (int r = 0; r < c; ++r) {
+                const double o = __shfl_sync(kAll, k, r);
+                const int oe = __shfl_sync(kAll, e, r);
+                rank += o > k || (o == k && oe < e);
+              }
+              __syncwarp();
+              if (lane < c && rank < a.K) list[rank].x = e;
+              __syncwarp();
+              if (lane < a.K) id = list[lane].x;
+            }
           }
         }
       }

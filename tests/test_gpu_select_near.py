@@ -1,0 +1,57 @@
+"""Choices that fp32 scores cannot make: keys next to one another with exact ties among them."""
+import pytest
+import torch
+
+import around_ref as A
+from gpu_util import ensure_lib
+from test_gpu_select import check
+
+pytestmark = pytest.mark.gpu
+
+FNS = ["softmax", "sqrt_softplus", "sigmoid"]
+
+
+@pytest.fixture(scope="module")
+def M():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    return ensure_lib()
+
+
+def test_a_key_behind_a_tie_at_the_border(M):
+    """sigmoid(20) and sigmoid(21) are one fp32 number, two equal experts of the former come first."""
+    for E in (4, 8, 60, 256):
+        for first in ([20.0, 20.0, 21.0], [20.0, 20.0, 20.0, 21.0], [20.0, 21.0, 20.0]):
+            l = torch.full((1, E), -3.0)
+            l[0, :len(first)] = torch.tensor(first)
+            for K in (1, 2, 3):
+                check(M, l, torch.zeros(E), K, "sigmoid")
+                if E % 4 == 0 and K <= E // 4:
+                    check(M, l, torch.zeros(E), K, "sigmoid", G=4, KG=1)
+
+
+@pytest.mark.parametrize("fn", FNS)
+@pytest.mark.parametrize("E", [8, 16, 31, 64, 100, 256])
+def test_equal_experts_and_one_near_them(M, fn, E):
+    """All experts are alike but one, whose bias brings its key next to theirs: by about a bias' last place, 1e-9, above or
+    below, far less than fp32 tells apart.  (Where fp32 finds it below, it comes behind a tie at the border.)"""
+    g = torch.Generator().manual_seed(E)
+    told = 0
+    for _ in range(16):
+        l = torch.full((1, E), float(torch.randn(1, generator=g)))
+        at = int(torch.randint(0, E, (1,), generator=g))
+        l[0, at] = float(torch.randn(1, generator=g))
+        s = A.score(l, fn)[0]
+        bias = torch.full((E,), 0.1)
+        other = (at + 1) % E
+        bias[at] = float(s[other] + bias[other].double() - s[at])
+        key = s + bias.double()
+        if abs(float(key[at] - key[other])) < 1e-13:
+            continue                     # 64-bit evaluations, good to 1e-15, have to tell them apart
+        told += 1
+        for K in (1, 2, 5):
+            check(M, l.expand(3, E).contiguous(), bias, K, fn)
+            if E % 8 == 0 and K <= E // 8 * 2:
+                check(M, l, bias, K, fn, G=8, KG=2)
+                check(M, l, bias, K, fn, G=8, KG=2, best=1)
+    assert told >= 8
