@@ -57,6 +57,14 @@ __device__ __forceinline__ float size_of(float f) {
   return a <= 3.402823466e38f ? a : 0.f;
 }
 
+// sqrt(softplus(l)).  Far below zero it is e^(l/2) (1 - e^l / 4 + ..), e^-20 / 4 < 2^-30: a normal number down to l = -174,
+// where e^l is subnormal from -87 on and 0 from -104 on.
+__device__ __forceinline__ float root_softplus(float l) {
+  const bool far = l < -20.f;
+  const float e = expf(far ? 0.5f * l : -fabsf(l));
+  return far ? e : sqrtf(fmaxf(l, 0.f) + log1pf(e));
+}
+
 // Scores (FN: moe_score_fn); softmax of a row: lmax its largest logit, sum its exponentials' (a masked expert, a logit of
 // -infinity, has 0, in a row of nothing else too).
 template <int FN>
@@ -64,7 +72,7 @@ struct Scores {
   float lmax, sum;
   __device__ __forceinline__ float operator()(float l) const {
     if (FN == 0) return l == -INFINITY ? 0.f : expf(l - lmax) / sum;
-    if (FN == 1) return sqrtf(fmaxf(l, 0.f) + log1pf(expf(-fabsf(l))));
+    if (FN == 1) return root_softplus(l);
     return 1.f / (1.f + expf(-l));
   }
 };
@@ -74,7 +82,7 @@ struct FastScores {
   float lmax, over;
   __device__ __forceinline__ float operator()(float l) const {
     if (FN == 0) return l == -INFINITY ? 0.f : __expf(l - lmax) * over;
-    if (FN == 1) return sqrtf(fmaxf(l, 0.f) + log1pf(expf(-fabsf(l))));
+    if (FN == 1) return root_softplus(l);
     float e, s;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(l * -1.4426950408889634f));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));
