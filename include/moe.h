@@ -625,7 +625,8 @@ typedef struct {
 /* Routing from logits [T, E] of type dt (moe_route's logits_out, or a product's output):
  *   s = fn(logits);  key = s + e_score_bias (fp32 [E], optional)
  *   topk_ids [T, K] int32 out: the K largest keys among the experts of the token's groups, descending
- *   topk_w   [T, K] fp32 out: scale * s of them (renormalize: / the sum of the K scores; all 0 where that is 0)
+ *   topk_w   [T, K] fp32 out: scale * s of them (renormalize: / the sum of the K scores; all 0 where that is 0).  A
+ *            token with a score below 2^-100 has them from 64-bit scores (which reach down to about e^-700).
  * Ties go to the lower group and expert id.  Keys are compared as 64-bit evaluations give them (without a bias: by the
  * logits themselves), whatever the kernel's own arithmetic; a NaN key counts as -infinity, a logit of -infinity (an
  * expert that is masked out) has score 0 under every fn, so ids are valid and different in any case.

@@ -217,6 +217,26 @@ __device__ __noinline__ int select_all64(const SelectArgs& a, const uint8_t* row
   return id;
 }
 
+// A token's weights from 64-bit scores (lane k has its k-th expert): for tokens with a score below kTiny.  fp32 has few bits
+// for those, or none, and they count where all of a token's are as small, or the scale is large.
+constexpr float kTiny = 0x1p-100f;
+template <int FN>
+__device__ __noinline__ void weights64(const SelectArgs& a, long long t, float lmax, int id) {
+  const int lane = threadIdx.x % 32;
+  const uint8_t* row = a.logits + t * a.row_bytes;
+  const float l = lane < a.K ? logit(a, row, id) : -INFINITY;
+  if (!__any_sync(kAll, l != -INFINITY)) return;          // masked experts all: zeros
+  const Scores64<FN> score = scores64<FN>(a, row, lmax);
+  double s = lane < a.K ? score(l) : 0.;
+  if (a.renorm) {
+    double all = s;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) all += __shfl_xor_sync(kAll, all, d);
+    s = all == 0. ? 0. : s / all;
+  }
+  if (lane < a.K) a.w[t * a.K + lane] = static_cast<float>(s * a.scale);
+}
+
 template <int FN, int PER, int V>
 __global__ void __launch_bounds__(kSelectWarps * 32, PER <= 8 ? kSelectCtas : 1) select_kernel(const SelectArgs a) {
   __shared__ uint2 s_near[kSelectWarps][34];           // experts that are near (id, key), then the chosen ones in order
@@ -495,9 +515,10 @@ __global__ void __launch_bounds__(kSelectWarps * 32, PER <= 8 ? kSelectCtas : 1)
     if (all64) id = select_all64<FN, PER>(a, row, lmax, id);
     __syncwarp();
     const Scores<FN> score{lmax, sum};
-    float s = lane < a.K ? score(logit(a, row, id)) : 0.f;
+    float s = lane < a.K ? score(logit(a, row, id)) : 1.f;
+    const bool tiny = __any_sync(kAll, s < kTiny);
     if (a.renorm) {
-      float all = s;
+      float all = lane < a.K ? s : 0.f;
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1) all += __shfl_xor_sync(kAll, all, d);
       s = all == 0.f ? 0.f : s / all;
@@ -506,6 +527,7 @@ __global__ void __launch_bounds__(kSelectWarps * 32, PER <= 8 ? kSelectCtas : 1)
       a.ids[t * a.K + lane] = id;
       a.w[t * a.K + lane] = s * a.scale;
     }
+    if (tiny) weights64<FN>(a, t, lmax, id);
   }
 }
 

@@ -52,3 +52,41 @@ def test_gradient_of_far_negative_logits(M, renorm):
     here = torch.zeros(T, E, dtype=R.F64).scatter_add_(1, ids.long(), wk * (dw.abs().double() + size / scale))
     R.check(out, ref, 2.0 ** -17 * here + R.tiny(torch.float32), "dlogits")
     assert M.get_error(ws) == M.OK
+
+
+# logits whose scores fp32 holds in few bits or not at all, but 64 bits do: sigmoid e^l, softmax e^(l - the largest)
+@pytest.mark.parametrize("fn,lo,hi", [("sigmoid", -700, -600), ("sigmoid", -104, -86), ("sigmoid", -89, -20), ("sigmoid", -120, 3),
+                                      ("sqrt_softplus", -700, -600), ("sqrt_softplus", -208, -172), ("sqrt_softplus", -230, 3)])
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+def test_weights_of_scores_below_fp32(M, fn, lo, hi, dt):
+    l = rows(24, 64, lo, hi, dt, 5)
+    push = torch.zeros(64)
+    push[::5] = 9.0                       # chooses experts of every score
+    for bias in (None, push):
+        for renorm in (True, False):
+            for scale in (1.0, -2.5, 1e20):
+                check(M, l, bias, 8, fn, renorm=renorm, scale=scale)
+                check(M, l, bias, 8, fn, renorm=renorm, scale=scale, G=8, KG=4)
+
+
+@pytest.mark.parametrize("drop", [60, 88, 104, 120, 600])
+def test_softmax_weights_of_experts_far_below_the_largest(M, drop):
+    """A bias may choose experts that have nearly nothing; their normalised weights are ordinary numbers."""
+    l = rows(24, 64, -4, 4, seed=6)
+    l[:, 7] += drop
+    push = torch.zeros(64)
+    push[20:40] = 9.0
+    for renorm in (True, False):
+        check(M, l, push, 8, "softmax", renorm=renorm)
+    l[:, 20:30] += drop / 3
+    for renorm in (True, False):
+        check(M, l, push, 12, "softmax", renorm=renorm)
+
+
+def test_a_row_that_64_bits_call_zero_has_no_weights(M):
+    for fn in ("softmax", "sqrt_softplus", "sigmoid"):
+        l = torch.full((3, 16), -2000.0)
+        l[0] = -float("inf")
+        l[1, 0] = 0.0
+        check(M, l, None, 4, fn)
+        check(M, l, None, 4, fn, renorm=False)
