@@ -364,7 +364,8 @@ __global__ void __launch_bounds__(kSelectWarps * 32, PER <= 8 ? kSelectCtas : 1)
         kth = best;
       }
       const float last = from_ordered(kth), next = from_ordered(__reduce_max_sync(kAll, mine));
-      if (nan || last - next <= tol) {
+      // (an infinite tol: some group's sum is past fp32's range, and last - next may be inf - inf)
+      if (tol == INFINITY || last - next <= tol) {
         // groups that are surely in, and those that may be: the latter in 64 bits, from their experts that may be among
         // the best two
         const bool in = used && worth - next > tol, maybe = used && !in && !(last - worth > tol);

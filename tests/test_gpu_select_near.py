@@ -55,3 +55,17 @@ def test_equal_experts_and_one_near_them(M, fn, E):
                 check(M, l, bias, K, fn, G=8, KG=2)
                 check(M, l, bias, K, fn, G=8, KG=2, best=1)
     assert told >= 8
+
+
+@pytest.mark.parametrize("fn", FNS)
+def test_groups_whose_sum_fp32_cannot_hold(M, fn):
+    """Two biases of fp32's lowest (or near its highest) value: their sum overflows in fp32, not in 64 bits, and such a group
+    is worth more than one of -infinity."""
+    low, inf = torch.finfo(torch.float32).min, float("inf")
+    l = torch.randn(9, 32, generator=torch.Generator().manual_seed(7))
+    for worst, mid in ((-inf, low), (-inf, 0.75 * low), (low, 0.875 * low), (-0.75 * low, -0.875 * low), (-inf, -low)):
+        b = torch.randn(8, 4, generator=torch.Generator().manual_seed(8)) * 0.1
+        b[0], b[1], b[4], b[6] = worst, worst, mid, mid
+        for KG in (1, 2, 3, 5, 6, 7):
+            for best in (1, 2):
+                check(M, l, b.reshape(-1), 3, fn, G=8, KG=KG, best=best)
