@@ -71,7 +71,11 @@ template <int FN>
 struct Scores {
   float lmax, sum;
   __device__ __forceinline__ float operator()(float l) const {
-    if (FN == 0) return l == -INFINITY ? 0.f : expf(l - lmax) / sum;
+    if (FN == 0) {
+      // (d is rounded by up to |d| 2^-24, which would be the exponential's relative error: it gets the rest back)
+      const float d = l - lmax, back = d - l, rest = (l - (d - back)) - (lmax + back), e = expf(d);
+      return l == -INFINITY ? 0.f : fmaf(e, rest, e) / sum;
+    }
     if (FN == 1) return root_softplus(l);
     return 1.f / (1.f + expf(-l));
   }
@@ -278,9 +282,15 @@ __global__ void __launch_bounds__(kSelectWarps * 32, PER <= 8 ? kSelectCtas : 1)
     if (FN != 2) lmax = from_ordered(__reduce_max_sync(kAll, top));
     if (FN == 0) {
       sum = 0.f;
+      if (a.renorm) {                   // (weights are divided by their own sum: the row's cancels, and is good enough for keys)
 #pragma unroll
-      for (int i = 0; i < PER; ++i)
-        if (key[i] && v[i] != -INFINITY) sum += __expf(v[i] - lmax);
+        for (int i = 0; i < PER; ++i)
+          if (key[i] && v[i] != -INFINITY) sum += __expf(v[i] - lmax);
+      } else {
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+          if (key[i] && v[i] != -INFINITY) sum += expf(v[i] - lmax);
+      }
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
     }

@@ -90,3 +90,21 @@ def test_a_row_that_64_bits_call_zero_has_no_weights(M):
         l[1, 0] = 0.0
         check(M, l, None, 4, fn)
         check(M, l, None, 4, fn, renorm=False)
+
+
+@pytest.mark.parametrize("E", [64, 256, 1000])
+@pytest.mark.parametrize("spread", [2.0, 10.0])
+def test_softmax_weights_as_they_are(M, E, spread):
+    """Unnormalised weights e^(l - m) / sum: the exponential within 2 units in the last place (4 of 2^-24, its argument's own
+    rounding made up for by one product), the sum's terms the same and |l - m| 2^-24 of theirs more, E / 32 + 5 additions, one
+    division.  (An argument rounded alone: up to |l - m| 2^-24, past 40 of them here; fast exponentials in the sum: as much of
+    each of its terms.)"""
+    l = torch.randn(4096, E, generator=torch.Generator().manual_seed(E)) * spread
+    ids, w = run(M, l, None, 8, "softmax", renorm=False)
+    p = torch.softmax(l.double(), 1)
+    d = l.double() - l.double().amax(1, keepdim=True)
+    ref = p.gather(1, ids.long())
+    units = 4 + 2 + 4 + (p * d.abs()).sum(1, keepdim=True) + E / 32 + 5 + 1
+    R.check(w, ref, ref * units * 2.0 ** -24 * 1.001 + 1e-37, "w")
+    # and not off to one side: the mean of 32768 of them is within a third of a unit
+    assert abs(float((w.double() / ref - 1)[ref > 1e-30].mean())) < 2.0 ** -24 / 3
