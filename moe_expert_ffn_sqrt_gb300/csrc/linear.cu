@@ -1632,9 +1632,10 @@ __global__ void __launch_bounds__(32 * kActRowLanes, Z8 ? 4 : 6)
 
 // The same values without the bias gradient's sums: `lanes` threads to a row (fewer than a CTA's where rows are narrow), two
 // rows of a thread on their way together; blockIdx.x: which `lanes` groups of eight columns, so that neighbouring CTAs read
-// one row.  Beside act_grad_kernel, with the dx product of K = 64 behind both: 4096 x 2048 SiLU 17.3 us of 19.7 and GELU 21.2
-// of 26.7, 128 x 4096 SwiGLU 12.1 of 14.0, 16384 x 7168 SiLU 161.8 of 160.3 and GELU 178.6 of 183.8; from 8 bits, 6971 x 80
-// ReLU 4 of 17 and 7 experts of 288 columns 6 of 14 (a warp of act_grad_kernel takes 256 columns of one row).  With one row
+// one row.  Beside act_grad_kernel, with the dx product of K = 64 behind both: 4096 x 2048 SiLU 18.3 us of 21.1 and GELU 21.7
+// of 28.7, 128 x 4096 SwiGLU 11.0 of 13.1, 16384 x 7168 SiLU 163.2 of 162.2 and GELU 180.6 of 185.7, 1000 x 4096 ReLU 14.9 of
+// 14.5; from 8 bits, 6971 x 80 ReLU 4 of 17 and 7 experts of 288 columns 6 of 14 (a warp of act_grad_kernel takes 256 columns
+// of one row).  With one row
 // at a time and six CTAs per SM the SiLU case of 16384 x 7168 is 174, with CTAs of one column group side by side 163.6.
 template <class T, bool Z8>
 __global__ void __launch_bounds__(256, 4)
@@ -1690,6 +1691,17 @@ __global__ void __launch_bounds__(256, 4)
   }
 }
 
+// CTAs along the rows of act_grad_rows_kernel (`per` rows a CTA at a time, two such steps on their way together): 8 per SM at
+// most, 16 where each has five steps or more all the same (16384 x 7168 SiLU 164.4 us with 8, 163.2 with 16, GELU 183.4 and
+// 180.5; but 4096 x 2048, 1.7 steps with 16, GELU 21.5 and 22.4), and no more than give a CTA two steps while that leaves two
+// CTAs per SM or so (1000 x 1408 SiLU 10.8 us with a step each, so 10.1; 2000 x 1408 ReLU 12.0, 11.3).
+unsigned act_row_blocks(long long rows, int E, int per, int nz) {
+  const long long steps = (rows / E + per) / per, beside = static_cast<long long>(nz) * E, most = 16LL * num_sms() / beside;
+  long long n = steps >= 5 * most ? most : steps < most / 2 ? steps : most / 2;
+  if (n * beside >= 2 * num_sms() && n > (steps + 1) / 2) n = (steps + 1) / 2;
+  return static_cast<unsigned>(n < 1 ? 1 : n);
+}
+
 __global__ void __launch_bounds__(256) bias_sum_kernel(const float* __restrict__ part, int S, int N, long long total,
                                                        float* __restrict__ db) {
   const long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
@@ -1741,7 +1753,7 @@ cudaError_t launch_act_grad(const LinearShape& p, RowsView dy, RowsView z, Rows8
       int lanes = 256;
       while (lanes > 8 && (packs + lanes - 1) / lanes * lanes - packs > packs / 8) lanes /= 2;
       const int nz = (packs + lanes - 1) / lanes, per = 256 / lanes;
-      const unsigned nx = row_blocks(p.counts ? live : p.rows, E, per, nz);
+      const unsigned nx = act_row_blocks(p.counts ? live : p.rows, E, per, nz);
       return launch_pdl(act_grad_rows_kernel<T, Z8>, dim3(static_cast<unsigned>(nz), static_cast<unsigned>(E), nx), dim3(256), 0,
                         stream, static_cast<const uint16_t*>(dy.ptr), dy.ld, zr, act, p.counts, p.align, p.rows, p.N,
                         static_cast<uint16_t*>(dz.ptr), dz.ld, lanes, status);
