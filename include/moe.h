@@ -486,8 +486,9 @@ moe_status moe_forward_batched_i8(const uint16_t* hidden, const float* w_gate, c
  * gradient of moe_combine_backward goes by the rows' 16-byte alignment).
  * Sorted buffers have U rows (moe_msum_upper, or E * max_tokens for the BatchedExperts layout); padding
  * rows never count and are never written.
- * ws: a workspace whose first 256 bytes hold the device status word, zero-filled once before first use.  Calls that
- * overlap, on other streams or host threads, take a workspace each.
+ * ws: a workspace whose first 256 bytes hold the device status word, zero-filled once before first use, on a 4-byte
+ * boundary (the products' on a 256-byte one).  Calls that overlap, on other streams or host threads, take a workspace
+ * each.  Arrays of int32 or float start on 4-byte boundaries where no more is asked.
  * ------------------------------------------------------------------------------------ */
 typedef enum { MOE_BF16 = 0, MOE_F16 = 1, MOE_F32 = 2 } moe_dtype;
 typedef struct {

@@ -20,6 +20,14 @@ inline RowsView view(const moe_rows& m) { return RowsView{m.ptr, static_cast<lon
 
 bool dtype_ok(moe_dtype dt) { return dt == MOE_BF16 || dt == MOE_F16 || dt == MOE_F32; }
 
+// Arrays of int32 or float, each given or not: on their elements' boundaries.
+template <class... A>
+bool words_ok(const A*... p) {
+  return (... && aligned(p, 4));
+}
+// A workspace of at least n bytes, its status word on a boundary.
+bool ws_ok(const void* ws, size_t ws_bytes, size_t n) { return ws && aligned(ws, 4) && ws_bytes >= n; }
+
 // A matrix with `cols` columns of the type: given, element-aligned, pitch at least its width.
 bool rows_ok(const moe_rows& m, int cols, moe_dtype dt) {
   return m.ptr && m.ld >= cols && m.ld <= kMaxLd && aligned(m.ptr, dtype_bytes(dt));
@@ -85,6 +93,7 @@ moe_status linear_common(moe_dtype dt, const int32_t* counts, int rows, int N, i
   if (!dtype_ok(dt) || !linear_dims_ok(rows, N, K, E, act)) return MOE_ERR_INVALID_ARG;
   if (dt == MOE_F32) return MOE_ERR_UNSUPPORTED;
   if ((E > 0) != (counts != nullptr) || (E > 0 && !pow2_align(align))) return MOE_ERR_INVALID_ARG;
+  if (!words_ok(counts)) return MOE_ERR_INVALID_ARG;
   if (!ws || !aligned(ws, kAlign)) return MOE_ERR_WORKSPACE;
   return MOE_OK;
 }
@@ -120,7 +129,8 @@ moe_status moe_dispatch(moe_dtype dt, const int32_t* topk_ids, moe_rows x, int T
   if (U > 0x7fffffff) return MOE_ERR_INVALID_ARG;
   if (!m_sum || (U > 0 && (!sorted_token_ids || !expert_ids))) return MOE_ERR_INVALID_ARG;
   if (T > 0 && (!topk_ids || !inv_perm || !rows_ok(x, H, dt) || !rows_ok(x_perm, H, dt))) return MOE_ERR_INVALID_ARG;
-  if (!ws || ws_bytes < kAlign + permute_scratch_bytes(T, K, E)) return MOE_ERR_WORKSPACE;
+  if (!words_ok(topk_ids, sorted_token_ids, expert_ids, inv_perm, m_sum, expert_counts)) return MOE_ERR_INVALID_ARG;
+  if (!ws_ok(ws, ws_bytes, kAlign + permute_scratch_bytes(T, K, E))) return MOE_ERR_WORKSPACE;
   if (dispatch_layout_supported(T, K, E))
     return cuda_status(launch_dispatch_layout(dt, topk_ids, view(x), T, H, E, K, align, static_cast<int>(U), view(x_perm),
                                               sorted_token_ids, expert_ids, inv_perm, m_sum, expert_counts,
@@ -144,7 +154,8 @@ moe_status moe_combine(moe_dtype dt, moe_rows y_perm, const int32_t* inv_perm, c
   if (!dtype_ok(dt) || !sorted_dims_ok(T, K, H, U)) return MOE_ERR_INVALID_ARG;
   if (T == 0) return MOE_OK;
   if (!inv_perm || !rows_ok(y_perm, H, dt) || !rows_ok(out, H, dt) || !opt_rows_ok(residual, H, dt)) return MOE_ERR_INVALID_ARG;
-  if (!ws || ws_bytes < kAlign) return MOE_ERR_WORKSPACE;
+  if (!words_ok(inv_perm, topk_w)) return MOE_ERR_INVALID_ARG;
+  if (!ws_ok(ws, ws_bytes, kAlign)) return MOE_ERR_WORKSPACE;
   return cuda_status(launch_sum_rows(dt, view(y_perm), inv_perm, topk_w, view(residual), T, K, H, U, view(out),
                                      status_of(ws), S(stream)));
 }
@@ -158,7 +169,8 @@ moe_status moe_combine_backward(moe_dtype dt, moe_rows dout, moe_rows y_perm, co
   // y_perm is read for the weights' gradient alone; a plain sum (topk_w NULL) has none
   if ((dtopk_w != nullptr) != (y_perm.ptr != nullptr) || !opt_rows_ok(y_perm, H, dt)) return MOE_ERR_INVALID_ARG;
   if (dtopk_w && !topk_w) return MOE_ERR_INVALID_ARG;
-  if (!ws || ws_bytes < kAlign) return MOE_ERR_WORKSPACE;
+  if (!words_ok(inv_perm, topk_w, dtopk_w)) return MOE_ERR_INVALID_ARG;
+  if (!ws_ok(ws, ws_bytes, kAlign)) return MOE_ERR_WORKSPACE;
   return cuda_status(launch_combine_grad(dt, view(dout), view(y_perm), inv_perm, topk_w, T, K, H, U, view(dy_perm),
                                          dtopk_w, status_of(ws), S(stream)));
 }
@@ -171,7 +183,8 @@ moe_status moe_route_backward(const float* logits, const int32_t* topk_ids, cons
   if (T == 0) return MOE_OK;
   if (!logits || !topk_ids || !topk_w || !dtopk_w || !dlogits) return MOE_ERR_INVALID_ARG;
   if (!aligned(logits, 16) || !aligned(dlogits, 16)) return MOE_ERR_INVALID_ARG;
-  if (!ws || ws_bytes < kAlign) return MOE_ERR_WORKSPACE;
+  if (!words_ok(topk_ids, topk_w, dtopk_w)) return MOE_ERR_INVALID_ARG;
+  if (!ws_ok(ws, ws_bytes, kAlign)) return MOE_ERR_WORKSPACE;
   return cuda_status(launch_route_grad(kF32, RowsView{const_cast<float*>(logits), E}, topk_ids, topk_w, dtopk_w, T, E, K, fn,
                                        renormalize != 0, 1.f, dt, RowsView{dlogits, E}, status_of(ws), S(stream)));
 }
@@ -276,6 +289,7 @@ moe_status moe_linear_backward8(moe_dtype dt, moe_rows dy, moe_rows x, moe_rows8
                                 moe_rows dx_residual, moe_rows dx, void* dw, float* dbias, void* ws, size_t ws_bytes,
                                 void* stream) {
   if (x_ids && (!x8.q || x_div < 1 || x_rows < 0)) return MOE_ERR_INVALID_ARG;
+  if (!words_ok(x_ids)) return MOE_ERR_INVALID_ARG;
   if (!opt_rows8_ok(x8, K) || !opt_rows8_ok(z8, N)) return MOE_ERR_INVALID_ARG;
   const Kept8 k8{x8, z8, x_ids, x_ids ? x_div : 1, x_ids ? x_rows : rows};
   return linear_backward(dt, dy, x, w, z, &k8, act, expert_counts, rows, N, K, E, align, dx_residual, dx, dw, dbias, ws,
@@ -289,7 +303,8 @@ moe_status moe_pack_rows8(moe_dtype dt, moe_rows x, const int32_t* expert_counts
     return MOE_ERR_INVALID_ARG;
   if (rows == 0) return MOE_OK;
   if (!rows_ok(x, cols, dt) || !rows8_ok(x8, cols)) return MOE_ERR_INVALID_ARG;
-  if (expert_counts && (!ws || ws_bytes < kAlign)) return MOE_ERR_WORKSPACE;
+  if (!words_ok(expert_counts)) return MOE_ERR_INVALID_ARG;
+  if (expert_counts && !ws_ok(ws, ws_bytes, kAlign)) return MOE_ERR_WORKSPACE;
   return cuda_status(launch_pack_rows8(dt, view(x), expert_counts, rows, cols, E, align, view8(x8), status_of(ws), S(stream)));
 }
 
@@ -302,7 +317,8 @@ moe_status moe_unpack_rows8(moe_dtype dt, moe_rows8 x8, const int32_t* x_ids, in
   if (x_ids && (x_div < 1 || x_rows < 0)) return MOE_ERR_INVALID_ARG;
   if (rows == 0) return MOE_OK;
   if (!rows_ok(x, cols, dt) || !rows8_ok(x8, cols)) return MOE_ERR_INVALID_ARG;
-  if ((expert_counts || x_ids) && (!ws || ws_bytes < kAlign)) return MOE_ERR_WORKSPACE;
+  if (!words_ok(expert_counts, x_ids)) return MOE_ERR_INVALID_ARG;
+  if ((expert_counts || x_ids) && !ws_ok(ws, ws_bytes, kAlign)) return MOE_ERR_WORKSPACE;
   return cuda_status(launch_unpack_rows8(dt, view8(x8), x_ids, x_div, x_rows, expert_counts, rows, cols, E, align, view(x),
                                          status_of(ws), S(stream)));
 }
@@ -351,6 +367,7 @@ moe_status moe_select(moe_dtype dt, moe_rows logits, const float* e_score_bias, 
   if (K > rule.topk_groups * (E / rule.n_groups)) return MOE_ERR_INVALID_ARG;
   if (T == 0) return MOE_OK;
   if (!rows_ok(logits, E, dt) || !topk_ids || !topk_w) return MOE_ERR_INVALID_ARG;
+  if (!words_ok(e_score_bias, topk_ids, topk_w)) return MOE_ERR_INVALID_ARG;
   const SelectRule r{rule.fn, rule.n_groups, rule.topk_groups, rule.group_best, rule.renormalize != 0, rule.scale};
   return cuda_status(launch_select(dt, view(logits), e_score_bias, T, E, K, r, topk_ids, topk_w, S(stream)));
 }
@@ -364,7 +381,8 @@ moe_status moe_select_backward(moe_dtype dt, moe_rows logits, const int32_t* top
   if (dt != MOE_F32 && grad_dt != dt) return MOE_ERR_UNSUPPORTED;
   if (T == 0) return MOE_OK;
   if (!rows_ok(logits, E, dt) || !topk_ids || !topk_w || !dtopk_w || !rows_ok(dlogits, E, grad_dt)) return MOE_ERR_INVALID_ARG;
-  if (!ws || ws_bytes < kAlign) return MOE_ERR_WORKSPACE;
+  if (!words_ok(topk_ids, topk_w, dtopk_w)) return MOE_ERR_INVALID_ARG;
+  if (!ws_ok(ws, ws_bytes, kAlign)) return MOE_ERR_WORKSPACE;
   return cuda_status(launch_route_grad(dt, view(logits), topk_ids, topk_w, dtopk_w, T, E, K, fn, renormalize != 0, scale,
                                        grad_dt, view(dlogits), status_of(ws), S(stream)));
 }
