@@ -1267,7 +1267,7 @@ struct LinPlan {
 // any case (experts' weight gradient).
 LinPlan lin_plan(const LinearShape& s, int i_cols, bool gated, long long j, long long q, bool b_mn, bool whole) {
   LinPlan p{};
-  const int sms = num_sms(), pairs = sms / 2, E = s.counts ? s.E : 0;
+  const int sms = num_sms(), pairs = sms > 1 ? sms / 2 : 1, E = s.counts ? s.E : 0;      // (no device: one SM)
   const long long slabs = (q + kLinSlab - 1) / kLinSlab;
   p.lanes = kLinBI;
   p.split = 1;
