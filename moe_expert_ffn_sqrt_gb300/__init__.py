@@ -2,10 +2,12 @@
 
 Argument marshalling only: every function takes torch CUDA tensors, checks them, and calls
 the C entry point of the same name on the current CUDA stream.  There is no fallback: if
-libmoe.so is missing or fails to load, importing the compute functions raises.
+libmoe.so is missing or fails to load, importing the compute functions raises.  (_native.so only checks and passes on
+arguments faster; without it the same is done here, after one warning.)
 """
 import ctypes
 import os
+import warnings
 
 import torch
 
@@ -56,17 +58,25 @@ _lib = None
 _fast = None
 
 
+class _NoNative:
+    """In the place of _native.so where it does not load: answers None to every call, whose own checks and ctypes call then run."""
+
+    def __getattr__(self, name):
+        return lambda *args: None
+
+
 def _load_native():
-    """The calls around the layer with their arguments marshalled in C++ (raises if it was not built)."""
+    """The calls around the layer with their arguments marshalled in C++; without _native.so they take 5 to 10 us longer."""
     global _fast
     if _fast is None:
         lib()
         try:
             from . import _native as n
+            n.bind(LIB_PATH)
         except ImportError as e:
-            raise RuntimeError("_native.so was not built for this torch: build it with "
-                               "`python -m moe_expert_ffn_sqrt_gb300.build`") from e
-        n.bind(LIB_PATH)
+            warnings.warn(f"_native.so was not built for this torch ({e}): calls around the layer are marshalled in Python; build "
+                          "it with `python -m moe_expert_ffn_sqrt_gb300.build`", RuntimeWarning, stacklevel=3)
+            n = _NoNative()
         _fast = n
     return _fast
 
@@ -862,8 +872,8 @@ def rms_norm_backward(dy, x, weight, eps, dx, ws, dweight=None, dsum=None):
     _at_home(dy, x, weight, dx, ws, dweight, dsum)
     _check(lib().moe_rms_norm_backward(_dtype(dy, "dy"), _rows(dy, dt, TH, "dy"), _rows(x, dt, TH, "x"),
                                        _full(weight, torch.float32, (H,), "weight"), eps, _rows(dsum, dt, TH, "dsum"), T, H,
-                                       _rows(dx, dt, TH, "dx"), _full(dweight, torch.float32, (H,), "dweight"), _space(ws),
-                                       ws.numel(), _stream()), "moe_rms_norm_backward")
+                                       _rows(dx, dt, TH, "dx"), _full(dweight, torch.float32, (H,), "dweight"), *_ws_opt(ws),
+                                       _stream()), "moe_rms_norm_backward")
 
 
 def select(logits, topk_ids, topk_w, score_fn, e_score_bias=None, n_groups=1, topk_groups=1, group_best=2, renormalize=True,
@@ -903,7 +913,7 @@ def select_backward(logits, topk_ids, topk_w, dtopk_w, dlogits, ws, score_fn, re
                                      _full(topk_ids, torch.int32, TK, "topk_ids"), _full(topk_w, torch.float32, TK, "topk_w"),
                                      _full(dtopk_w, torch.float32, TK, "dtopk_w"), T, E, K,
                                      fn, int(renormalize), scale, _dtype(dlogits, "dlogits"),
-                                     _rows(dlogits, dlogits.dtype, (T, E), "dlogits"), _space(ws), ws.numel(), _stream()),
+                                     _rows(dlogits, dlogits.dtype, (T, E), "dlogits"), *_ws_opt(ws), _stream()),
            "moe_select_backward")
 
 
@@ -976,7 +986,7 @@ def linear_backward8(dy, w, ws, x=None, x8=None, z=None, z8=None, x_ids=None, x_
                                       _full(expert_counts, torch.int32, (E,), "expert_counts"), rows, N, K, E, align,
                                       _rows(dx_residual, dt, (rows, K), "dx_residual"), _rows(dx, dt, (rows, K), "dx"),
                                       _full(dw, dt, w.shape, "dw"), _full(dbias, torch.float32, w.shape[:-1], "dbias"),
-                                      _space(ws), ws.numel(), _stream()), "moe_linear_backward8")
+                                      *_ws_opt(ws), _stream()), "moe_linear_backward8")
 
 
 def selftest_wait_timeout(ws, mode):
