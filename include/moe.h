@@ -596,8 +596,10 @@ typedef struct {
  * x [T, H]; residual, sum, y, y8 [T, H] are optional, one output at least; weight [H] fp32, 16-byte aligned.  The norm
  * is of the rounded sum, stored or not; y and y8 are each rounded once from fp32.  sum and y may be x or residual
  * themselves (not both the same one: refused).  1 <= H <= 2^24, eps >= 0.  The squares are added up in fp32: a row whose
- * sum of squares passes 3.4e38 comes out as zeros (its infinities as NaN), one whose sum is 0 needs an eps.  A row's sum is
- * taken in an order that goes by dt, T, H, the rows' 16-byte alignment and whether there is a residual, not by the outputs.
+ * sum of squares passes 3.4e38 comes out as zeros (its infinities as NaN), one whose sum is 0 needs an eps, and one of values
+ * below 1e-19 an eps of 1e-35 or more (its squares have few bits or none).  A row's sum is taken in an order that goes by dt,
+ * T, H, whether there is a residual, and whether all of x, residual, sum and y that are given have their rows on 16-byte
+ * boundaries: a call with a y off them may differ in the last bits of y8 from one without it.
  * (A bounded wait inside that runs out leaves NaN.) */
 moe_status moe_rms_norm(moe_dtype dt, moe_rows x, moe_rows residual, const float* weight, float eps, int T, int H,
                         moe_rows sum, moe_rows y, moe_rows8 y8, void* stream);
@@ -608,8 +610,9 @@ moe_status moe_workspace_size_norm(int T, int H, size_t* bytes);
 /* Gradients of moe_rms_norm with respect to sum (x and residual have the same) and weight.  x: the forward's sum (its
  * x where there was no residual).  dsum [T, H] (optional): the gradient that reaches sum on its other way, added to dx.
  * dx [T, H] and dweight [H] (fp32, 16-byte aligned) are optional, one at least.  dx may be dy, x or dsum itself.  No
- * rows: dweight is zero.  Sums over rows are taken in a fixed order (by T, H and alignment).  ws 16-byte
- * aligned, its first 256 bytes the status word, zero-filled once; calls that may overlap, replays of captured ones among
+ * rows: dweight is zero.  Sums are taken in a fixed order (by dt, T, H, whether there is a dsum, and whether all of dy, x, dsum
+ * and dx that are given have their rows on 16-byte boundaries); a row's sum of squares is the forward's, with its limits.  ws
+ * 16-byte aligned, its first 256 bytes the status word, zero-filled once; calls that may overlap, replays of captured ones among
  * them, take a workspace each. */
 moe_status moe_rms_norm_backward(moe_dtype dt, moe_rows dy, moe_rows x, const float* weight, float eps, moe_rows dsum,
                                  int T, int H, moe_rows dx, float* dweight, void* ws, size_t ws_bytes, void* stream);
