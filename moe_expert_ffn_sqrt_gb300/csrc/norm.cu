@@ -324,7 +324,8 @@ constexpr int kRingAhead = 60 * 1024;
 // alone 44.8 us instead of 68 and to fp32 44.6 of 47.7 (with residual 95 of 88), 9000 x 6001 bf16 167 instead of 208.  In 16
 // bits on boundaries they do not fit the 64 registers: 16384 x 7168 to 8 bits alone 100 us of 110, but to bf16 84 of 75 and
 // with residual 191 of 159.  From 320 to 440 packs either is as fast (2801 odd bf16 columns 33.9 with four, 32.5; 3501 fp16
-// 40.3, 40.9).  Three where they make one warp of a group of two: 9887 x 545 fp16 36 us, so 25.8.
+// 40.3, 40.9).  Three where they make one warp of a group of two (65 to 96 packs): 2000 x 521 bf16 4.7 us instead of 6.1, 20000
+// x 765 22.4 instead of 35.0, 2000 x 261 fp32 4.0 of 5.2, 20000 x 383 18.2 of 25.9.
 constexpr int kRingPer = 2, kRingWide = 512;
 
 struct Ring {
@@ -961,8 +962,10 @@ NormPlan norm_plan(int T, int H, int dt, const NormLimits& m, int inputs, bool a
     p.grid = ctas < all ? ctas : all;
     return p;
   }
-  // few rows: all at a time, a pack a thread (500 x 2048 bf16 3.0 us, through the ring 3.6; 333 x 1001 fp32 backward 5.4, 7.3;
-  // but 500 x 2048 backward, whose partial sums of dw are 4 MB then, 10.1, 6.5)
+  // few rows: all at a time, a pack a thread (500 x 2048 bf16 3.0 us, through the ring 3.6).  Backward as long as the partial
+  // sums of dw, one row of them for each row, are few: 160 x 1024 bf16 4.3 us of 5.5, but 304 x 1024 6.1 of 5.5, 240 x 1536 6.5
+  // of 5.6 and 456 x 2048 9.3 of 5.9; off boundaries, where the ring takes longer, 160 x 2001 6.5 of 7.4, but 160 x 2500 8.6 of
+  // 7.6; fp32, with twice the threads, 304 x 1001 5.9 of 6.6 and 304 x 1024 4.9 of 5.0, but 456 x 1024 5.5 of 5.3
   const int one = (packs + 31) / 32 * 32, at_once = one <= 1024 ? 1024 / one : 1;
   const bool few = T <= sms || (T <= sms * (at_once < 4 ? at_once : 4) && static_cast<long long>(T) * H <= m.few);
   if (packs <= m.ring_per * 32 * m.ring_warps && !few) {
@@ -1003,7 +1006,8 @@ NormPlan norm_forward_plan(int T, int H, int dt, int inputs, bool al) {
   return norm_plan(T, H, dt, NormLimits{128, 2, per, threads, warps < kRingWarps ? warps : kRingWarps, 1, 1 << 30}, inputs, al);
 }
 NormPlan norm_grad_plan(int T, int H, int dt, int inputs, bool al) {
-  return norm_plan(T, H, dt, NormLimits{64, 1, kRingPer, kRingGradThreads, kRingGradWarps, 2, 400000}, inputs, al);
+  return norm_plan(T, H, dt, NormLimits{64, 1, kRingPer, kRingGradThreads, kRingGradWarps, 2, dt != kF32 && al ? 250000 : 350000},
+                   inputs, al);
 }
 
 template <class K, class A>
