@@ -74,7 +74,7 @@ struct Scores {
     if (FN == 0) {
       // (d is rounded by up to |d| 2^-24, which would be the exponential's relative error: it gets the rest back)
       const float d = l - lmax, back = d - l, rest = (l - (d - back)) - (lmax + back), e = expf(d);
-      return l == -INFINITY ? 0.f : fmaf(e, rest, e) / sum;
+      return l == -INFINITY ? 0.f : (e > 0.f ? fmaf(e, rest, e) : e) / sum;       // (d may be -infinity: no rest)
     }
     if (FN == 1) return root_softplus(l);
     return 1.f / (1.f + expf(-l));

@@ -108,3 +108,19 @@ def test_softmax_weights_as_they_are(M, E, spread):
     R.check(w, ref, ref * units * 2.0 ** -24 * 1.001 + 1e-37, "w")
     # and not off to one side: the mean of 32768 of them is within a third of a unit
     assert abs(float((w.double() / ref - 1)[ref > 1e-30].mean())) < 2.0 ** -24 / 3
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16, torch.float16])
+def test_logits_of_a_types_largest_and_lowest_value(M, dt):
+    """Their difference is past fp32's range: a weight of zero, not NaN."""
+    f = torch.finfo(dt)
+    l = rows(12, 16, -2, 2, dt, 9)
+    l[:4, 3], l[2:8, 5], l[:, 9] = f.max, f.max, f.min
+    l[6:, 10:14] = f.max
+    push = (torch.arange(16) == 9).float()
+    for fn in ("softmax", "sqrt_softplus", "sigmoid"):
+        for bias in (None, torch.zeros(16), push * (50 if fn != "sqrt_softplus" else 1e30)):
+            for renorm in (True, False):
+                for K in (3, 5):
+                    check(M, l, bias, K, fn, renorm=renorm)
+                    check(M, l, bias, K, fn, renorm=renorm, G=4, KG=2)
