@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(kSelectWarps * 32, PER <= 8 ? kSelectCtas : 1)
       for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
     }
     const FastScores<FN> fast{lmax, 1.f / sum};
-    const float near = fast.template apart<PER>();
+    const float near = fmaxf(fast.template apart<PER>(), 0.f);         // (NaN: there are no scores but masked experts' zeros)
     if (a.bias) {
 #pragma unroll
       for (int i = 0; i < PER; ++i)
@@ -356,9 +356,11 @@ __global__ void __launch_bounds__(kSelectWarps * 32, PER <= 8 ? kSelectCtas : 1)
         }
       }
       uint32_t mine = used && sub == 0 ? ordered(worth) : 0;
-      // (a NaN logit is -infinity in the keys here, whose score is 0: where one may count, all groups take the second look)
-      bool nan = false;
-      if (!a.bias && __any_sync(kAll, f2 == -INFINITY)) {
+      // (without a bias a NaN logit is -infinity in the keys here, whose score is 0: where one may count, all groups take the
+      // second look; where all scores are NaN but masked experts' zeros, from all of their experts)
+      const bool none = FN == 0 && !a.bias && sum != sum;
+      bool nan = none;
+      if (!a.bias && !none && __any_sync(kAll, f2 == -INFINITY)) {
 #pragma unroll
         for (int i = 0; i < PER; ++i) nan = nan || v[i] != v[i];
         nan = __any_sync(kAll, nan);
@@ -379,7 +381,7 @@ __global__ void __launch_bounds__(kSelectWarps * 32, PER <= 8 ? kSelectCtas : 1)
         // groups that are surely in, and those that may be: the latter in 64 bits, from their experts that may be among
         // the best two
         const bool in = used && worth - next > tol, maybe = used && !in && !(last - worth > tol);
-        const uint32_t bound = !maybe ? 0xffffffffu : a.bias ? ordered(f2 - tol) : two ? g2 : g1;
+        const uint32_t bound = !maybe ? 0xffffffffu : a.bias ? ordered(f2 - tol) : none ? 1u : two ? g2 : g1;
         const int c = collect([&](int i) { return maybe && key[i] >= bound; });
         all64 = c > 32;
         if (!all64) {

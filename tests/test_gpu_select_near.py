@@ -4,7 +4,7 @@ import torch
 
 import around_ref as A
 from gpu_util import ensure_lib
-from test_gpu_select import check
+from test_gpu_select import check, run
 
 pytestmark = pytest.mark.gpu
 
@@ -69,3 +69,30 @@ def test_groups_whose_sum_fp32_cannot_hold(M, fn):
         for KG in (1, 2, 3, 5, 6, 7):
             for best in (1, 2):
                 check(M, l, b.reshape(-1), 3, fn, G=8, KG=KG, best=best)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("E,G,KG,K,best", [(16, 4, 1, 3, 2), (16, 4, 2, 5, 1), (96, 12, 3, 8, 2), (256, 8, 4, 8, 2), (384, 12, 1, 10, 2)])
+def test_softmax_rows_without_a_sum(M, bad, E, G, KG, K, best):
+    """A NaN or infinite logit leaves a softmax row no sum: every score is NaN (a key of -infinity) but a masked expert's, which
+    is 0 under every score function.  Groups go by that, experts without a bias by their logits."""
+    g = torch.Generator().manual_seed(E + K)
+    inf = float("inf")
+    l = torch.randn(80, E, generator=g)
+    l[torch.rand(80, E, generator=g) < torch.linspace(0, 0.9, 80)[:, None]] = -inf
+    l[torch.arange(80), torch.randint(0, E, (80,), generator=g)] = bad
+    ids, w = run(M, l, None, K, "softmax", G=G, KG=KG, best=best)
+    n = E // G
+    for t in range(80):
+        key = [0.0 if v == -inf else -inf for v in l[t].tolist()]
+        order = [-inf if v != v else v for v in l[t].tolist()]
+        worth = [sum(sorted(key[i * n:(i + 1) * n], reverse=True)[:best]) for i in range(G)]
+        groups = sorted(range(G), key=lambda i: (-worth[i], i))[:KG]
+        allowed = [e for i in groups for e in range(i * n, (i + 1) * n)]
+        assert ids[t].tolist() == sorted(allowed, key=lambda e: (-order[e], e))[:K], t
+    # and two biases of fp32's lowest value in such a row
+    low = torch.full((E,), torch.finfo(torch.float32).min)
+    low[:n] = -inf
+    l[:, n:2 * n] = -inf
+    ids, _ = run(M, l, low, min(K, n), "softmax", G=G, KG=1, best=best)
+    assert (ids >= n).all()
