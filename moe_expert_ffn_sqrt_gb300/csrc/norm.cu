@@ -7,12 +7,22 @@
 // row gives both of the backward's sums (s^2 and s g), so nothing but s is kept from the forward.
 //
 // HBM bounds them where rows are many: each value is read and written once.  16384 x 7168 bf16 with residual, 16-bit and
-// 8-bit outputs, 1.06 GB in 160 us (98% of a plain copy's rate); without residual 114 us (76%: about 170 instructions a
-// pack); gradients of 8192 x 7168 with dsum 75.5 us (92%), 4 us of it the launch that adds the CTAs' parts of dw up.  8192 x
-// 4096 fp32 88 us (95%), 16384 x 2048 bf16 49 (91%), its gradients 43 (92%).  Rows that start on no 16-byte boundary are
-// bound by the shifts' instructions: 9000 x 6001 bf16 167 us of 72, 1450 x 2521 fp16 17 of 5.  A row of 7168 alone takes 2.9
-// us: launch, one load, the reduction's two steps, the stores.  (Reading each row twice, from L1 and L2 the second time:
-// 205 us and, the gradients, 266; a row in registers with the next one's loads ahead, two CTAs of 448 threads: 243, 151.)
+// 8-bit outputs, 1.06 GB in 159 us (98% of a plain copy's rate); without residual 114 us (76%: about 170 instructions a
+// pack); gradients of 8192 x 7168 with dsum 75.2 us (92%), 4 us of it the launch that adds the CTAs' parts of dw up.  8192 x
+// 4096 fp32 with residual 81 us (98%), 16384 x 2048 bf16 42 (94%), its gradients 44 (90%).  Rows that start on no 16-byte
+// boundary are bound by the shifts' instructions: 9000 x 6001 bf16, residual and all outputs, 168 us of 72 (no residual, y
+// alone 76 of 32), 20000 x 300 31 of 8, 1450 x 2521 fp16 17 of 5.  A row of 7168 alone takes 2.9 us: launch, one load, the
+// reduction's two steps, the stores.
+//
+// Rows past the ring are further from their bytes.  Gradients of 1025 to 2048 packs, one CTA of 1024 threads per SM with
+// nothing of the next row on its way and, in 16 bits, spilled registers: 8192 x 8704 bf16 with dsum 163 us of 84, 2000 x 12000
+// 62 of 28, 8192 x 7168 fp32 155 of 138.  Beyond 2048 packs x and dy are read four times (sums, dw, sums again, dx), w an
+// element at a time, which keeps L1 busy for 94% of the time: 2000 x 17000 bf16 165 us of 40, 2000 x 17001 250, 2000 x 30000
+// 285 of 71, 3000 x 9000 fp32 166 of 64.  Forward, twice: 2000 x 17000 bf16 with residual to 16 bits 68 us of 40, off
+// boundaries 83.
+//
+// (Reading each row twice, from L1 and L2 the second time: 205 us and, the gradients, 266; a row in registers with the next
+// one's loads ahead, two CTAs of 448 threads: 243, 151.)
 #include "rows8.cuh"
 
 namespace moe {

@@ -17,10 +17,12 @@
 // equal logit and bias are an exact tie and need no second look, unless they are the last one in and the first one out and a
 // third, other key is near them.  Without a bias keys go by the logits themselves, which all scores rise with.
 //
-// 16384 tokens of 256 experts in 8 groups, 6 of them, sigmoid and bias: 19.4 us, of 2.6 for the bytes.  The instructions
-// bound it, about 900 a token, with the schedulers busy for 60% of the time (64 registers, 32 warps per SM; 80 registers
-// 20.9 us, five CTAs of 8 warps 21.4).  The second looks take 0.2 us of it.  K rounds of a maximum instead of the ranking
-// took 43 us.  8 tokens: 3.5 us, one warp's chain.  Where all experts' keys are alike (say a row of padding, a zero bias and
+// 16384 tokens of 256 experts in 8 groups, 4 of them used, K = 6: sigmoid and bias 19.1 us, of 2.6 for the bytes; sqrt(softplus)
+// 27.5 (an accurate exponential, logarithm and root for every expert), softmax 29.0 (the row's sum); without a bias, where keys
+// are the logits, 16.0, 18.0 and 22.9.  One group, K = 8: 16.5, 24.7 and 26.8, without a bias 12.9, 14.3 and 15.6.  The
+// instructions bound it, 861 a token (sigmoid), with the schedulers busy for 60% (64 registers, 32 warps per SM; 80 registers
+// 20.9 us, five CTAs of 8 warps 21.4).  The second looks take 0.2 us of it.  K rounds of a maximum instead of the ranking took
+// 43 us.  8 tokens: 3.5 us, one warp's chain.  Where all experts' keys are alike (say a row of padding, a zero bias and
 // groups) the groups' order takes a 64-bit evaluation of every expert, some 10 us for the warps that have such tokens.
 #include "rows.cuh"
 
@@ -546,7 +548,7 @@ __global__ void __launch_bounds__(kSelectWarps * 32, PER <= 8 ? kSelectCtas : 1)
 
 template <int FN, int PER, int V>
 cudaError_t select_launch(const SelectArgs& a, cudaStream_t stream) {
-  // (as many tokens to every warp that is there at a time: 16384 tokens 21.8 us instead of 19.4; a warp a token 22)
+  // (as many tokens to every warp that is there at a time: 16384 tokens 21.8 us when this took 19.4; a warp a token 22)
   const int ctas = (a.T - 1) / kSelectWarps + 1, most = 2 * kSelectCtas * num_sms();
   return launch_pdl(select_kernel<FN, PER, V>, dim3(ctas < most ? ctas : most), dim3(kSelectWarps * 32), 0, stream, a);
 }
