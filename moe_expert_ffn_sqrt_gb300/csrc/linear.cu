@@ -1630,41 +1630,90 @@ __global__ void __launch_bounds__(32 * kActRowLanes, Z8 ? 4 : 6)
   }
 }
 
+// Where the experts' rows lie: expert e's segment starts at row[e] and has cnt[e] rows; end[e]: the chunks of `chunk` rows of
+// experts 0 to e.  CTAs that walk over all experts' chunks share the work evenly, however the rows are spread.
+struct LiveChunks {
+  int row[kLinearMaxExperts], cnt[kLinearMaxExperts], end[kLinearMaxExperts];
+};
+
+// What the threads before this one of a CTA of 256 have in all, no more than `most` (sums: a warp's, one array per call).
+__device__ __forceinline__ int sum_before(int mine, int most, int (&sums)[8]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int all = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, all, d);
+    if (lane >= d) all = min(all + o, most);
+  }
+  int before = __shfl_up_sync(0xffffffffu, all, 1);
+  if (lane == 0) before = 0;
+  if (lane == 31) sums[warp] = all;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) before = min(before + sums[w], most);
+  return before;
+}
+
+// Called by the whole CTA of 256 threads; where `report`, segments that would leave the buffers are recorded; they are cut in
+// any case, as in expert_segment.
+__device__ __forceinline__ void live_chunks(const int32_t* counts, int E, int align, int rows, int chunk, bool report,
+                                            LiveChunks& s, uint32_t* status) {
+  __shared__ int s_sums[2][8];
+  const int q = (E + 255) / 256, e0 = threadIdx.x * q;
+  int padded = 0, chunks = 0;
+  for (int e = e0; e < min(e0 + q, E); ++e) {
+    const int c = min(max(__ldg(counts + e), 0), rows);
+    padded = min(padded + (c + align - 1) / align * align, rows);
+  }
+  int seg = sum_before(padded, rows, s_sums[0]);
+  for (int e = e0; e < min(e0 + q, E); ++e) {
+    const int all = __ldg(counts + e), cnt = min(max(all, 0), rows - seg);
+    if (report && (all < 0 || all > cnt)) record_error(status, kDevErrIndex);
+    s.row[e] = seg;
+    s.cnt[e] = cnt;
+    chunks += (cnt + chunk - 1) / chunk;
+    seg = min(seg + (min(max(all, 0), rows) + align - 1) / align * align, rows);
+  }
+  int end = sum_before(chunks, 0x7fffffff, s_sums[1]);
+  for (int e = e0; e < min(e0 + q, E); ++e) {
+    end += (s.cnt[e] + chunk - 1) / chunk;
+    s.end[e] = end;
+  }
+  __syncthreads();
+}
+
 // The same values without the bias gradient's sums: `lanes` threads to a row (fewer than a CTA's where rows are narrow), two
-// rows of a thread on their way together; blockIdx.x: which `lanes` groups of eight columns, so that neighbouring CTAs read
+// rows of a thread on their way together (experts: CTAs walk over chunks of `chunk` rows, act_walk); blockIdx.x: which `lanes` groups of eight columns, so that neighbouring CTAs read
 // one row.  Beside act_grad_kernel, with the dx product of K = 64 behind both: 4096 x 2048 SiLU 18.3 us of 21.1 and GELU 21.7
 // of 28.7, 128 x 4096 SwiGLU 11.0 of 13.1, 16384 x 7168 SiLU 163.2 of 162.2 and GELU 180.6 of 185.7, 1000 x 4096 ReLU 14.9 of
 // 14.5; from 8 bits, 6971 x 80 ReLU 4 of 17 and 7 experts of 288 columns 6 of 14 (a warp of act_grad_kernel takes 256 columns
 // of one row).  With one row
 // at a time and six CTAs per SM the SiLU case of 16384 x 7168 is 174, with CTAs of one column group side by side 163.6.
-template <class T, bool Z8>
+template <class T, bool Z8, bool EXPERTS>
 __global__ void __launch_bounds__(256, 4)
     act_grad_rows_kernel(const uint16_t* __restrict__ dy, long long lddy, const ZRows<T, Z8> z, int act,
-                         const int32_t* __restrict__ counts, int align, int rows, int N, uint16_t* __restrict__ dz,
-                         long long lddz, int lanes, uint32_t* status) {
+                         const int32_t* __restrict__ counts, int E, int align, int rows, int N, uint16_t* __restrict__ dz,
+                         long long lddz, int lanes, int chunk, uint32_t* status) {
   constexpr int kAhead = 2;
   grid_dependency_wait();
   grid_launch_dependents();
-  int cnt, seg;
-  expert_segment(counts, blockIdx.y, align, rows, blockIdx.x == 0 && blockIdx.z == 0, seg, cnt, status);
   const bool gated = act == kActSwiglu;
-  const int cols = gated ? N / 2 : N;
-  const int c = (blockIdx.x * lanes + threadIdx.x % lanes) * 8, per = 256 / lanes, step = gridDim.z * per;
-  if (c >= cols) return;
-  for (long long r = static_cast<long long>(blockIdx.z) * per + threadIdx.x / lanes; r < cnt; r += kAhead * step) {
+  const int cols = gated ? N / 2 : N, per = 256 / lanes;
+  const int c = (blockIdx.x * lanes + threadIdx.x % lanes) * 8, mine = threadIdx.x / lanes;
+  // rows r and r + step, below past
+  const auto two_rows = [&](long long r, long long step, long long past) {
     Pack<T> g[kAhead];
     decltype(z.get(0, 0)) a[kAhead], b[kAhead];
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
-      const long long row = seg + (r + k * step < cnt ? r + k * step : r);
+      const long long row = r + k * step < past ? r + k * step : r;
       g[k] = load_pack<T>(dy + row * lddy + c);
       a[k] = z.get(row, c);
       if (gated) b[k] = z.get(row, cols + c);
     }
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
-      if (r + k * step >= cnt) break;
-      uint16_t* out = dz + (seg + r + k * step) * lddz + c;
+      if (r + k * step >= past) break;
+      uint16_t* out = dz + (r + k * step) * lddz + c;
       Pack<T> o;
       if (gated) {
         Pack<T> o2;
@@ -1688,6 +1737,33 @@ __global__ void __launch_bounds__(256, 4)
       }
       store_pack<T>(out, o);
     }
+  };
+  if constexpr (EXPERTS) {
+    __shared__ LiveChunks live;
+    live_chunks(counts, E, align, rows, chunk, blockIdx.x == 0 && blockIdx.z == 0, live, status);
+    if (c >= cols) return;
+    const int all = live.end[E - 1];
+    int e = -1, end = 0, base = 0, past = 0;        // the expert, where its chunks end, its rows' place less its chunks', its end
+    for (int j = blockIdx.z; j < all; j += gridDim.z) {
+      if (j >= end) {                               // the first expert whose chunks reach past j
+        int lo = e + 1, hi = E - 1;
+        while (lo < hi) {
+          const int mid = (lo + hi) / 2;
+          if (j >= live.end[mid]) lo = mid + 1;
+          else hi = mid;
+        }
+        e = lo;
+        end = live.end[e];
+        base = live.row[e] - (e ? live.end[e - 1] : 0) * chunk;
+        past = live.row[e] + live.cnt[e];
+      }
+      const int first = base + j * chunk, last = min(past, first + chunk);
+      for (int r = first + mine; r < last; r += kAhead * per) two_rows(r, per, last);
+    }
+  } else {
+    if (c >= cols) return;
+    const int step = gridDim.z * per;
+    for (long long r = static_cast<long long>(blockIdx.z) * per + mine; r < rows; r += kAhead * step) two_rows(r, step, rows);
   }
 }
 
@@ -1695,11 +1771,29 @@ __global__ void __launch_bounds__(256, 4)
 // most, 16 where each has five steps or more all the same (16384 x 7168 SiLU 164.4 us with 8, 163.2 with 16, GELU 183.4 and
 // 180.5; but 4096 x 2048, 1.7 steps with 16, GELU 21.5 and 22.4), and no more than give a CTA two steps while that leaves two
 // CTAs per SM or so (1000 x 1408 SiLU 10.8 us with a step each, so 10.1; 2000 x 1408 ReLU 12.0, 11.3).
-unsigned act_row_blocks(long long rows, int E, int per, int nz) {
-  const long long steps = (rows / E + per) / per, beside = static_cast<long long>(nz) * E, most = 16LL * num_sms() / beside;
+unsigned act_row_blocks(long long rows, int per, int nz) {
+  const long long steps = (rows + per) / per, most = 16LL * num_sms() / nz;
   long long n = steps >= 5 * most ? most : steps < most / 2 ? steps : most / 2;
-  if (n * beside >= 2 * num_sms() && n > (steps + 1) / 2) n = (steps + 1) / 2;
+  if (n * nz >= 2 * num_sms() && n > (steps + 1) / 2) n = (steps + 1) / 2;
   return static_cast<unsigned>(n < 1 ? 1 : n);
+}
+
+// The same for experts with `rows` rows in all, and the rows of a chunk.  CTAs that each had an expert took as long as the
+// largest one: 12288 rows of 256 experts, SwiGLU, 4096 columns, routed at random with uneven shares 145 us, so 103; all alike 114
+// and 101; half of the rows one expert's, a quarter the next one's, .. 783 and 77.  Chunks of eight steps where a CTA has 16
+// or more (12288 rows of 32 experts, GELU, 4096 columns 97 us, with two 104.6; but 4096 of 8, 2048 columns, three steps to a CTA,
+// SwiGLU 22.4 with eight, 18.3 with two), and then 8 CTAs per SM, 4 otherwise (that case 19.0 with 8).
+struct ActWalk {
+  unsigned ctas;
+  int chunk;
+};
+ActWalk act_walk(long long rows, int E, int per, int nz) {
+  const long long most = 8LL * num_sms() / nz;
+  if (rows >= 16 * most * per) return {static_cast<unsigned>(most < 1 ? 1 : most), 8 * per};
+  long long n = rows / (2 * per) + E;               // (an expert's last chunk may be short)
+  if (n > rows) n = rows;
+  if (n > most / 2) n = most / 2;
+  return {static_cast<unsigned>(n < 1 ? 1 : n), 2 * per};
 }
 
 __global__ void __launch_bounds__(256) bias_sum_kernel(const float* __restrict__ part, int S, int N, long long total,
@@ -1753,10 +1847,13 @@ cudaError_t launch_act_grad(const LinearShape& p, RowsView dy, RowsView z, Rows8
       int lanes = 256;
       while (lanes > 8 && (packs + lanes - 1) / lanes * lanes - packs > packs / 8) lanes /= 2;
       const int nz = (packs + lanes - 1) / lanes, per = 256 / lanes;
-      const unsigned nx = act_row_blocks(p.counts ? live : p.rows, E, per, nz);
-      return launch_pdl(act_grad_rows_kernel<T, Z8>, dim3(static_cast<unsigned>(nz), static_cast<unsigned>(E), nx), dim3(256), 0,
-                        stream, static_cast<const uint16_t*>(dy.ptr), dy.ld, zr, act, p.counts, p.align, p.rows, p.N,
-                        static_cast<uint16_t*>(dz.ptr), dz.ld, lanes, status);
+      // (rows that are likely there: at least one in each aligned block of them)
+      const ActWalk walk = p.counts ? act_walk(live > p.rows / p.align ? live : p.rows / p.align, E, per, nz)
+                                    : ActWalk{act_row_blocks(p.rows, per, nz), 0};
+      const auto kernel = p.counts ? act_grad_rows_kernel<T, Z8, true> : act_grad_rows_kernel<T, Z8, false>;
+      return launch_pdl(kernel, dim3(static_cast<unsigned>(nz), 1, walk.ctas), dim3(256), 0, stream,
+                        static_cast<const uint16_t*>(dy.ptr), dy.ld, zr, act, p.counts, E, p.align, p.rows, p.N,
+                        static_cast<uint16_t*>(dz.ptr), dz.ld, lanes, walk.chunk, status);
     }
     return launch_pdl(act_grad_kernel<T, Z8>, grid, dim3(32 * kActRowLanes), 0, stream, static_cast<const uint16_t*>(dy.ptr),
                       dy.ld, zr, act, p.counts, E, p.align, p.rows, p.N, static_cast<uint16_t*>(dz.ptr), dz.ld, pp, S, status);
