@@ -1682,12 +1682,13 @@ __device__ __forceinline__ void live_chunks(const int32_t* counts, int E, int al
 }
 
 // The same values without the bias gradient's sums: `lanes` threads to a row (fewer than a CTA's where rows are narrow), two
-// rows of a thread on their way together (experts: CTAs walk over chunks of `chunk` rows, act_walk); blockIdx.x: which `lanes` groups of eight columns, so that neighbouring CTAs read
-// one row.  Beside act_grad_kernel, with the dx product of K = 64 behind both: 4096 x 2048 SiLU 18.3 us of 21.1 and GELU 21.7
-// of 28.7, 128 x 4096 SwiGLU 11.0 of 13.1, 16384 x 7168 SiLU 163.2 of 162.2 and GELU 180.6 of 185.7, 1000 x 4096 ReLU 14.9 of
-// 14.5; from 8 bits, 6971 x 80 ReLU 4 of 17 and 7 experts of 288 columns 6 of 14 (a warp of act_grad_kernel takes 256 columns
-// of one row).  With one row
-// at a time and six CTAs per SM the SiLU case of 16384 x 7168 is 174, with CTAs of one column group side by side 163.6.
+// rows of a thread on their way together (experts: CTAs walk over chunks of `chunk` rows, act_walk); blockIdx.x: which `lanes`
+// groups of eight columns, so that neighbouring CTAs read one row.  Beside act_grad_kernel, with the dx product of K = 64 behind
+// both: 4096 x 2048 SiLU 18.3 us of 21.1 and GELU 21.7 of 28.7, 128 x 4096 SwiGLU 11.0 of 13.1, 16384 x 7168 SiLU 163.2 of 162.2
+// and GELU 180.6 of 185.7, 1000 x 4096 ReLU 14.9 of 14.5, 4096 rows of 8 experts, 2048 columns, all alike, GELU 26.4 of 24.2;
+// from 8 bits, 6971 x 80 ReLU 4 of 17 and 7 experts of 288 columns 6 of 14 (a warp of act_grad_kernel takes 256 columns of one
+// row).  With one row at a time and six CTAs per SM the SiLU case of 16384 x 7168 is 174, with CTAs of one column group side by
+// side 163.6.
 template <class T, bool Z8, bool EXPERTS>
 __global__ void __launch_bounds__(256, 4)
     act_grad_rows_kernel(const uint16_t* __restrict__ dy, long long lddy, const ZRows<T, Z8> z, int act,
